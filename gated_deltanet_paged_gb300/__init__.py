@@ -1,4 +1,5 @@
-"""Paged Gated Delta-Rule (GDN) prefill and decode for GB300 (sm_103a).
+"""Paged Gated Delta-Rule (GDN) prefill and decode for GB300 (sm_103a), and the
+attention layer that runs over the same page table.
 
 Thin ctypes binding over the C ABI in ``include/gdn_paged.h``: each function
 checks tensor dtypes / devices, passes ``data_ptr()`` values and the current
@@ -26,6 +27,13 @@ __all__ = [
     "gdn_pool_copy_rows",
     "gdn_pool_zero_rows",
     "gdn_prefill_workspace_bytes",
+    "gdn_rope_frequencies",
+    "gdn_rope",
+    "gdn_kv_append_paged",
+    "gdn_attention_paged",
+    "gdn_attention_decode_paged",
+    "gdn_attention_workspace_bytes",
+    "gdn_attention_decode_workspace_bytes",
     "gdn_status_string",
     "library",
     "GdnError",
@@ -54,6 +62,22 @@ class _DecodeSlots(ctypes.Structure):
     _fields_ = [("initial_state_indices", ctypes.c_void_p), ("output_state_indices", ctypes.c_void_p)]
 
 
+class _KVCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _PageTable(ctypes.Structure):
+    _fields_ = [("page_indices", ctypes.c_void_p), ("num_entries", ctypes.c_int32), ("page_indptr", ctypes.c_void_p),
+                ("last_page_len", ctypes.c_void_p), ("num_seqs", ctypes.c_int32)]
+
+
+class _AttentionOptions(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("window", ctypes.c_int32),
+                ("full_lens", ctypes.c_void_p)]
+
+
 def library():
     """Load libgdn_paged.so (building it first if the sources are newer)."""
     global _lib
@@ -67,6 +91,7 @@ def library():
                     raise RuntimeError("libgdn_paged.so is missing or stale and could not be built: %s" % e)
             lib = ctypes.CDLL(LIB_PATH)
             P, i32, i64, f32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+            f64 = ctypes.c_double
             sig = {
                 "gdn_paged_prefill_slots": [P, P, P, P, i32, i32, P, P, P, P, P],
                 "gdn_paged_decode_slots": [P, P, P, i32, P, P, P],
@@ -84,13 +109,21 @@ def library():
                                                          P, i32, i32, P, P, P, P, P, P],
                 "gdn_pool_copy_rows": [P, i64, i64, P, P, i32, i32, P, P],
                 "gdn_pool_zero_rows": [P, i64, i64, P, i32, i32, P, P],
+                "gdn_rope_frequencies": [i32, f64, f64, f64, f64, f64, P],
+                "gdn_rope": [P, i64, P, i64, P, P, i32, i32, i32, i32, i32, i32, f32, P],
+                "gdn_kv_append_paged": [P, i64, P, P, i64, P, i64, P, i32, i32, P, P, P, i32, i32, f32, P, P],
+                "gdn_attention_paged": [P, i64, P, P, P, i32, i32, P, P, f32, P, P, sz, P, P],
+                "gdn_attention_decode_paged": [P, i64, P, P, i32, P, P, f32, P, P, sz, P, P],
             }
             for name, args in sig.items():
                 fn = getattr(lib, name)
                 fn.argtypes = args
                 fn.restype = ctypes.c_int
-            lib.gdn_prefill_workspace_bytes.argtypes = [i32, i32, i32]
-            lib.gdn_prefill_workspace_bytes.restype = ctypes.c_size_t
+            sizes = {"gdn_prefill_workspace_bytes": [i32] * 3, "gdn_attention_workspace_bytes": [i32] * 5,
+                     "gdn_attention_decode_workspace_bytes": [i32] * 4}
+            for name, args in sizes.items():
+                getattr(lib, name).argtypes = args
+                getattr(lib, name).restype = ctypes.c_size_t
             lib.gdn_status_string.argtypes = [ctypes.c_int]
             lib.gdn_status_string.restype = ctypes.c_char_p
             lib.gdn_debug_set_wait_stall.argtypes = [i32]
@@ -386,3 +419,235 @@ def gdn_pool_zero_rows(pool, rows, err_word=None):
         _ptr(pool), row_bytes, stride_bytes, _ptr(rows), rows.numel(), pool.shape[0],
         _ptr(_opt(err_word, i32, "err_word")), _stream(pool)))
     return pool
+
+
+# ---------------------------------------------------------------------------
+# The attention layer: rotary positions, the paged key / value cache, attention
+# ---------------------------------------------------------------------------
+def _heads_arg(t, name, D=None):
+    """A bf16 [T, H, D] tensor with dense heads; the token stride may be padded
+    (a slice of a fused projection).  Returns the token stride."""
+    if t is None:
+        raise ValueError("%s is required" % name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dim() != 3:
+        raise ValueError("%s must have 3 dims" % name)
+    T, H, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d) or (T > 1 and t.stride(0) < H * d):
+        raise ValueError("%s must be [T, H, D] with dense heads" % name)
+    if D is not None and d != D:
+        raise ValueError("%s must have %d dimensions per head, got %d" % (name, D, d))
+    return t.stride(0) if T > 1 else H * d
+
+
+def _same_device(t, *others):
+    for x in others:
+        if x is not None and x.device != t.device:
+            raise ValueError("all tensors must be on %s, got one on %s" % (t.device, x.device))
+
+
+def _kv_cache_arg(k_cache, v_cache):
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.dtype != torch.bfloat16:
+            raise TypeError("%s must be %s, got %s" % (n, torch.bfloat16, t.dtype))
+        if not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % n)
+        if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
+            raise ValueError("%s must be [num_pages, page_size, Hkv, D] with dense D" % n)
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    _same_device(k_cache, v_cache)
+    n, ps, h, d = k_cache.shape
+    return _KVCache(_ptr(k_cache), _ptr(v_cache), n, ps, h, d, *k_cache.stride()[:3])
+
+
+def _page_table_arg(page_indices, page_indptr, last_page_len):
+    for t, n in ((page_indices, "page_indices"), (page_indptr, "page_indptr"), (last_page_len, "last_page_len")):
+        _need(t, torch.int32, n, 1)
+    S = last_page_len.numel()
+    if page_indptr.numel() != S + 1:
+        raise ValueError("page_indptr must hold one entry more than last_page_len")
+    return _PageTable(_ptr(page_indices), page_indices.numel(), _ptr(page_indptr), _ptr(last_page_len), S)
+
+
+def _cu_seqlens_arg(cu_seqlens, T, S):
+    if cu_seqlens is None:
+        if T != S:
+            raise ValueError("without cu_seqlens every sequence has one new token: got %d tokens, %d sequences" % (T, S))
+        return
+    _need(cu_seqlens, torch.int32, "cu_seqlens", 1)
+    if cu_seqlens.numel() != S + 1:
+        raise ValueError("cu_seqlens must hold one entry more than last_page_len")
+
+
+def _frequencies_arg(frequencies, D):
+    """rotary_dim of an int64 frequency tensor (None: 0)."""
+    if frequencies is None:
+        return 0
+    _need(frequencies, torch.int64, "frequencies", 1)
+    if not 0 < 2 * frequencies.numel() <= D:
+        raise ValueError("frequencies must hold between 1 and D / 2 entries")
+    return 2 * frequencies.numel()
+
+
+def gdn_rope_frequencies(rotary_dim, base=10000.0, *, factor=1.0, original_len=0, low_turns=1.0, high_turns=32.0,
+                         device="cuda"):
+    """Rotation frequencies, int64 [rotary_dim / 2]: the angle of each pair per
+    position in units of 2^-64 turns.  ``factor`` > 1 stretches the context by
+    it: every pair alike where ``original_len`` is 0 (interpolated positions),
+    else a pair that makes fewer than ``low_turns`` turns in original_len
+    positions is slowed by the factor, one that makes more than ``high_turns``
+    keeps its speed, and those between are blended."""
+    out = (ctypes.c_int64 * max(int(rotary_dim) // 2, 1))()
+    _check("gdn_rope_frequencies", library().gdn_rope_frequencies(
+        int(rotary_dim), float(base), float(factor), float(original_len), float(low_turns), float(high_turns), out))
+    return torch.tensor(list(out), dtype=torch.int64, device=device)
+
+
+def gdn_rope(x, frequencies, positions, *, interleaved=False, inverse=False, amplitude=1.0, out=None):
+    """Rotary positions: the first 2 len(frequencies) dimensions of every head of
+    x (bf16 [T, H, D], token stride free) turned by positions (int32 [T]) times
+    frequencies, and scaled by ``amplitude``; pairs are (i, i + rotary_dim / 2),
+    or (2 i, 2 i + 1) with ``interleaved``.  ``inverse`` applies the transposed
+    map (the gradient's).  ``out`` may be x itself."""
+    xs = _heads_arg(x, "x")
+    T, H, D = x.shape
+    rotary = _frequencies_arg(frequencies, D)
+    if rotary == 0:
+        raise ValueError("frequencies is required")
+    _need(positions, torch.int32, "positions", 1)
+    if positions.numel() != T:
+        raise ValueError("positions must hold one entry per token")
+    if out is None:
+        out = torch.empty(T, H, D, dtype=torch.bfloat16, device=x.device)
+    ys = _heads_arg(out, "out", D)
+    if out.shape != x.shape:
+        raise ValueError("out must have the shape of x")
+    _same_device(x, frequencies, positions, out)
+    _check("gdn_rope", library().gdn_rope(_ptr(x), xs, _ptr(out), ys, _ptr(positions), _ptr(frequencies), T, H, D,
+                                          rotary, int(bool(interleaved)), int(bool(inverse)), float(amplitude),
+                                          _stream(x)))
+    return out
+
+
+def gdn_kv_append_paged(k, v, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, *, q=None,
+                        frequencies=None, interleaved=False, amplitude=1.0, q_out=None, err_word=None):
+    """Append the new tokens' keys and values (bf16 [T, Hkv, D]) to the paged
+    cache (bf16 [num_pages, page_size, Hkv, D], any strides), keys rotated to
+    their positions on the way, and rotate the queries q (bf16 [T, Hq, D]) along.
+    ``cu_seqlens`` None: one new token per sequence.  Returns the rotated queries
+    (None without q); the caches are updated in place."""
+    cache = _kv_cache_arg(k_cache, v_cache)
+    D = cache.head_dim
+    ks, vs = _heads_arg(k, "k", D), _heads_arg(v, "v", D)
+    T = k.shape[0]
+    if k.shape != v.shape or k.shape[1] != cache.num_heads:
+        raise ValueError("k and v must be [T, Hkv, D]")
+    table = _page_table_arg(page_indices, page_indptr, last_page_len)
+    _cu_seqlens_arg(cu_seqlens, T, table.num_seqs)
+    rotary = _frequencies_arg(frequencies, D)
+    qs = Hq = 0
+    if q is not None:
+        qs, Hq = _heads_arg(q, "q", D), q.shape[1]
+        if q.shape[0] != T:
+            raise ValueError("q must hold as many tokens as k")
+        if q_out is None:
+            q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
+        _need(q_out, torch.bfloat16, "q_out", 3)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    _same_device(k, v, k_cache, cu_seqlens, page_indices, page_indptr, last_page_len, q, q_out, frequencies, err_word)
+    _check("gdn_kv_append_paged", library().gdn_kv_append_paged(
+        _ptr(q), qs, _ptr(q_out), _ptr(k), ks, _ptr(v), vs, _ptr(cu_seqlens), T, Hq, ctypes.byref(cache),
+        ctypes.byref(table), _ptr(frequencies), rotary, int(bool(interleaved)), float(amplitude),
+        _ptr(_opt(err_word, torch.int32, "err_word")), _stream(k)))
+    return q_out
+
+
+def gdn_attention_workspace_bytes(num_seqs: int, total_tokens: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(library().gdn_attention_workspace_bytes(num_seqs, total_tokens, Hq, Hkv, D))
+
+
+def gdn_attention_decode_workspace_bytes(num_seqs: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(library().gdn_attention_decode_workspace_bytes(num_seqs, Hq, Hkv, D))
+
+
+def _attention_args(q, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, softcap, window, slopes,
+                    full_lens, o, lse, return_lse, err_word):
+    cache = _kv_cache_arg(k_cache, v_cache)
+    qs = _heads_arg(q, "q", cache.head_dim)
+    T, Hq, D = q.shape
+    table = _page_table_arg(page_indices, page_indptr, last_page_len)
+    _cu_seqlens_arg(cu_seqlens, T, table.num_seqs)
+    if slopes is not None and _need(slopes, torch.float32, "slopes", 1).numel() != Hq:
+        raise ValueError("slopes must hold one entry per query head")
+    if full_lens is not None and _need(full_lens, torch.int32, "full_lens", 1).numel() != table.num_seqs:
+        raise ValueError("full_lens must hold one entry per sequence")
+    if o is None:
+        o = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
+    if _need(o, torch.bfloat16, "o", 3).shape != q.shape:
+        raise ValueError("o must have the shape of q")
+    if lse is None and return_lse:
+        lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
+    if lse is not None and _need(lse, torch.float32, "lse", 2).shape != (T, Hq):
+        raise ValueError("lse must be [T, Hq]")
+    _same_device(q, k_cache, cu_seqlens, page_indices, page_indptr, last_page_len, slopes, full_lens, o, lse, err_word)
+    options = _AttentionOptions(float(softcap), _ptr(slopes), -1 if window is None else int(window), _ptr(full_lens))
+    return cache, table, options, qs, o, lse
+
+
+def _attention_workspace(workspace, need, device):
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    _need(workspace, torch.uint8, "workspace")
+    if workspace.numel() < need:
+        raise ValueError("workspace holds %d bytes, the call needs %d" % (workspace.numel(), need))
+    return workspace
+
+
+def gdn_attention_paged(q, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, *, scale=0.0,
+                        softcap=0.0, window=-1, slopes=None, full_lens=None, o=None, lse=None, return_lse=False,
+                        err_word=None, workspace=None):
+    """Causal attention of the new tokens q (bf16 [T, Hq, D]) over the paged
+    cache, which already holds their own keys and values.  Options on a score,
+    in this order: ``softcap`` c > 0 (c tanh(s / c)), ``slopes`` (fp32 [Hq]:
+    s - slope |i - j|), ``window`` >= 0 (only keys j >= i - window), and
+    ``full_lens`` (int32 [num_seqs]: prefix mask, keys below it seen by every new
+    token).  ``cu_seqlens`` None: one new token per sequence.  ``workspace``:
+    optional uint8 device tensor of at least gdn_attention_workspace_bytes(...)
+    bytes.  Returns o (bf16 [T, Hq, D]), with ``return_lse`` (o, lse), lse the
+    natural logarithm of the sum of exponentials (fp32 [T, Hq])."""
+    cache, table, options, qs, o, lse = _attention_args(
+        q, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, softcap, window, slopes, full_lens,
+        o, lse, return_lse, err_word)
+    T, Hq, D = q.shape
+    ws = _attention_workspace(workspace, gdn_attention_workspace_bytes(table.num_seqs, T, Hq, cache.num_heads, D),
+                              q.device)
+    _check("gdn_attention_paged", library().gdn_attention_paged(
+        _ptr(q), qs, _ptr(o), _ptr(lse), _ptr(cu_seqlens), T, Hq, ctypes.byref(cache), ctypes.byref(table),
+        float(scale), ctypes.byref(options), _ptr(ws), ws.numel(), _ptr(_opt(err_word, torch.int32, "err_word")),
+        _stream(q)))
+    return (o, lse) if return_lse else o
+
+
+def gdn_attention_decode_paged(q, k_cache, v_cache, page_indices, page_indptr, last_page_len, *, scale=0.0,
+                               softcap=0.0, window=-1, slopes=None, full_lens=None, o=None, lse=None,
+                               return_lse=False, err_word=None, workspace=None):
+    """The single-token form of gdn_attention_paged: q is [num_seqs, Hq, D], the
+    last token of every sequence; the rest as there (``workspace``:
+    gdn_attention_decode_workspace_bytes)."""
+    cache, table, options, qs, o, lse = _attention_args(
+        q, k_cache, v_cache, None, page_indices, page_indptr, last_page_len, softcap, window, slopes, full_lens,
+        o, lse, return_lse, err_word)
+    _, Hq, D = q.shape
+    ws = _attention_workspace(workspace, gdn_attention_decode_workspace_bytes(table.num_seqs, Hq, cache.num_heads, D),
+                              q.device)
+    _check("gdn_attention_decode_paged", library().gdn_attention_decode_paged(
+        _ptr(q), qs, _ptr(o), _ptr(lse), Hq, ctypes.byref(cache), ctypes.byref(table), float(scale),
+        ctypes.byref(options), _ptr(ws), ws.numel(), _ptr(_opt(err_word, torch.int32, "err_word")), _stream(q)))
+    return (o, lse) if return_lse else o

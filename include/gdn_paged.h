@@ -331,6 +331,143 @@ size_t gdn_prefill_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32
  * enable 0 disables it again.  Not for production use. */
 void gdn_debug_set_wait_stall(int32_t enable);
 
+/* ------------------------------------------------------------------------
+ * Attention layers beside the recurrent ones.
+ *
+ * A model that mixes Gated Delta-Rule layers with softmax-attention layers
+ * runs both over one CSR page table: page j of a sequence then also names the
+ * page of the key / value cache that holds the keys and values of its tokens
+ * [j * page_size, (j + 1) * page_size).  The calls below are what such a layer
+ * runs in a step: rotate and append the new tokens' keys and values, then let
+ * the new tokens attend to everything their sequence has cached.  The
+ * published API has no counterpart of them.
+ *
+ * Shared conventions, beside those at the top of this file
+ *   - D is the head dimension, Hq the query heads and Hkv the key / value
+ *     heads; Hq is a multiple of Hkv and query head h reads key / value head
+ *     h / (Hq / Hkv).
+ *   - q, k, v are [T, H, D] with dense heads and a token stride given in
+ *     elements (a slice of a fused projection needs no copy): at least H * D,
+ *     a multiple of 8.  q_out, o and lse are dense.
+ *   - A NULL cu_seqlens means one new token per sequence (total_tokens ==
+ *     num_seqs).
+ *   - A sequence without new tokens is skipped.  So is one whose page table is
+ *     refused (no page, last_page_len outside 1..page_size, more new tokens
+ *     than tokens, tokens past total_tokens, table entries past num_entries, or
+ *     more than 2^30 - 1 tokens): its outputs are left as they were, and with
+ *     err_word it is reported as GDN_DEVERR_PAGE_TABLE.  These checks always
+ *     run, with or without err_word.
+ *   - A page id outside [0, num_pages) is never followed: an append skips the
+ *     token, an attention call reads zeros; with err_word both report
+ *     GDN_DEVERR_PAGE_ID.
+ *   - All kernels are programmatic dependents of the kernel before them on the
+ *     stream and wait for it before they read anything.
+ * ------------------------------------------------------------------------ */
+
+/* Paged key / value cache, two bf16 arrays [num_pages, page_size, Hkv, D] with
+ * dense D and the same strides (elements, each a multiple of 8): any order of
+ * pages, slots and heads in memory, and views into one allocation.  page_size
+ * is at least 1; page sizes that share a power of two of 8 or more with 128
+ * load in few copies (see gdn_attention_paged). */
+typedef struct {
+    gdn_bf16 *k;
+    gdn_bf16 *v;
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t num_heads;    /* Hkv */
+    int32_t head_dim;     /* D */
+    int64_t page_stride;  /* elements between pages */
+    int64_t token_stride; /* elements between the slots of a page */
+    int64_t head_stride;  /* elements between heads */
+} gdn_kv_cache;
+
+/* CSR page table of num_seqs sequences, counting the new tokens. */
+typedef struct {
+    const int32_t *page_indices;  /* [num_entries] */
+    int32_t num_entries;
+    const int32_t *page_indptr;   /* [num_seqs + 1] */
+    const int32_t *last_page_len; /* [num_seqs] */
+    int32_t num_seqs;
+} gdn_page_table;
+
+/* What an attention call does to a score before the softmax, in this order;
+ * with every member off (or a NULL pointer) it is plain causal attention. */
+typedef struct {
+    float softcap;             /* > 0: s = softcap * tanh(s / softcap) */
+    const float *slopes;       /* [Hq] or NULL: s -= slopes[h] * |i - j| */
+    int32_t window;            /* >= 0: token i sees keys j >= i - window only; < 0: off */
+    const int32_t *full_lens;  /* [num_seqs] or NULL: prefix mask, every new token of the sequence
+                                  also sees the keys j < full_lens[b], later ones included; not
+                                  together with window */
+} gdn_attention_options;
+
+/* Rotation frequencies, on the host: out[i], i < rotary_dim / 2, is the angle
+ * that pair i turns per position, in units of 2^-64 turns.  An angle is then
+ * position * out[i] modulo 2^64: exact for every position, where a product of
+ * 32-bit floats has lost a hundredth of a radian by position 262,144.
+ *   theta_i = base^(-2 i / rotary_dim) radians per position; for factor > 1
+ *   theta_i is divided by factor where original_len <= 0 (positions
+ *   interpolated), else blended by the turns r = original_len * theta_i / 2 pi
+ *   that the pair makes in the original context:
+ *   theta_i * (c + (1 - c) / factor), c = clamp((r - low_turns) / (high_turns - low_turns), 0, 1).
+ * rotary_dim is even and positive, base >= 1, factor >= 1 and, with
+ * original_len > 0, high_turns > low_turns. */
+int gdn_rope_frequencies(int32_t rotary_dim, double base, double factor, double original_len, double low_turns,
+                         double high_turns, int64_t *out);
+
+/* Rotary positions: y = x with the first rotary_dim dimensions of every head
+ * rotated, pair i by the angle a = 2 pi * positions[t] * frequencies[i] / 2^64:
+ *   y_a = amplitude * (x_a cos a - x_b sin a),  y_b = amplitude * (x_a sin a + x_b cos a)
+ * with (a, b) = (2 i, 2 i + 1) where interleaved != 0, else (i, i +
+ * rotary_dim / 2); the other dimensions are copied.  inverse != 0 turns the
+ * other way (the transposed map: the gradient's rotation; with amplitude 1 it
+ * undoes the rotation).  x is [T, H, D] with a token stride, y likewise; y may
+ * be x itself (same pointer and stride), otherwise they do not overlap.  D is
+ * a multiple of 8, rotary_dim even and at most D.  frequencies is a device
+ * array of rotary_dim / 2 entries, positions int32 [T] (any sign). */
+int gdn_rope(const gdn_bf16 *x, int64_t x_token_stride, gdn_bf16 *y, int64_t y_token_stride,
+             const int32_t *positions, const int64_t *frequencies, int32_t total_tokens, int32_t H, int32_t D,
+             int32_t rotary_dim, int32_t interleaved, int32_t inverse, float amplitude, void *stream);
+
+/* Append: new token i of sequence b stands at position len_b - n_b + i (len_b
+ * tokens after the call, n_b of them new).  Its key is rotated there (as by
+ * gdn_rope; not at all where frequencies is NULL) and written with its value
+ * to the slot of that position; its queries are rotated into q_out.  q and
+ * q_out are both NULL (with Hq 0) or both given; q_out [T, Hq, D] is dense and
+ * may be q where q is dense.  Every other slot of the cache stays as it is. */
+int gdn_kv_append_paged(const gdn_bf16 *q, int64_t q_token_stride, gdn_bf16 *q_out, const gdn_bf16 *k,
+                        int64_t k_token_stride, const gdn_bf16 *v, int64_t v_token_stride,
+                        const int32_t *cu_seqlens, int32_t total_tokens, int32_t Hq, const gdn_kv_cache *cache,
+                        const gdn_page_table *table, const int64_t *frequencies, int32_t rotary_dim,
+                        int32_t interleaved, float amplitude, int32_t *err_word, void *stream);
+
+/* Attention of the new tokens over the cache, which holds their own keys and
+ * values already: for new token t at position i and head h
+ *   s_j = scale * q[t, h] . k_j  (then the options), over the keys j <= i that
+ *   the options leave visible;  o[t, h] = sum_j softmax(s)_j v_j,
+ *   lse[t, h] = log sum_j exp(s_j) (natural logarithm; NULL: not wanted).
+ * scale <= 0 selects 1 / sqrt(D).  D is 64 or 128 and Hq / Hkv at most 128.
+ * Slots past a sequence's end and keys outside every token's window are not
+ * read into any sum, whatever they hold; the keys and values of a sequence's
+ * own tokens inside the window have to be finite.
+ * workspace: device memory, 16-byte aligned, of at least
+ * gdn_attention_workspace_bytes(...) bytes; it needs no initialisation. */
+int gdn_attention_paged(const gdn_bf16 *q, int64_t q_token_stride, gdn_bf16 *o, float *lse,
+                        const int32_t *cu_seqlens, int32_t total_tokens, int32_t Hq, const gdn_kv_cache *cache,
+                        const gdn_page_table *table, float scale, const gdn_attention_options *options,
+                        void *workspace, size_t workspace_bytes, int32_t *err_word, void *stream);
+
+/* The single-token form: one new token per sequence (q, o [num_seqs, Hq, D],
+ * lse [num_seqs, Hq]); otherwise as gdn_attention_paged. */
+int gdn_attention_decode_paged(const gdn_bf16 *q, int64_t q_token_stride, gdn_bf16 *o, float *lse, int32_t Hq,
+                               const gdn_kv_cache *cache, const gdn_page_table *table, float scale,
+                               const gdn_attention_options *options, void *workspace, size_t workspace_bytes,
+                               int32_t *err_word, void *stream);
+
+/* Bytes of workspace of the two calls above (0 for invalid arguments). */
+size_t gdn_attention_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32_t Hq, int32_t Hkv, int32_t D);
+size_t gdn_attention_decode_workspace_bytes(int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D);
+
 /* Static text for a status code. */
 const char *gdn_status_string(int status);
 

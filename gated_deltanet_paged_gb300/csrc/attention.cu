@@ -12,9 +12,9 @@ using gdn::SeqRange;
 
 constexpr int kWarps = 4;
 constexpr int kKeys = 4;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = gdn::kLog2e;
 
-struct AttnArgs {
+struct SimpleArgs {
   const __nv_bfloat16* q;
   int64_t q_stride;
   __nv_bfloat16* o;
@@ -31,7 +31,7 @@ struct AttnArgs {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) attention_simple_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) attention_simple_kernel(const SimpleArgs a) {
   constexpr int kE = D / 32;  // elements per lane
   gdn::pdl_wait();
   gdn::pdl_launch_dependents();
@@ -129,7 +129,7 @@ int attend(const gdn_bf16* q, int64_t q_token_stride, gdn_bf16* o, float* lse, c
   if (!workspace || !gdn_host::aligned16(workspace) || workspace_bytes < need) return GDN_ERR_INVALID_ARGUMENT;
   rc = gdn_host::check_device(nullptr);
   if (rc != GDN_OK) return rc;
-  AttnArgs a = {};
+  SimpleArgs a = {};
   a.q = reinterpret_cast<const __nv_bfloat16*>(q);
   a.q_stride = q_token_stride;
   a.o = reinterpret_cast<__nv_bfloat16*>(o);
@@ -159,10 +159,6 @@ extern "C" size_t gdn_attention_workspace_bytes(int32_t num_seqs, int32_t total_
   return num_seqs < 0 || total_tokens < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || (D != 64 && D != 128) ? 0 : 16;
 }
 
-extern "C" size_t gdn_attention_decode_workspace_bytes(int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D) {
-  return gdn_attention_workspace_bytes(num_seqs, num_seqs, Hq, Hkv, D);
-}
-
 extern "C" int gdn_attention_paged(const gdn_bf16* q, int64_t q_token_stride, gdn_bf16* o, float* lse,
                                    const int32_t* cu_seqlens, int32_t total_tokens, int32_t Hq,
                                    const gdn_kv_cache* cache, const gdn_page_table* table, float scale,
@@ -170,12 +166,4 @@ extern "C" int gdn_attention_paged(const gdn_bf16* q, int64_t q_token_stride, gd
                                    int32_t* err_word, void* stream) {
   return attend(q, q_token_stride, o, lse, cu_seqlens, total_tokens, Hq, cache, table, scale, options, workspace,
                 workspace_bytes, 16, err_word, stream);
-}
-
-extern "C" int gdn_attention_decode_paged(const gdn_bf16* q, int64_t q_token_stride, gdn_bf16* o, float* lse,
-                                          int32_t Hq, const gdn_kv_cache* cache, const gdn_page_table* table,
-                                          float scale, const gdn_attention_options* options, void* workspace,
-                                          size_t workspace_bytes, int32_t* err_word, void* stream) {
-  return attend(q, q_token_stride, o, lse, nullptr, table ? table->num_seqs : 0, Hq, cache, table, scale, options,
-                workspace, workspace_bytes, 16, err_word, stream);
 }

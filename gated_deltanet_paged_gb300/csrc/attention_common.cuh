@@ -2,6 +2,8 @@
 // kernels (rope.cu, attention.cu, attention_decode.cu) and their host checks.
 #pragma once
 
+#include <math.h>
+
 #include "common.cuh"
 
 namespace gdn {
@@ -49,6 +51,44 @@ __device__ __forceinline__ SeqRange seq_range(const PagedTokens& p, int b) {
   return s;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+// What both attention kernels take.  Scores are kept in units of log2, so that
+// every exponential is one exp2.
+struct AttnArgs {
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  __nv_bfloat16* o;
+  float* lse;  // nullptr: not wanted
+  PagedTokens paged;
+  int32_t Hq, Hkv, group;
+  float scale_log2;           // scale * log2(e); with a cap: 2 scale log2(e) / cap, the tanh's argument
+  float cap_log2;             // cap * log2(e), 0: no cap
+  const float* slopes;        // [Hq] or nullptr
+  const int32_t* full_lens;   // [num_seqs] or nullptr
+  int32_t window;             // < 0: none
+  int32_t box_rows;           // tokens per copy of a page
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// cap * tanh(s * scale / cap) in units of log2: tanh(z) = 1 - 2 / (e^(2 z) + 1),
+// with x = 2 z log2(e).  Off by about 2^-23 of the cap, and exact at the ends
+// (e^(2 z) overflows to infinity or vanishes); the hardware tanh is off by
+// 2^-11 of it, a weight error of 1 percent under a cap of 30.
+__device__ __forceinline__ float capped(float x, float cap_log2) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(exp2_approx(x) + 1.f));
+  return fmaf(-2.f * cap_log2, r, cap_log2);
+}
+
+// Keys that a token at `pos` sees: [lo, hi).
+__device__ __forceinline__ int key_lo(const AttnArgs& a, int pos) { return a.window >= 0 ? max(0, pos - a.window) : 0; }
+
 }  // namespace gdn
 
 namespace gdn_host {
@@ -91,6 +131,57 @@ inline gdn::PagedTokens paged_tokens(const gdn_kv_cache* c, const gdn_page_table
   p.total_tokens = total_tokens;
   p.err_word = err_word;
   return p;
+}
+
+// Argument checks of the two attention calls, and their common arguments.
+// tile_keys: keys per tile, a power of two; a copy moves the largest power of two
+// of tokens that divides both a page and a tile.
+inline int attention_args(gdn::AttnArgs* a, const gdn_bf16* q, int64_t q_stride, gdn_bf16* o, float* lse,
+                          const int32_t* cu_seqlens, int32_t total_tokens, int32_t Hq, const gdn_kv_cache* cache,
+                          const gdn_page_table* table, float scale, const gdn_attention_options* options,
+                          const void* workspace, size_t workspace_bytes, size_t need, int32_t* err_word,
+                          int tile_keys) {
+  const int rc = check_paged(cache, table, cu_seqlens, total_tokens);
+  if (rc != GDN_OK) return rc;
+  const int32_t D = cache->head_dim, Hkv = cache->num_heads;
+  if (Hq < 1 || Hq % Hkv != 0) return GDN_ERR_INVALID_ARGUMENT;
+  if ((D != 64 && D != 128) || Hq / Hkv > 128) return GDN_ERR_UNSUPPORTED;
+  const float cap = options ? options->softcap : 0.f;
+  if (!(fabsf(cap) <= 3.0e38f) || scale != scale) return GDN_ERR_INVALID_ARGUMENT;
+  if (options && options->window >= 0 && options->full_lens) return GDN_ERR_UNSUPPORTED;
+  if (table->num_seqs == 0 || total_tokens == 0) return GDN_OK;
+  if (bad_tokens(q, q_stride, Hq, D) || !o || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < need) return GDN_ERR_INVALID_ARGUMENT;
+  *a = gdn::AttnArgs{};
+  a->q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a->q_stride = q_stride;
+  a->o = reinterpret_cast<__nv_bfloat16*>(o);
+  a->lse = lse;
+  a->paged = paged_tokens(cache, table, cu_seqlens, total_tokens, err_word);
+  a->Hq = Hq;
+  a->Hkv = Hkv;
+  a->group = Hq / Hkv;
+  const float s = scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(D));
+  a->cap_log2 = cap > 0.f ? cap * gdn::kLog2e : 0.f;
+  a->scale_log2 = cap > 0.f ? 2.f * s / cap * gdn::kLog2e : s * gdn::kLog2e;
+  a->slopes = options ? options->slopes : nullptr;
+  a->full_lens = options ? options->full_lens : nullptr;
+  a->window = options ? options->window : -1;
+  a->box_rows = 1;
+  while (a->box_rows < tile_keys && cache->page_size % (2 * a->box_rows) == 0) a->box_rows *= 2;
+  return GDN_OK;
+}
+
+// Tensor map of one cache array, {D, heads, slots, pages}, with boxes of 64
+// dimensions of one head of box_rows slots.  An axis of one entry may carry any
+// stride; the map wants a multiple of 16 bytes.
+inline int encode_cache_map(CUtensorMap* map, const gdn_bf16* base, const gdn_kv_cache* c, int box_rows) {
+  const int64_t dims[4] = {c->head_dim, c->num_heads, c->page_size, c->num_pages};
+  const int64_t strides[3] = {2 * (c->num_heads > 1 ? c->head_stride : c->head_dim),
+                              2 * (c->page_size > 1 ? c->token_stride : c->head_dim),
+                              2 * (c->num_pages > 1 ? c->page_stride : c->head_dim)};
+  return encode_map_4d(map, base, dims, strides, 1, box_rows);
 }
 
 }  // namespace gdn_host

@@ -1,0 +1,583 @@
+// attention_decode.cu -- paged attention of one new token per sequence.
+//
+// Mathematics: o = sum_j p_j v_j / sum_j p_j with p_j = 2^(x_j - m), x_j the
+// score in units of log2 and m a running maximum; partial results (m, l, o) of
+// disjoint key ranges join exactly by 2^(m_i - m).
+//
+// Bound: HBM.  Every key and value is read once, 4 D bytes per (key, head), for
+// 4 D G flops (G query heads per key head), far below the ridge.  What the
+// kernel needs is bytes in flight and equal shares:
+//   - the whole batch is one line of 64-key blocks, (sequence, head) after
+//     (sequence, head), and each CTA takes an equal piece of it, cutting
+//     (sequence, head) items wherever the piece ends.  Every CTA derives its
+//     piece from the page table itself: no planning launch, no host
+//     synchronisation.  A cut item leaves partial results in the workspace, and
+//     a small second kernel joins them in a fixed order.
+//   - a producer warp keeps three 64-key stages of K and V (32 KB each at D =
+//     128) in flight by TMA, page by page; two CTAs per SM.
+//   - four consumer warps take 16 keys of a block each and never wait for one
+//     another inside an item: mma.sync with the G query heads as the 16 rows
+//     (the matrix work is a tenth of the copy time), private (m, l, o), joined
+//     through shared memory when the item ends.
+#include "attention_common.cuh"
+
+namespace {
+
+using gdn::AttnArgs;
+using gdn::SeqRange;
+
+constexpr int kBlock = 64;    // keys per stage
+constexpr int kStages = 3;
+constexpr int kConsumers = 4;  // warps, 16 keys of a block each
+constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kRows = 16;     // query heads per pass of an item
+// Fixed cost of an item (its queries, the join of the warps, its stores) in
+// blocks, so that shares of many short items weigh the same as shares of long ones.
+constexpr int kItemCost = 2;
+constexpr int kMinShare = 6;  // blocks below which a cut costs more than it saves
+constexpr int kWholeBlocks = 8;  // longest item that is never cut (see launch)
+
+struct DecodeArgs {
+  AttnArgs a;
+  float* part_o;     // [2 grid][kRows][D]
+  float2* part_ml;   // [2 grid][kRows]
+  int4* cuts;        // [grid]: (sequence, head, row pass, last CTA) of an item cut at this CTA's end, or -1
+  int32_t whole;     // items are not cut
+  int32_t passes;    // ceil(group / kRows): an item is (sequence, head, pass)
+};
+
+// The key range of sequence b's token in blocks, and its cost.
+struct Item {
+  SeqRange s;
+  int lo, hi;      // visible keys
+  int first;       // block of lo
+  int blocks;
+  int cost;        // 0: nothing to do
+};
+__device__ __forceinline__ Item load_item(const AttnArgs& a, int b) {
+  Item it;
+  it.s = gdn::seq_range(a.paged, b);
+  it.hi = it.s.len;
+  it.lo = gdn::key_lo(a, it.s.len - 1);
+  it.first = it.lo / kBlock;
+  it.blocks = (it.hi + kBlock - 1) / kBlock - it.first;
+  it.cost = it.s.new_tokens ? it.blocks + kItemCost : 0;
+  return it;
+}
+
+// A CTA's share, walked item by item by producer and consumers alike.
+struct Walk {
+  int64_t pos, end;   // units of the batch's line (whole: item numbers)
+  int64_t base;       // line position of sequence b
+  int b;
+  int head;           // (head, pass) number within the sequence
+  Item it;
+  int blk0, blk1;     // blocks of the item in this segment
+  int64_t item0;      // line position of the item
+};
+__device__ __forceinline__ bool next_segment(const DecodeArgs& d, Walk& w) {
+  const int per_seq = d.a.Hkv * d.passes;
+  if (d.whole) {
+    while (w.pos < w.end) {
+      const int id = static_cast<int>(w.pos);
+      w.pos += gridDim.x;
+      const int b = id / per_seq;
+      if (b != w.b) w.b = b, w.it = load_item(d.a, b);
+      w.head = id - b * per_seq;
+      w.blk0 = 0;
+      w.blk1 = w.it.blocks;
+      if (w.it.cost) return true;
+    }
+    return false;
+  }
+  while (w.pos < w.end) {
+    const int64_t span = static_cast<int64_t>(w.it.cost) * per_seq;
+    if (w.pos >= w.base + span) {
+      w.base += span;
+      w.it = load_item(d.a, ++w.b);
+      continue;
+    }
+    w.head = static_cast<int>((w.pos - w.base) / w.it.cost);
+    w.item0 = w.base + static_cast<int64_t>(w.head) * w.it.cost;
+    const int64_t stop = min(w.end, w.item0 + w.it.cost);
+    w.blk0 = max(0, static_cast<int>(w.pos - w.item0) - kItemCost);
+    w.blk1 = static_cast<int>(stop - w.item0) - kItemCost;
+    w.pos = stop;
+    if (w.blk1 > w.blk0) return true;
+  }
+  return false;
+}
+
+template <int D>
+struct Smem {
+  static constexpr int kTile = kBlock * D * 2;  // one of K, V
+  alignas(1024) uint8_t kv[kStages][2][kTile];
+  float4 join_o[D / 8][32];  // one warp's partial result, lane by lane
+  float4 join_ml[32];        // m, l of its two rows
+  uint64_t full[kStages];
+  uint64_t empty[kStages];
+  int64_t scan[kThreads / 32 + 1];
+  Walk walk;
+  int abort;
+  int stop;
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
+}
+
+// The piece [start, end) of the batch's line that CTA c takes, and the CTA that
+// holds line position x.  eff: CTAs that get one.
+__device__ __forceinline__ int64_t share_start(int64_t total, int eff, int c) { return total * c / eff; }
+__device__ __forceinline__ int share_owner(int64_t total, int eff, int64_t x) {
+  int c = static_cast<int>(x * eff / total);
+  while (c + 1 < eff && share_start(total, eff, c + 1) <= x) ++c;
+  while (share_start(total, eff, c) > x) --c;
+  return c;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+    decode_attention_kernel(const __grid_constant__ DecodeArgs d, const __grid_constant__ CUtensorMap k_map,
+                            const __grid_constant__ CUtensorMap v_map) {
+  extern __shared__ uint8_t raw[];
+  Smem<D>& sh = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  const AttnArgs& a = d.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      gdn::mbar_init(&sh.full[i], 1);
+      gdn::mbar_init(&sh.empty[i], kConsumers);
+    }
+    sh.abort = 0;
+    gdn::fence_mbar_init();
+  }
+  gdn::pdl_wait();
+  gdn::pdl_launch_dependents();
+
+  // ---- this CTA's share of the line ----
+  const int per_seq = a.Hkv * d.passes;
+  Walk w;
+  int64_t total = 0;
+  int eff = gridDim.x;
+  if (d.whole) {
+    w.pos = blockIdx.x;
+    w.end = static_cast<int64_t>(a.paged.num_seqs) * per_seq;
+    w.b = -1;
+    if (blockIdx.x == 0)
+      for (int b = tid; b < a.paged.num_seqs; b += kThreads)
+        if (gdn::seq_range(a.paged, b).refused) gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_TABLE, b);
+    __syncthreads();
+  } else {
+    const int per = (a.paged.num_seqs + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, a.paged.num_seqs), b1 = min(b0 + per, a.paged.num_seqs);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Item it = load_item(a, b);
+      if (it.s.refused && blockIdx.x == 0) gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_TABLE, b);
+      mine += it.cost;
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) sh.scan[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - mine;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) before += sh.scan[i];
+      total += sh.scan[i];
+    }
+    total *= per_seq;
+    const int64_t most = total / kMinShare;
+    eff = static_cast<int>(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
+    const int c = blockIdx.x;
+    const int64_t start = c < eff ? share_start(total, eff, c) : total;
+    const int64_t end = c < eff ? share_start(total, eff, c + 1) : total;
+    // The thread whose sequences hold `start` sets up the walk.
+    if (start < end && before * per_seq <= start && start < (before + mine) * per_seq) {
+      Walk x;
+      x.pos = start;
+      x.end = end;
+      x.base = before * per_seq;
+      x.b = b0;
+      x.it = load_item(a, b0);
+      while (start >= x.base + static_cast<int64_t>(x.it.cost) * per_seq) {
+        x.base += static_cast<int64_t>(x.it.cost) * per_seq;
+        x.it = load_item(a, ++x.b);
+      }
+      sh.walk = x;
+    }
+    if (tid == 0) d.cuts[c] = make_int4(-1, 0, 0, 0);
+    __syncthreads();
+    if (start >= end) return;
+    w = sh.walk;
+  }
+
+  if (warp == kConsumers) {
+    // ---------------------------------------------------------- producer
+    int n = 0;  // blocks issued
+    bool ok = true;
+    while (ok && next_segment(d, w)) {
+      const int head = w.head / d.passes;
+      for (int blk = w.blk0; ok && blk < w.blk1; ++blk, ++n) {
+        const int stage = n % kStages;
+        const int key0 = (w.it.first + blk) * kBlock;
+        // The copies of this block: only those that hold a visible key.
+        const int first = max(0, w.it.lo - key0) / a.box_rows;
+        const int last = (min(kBlock, w.it.hi - key0) + a.box_rows - 1) / a.box_rows;
+        int page[2], slot[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int box = lane + 32 * i;
+          page[i] = 0;
+          if (box >= first && box < last) {
+            const int key = key0 + box * a.box_rows;
+            const int entry = key / a.paged.page_size;
+            slot[i] = key - entry * a.paged.page_size;
+            page[i] = a.paged.pages[w.it.s.entry + entry];
+            if (page[i] < 0 || page[i] >= a.paged.num_pages) {
+              gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_ID, w.b);
+              page[i] = a.paged.num_pages;  // outside the map: zeros
+            }
+          }
+        }
+        if (lane == 0) {
+          if (n >= kStages) ok = gdn::mbar_wait_or_abort(&sh.empty[stage], ((n / kStages) - 1) & 1, &sh.abort);
+          if (ok) gdn::mbar_arrive_expect_tx(&sh.full[stage], (last - first) * a.box_rows * D * 4);
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int box = lane + 32 * i;
+          if (box >= first && box < last) {
+            const int at = box * a.box_rows * 128;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+              gdn::tma_load_4d(sh.kv[stage][0] + c * kBlock * 128 + at, &k_map, &sh.full[stage], c * 64, head, slot[i],
+                               page[i]);
+              gdn::tma_load_4d(sh.kv[stage][1] + c * kBlock * 128 + at, &v_map, &sh.full[stage], c * 64, head, slot[i],
+                               page[i]);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok) {
+      // Leave no copy in flight behind: the stages that were issued complete by
+      // themselves (bounded wait, as everywhere).
+      if (lane == 0) {
+        sh.abort = 1;
+        for (int i = max(0, n - kStages); i < n; ++i) gdn::mbar_wait(&sh.full[i % kStages], (i / kStages) & 1);
+        gdn::record_error(a.paged.err_word, GDN_DEVERR_TIMEOUT, 0);
+      }
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------ consumers
+  const int g = lane >> 2, t = lane & 3;  // fragment row and column pair
+  int n = 0;
+  while (next_segment(d, w)) {
+    const int head = w.head / d.passes, pass = w.head % d.passes;
+    const int h0 = head * a.group + pass * kRows;             // first query head of the rows
+    const int rows = min(kRows, a.group - pass * kRows);
+    // Queries as A fragments; rows past the group are zero.
+    uint32_t q[D / 16][4];
+    {
+      const __nv_bfloat16* base = a.q + static_cast<int64_t>(w.b) * a.q_stride + static_cast<int64_t>(h0) * D;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = g + (i & 1) * 8, c = k * 16 + 2 * t + (i >> 1) * 8;
+          q[k][i] = r < rows ? *reinterpret_cast<const uint32_t*>(base + r * D + c) : 0u;
+        }
+    }
+    float slope[2] = {0.f, 0.f};
+    if (a.slopes) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (g + 8 * i < rows) slope[i] = a.slopes[h0 + g + 8 * i] * gdn::kLog2e;
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    for (int blk = w.blk0; blk < w.blk1; ++blk, ++n) {
+      const int stage = n % kStages;
+      if (!gdn::mbar_wait_or_abort(&sh.full[stage], (n / kStages) & 1, &sh.abort)) {
+        sh.abort = 1;
+        break;
+      }
+      const int key0 = (w.it.first + blk) * kBlock + warp * 16;  // this warp's keys
+      const int lo = w.it.lo - key0, hi = w.it.hi - key0;
+      if (hi > 0 && lo < 16) {
+        const uint32_t kt = gdn::smem_u32(sh.kv[stage][0]), vt = gdn::smem_u32(sh.kv[stage][1]);
+        float s[2][4] = {};
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t b[4];
+          const uint32_t r = warp * 16 + (lane >> 4) * 8 + (lane & 7), c = 2 * k + ((lane >> 3) & 1);
+          ldmatrix4(kt + (c >> 3) * (kBlock * 128) + gdn::swz(r, c & 7), b);
+          mma_16816(s[0], q[k], b[0], b[1]);
+          mma_16816(s[1], q[k], b[2], b[3]);
+        }
+        const bool edge = lo > 0 || hi < 16;
+        float top[2] = {m[0], m[1]};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float x = s[j][i] * a.scale_log2;
+            if (a.cap_log2 > 0.f) x = gdn::capped(x, a.cap_log2);
+            const int key = j * 8 + 2 * t + (i & 1);
+            if (a.slopes) x = fmaf(-slope[i >> 1], static_cast<float>(w.it.s.len - 1 - (key0 + key)), x);
+            if (edge && (key < lo || key >= hi)) x = -INFINITY;
+            s[j][i] = x;
+            top[i >> 1] = fmaxf(top[i >> 1], x);
+          }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
+        }
+        // The accumulators are rescaled only in the blocks that raise a maximum.
+        if (__any_sync(0xFFFFFFFFu, top[0] > m[0] || top[1] > m[1])) {
+          float r[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            r[i] = top[i] > m[i] ? gdn::exp2_approx(m[i] - top[i]) : 1.f;
+            m[i] = top[i];
+            l[i] *= r[i];
+          }
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            o[i][0] *= r[0], o[i][1] *= r[0];
+            o[i][2] *= r[1], o[i][3] *= r[1];
+          }
+        }
+        // Weights: fp32 into the sum, bf16 (as the values are) into the product.
+        uint32_t p[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // A row that has seen nothing yet keeps m = -inf; its weights are 0.
+            s[j][i] = s[j][i] == -INFINITY ? 0.f : gdn::exp2_approx(s[j][i] - m[i >> 1]);
+            l[i >> 1] += s[j][i];
+          }
+          p[2 * j] = gdn::pack_bf162(s[j][0], s[j][1]);
+          p[2 * j + 1] = gdn::pack_bf162(s[j][2], s[j][3]);
+        }
+        // Values of keys outside [lo, hi) are cleared: 0 * NaN would reach the sum.
+        uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int key = 2 * t + 8 * i;
+            keep[i] = ((key >= lo && key < hi) ? 0x0000FFFFu : 0u) | ((key + 1 >= lo && key + 1 < hi) ? 0xFFFF0000u : 0u);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t b[4];
+          const uint32_t r = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), c = 2 * k + (lane >> 4);
+          ldmatrix4_trans(vt + (c >> 3) * (kBlock * 128) + gdn::swz(r, c & 7), b);
+          mma_16816(o[2 * k], p, b[0] & keep[0], b[1] & keep[1]);
+          mma_16816(o[2 * k + 1], p, b[2] & keep[0], b[3] & keep[1]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) gdn::mbar_arrive(&sh.empty[stage]);
+    }
+
+    // ---- join the four warps into warp 0, one after the other (one buffer:
+    // a second would cost the third stage its place beside a second CTA) ----
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
+    }
+    for (int from = 1; from < kConsumers; ++from) {
+      if (warp == from) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) sh.join_o[i][lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        sh.join_ml[lane] = make_float4(m[0], m[1], l[0], l[1]);
+      }
+      if (tid == 0) sh.stop = *static_cast<volatile int*>(&sh.abort);  // one reading for all warps
+      consumers_sync();
+      if (warp == 0) {
+        const float4 ml = sh.join_ml[lane];
+        const float mb[2] = {ml.x, ml.y}, lb[2] = {ml.z, ml.w};
+        float ra[2], rb[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float top = fmaxf(m[i], mb[i]);
+          ra[i] = m[i] == -INFINITY ? 0.f : gdn::exp2_approx(m[i] - top);
+          rb[i] = mb[i] == -INFINITY ? 0.f : gdn::exp2_approx(mb[i] - top);
+          l[i] = l[i] * ra[i] + lb[i] * rb[i];
+          m[i] = top;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const float4 x = sh.join_o[i][lane];
+          o[i][0] = o[i][0] * ra[0] + x.x * rb[0];
+          o[i][1] = o[i][1] * ra[0] + x.y * rb[0];
+          o[i][2] = o[i][2] * ra[1] + x.z * rb[1];
+          o[i][3] = o[i][3] * ra[1] + x.w * rb[1];
+        }
+      }
+      const int stop = sh.stop;
+      consumers_sync();
+      if (stop) return;
+    }
+    if (warp == 0) {
+      const bool starts = w.blk0 == 0, ends = w.blk1 == w.it.blocks;
+      if (starts && ends) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = g + 8 * i;
+          if (r >= rows) continue;
+          const float inv = 1.f / l[i];
+          const int64_t row = static_cast<int64_t>(w.b) * a.Hq + h0 + r;
+          uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + row * D);
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) dst[k * 4 + t] = gdn::pack_bf162(o[k][2 * i] * inv, o[k][2 * i + 1] * inv);
+          if (a.lse && t == 0) a.lse[row] = (m[i] + log2f(l[i])) / gdn::kLog2e;
+        }
+      } else {
+        // One segment of a CTA at most starts an item that it does not end, and
+        // one at most continues one: two slots per CTA.
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (starts ? 1 : 0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = g + 8 * i;
+          if (r >= rows) continue;
+          float2* dst = reinterpret_cast<float2*>(d.part_o + (slot * kRows + r) * D);
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) dst[k * 4 + t] = make_float2(o[k][2 * i], o[k][2 * i + 1]);
+          if (t == 0) d.part_ml[slot * kRows + r] = make_float2(m[i], l[i]);
+        }
+        if (starts && lane == 0)
+          d.cuts[blockIdx.x] = make_int4(w.b, head, pass, share_owner(total, eff, w.item0 + w.it.cost - 1));
+      }
+    }
+  }
+}
+
+// Joins the partial results of the items that CTAs of the kernel above cut: block
+// c takes the item that CTA c started and did not end (slot 2 c + 1, then slot 0
+// of every CTA up to the one that ended it), one thread per dimension.
+template <int D>
+__global__ void __launch_bounds__(D) decode_join_kernel(const __grid_constant__ DecodeArgs d) {
+  gdn::pdl_wait();
+  gdn::pdl_launch_dependents();
+  const int c = blockIdx.x;
+  const int4 cut = d.cuts[c];
+  if (cut.x < 0) return;
+  const AttnArgs& a = d.a;
+  const int rows = min(kRows, a.group - cut.z * kRows);
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    float m = -INFINITY, l = 0.f, o = 0.f;
+    for (int i = c; i <= cut.w; ++i) {
+      const int64_t at = (2 * static_cast<int64_t>(i) + (i == c ? 1 : 0)) * kRows + r;
+      const float2 ml = d.part_ml[at];
+      const float x = d.part_o[at * D + threadIdx.x];
+      const float top = fmaxf(m, ml.x);
+      const float ra = m == -INFINITY ? 0.f : gdn::exp2_approx(m - top);
+      const float rb = ml.x == -INFINITY ? 0.f : gdn::exp2_approx(ml.x - top);
+      o = o * ra + x * rb;
+      l = l * ra + ml.y * rb;
+      m = top;
+    }
+    const int64_t row = static_cast<int64_t>(cut.x) * a.Hq + cut.y * a.group + cut.z * kRows + r;
+    a.o[row * D + threadIdx.x] = __float2bfloat16(o / l);
+    if (a.lse && threadIdx.x == 0) a.lse[row] = (m + log2f(l)) / gdn::kLog2e;
+  }
+}
+
+constexpr int kMaxGrid = 2 * 160;  // two CTAs per SM
+
+size_t workspace_bytes_of(int D) {
+  return static_cast<size_t>(2) * kMaxGrid * kRows * (D * 4 + 8) + kMaxGrid * sizeof(int4);
+}
+
+template <int D>
+int launch(const DecodeArgs& base, const gdn_kv_cache* cache, const gdn_page_table* table, void* workspace, int sms,
+           cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  constexpr int smem = sizeof(Smem<D>) + 1024;
+  int rc = gdn_host::func_attr_once(decode_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem, done);
+  if (rc != GDN_OK) return rc;
+  DecodeArgs d = base;
+  CUtensorMap k_map, v_map;
+  if ((rc = gdn_host::encode_cache_map(&k_map, cache->k, cache, d.a.box_rows)) != GDN_OK) return rc;
+  if ((rc = gdn_host::encode_cache_map(&v_map, cache->v, cache, d.a.box_rows)) != GDN_OK) return rc;
+  d.passes = (d.a.group + kRows - 1) / kRows;
+  const int64_t items = static_cast<int64_t>(table->num_seqs) * d.a.Hkv * d.passes;
+  int grid = 2 * sms < kMaxGrid ? 2 * sms : kMaxGrid;
+  // The longest sequence the table can hold has every entry that the others do
+  // not need.  Where even that is a few blocks, one CTA takes a whole item: the
+  // scan of the batch and the join's launch would cost more than the blocks.
+  const int64_t longest = (static_cast<int64_t>(table->num_entries) - table->num_seqs + 1) * cache->page_size;
+  d.whole = longest <= kWholeBlocks * kBlock;
+  if (d.whole && items < grid) grid = static_cast<int>(items);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  d.cuts = reinterpret_cast<int4*>(ws);
+  d.part_ml = reinterpret_cast<float2*>(ws + kMaxGrid * sizeof(int4));
+  d.part_o = reinterpret_cast<float*>(ws + kMaxGrid * sizeof(int4) + sizeof(float2) * 2 * kMaxGrid * kRows);
+  rc = gdn_host::launch_pdl(decode_attention_kernel<D>, dim3(grid), dim3(kThreads), smem, stream, d, k_map, v_map);
+  if (rc != GDN_OK || d.whole) return rc;
+  return gdn_host::launch_pdl(decode_join_kernel<D>, dim3(grid, 4), dim3(D), 0, stream, d);
+}
+
+}  // namespace
+
+extern "C" size_t gdn_attention_decode_workspace_bytes(int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D) {
+  if (num_seqs < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
+  return workspace_bytes_of(D);
+}
+
+extern "C" int gdn_attention_decode_paged(const gdn_bf16* q, int64_t q_token_stride, gdn_bf16* o, float* lse,
+                                          int32_t Hq, const gdn_kv_cache* cache, const gdn_page_table* table,
+                                          float scale, const gdn_attention_options* options, void* workspace,
+                                          size_t workspace_bytes, int32_t* err_word, void* stream) {
+  DecodeArgs d = {};
+  const int32_t n = table ? table->num_seqs : 0;
+  const size_t need = cache ? workspace_bytes_of(cache->head_dim) : 0;
+  int rc = gdn_host::attention_args(&d.a, q, q_token_stride, o, lse, nullptr, n, Hq, cache, table, scale, options,
+                                    workspace, workspace_bytes, need, err_word, kBlock);
+  if (rc != GDN_OK || n == 0) return rc;
+  int sms = 0;
+  rc = gdn_host::check_device(&sms);
+  if (rc != GDN_OK) return rc;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cache->head_dim == 64 ? launch<64>(d, cache, table, workspace, sms, s)
+                               : launch<128>(d, cache, table, workspace, sms, s);
+}

@@ -155,6 +155,16 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
+// 4-D tiled tensor load; rows outside the tensor arrive as zeros.
+__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int32_t c0,
+                                            int32_t c1, int32_t c2, int32_t c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
 // 3-D tiled tensor store from shared memory (bulk group of this thread);
 // rows outside the tensor are not written.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int32_t c0, int32_t c1,
@@ -485,6 +495,10 @@ int encode_tokens_map(CUtensorMap* map, const void* base, int64_t T, int64_t H, 
 // Encode a 2-D fp16 tensor map over [rows, cols] (cols a multiple of 64) with
 // a box of 64 x 64 and 128-byte swizzle.
 int encode_tiles_map_f16(CUtensorMap* map, const void* base, int64_t rows, int64_t cols);
+// Encode a 4-D bf16 tensor map over dims (innermost first; strides in bytes of
+// dims 1-3) with a box of 64 x box1 x box2 x 1 elements and 128-byte swizzle.
+int encode_map_4d(CUtensorMap* map, const void* base, const int64_t (&dims)[4], const int64_t (&strides)[3], int box1,
+                  int box2);
 int encode_tokens_map_32(CUtensorMap* map, const void* base, int64_t T, int64_t H, int64_t D);  // 64B swizzle
 
 inline int launch_status() { return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }

@@ -13,7 +13,9 @@ Source: "flashinfer.gdn_paged" (docs.flashinfer.ai/api/gdn_paged.html).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 import threading
 
 import torch
@@ -62,25 +64,18 @@ class _DecodeSlots(ctypes.Structure):
     _fields_ = [("initial_state_indices", ctypes.c_void_p), ("output_state_indices", ctypes.c_void_p)]
 
 
-class _KVCache(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
-                ("page_size", ctypes.c_int32), ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
-                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
-
-
-class _PageTable(ctypes.Structure):
-    _fields_ = [("page_indices", ctypes.c_void_p), ("num_entries", ctypes.c_int32), ("page_indptr", ctypes.c_void_p),
-                ("last_page_len", ctypes.c_void_p), ("num_seqs", ctypes.c_int32)]
-
-
-class _AttentionOptions(ctypes.Structure):
-    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("window", ctypes.c_int32),
-                ("full_lens", ctypes.c_void_p)]
+# gdn_kv_cache, gdn_page_table and gdn_attention_options of the C header in native
+# layout, packed into bytes (a ctypes.Structure takes a microsecond to fill).
+_KV_CACHE = struct.Struct("@PPiiiiqqq")
+_PAGE_TABLE = struct.Struct("@PiPPi4x")
+_ATTENTION_OPTIONS = struct.Struct("@f4xPi4xP")
 
 
 def library():
     """Load libgdn_paged.so (building it first if the sources are newer)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             from . import build as _build
@@ -146,7 +141,8 @@ def _ptr(t):
 
 
 def _stream(t):
-    return torch.cuda.current_stream(t.device).cuda_stream
+    # The handle of torch.cuda.current_stream(t.device), without building a Stream (2 us).
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def _need(t, dtype, name, ndim=None):
@@ -424,73 +420,80 @@ def gdn_pool_zero_rows(pool, rows, err_word=None):
 # ---------------------------------------------------------------------------
 # The attention layer: rotary positions, the paged key / value cache, attention
 # ---------------------------------------------------------------------------
+# A call of these at decode sizes lasts a few microseconds on the GPU, so the
+# checks below read each property of a tensor once and leave the wording of an
+# error to the slow path.
 def _heads_arg(t, name, D=None):
     """A bf16 [T, H, D] tensor with dense heads; the token stride may be padded
-    (a slice of a fused projection).  Returns the token stride."""
+    (a slice of a fused projection).  Returns (T, H, D, token stride)."""
     if t is None:
         raise ValueError("%s is required" % name)
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.dim() != 3:
         raise ValueError("%s must have 3 dims" % name)
     T, H, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d) or (T > 1 and t.stride(0) < H * d):
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (H > 1 and s1 != d) or (T > 1 and s0 < H * d):
         raise ValueError("%s must be [T, H, D] with dense heads" % name)
     if D is not None and d != D:
         raise ValueError("%s must have %d dimensions per head, got %d" % (name, D, d))
-    return t.stride(0) if T > 1 else H * d
+    return T, H, d, s0 if T > 1 else H * d
 
 
-def _same_device(t, *others):
+def _vector(t, dtype, name):
+    """The length of a contiguous 1-d CUDA tensor."""
+    if t is None or t.dtype is not dtype or not t.is_cuda or t.dim() != 1 or not t.is_contiguous():
+        _need(t, dtype, name, 1)
+    return t.shape[0]
+
+
+def _same_device(device, *others):
     for x in others:
-        if x is not None and x.device != t.device:
-            raise ValueError("all tensors must be on %s, got one on %s" % (t.device, x.device))
+        if x is not None and x.device != device:
+            raise ValueError("all tensors must be on %s, got one on %s" % (device, x.device))
 
 
 def _kv_cache_arg(k_cache, v_cache):
+    """(gdn_kv_cache bytes, Hkv, D)."""
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype != torch.bfloat16:
+        if t.dtype is not torch.bfloat16:
             raise TypeError("%s must be %s, got %s" % (n, torch.bfloat16, t.dtype))
         if not t.is_cuda:
             raise ValueError("%s must be a CUDA tensor" % n)
-        if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
-            raise ValueError("%s must be [num_pages, page_size, Hkv, D] with dense D" % n)
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or (shape[3] > 1 and strides[3] != 1):
+        raise ValueError("k_cache must be [num_pages, page_size, Hkv, D] with dense D")
+    if v_cache.shape != shape or v_cache.stride() != strides:
         raise ValueError("k_cache and v_cache must have the same shape and strides")
-    _same_device(k_cache, v_cache)
-    n, ps, h, d = k_cache.shape
-    return _KVCache(_ptr(k_cache), _ptr(v_cache), n, ps, h, d, *k_cache.stride()[:3])
+    return _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), *shape, *strides[:3]), shape[2], shape[3]
 
 
-def _page_table_arg(page_indices, page_indptr, last_page_len):
-    for t, n in ((page_indices, "page_indices"), (page_indptr, "page_indptr"), (last_page_len, "last_page_len")):
-        _need(t, torch.int32, n, 1)
-    S = last_page_len.numel()
-    if page_indptr.numel() != S + 1:
+def _page_table_arg(page_indices, page_indptr, last_page_len, cu_seqlens, T):
+    """(gdn_page_table bytes, num_seqs), checked against T new tokens."""
+    i32 = torch.int32
+    n = _vector(page_indices, i32, "page_indices")
+    S = _vector(last_page_len, i32, "last_page_len")
+    if _vector(page_indptr, i32, "page_indptr") != S + 1:
         raise ValueError("page_indptr must hold one entry more than last_page_len")
-    return _PageTable(_ptr(page_indices), page_indices.numel(), _ptr(page_indptr), _ptr(last_page_len), S)
-
-
-def _cu_seqlens_arg(cu_seqlens, T, S):
     if cu_seqlens is None:
         if T != S:
             raise ValueError("without cu_seqlens every sequence has one new token: got %d tokens, %d sequences" % (T, S))
-        return
-    _need(cu_seqlens, torch.int32, "cu_seqlens", 1)
-    if cu_seqlens.numel() != S + 1:
+    elif _vector(cu_seqlens, i32, "cu_seqlens") != S + 1:
         raise ValueError("cu_seqlens must hold one entry more than last_page_len")
+    return _PAGE_TABLE.pack(page_indices.data_ptr(), n, page_indptr.data_ptr(), last_page_len.data_ptr(), S), S
 
 
 def _frequencies_arg(frequencies, D):
     """rotary_dim of an int64 frequency tensor (None: 0)."""
     if frequencies is None:
         return 0
-    _need(frequencies, torch.int64, "frequencies", 1)
-    if not 0 < 2 * frequencies.numel() <= D:
+    n = _vector(frequencies, torch.int64, "frequencies")
+    if not 0 < 2 * n <= D:
         raise ValueError("frequencies must hold between 1 and D / 2 entries")
-    return 2 * frequencies.numel()
+    return 2 * n
 
 
 def gdn_rope_frequencies(rotary_dim, base=10000.0, *, factor=1.0, original_len=0, low_turns=1.0, high_turns=32.0,
@@ -513,23 +516,23 @@ def gdn_rope(x, frequencies, positions, *, interleaved=False, inverse=False, amp
     frequencies, and scaled by ``amplitude``; pairs are (i, i + rotary_dim / 2),
     or (2 i, 2 i + 1) with ``interleaved``.  ``inverse`` applies the transposed
     map (the gradient's).  ``out`` may be x itself."""
-    xs = _heads_arg(x, "x")
-    T, H, D = x.shape
+    T, H, D, xs = _heads_arg(x, "x")
     rotary = _frequencies_arg(frequencies, D)
     if rotary == 0:
         raise ValueError("frequencies is required")
-    _need(positions, torch.int32, "positions", 1)
-    if positions.numel() != T:
+    if _vector(positions, torch.int32, "positions") != T:
         raise ValueError("positions must hold one entry per token")
     if out is None:
-        out = torch.empty(T, H, D, dtype=torch.bfloat16, device=x.device)
-    ys = _heads_arg(out, "out", D)
-    if out.shape != x.shape:
-        raise ValueError("out must have the shape of x")
-    _same_device(x, frequencies, positions, out)
-    _check("gdn_rope", library().gdn_rope(_ptr(x), xs, _ptr(out), ys, _ptr(positions), _ptr(frequencies), T, H, D,
-                                          rotary, int(bool(interleaved)), int(bool(inverse)), float(amplitude),
-                                          _stream(x)))
+        out = x.new_empty((T, H, D))
+        ys = H * D
+    else:
+        To, Ho, _, ys = _heads_arg(out, "out", D)
+        if (To, Ho) != (T, H):
+            raise ValueError("out must have the shape of x")
+    _same_device(x.device, frequencies, positions, out)
+    _check("gdn_rope", library().gdn_rope(x.data_ptr(), xs, out.data_ptr(), ys, positions.data_ptr(),
+                                          frequencies.data_ptr(), T, H, D, rotary, 1 if interleaved else 0,
+                                          1 if inverse else 0, amplitude, _stream(x)))
     return out
 
 
@@ -540,74 +543,82 @@ def gdn_kv_append_paged(k, v, k_cache, v_cache, cu_seqlens, page_indices, page_i
     their positions on the way, and rotate the queries q (bf16 [T, Hq, D]) along.
     ``cu_seqlens`` None: one new token per sequence.  Returns the rotated queries
     (None without q); the caches are updated in place."""
-    cache = _kv_cache_arg(k_cache, v_cache)
-    D = cache.head_dim
-    ks, vs = _heads_arg(k, "k", D), _heads_arg(v, "v", D)
-    T = k.shape[0]
-    if k.shape != v.shape or k.shape[1] != cache.num_heads:
+    cache, Hkv, D = _kv_cache_arg(k_cache, v_cache)
+    T, Hk, _, ks = _heads_arg(k, "k", D)
+    Tv, Hv, _, vs = _heads_arg(v, "v", D)
+    if Tv != T or Hk != Hkv or Hv != Hkv:
         raise ValueError("k and v must be [T, Hkv, D]")
-    table = _page_table_arg(page_indices, page_indptr, last_page_len)
-    _cu_seqlens_arg(cu_seqlens, T, table.num_seqs)
+    table, _ = _page_table_arg(page_indices, page_indptr, last_page_len, cu_seqlens, T)
     rotary = _frequencies_arg(frequencies, D)
     qs = Hq = 0
     if q is not None:
-        qs, Hq = _heads_arg(q, "q", D), q.shape[1]
-        if q.shape[0] != T:
+        Tq, Hq, _, qs = _heads_arg(q, "q", D)
+        if Tq != T:
             raise ValueError("q must hold as many tokens as k")
         if q_out is None:
-            q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
-        _need(q_out, torch.bfloat16, "q_out", 3)
-        if q_out.shape != q.shape:
+            q_out = q.new_empty((T, Hq, D))
+        elif _need(q_out, torch.bfloat16, "q_out", 3).shape != q.shape:
             raise ValueError("q_out must have the shape of q")
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    _same_device(k, v, k_cache, cu_seqlens, page_indices, page_indptr, last_page_len, q, q_out, frequencies, err_word)
+    _same_device(k.device, v, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, q, q_out,
+                 frequencies, err_word)
     _check("gdn_kv_append_paged", library().gdn_kv_append_paged(
-        _ptr(q), qs, _ptr(q_out), _ptr(k), ks, _ptr(v), vs, _ptr(cu_seqlens), T, Hq, ctypes.byref(cache),
-        ctypes.byref(table), _ptr(frequencies), rotary, int(bool(interleaved)), float(amplitude),
-        _ptr(_opt(err_word, torch.int32, "err_word")), _stream(k)))
+        _ptr(q), qs, _ptr(q_out), k.data_ptr(), ks, v.data_ptr(), vs, _ptr(cu_seqlens), T, Hq, cache, table,
+        _ptr(frequencies), rotary, 1 if interleaved else 0, amplitude, _ptr(_opt(err_word, torch.int32, "err_word")),
+        _stream(k)))
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
 def gdn_attention_workspace_bytes(num_seqs: int, total_tokens: int, Hq: int, Hkv: int, D: int) -> int:
     return int(library().gdn_attention_workspace_bytes(num_seqs, total_tokens, Hq, Hkv, D))
 
 
+@functools.lru_cache(maxsize=256)
 def gdn_attention_decode_workspace_bytes(num_seqs: int, Hq: int, Hkv: int, D: int) -> int:
     return int(library().gdn_attention_decode_workspace_bytes(num_seqs, Hq, Hkv, D))
 
 
-def _attention_args(q, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, softcap, window, slopes,
-                    full_lens, o, lse, return_lse, err_word):
-    cache = _kv_cache_arg(k_cache, v_cache)
-    qs = _heads_arg(q, "q", cache.head_dim)
-    T, Hq, D = q.shape
-    table = _page_table_arg(page_indices, page_indptr, last_page_len)
-    _cu_seqlens_arg(cu_seqlens, T, table.num_seqs)
-    if slopes is not None and _need(slopes, torch.float32, "slopes", 1).numel() != Hq:
-        raise ValueError("slopes must hold one entry per query head")
-    if full_lens is not None and _need(full_lens, torch.int32, "full_lens", 1).numel() != table.num_seqs:
-        raise ValueError("full_lens must hold one entry per sequence")
+def _attention(decode, q, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, scale, softcap, window,
+               slopes, full_lens, o, lse, return_lse, err_word, workspace):
+    cache, Hkv, D = _kv_cache_arg(k_cache, v_cache)
+    T, Hq, _, qs = _heads_arg(q, "q", D)
+    table, S = _page_table_arg(page_indices, page_indptr, last_page_len, cu_seqlens, T)
+    window = -1 if window is None else int(window)
+    options = None
+    if softcap or window >= 0 or slopes is not None or full_lens is not None:
+        if slopes is not None and _vector(slopes, torch.float32, "slopes") != Hq:
+            raise ValueError("slopes must hold one entry per query head")
+        if full_lens is not None and _vector(full_lens, torch.int32, "full_lens") != S:
+            raise ValueError("full_lens must hold one entry per sequence")
+        options = _ATTENTION_OPTIONS.pack(softcap, _ptr(slopes) or 0, window, _ptr(full_lens) or 0)
     if o is None:
-        o = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
-    if _need(o, torch.bfloat16, "o", 3).shape != q.shape:
+        o = q.new_empty((T, Hq, D))
+    elif _need(o, torch.bfloat16, "o", 3).shape != q.shape:
         raise ValueError("o must have the shape of q")
-    if lse is None and return_lse:
-        lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
-    if lse is not None and _need(lse, torch.float32, "lse", 2).shape != (T, Hq):
-        raise ValueError("lse must be [T, Hq]")
-    _same_device(q, k_cache, cu_seqlens, page_indices, page_indptr, last_page_len, slopes, full_lens, o, lse, err_word)
-    options = _AttentionOptions(float(softcap), _ptr(slopes), -1 if window is None else int(window), _ptr(full_lens))
-    return cache, table, options, qs, o, lse
-
-
-def _attention_workspace(workspace, need, device):
+    if lse is not None:
+        if _need(lse, torch.float32, "lse", 2).shape != (T, Hq):
+            raise ValueError("lse must be [T, Hq]")
+    elif return_lse:
+        lse = q.new_empty((T, Hq), dtype=torch.float32)
+    need = (gdn_attention_decode_workspace_bytes(S, Hq, Hkv, D) if decode
+            else gdn_attention_workspace_bytes(S, T, Hq, Hkv, D))
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    _need(workspace, torch.uint8, "workspace")
-    if workspace.numel() < need:
+        workspace = q.new_empty((max(need, 16),), dtype=torch.uint8)
+    elif _vector(workspace, torch.uint8, "workspace") < need:
         raise ValueError("workspace holds %d bytes, the call needs %d" % (workspace.numel(), need))
-    return workspace
+    _same_device(q.device, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, slopes, full_lens, o,
+                 lse, err_word, workspace)
+    tail = (cache, table, scale, options, workspace.data_ptr(), workspace.shape[0],
+            _ptr(_opt(err_word, torch.int32, "err_word")), _stream(q))
+    if decode:
+        _check("gdn_attention_decode_paged", library().gdn_attention_decode_paged(
+            q.data_ptr(), qs, o.data_ptr(), _ptr(lse), Hq, *tail))
+    else:
+        _check("gdn_attention_paged", library().gdn_attention_paged(
+            q.data_ptr(), qs, o.data_ptr(), _ptr(lse), _ptr(cu_seqlens), T, Hq, *tail))
+    return (o, lse) if return_lse else o
 
 
 def gdn_attention_paged(q, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, *, scale=0.0,
@@ -622,17 +633,8 @@ def gdn_attention_paged(q, k_cache, v_cache, cu_seqlens, page_indices, page_indp
     optional uint8 device tensor of at least gdn_attention_workspace_bytes(...)
     bytes.  Returns o (bf16 [T, Hq, D]), with ``return_lse`` (o, lse), lse the
     natural logarithm of the sum of exponentials (fp32 [T, Hq])."""
-    cache, table, options, qs, o, lse = _attention_args(
-        q, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, softcap, window, slopes, full_lens,
-        o, lse, return_lse, err_word)
-    T, Hq, D = q.shape
-    ws = _attention_workspace(workspace, gdn_attention_workspace_bytes(table.num_seqs, T, Hq, cache.num_heads, D),
-                              q.device)
-    _check("gdn_attention_paged", library().gdn_attention_paged(
-        _ptr(q), qs, _ptr(o), _ptr(lse), _ptr(cu_seqlens), T, Hq, ctypes.byref(cache), ctypes.byref(table),
-        float(scale), ctypes.byref(options), _ptr(ws), ws.numel(), _ptr(_opt(err_word, torch.int32, "err_word")),
-        _stream(q)))
-    return (o, lse) if return_lse else o
+    return _attention(False, q, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, scale, softcap,
+                      window, slopes, full_lens, o, lse, return_lse, err_word, workspace)
 
 
 def gdn_attention_decode_paged(q, k_cache, v_cache, page_indices, page_indptr, last_page_len, *, scale=0.0,
@@ -641,13 +643,5 @@ def gdn_attention_decode_paged(q, k_cache, v_cache, page_indices, page_indptr, l
     """The single-token form of gdn_attention_paged: q is [num_seqs, Hq, D], the
     last token of every sequence; the rest as there (``workspace``:
     gdn_attention_decode_workspace_bytes)."""
-    cache, table, options, qs, o, lse = _attention_args(
-        q, k_cache, v_cache, None, page_indices, page_indptr, last_page_len, softcap, window, slopes, full_lens,
-        o, lse, return_lse, err_word)
-    _, Hq, D = q.shape
-    ws = _attention_workspace(workspace, gdn_attention_decode_workspace_bytes(table.num_seqs, Hq, cache.num_heads, D),
-                              q.device)
-    _check("gdn_attention_decode_paged", library().gdn_attention_decode_paged(
-        _ptr(q), qs, _ptr(o), _ptr(lse), Hq, ctypes.byref(cache), ctypes.byref(table), float(scale),
-        ctypes.byref(options), _ptr(ws), ws.numel(), _ptr(_opt(err_word, torch.int32, "err_word")), _stream(q)))
-    return (o, lse) if return_lse else o
+    return _attention(True, q, k_cache, v_cache, None, page_indices, page_indptr, last_page_len, scale, softcap, window,
+                      slopes, full_lens, o, lse, return_lse, err_word, workspace)

@@ -14,13 +14,23 @@ int check_device(int* sm_count) {
     cudaGetLastError();
     return GDN_ERR_CUDA;
   }
-  int major = 0, minor = 0, sms = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return GDN_ERR_CUDA;
+  // A device's attributes do not change: read once per device, as (sms << 16 | major << 8 | minor) + 1.
+  static std::atomic<uint32_t> known[64];
+  const bool cached = dev >= 0 && dev < 64;
+  uint32_t packed = cached ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (!packed) {
+    int major = 0, minor = 0, sms = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      return GDN_ERR_CUDA;
+    }
+    packed = (static_cast<uint32_t>(sms) << 16 | static_cast<uint32_t>(major) << 8 | static_cast<uint32_t>(minor)) + 1;
+    if (cached) known[dev].store(packed, std::memory_order_relaxed);
   }
+  packed -= 1;
+  const int major = (packed >> 8) & 0xFF, minor = packed & 0xFF, sms = packed >> 16;
   if (major != 10 || minor != 3) return GDN_ERR_UNSUPPORTED;
   if (sm_count) *sm_count = sms;
   return GDN_OK;

@@ -15,19 +15,19 @@ def cache(**kw):
     a = dict(k=FAKE, v=FAKE, num_pages=4, page_size=16, num_heads=2, head_dim=128, page_stride=16 * 256,
              token_stride=256, head_stride=128)
     a.update(kw)
-    return ctypes.byref(gdn._KVCache(*a.values()))
+    return gdn._KV_CACHE.pack(*[v or 0 for v in a.values()])
 
 
 def table(**kw):
     a = dict(page_indices=FAKE, num_entries=4, page_indptr=FAKE, last_page_len=FAKE, num_seqs=2)
     a.update(kw)
-    return ctypes.byref(gdn._PageTable(*a.values()))
+    return gdn._PAGE_TABLE.pack(*[v or 0 for v in a.values()])
 
 
 def options(**kw):
     a = dict(softcap=0.0, slopes=None, window=-1, full_lens=None)
     a.update(kw)
-    return ctypes.byref(gdn._AttentionOptions(*a.values()))
+    return gdn._ATTENTION_OPTIONS.pack(*[v or 0 for v in a.values()])
 
 
 def rope(**kw):

@@ -523,7 +523,7 @@ def gdn_rope(x, frequencies, positions, *, interleaved=False, inverse=False, amp
     if _vector(positions, torch.int32, "positions") != T:
         raise ValueError("positions must hold one entry per token")
     if out is None:
-        out = x.new_empty((T, H, D))
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=x.device)
         ys = H * D
     else:
         To, Ho, _, ys = _heads_arg(out, "out", D)
@@ -556,7 +556,7 @@ def gdn_kv_append_paged(k, v, k_cache, v_cache, cu_seqlens, page_indices, page_i
         if Tq != T:
             raise ValueError("q must hold as many tokens as k")
         if q_out is None:
-            q_out = q.new_empty((T, Hq, D))
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
         elif _need(q_out, torch.bfloat16, "q_out", 3).shape != q.shape:
             raise ValueError("q_out must have the shape of q")
     elif q_out is not None:
@@ -594,18 +594,18 @@ def _attention(decode, q, k_cache, v_cache, cu_seqlens, page_indices, page_indpt
             raise ValueError("full_lens must hold one entry per sequence")
         options = _ATTENTION_OPTIONS.pack(softcap, _ptr(slopes) or 0, window, _ptr(full_lens) or 0)
     if o is None:
-        o = q.new_empty((T, Hq, D))
+        o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
     elif _need(o, torch.bfloat16, "o", 3).shape != q.shape:
         raise ValueError("o must have the shape of q")
     if lse is not None:
         if _need(lse, torch.float32, "lse", 2).shape != (T, Hq):
             raise ValueError("lse must be [T, Hq]")
     elif return_lse:
-        lse = q.new_empty((T, Hq), dtype=torch.float32)
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     need = (gdn_attention_decode_workspace_bytes(S, Hq, Hkv, D) if decode
             else gdn_attention_workspace_bytes(S, T, Hq, Hkv, D))
     if workspace is None:
-        workspace = q.new_empty((max(need, 16),), dtype=torch.uint8)
+        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=q.device)
     elif _vector(workspace, torch.uint8, "workspace") < need:
         raise ValueError("workspace holds %d bytes, the call needs %d" % (workspace.numel(), need))
     _same_device(q.device, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, slopes, full_lens, o,

@@ -32,8 +32,14 @@ using gdn::AttnArgs;
 
 constexpr int kRows = 128;   // rows per tile
 constexpr int kKeys = 128;   // keys per block
-constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kClearWarp = 10, kAllocWarp = 11;
+// Warps 0-3 and 4-7: softmax of tiles 0 and 1; 8 and 9: products of tiles 0 and
+// 1; 10: segments and copies; 11: clearing; 12-15: epilogue.
+constexpr int kThreads = 512;
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kClearWarp = 11;
+// 65,536 registers: 256 softmax threads hold 128 scores each, the others little.
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 56;
+static_assert(256 * (kSoftmaxRegs + kOtherRegs) == 65536, "register split of the block");
+constexpr int kSegments = 4;  // segments announced ahead
 // Fixed cost of an item (queries, pipeline fill, epilogue) in keys.
 constexpr int kItemCost = 2 * kKeys;
 constexpr int kMinShare = 4 * kKeys;  // keys below which a cut costs more than it saves
@@ -44,6 +50,7 @@ struct ChunkArgs {
   int32_t tile_tokens;  // tokens per tile: 128 / group
   float4* part_o;       // [2 grid][2 tiles][D / 4][128 rows]
   float2* part_ml;      // [2 grid][2 tiles][128 rows]
+  int32_t whole;        // items are not cut: a CTA takes those that begin in its piece
   int4* cuts;           // [grid]: (sequence, token tile pair, key head, last CTA) of an item cut at this CTA's end, or -1
 };
 
@@ -75,14 +82,14 @@ __device__ __forceinline__ int pair_cost(const ChunkArgs& d, const Seq& s, int i
   return pair_hi(d, s, i) - pair_lo(d, s, i) + kItemCost;
 }
 // sum over i < n of max(c, a + i step).
-__device__ __forceinline__ int64_t sum_max(int64_t c, int64_t a, int64_t step, int64_t n) {
-  int64_t k = c > a ? (c - a + step - 1) / step : 0;  // the first k terms are c
-  k = k < n ? k : n;
-  return c * k + a * (n - k) + step * (n * (n - 1) - k * (k - 1)) / 2;
+__device__ __forceinline__ int64_t sum_max(int c, int a, int step, int n) {
+  const int64_t k = c > a ? min((c - a + step - 1) / step, n) : 0;  // the first k terms are c
+  const int64_t m = n;
+  return c * k + a * (m - k) + step * (m * (m - 1) - k * (k - 1)) / 2;
 }
 // sum of pair_cost over the pairs before i (i < pairs: all of them full).
 __device__ __forceinline__ int64_t cost_before(const ChunkArgs& d, const Seq& s, int i) {
-  const int64_t p = s.len - s.n, step = 2 * d.tile_tokens;
+  const int p = s.len - s.n, step = 2 * d.tile_tokens;
   int64_t sum = sum_max(s.full, p + step, step, i) + static_cast<int64_t>(i) * kItemCost;
   if (d.a.window >= 0) sum -= sum_max(0, p - d.a.window, step, i);
   return sum;
@@ -122,7 +129,7 @@ __device__ __forceinline__ bool next_segment(const ChunkArgs& d, Walk& w) {
     w.hi = pair_hi(d, w.s, w.pair);
     w.first = w.lo / kKeys;
     w.blocks = (w.hi + kKeys - 1) / kKeys - w.first;
-    const int64_t stop = min(w.end, w.item0 + w.cost);
+    const int64_t stop = d.whole ? w.item0 + w.cost : min(w.end, w.item0 + w.cost);
     w.blk0 = max(0, (static_cast<int>(w.pos - w.item0) - kItemCost) / kKeys);
     w.blk1 = stop == w.item0 + w.cost ? w.blocks : max(0, (static_cast<int>(stop - w.item0) - kItemCost) / kKeys);
     w.pos = stop;
@@ -130,16 +137,6 @@ __device__ __forceinline__ bool next_segment(const ChunkArgs& d, Walk& w) {
   }
   return false;
 }
-// Keys of the block that no row of the item sees.
-__device__ __forceinline__ bool needs_clearing(const Walk& w, int key0) { return key0 < w.lo || key0 + kKeys > w.hi; }
-__device__ __forceinline__ int64_t share_start(int64_t total, int eff, int c) { return total * c / eff; }
-__device__ __forceinline__ int share_owner(int64_t total, int eff, int64_t x) {
-  int c = static_cast<int>(x * eff / total);
-  while (c + 1 < eff && share_start(total, eff, c + 1) <= x) ++c;
-  while (share_start(total, eff, c) > x) --c;
-  return c;
-}
-
 template <int D>
 struct Layout {
   static constexpr int kHalf = kRows * 128;            // 64 dimensions of 128 rows
@@ -149,16 +146,35 @@ struct Layout {
   static constexpr uint32_t kColS = 0, kColO = 256;    // TMEM columns: S of both tiles, O of both tiles
 };
 
+// One segment of the CTA's share, as the copying warp announces it to the others.
+struct alignas(16) Segment {
+  int blocks;       // in this segment; 0: no more segments
+  int key0;         // first key of the first block
+  int lo, hi;       // keys that the item's rows see between them
+  int first_token;  // row of the item's first token in q and o
+  int tokens;       // of the item
+  int pos;          // position of its first token
+  int full;         // prefix mask
+  int head;
+  int part;         // -1: the whole item; else its partial slot
+};
+
 template <int D>
 struct Smem {
   uint64_t full[Layout<D>::kStages];
   uint64_t empty[Layout<D>::kStages];
   uint64_t raw[Layout<D>::kStages];  // copies of values that are to be cleared before they are `full`
-  uint64_t q_full, q_empty, done;
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t q_full, q_empty, done[2];
+  uint64_t s_full[2];      // S is there, and the O of the blocks before is complete
+  uint64_t p_full[2][2];   // [tile][half]: 64 keys' weights are there
+  uint64_t o_last[2];      // O of a segment is complete
+  uint64_t o_free[2];      // ... and has been read
+  uint64_t stat_full[2];
+  uint64_t seg_full[kSegments], seg_empty[kSegments];
   int64_t scan[kThreads / 32];
   Walk walk;
-  Walk softmax_walk[8];  // one per softmax warp, kept here: its registers hold scores
+  Segment seg[kSegments];
+  float2 stat[2][kRows];  // [tile][row]: reference and sum of a segment
   uint32_t tmem;
   int abort;
 };
@@ -180,6 +196,31 @@ __device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, cons
   while (!gdn::mbar_try_wait_suspend(bar, parity))
     if (*abort || gdn::globaltimer_ns() - t0 > 2000000000ull) return false;
   return true;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// This warp has read its part of O.
+__device__ __forceinline__ void release(uint64_t* bar, int lane) {
+  gdn::tc_fence_before();
+  __syncwarp();
+  if (lane == 0) gdn::mbar_arrive(bar);
+}
+// 32 bytes of a row at once, a whole sector of HBM per lane, where the address
+// allows it.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8], bool aligned32) {
+  if (!aligned32) {
+    static_cast<uint4*>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    return;
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // 128 fp32 columns of this thread's TMEM lane: four loads in flight, one wait.
@@ -233,34 +274,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     chunk_attention_kernel(const __grid_constant__ ChunkArgs d, const __grid_constant__ CUtensorMap q_map,
                            const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using L = Layout<D>;
-  extern __shared__ uint8_t raw[];
-  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  // Dynamic shared memory starts behind the 1 KB that the system keeps, on a
+  // 1,024-byte boundary as the swizzle needs; there is no room to round up.
+  extern __shared__ __align__(1024) uint8_t tiles[];
   Smem<D>& sh = *reinterpret_cast<Smem<D>*>(tiles + L::kBytes);
   uint8_t* ring = tiles + 2 * L::kTile;
   const AttnArgs& a = d.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // uniform, so that the roles' addresses are
   volatile int* const abort_flag = &sh.abort;
 
+  if ((gdn::smem_u32(tiles) & 1023u) != 0) {
+    if (tid == 0) gdn::record_error(a.paged.err_word, GDN_DEVERR_TIMEOUT, 0);
+    return;
+  }
   if (tid == 0) {
     for (int i = 0; i < L::kStages; ++i) {
       gdn::mbar_init(&sh.full[i], 1);
-      gdn::mbar_init(&sh.empty[i], 1);
+      gdn::mbar_init(&sh.empty[i], 2);
       gdn::mbar_init(&sh.raw[i], 1);
     }
     gdn::mbar_init(&sh.q_full, 1);
-    gdn::mbar_init(&sh.q_empty, 1);
-    gdn::mbar_init(&sh.done, 1);
+    gdn::mbar_init(&sh.q_empty, 2);
     for (int t = 0; t < 2; ++t) {
+      gdn::mbar_init(&sh.done[t], 1);
       gdn::mbar_init(&sh.s_full[t], 1);
-      gdn::mbar_init(&sh.p_full[t], 4);
-      gdn::mbar_init(&sh.o_full[t], 1);
+      gdn::mbar_init(&sh.p_full[t][0], 4);
+      gdn::mbar_init(&sh.p_full[t][1], 4);
+      gdn::mbar_init(&sh.o_last[t], 1);
+      gdn::mbar_init(&sh.o_free[t], 4);
+      gdn::mbar_init(&sh.stat_full[t], 4);
+    }
+    for (int i = 0; i < kSegments; ++i) {
+      gdn::mbar_init(&sh.seg_full[i], 1);
+      gdn::mbar_init(&sh.seg_empty[i], kThreads / 32 - 1);
     }
     sh.abort = 0;
     gdn::fence_mbar_init();
   }
   // Rows past the group's share of a tile are never copied; they start at zero.
-  for (int i = tid; i < 2 * L::kTile / 16; i += kThreads) reinterpret_cast<uint4*>(tiles)[i] = make_uint4(0, 0, 0, 0);
-  if (warp == kAllocWarp) {
+  if (a.group * d.tile_tokens < kRows)
+    for (int i = tid; i < 2 * L::kTile / 16; i += kThreads) reinterpret_cast<uint4*>(tiles)[i] = make_uint4(0, 0, 0, 0);
+  if (tid == kLoadWarp * 32) {
+    gdn::prefetch_tensormap(&q_map);
+    gdn::prefetch_tensormap(&k_map);
+    gdn::prefetch_tensormap(&v_map);
+  }
+  if (warp == kMmaWarp) {
     gdn::tmem_alloc(&sh.tmem, 512);
     gdn::tmem_relinquish();
   }
@@ -268,8 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   gdn::pdl_launch_dependents();
 
   // ---- this CTA's share of the line ----
-  int64_t total = 0;
-  int eff = gridDim.x;
+  gdn::Shares shares(0, 1, 1);
   bool idle;
   {
     const int per = (a.paged.num_seqs + kThreads - 1) / kThreads;
@@ -288,17 +347,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 31) sh.scan[warp] = incl;
     __syncthreads();
-    int64_t before = incl - mine;
+    int64_t before = incl - mine, total = 0;
     for (int i = 0; i < kThreads / 32; ++i) {
       if (i < warp) before += sh.scan[i];
       total += sh.scan[i];
     }
     total *= a.Hkv;
-    const int64_t most = total / kMinShare;
-    eff = static_cast<int>(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
+    shares = gdn::Shares(total, total / kMinShare, gridDim.x);
     const int c = blockIdx.x;
-    const int64_t start = c < eff ? share_start(total, eff, c) : total;
-    const int64_t end = c < eff ? share_start(total, eff, c + 1) : total;
+    const int64_t start = c < shares.eff ? shares.start(c) : total;
+    const int64_t end = c < shares.eff ? shares.start(c + 1) : total;
     idle = start >= end;
     // The thread whose sequences hold `start` sets up the walk.
     if (!idle && before * a.Hkv <= start && start < (before + mine) * a.Hkv) {
@@ -314,16 +372,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         base += span;
       }
       int i = 0;  // the last pair that begins at or before start
-      for (int step = 1 << 30; step; step >>= 1)
+      for (int step = x.s.pairs > 1 ? 1 << (31 - __clz(x.s.pairs - 1)) : 0; step; step >>= 1)
         if (step < x.s.pairs - i && cost_before(d, x.s, i + step) * a.Hkv <= start - base) i += step;
       x.pair = i;
       x.cost = pair_cost(d, x.s, i);
       base += cost_before(d, x.s, i) * a.Hkv;
-      x.head = static_cast<int>((start - base) / x.cost);
+      x.head = gdn::small_quotient(start - base, x.cost, a.Hkv);
       x.item0 = base + static_cast<int64_t>(x.head) * x.cost;
+      if (d.whole && start > x.item0) x.pos = x.item0 + x.cost;
       sh.walk = x;
     }
-    if (tid == 0) d.cuts[c] = make_int4(-1, 0, 0, 0);
+    if (tid == 0 && !d.whole) d.cuts[c] = make_int4(-1, 0, 0, 0);
   }
   gdn::fence_proxy_async();
   gdn::tc_fence_before();
@@ -335,27 +394,87 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (idle) {
     // nothing to do but to give TMEM back below
   } else if (warp >= 8) {
-    regs_dec<88>();
-    Walk w = sh.walk;
+    regs_dec<kOtherRegs>();
     bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && wait_inline(bar, parity, abort_flag); };
+    // Segment i as announced; false when there is none or a wait ran out.
+    auto next = [&](uint32_t i, Segment& g) {
+      if (!wait(&sh.seg_full[i % kSegments], (i / kSegments) & 1)) return false;
+      g = sh.seg[i % kSegments];
+      __syncwarp();
+      if (lane == 0) gdn::mbar_arrive(&sh.seg_empty[i % kSegments]);
+      return g.blocks > 0;
+    };
     if (warp == kLoadWarp) {
-      // ------------------------------------------------------------- copies
-      int n = 0, seg = 0;                    // tiles issued, segments begun
+      // --------------------------------------------- segments and copies
+      Walk w = sh.walk;
+      uint32_t n = 0, segs = 0;                // tiles issued, segments announced
       uint32_t raw_parity = 0, raw_last = 0;  // per stage: parity of its next raw copy; its last copy was one
-      const int boxes = kKeys / a.box_rows;
-      while (ok && next_segment(d, w)) {
-        const int token = w.s.first_token + w.pair * 2 * tile_tokens;
-        const bool two = w.pair * 2 * tile_tokens + tile_tokens < w.s.n;
+      bool q_in_flight = false;
+      const int boxes = kKeys >> a.box_shift, box_rows = 1 << a.box_shift;
+      for (bool more = true; more; ++segs) {
+        more = next_segment(d, w);
+        const int pair0 = w.pair * 2 * tile_tokens;  // first token of the item within the sequence's new ones
+        const int token = w.s.first_token + pair0;
+        const bool two = pair0 + tile_tokens < w.s.n;
+        if (segs >= kSegments && !wait(&sh.seg_empty[segs % kSegments], ((segs / kSegments) - 1) & 1)) break;
+        if (lane == 0) {
+          Segment g = {};
+          if (more) {
+            const bool starts = w.blk0 == 0, ends = w.blk1 == w.blocks;
+            g.blocks = w.blk1 - w.blk0;
+            g.key0 = (w.first + w.blk0) * kKeys;
+            g.lo = w.lo;
+            g.hi = w.hi;
+            g.first_token = token;
+            g.tokens = min(2 * tile_tokens, w.s.n - pair0);
+            g.pos = w.s.len - w.s.n + pair0;
+            g.full = w.s.full;
+            g.head = w.head;
+            // One segment of a CTA at most starts an item that it does not end,
+            // and one at most continues one: two partial slots per CTA.
+            g.part = starts && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
+            if (starts && !ends)
+              d.cuts[blockIdx.x] = make_int4(w.b, w.pair, w.head, shares.owner(w.item0 + w.cost - 1));
+          }
+          sh.seg[segs % kSegments] = g;
+          gdn::mbar_arrive(&sh.seg_full[segs % kSegments]);
+        }
+        __syncwarp();
+        if (!more) break;
+        // The queries go first where their room is free; else behind the first
+        // block's keys and values, which need none that the segment before holds.
+        auto send_queries = [&](bool must) {
+          if (segs > 0) {
+            const uint32_t parity = (segs - 1) & 1;
+            if (must) {
+              if (!wait(&sh.q_empty, parity)) return false;
+            } else if (!__all_sync(0xFFFFFFFFu, gdn::mbar_test(&sh.q_empty, parity))) {
+              return false;
+            }
+          }
+          if (lane == 0) {
+            const int bytes = a.group * tile_tokens * D * 2;
+            gdn::mbar_arrive_expect_tx(&sh.q_full, two ? 2 * bytes : bytes);
+            for (int t = 0; t < (two ? 2 : 1); ++t)
+              for (int c = 0; c < D / 64; ++c)
+                gdn::tma_load_4d(tiles + t * L::kTile + c * L::kHalf, &q_map, &sh.q_full, c * 64, 0,
+                                 token + t * tile_tokens, w.head);
+          }
+          q_in_flight = true;
+          return true;
+        };
+        bool q_sent = send_queries(false);
         for (int blk = w.blk0; ok && blk < w.blk1; ++blk) {
           const int key0 = (w.first + blk) * kKeys;
-          const int first = max(0, w.lo - key0) / a.box_rows;
-          const int last = (min(kKeys, w.hi - key0) + a.box_rows - 1) / a.box_rows;
+          const int first = max(0, w.lo - key0) >> a.box_shift;
+          const int last = (min(kKeys, w.hi - key0) + box_rows - 1) >> a.box_shift;
           int page[4], slot[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int box = lane + 32 * i;
             if (32 * i < boxes && box >= first && box < last) {
-              const int key = key0 + box * a.box_rows;
+              const int key = key0 + box * box_rows;
               const int entry = key / a.paged.page_size;
               slot[i] = key - entry * a.paged.page_size;
               page[i] = a.paged.pages[w.s.entry + entry];
@@ -368,15 +487,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++n) {
             const int stage = n % L::kStages;
-            const bool clear = kv && needs_clearing(w, key0);
+            const bool clear = kv && (key0 < w.lo || key0 + kKeys > w.hi);
             uint64_t* bar = clear ? &sh.raw[stage] : &sh.full[stage];
-            if (lane == 0) {
-              if (n >= L::kStages)
-                ok = wait_inline(&sh.empty[stage], ((n / L::kStages) - 1) & 1, abort_flag);
-              if (ok) gdn::mbar_arrive_expect_tx(bar, (last - first) * a.box_rows * D * 2);
-            }
-            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-            if (!ok) break;
+            if (n >= L::kStages && !wait(&sh.empty[stage], ((n / L::kStages) - 1) & 1)) break;
+            if (lane == 0) gdn::mbar_arrive_expect_tx(bar, (last - first) * box_rows * D * 2);
+            __syncwarp();
             raw_last = clear ? raw_last | (1u << stage) : raw_last & ~(1u << stage);
             raw_parity ^= clear ? 1u << stage : 0u;
             uint8_t* dst = ring + stage * L::kTile;
@@ -387,134 +502,118 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (32 * i < boxes && box >= first && box < last) {
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
-                  gdn::tma_load_4d(dst + c * L::kHalf + box * a.box_rows * 128, map, bar, c * 64, w.head,
-                                   slot[i], page[i]);
+                  gdn::tma_load_4d(dst + c * L::kHalf + box * box_rows * 128, map, bar, c * 64, w.head, slot[i], page[i]);
               }
             }
             __syncwarp();
           }
-          // The queries, behind the first block's keys and values: those need
-          // no room that the segment before still holds.
-          if (ok && blk == w.blk0) {
-            if (lane == 0) {
-              if (seg > 0) ok = wait_inline(&sh.q_empty, (seg - 1) & 1, abort_flag);
-              if (ok) {
-                const int bytes = a.group * tile_tokens * D * 2;
-                gdn::mbar_arrive_expect_tx(&sh.q_full, two ? 2 * bytes : bytes);
-                for (int t = 0; t < (two ? 2 : 1); ++t)
-                  for (int c = 0; c < D / 64; ++c)
-                    gdn::tma_load_4d(tiles + t * L::kTile + c * L::kHalf, &q_map, &sh.q_full, c * 64, 0,
-                                     token + t * tile_tokens, w.head);
-              }
-            }
-            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-            ++seg;
-          }
+          if (ok && !q_sent) q_sent = send_queries(true);
         }
+        if (!ok) break;
       }
       if (!ok && lane == 0) {
         // Leave no copy in flight behind (bounded waits, as everywhere).
         *abort_flag = 1;
-        for (int i = max(0, n - L::kStages); i < n; ++i) {
+        for (uint32_t i = n > L::kStages ? n - L::kStages : 0; i < n; ++i) {
           const int stage = i % L::kStages;
           if ((raw_last >> stage) & 1)
             gdn::mbar_wait(&sh.raw[stage], ((raw_parity >> stage) & 1) ^ 1);
           else
             gdn::mbar_wait(&sh.full[stage], (i / L::kStages) & 1);
         }
-        if (seg > 0) gdn::mbar_wait(&sh.q_full, (seg - 1) & 1);
+        if (q_in_flight) gdn::mbar_wait(&sh.q_full, segs & 1);
       }
-    } else if (warp == kMmaWarp) {
+    } else if (warp < kLoadWarp) {
       // ----------------------------------------------------------- products
-      if (lane == 0) {
-        const uint32_t id_s = gdn::idesc_f16(kRows, kKeys, true, true, false, false);
-        const uint32_t id_o = gdn::idesc_f16(kRows, D, true, true, false, true);
-        const uint32_t q_addr = gdn::smem_u32(tiles), ring_addr = gdn::smem_u32(ring);
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-          ok = ok && wait_inline(bar, parity, abort_flag);
-          return ok;
-        };
-        // S_t = Q_t K^T
-        auto scores = [&](int t, int stage) {
-          const uint64_t qd = gdn::sdesc(q_addr + t * L::kTile, 16, 1024);
-          const uint64_t kd = gdn::sdesc(ring_addr + stage * L::kTile, 16, 1024);
+      // One warp per tile.  A warp's products run in the order of their issue, so
+      // S of the next block may overwrite the weights that P V before it reads.
+      const int t = warp - kMmaWarp;
+      const uint32_t id_s = gdn::idesc_f16(kRows, kKeys, true, true, false, false);
+      const uint32_t id_o = gdn::idesc_f16(kRows, D, true, true, false, true);
+      const uint64_t q_desc = gdn::sdesc(gdn::smem_u32(tiles) + t * L::kTile, 16, 1024);
+      const uint64_t k_desc = gdn::sdesc(gdn::smem_u32(ring), 16, 1024);
+      const uint64_t v_desc = gdn::sdesc(gdn::smem_u32(ring), L::kHalf, 1024);
+      const uint32_t s_col = tmem + L::kColS + t * kKeys, o_col = tmem + L::kColO + t * D;
+      constexpr uint32_t kStep = L::kTile >> 4;  // a stage, in descriptor units
+      uint32_t n = 0, np = 0, done_segs = 0;     // ring tiles, blocks of this tile, segments of this tile
+      uint32_t stage = 0, phase = 0;
+      auto advance = [&] {
+        ++n;
+        if (++stage == L::kStages) stage = 0, phase ^= 1;
+      };
+      // S = Q K^T of the ring's current tile, which is released with it.
+      auto scores = [&](bool last) {
+        if (!wait(&sh.full[stage], phase)) return;
+        gdn::tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            gdn::tc_mma4(tmem + L::kColS + t * kKeys, qd + c * (L::kHalf >> 4), 2, kd + c * (L::kHalf >> 4), 2, id_s, c);
+            gdn::tc_mma4(s_col, q_desc + c * (L::kHalf >> 4), 2, k_desc + stage * kStep + c * (L::kHalf >> 4), 2, id_s, c);
           gdn::tc_commit(&sh.s_full[t]);
-        };
-        // O_t += P_t V, P_t in TMEM over the first half of S_t
-        auto values = [&](int t, int stage, uint32_t acc) {
-          const uint64_t vd = gdn::sdesc(ring_addr + stage * L::kTile, L::kHalf, 1024);
-          const uint32_t p = tmem + L::kColS + t * kKeys, o = tmem + L::kColO + t * D;
-          gdn::tc_mma4_ts(o, p, 8, vd, 128, id_o, acc);
-          gdn::tc_mma4_ts(o, p + 32, 8, vd + 4 * 128, 128, id_o, 1);
-          gdn::tc_commit(&sh.o_full[t]);
-        };
-        uint32_t n = 0, seg = 0, np[2] = {0, 0};  // ring tiles, segments, weights taken
-        while (ok && next_segment(d, w)) {
-          const bool two = w.pair * 2 * tile_tokens + tile_tokens < w.s.n;
-          const int nb = w.blk1 - w.blk0;
-          wait(&sh.q_full, seg & 1);
-          ++seg;
-          if (!wait(&sh.full[n % L::kStages], (n / L::kStages) & 1)) break;
-          gdn::tc_fence_after();
-          scores(0, n % L::kStages);
-          if (two) scores(1, n % L::kStages);
-          gdn::tc_commit(&sh.empty[n % L::kStages]);
-          if (nb == 1) gdn::tc_commit(&sh.q_empty);
-          ++n;
-          for (int j = 0; j < nb; ++j) {
-            const uint32_t v = n, k = n + 1;  // ring tiles of V(j) and K(j + 1)
-            const bool more = j + 1 < nb;
-            wait(&sh.full[v % L::kStages], (v / L::kStages) & 1);
-            if (!wait(&sh.p_full[0], np[0]++ & 1)) break;
-            gdn::tc_fence_after();
-            values(0, v % L::kStages, j > 0);
-            if (more) {
-              if (!wait(&sh.full[k % L::kStages], (k / L::kStages) & 1)) break;
-              gdn::tc_fence_after();
-              scores(0, k % L::kStages);
-            }
-            if (two) {
-              if (!wait(&sh.p_full[1], np[1]++ & 1)) break;
-              gdn::tc_fence_after();
-              values(1, v % L::kStages, j > 0);
-            }
-            gdn::tc_commit(&sh.empty[v % L::kStages]);
-            if (more) {
-              if (two) scores(1, k % L::kStages);
-              gdn::tc_commit(&sh.empty[k % L::kStages]);
-              if (j + 2 == nb) gdn::tc_commit(&sh.q_empty);
-            }
-            n += more ? 2 : 1;
-          }
+          gdn::tc_commit(&sh.empty[stage]);
+          if (last) gdn::tc_commit(&sh.q_empty);
         }
-        if (!ok) *abort_flag = 1;
-        // Every product is complete before TMEM is given back.
-        gdn::tc_commit(&sh.done);
-        gdn::mbar_wait(&sh.done, 0);
+        __syncwarp();
+        advance();
+      };
+      Segment g;
+      for (uint32_t segs = 0; next(segs, g); ++segs) {
+        const bool active = t * tile_tokens < g.tokens;
+        if (!wait(&sh.q_full, segs & 1)) break;
+        if (!active) {
+          // Keep in step: release every tile of the segment unread.
+          if (lane == 0) gdn::mbar_arrive(&sh.q_empty);
+          for (int i = 0; ok && i < 2 * g.blocks; ++i) {
+            if (!wait(&sh.full[stage], phase)) break;
+            if (lane == 0) gdn::mbar_arrive(&sh.empty[stage]);
+            advance();
+          }
+          continue;
+        }
+        scores(g.blocks == 1);
+        for (int j = 0; ok && j < g.blocks; ++j) {
+          const uint32_t v_stage = stage;
+          if (!wait(&sh.full[stage], phase)) break;
+          advance();
+          if (j == 0 && done_segs > 0 && !wait(&sh.o_free[t], (done_segs - 1) & 1)) break;
+          if (!wait(&sh.p_full[t][0], np & 1)) break;
+          gdn::tc_fence_after();
+          if (elect_one()) gdn::tc_mma4_ts(o_col, s_col, 8, v_desc + v_stage * kStep, 128, id_o, j > 0);
+          __syncwarp();
+          if (!wait(&sh.p_full[t][1], np & 1)) break;
+          gdn::tc_fence_after();
+          if (elect_one()) {
+            gdn::tc_mma4_ts(o_col, s_col + 32, 8, v_desc + v_stage * kStep + 4 * 128, 128, id_o, 1);
+            if (j + 1 == g.blocks) gdn::tc_commit(&sh.o_last[t]);
+            gdn::tc_commit(&sh.empty[v_stage]);
+          }
+          __syncwarp();
+          ++np;
+          if (j + 1 < g.blocks) scores(j + 2 == g.blocks);
+        }
+        ++done_segs;
       }
+      if (!ok) *abort_flag = 1;
+      // Every product is complete before TMEM is given back.
+      if (elect_one()) gdn::tc_commit(&sh.done[t]);
       __syncwarp();
+      gdn::mbar_wait(&sh.done[t], 0);
     } else if (warp == kClearWarp) {
       // ------------------------------ value rows that no row of the item sees
       // Slots past the sequence's end or before every window may hold anything,
       // and 0 * NaN would reach the sum: they become zeros in shared memory.
       // Their copies complete on `raw`, and this warp completes `full`.
       uint32_t n = 0, raw_parity = 0;
-      while (ok && next_segment(d, w)) {
-        for (int blk = w.blk0; blk < w.blk1; ++blk, n += 2) {
-          const int key0 = (w.first + blk) * kKeys;
-          if (!needs_clearing(w, key0)) continue;
+      Segment g;
+      for (uint32_t segs = 0; ok && next(segs, g); ++segs) {
+        for (int j = 0; j < g.blocks; ++j, n += 2) {
+          const int key0 = g.key0 + j * kKeys;
+          if (key0 >= g.lo && key0 + kKeys <= g.hi) continue;
           const uint32_t stage = (n + 1) % L::kStages;  // K, V, K, V, ...
-          ok = wait_inline(&sh.raw[stage], (raw_parity >> stage) & 1, abort_flag);
+          if (!wait(&sh.raw[stage], (raw_parity >> stage) & 1)) break;
           raw_parity ^= 1u << stage;
-          if (!__all_sync(0xFFFFFFFFu, ok)) {
-            ok = false;
-            break;
-          }
           uint8_t* dst = ring + stage * L::kTile;
-          const int from = max(0, w.lo - key0), to = min(kKeys, w.hi - key0);
+          const int from = max(0, g.lo - key0), to = min(kKeys, g.hi - key0);
           for (int i = lane; i < kKeys * D / 8; i += 32) {
             const int row = (i >> 3) & (kKeys - 1);
             if (row < from || row >= to) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
@@ -525,39 +624,93 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) *abort_flag = 1;
+    } else {
+      // ----------------------------------------------------------- epilogue
+      // Reads a segment's O while the softmax warps are on the next one.
+      const int row = (warp & 3) * 32 + lane;
+      const uint32_t o_addr = tmem + L::kColO + (static_cast<uint32_t>(warp & 3) << 21);  // TMEM lane 32 (warp % 4)
+      const int my_token = row / a.group, my_head = row % a.group;
+      const bool aligned32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
+      uint32_t taken[2] = {0, 0};  // segments of each tile
+      Segment g;
+      for (uint32_t segs = 0; ok && next(segs, g); ++segs) {
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t) {
+          if (t * tile_tokens >= g.tokens) continue;
+          if (!wait(&sh.stat_full[t], taken[t] & 1) || !wait(&sh.o_last[t], taken[t] & 1)) break;
+          gdn::tc_fence_after();
+          const float2 ml = sh.stat[t][row];
+          ++taken[t];
+          const uint32_t o = o_addr + t * D;
+          const int token = t * tile_tokens + my_token;
+          const bool valid = my_token < tile_tokens && token < g.tokens;
+          if (g.part < 0) {
+            const float inv = 1.f / ml.y;
+            const int64_t out = (static_cast<int64_t>(g.first_token) + token) * a.Hq + g.head * a.group + my_head;
+            __nv_bfloat16* dst = a.o + out * D;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float x[32];
+              gdn::tmem_ld32(o + c, x);
+              if (c + 32 == D) release(&sh.o_free[t], lane);
+              if (valid) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  uint32_t y[8];
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) y[e] = gdn::pack_bf162(x[16 * i + 2 * e] * inv, x[16 * i + 2 * e + 1] * inv);
+                  store32(dst + c + 16 * i, y, aligned32);
+                }
+              }
+            }
+            if (valid && a.lse) a.lse[out] = (ml.x + log2f(ml.y)) / gdn::kLog2e;
+          } else {
+            const int64_t slot = 2 * static_cast<int64_t>(g.part) + t;
+            float4* dst = d.part_o + slot * (D / 4) * kRows + row;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float x[32];
+              gdn::tmem_ld32(o + c, x);
+              if (c + 32 == D) release(&sh.o_free[t], lane);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[(c / 4 + i) * kRows] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            }
+            d.part_ml[slot * kRows + row] = ml;
+          }
+        }
+      }
+      if (!ok) *abort_flag = 1;
     }
   } else {
     // --------------------------------------------------------------- softmax
-    regs_inc<208>();
-    Walk& w = sh.softmax_walk[warp];
-    if (lane == 0) w = sh.walk;
-    auto next = [&] {
-      int more = 0;
-      __syncwarp();
-      if (lane == 0) more = next_segment(d, w);
-      return __shfl_sync(0xFFFFFFFFu, more, 0) != 0;
-    };
-    const int t = warp >> 2;                       // tile
+    regs_inc<kSoftmaxRegs>();
+    const int t = warp >> 2;  // tile
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_bits = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (warp % 4)
     const uint32_t s_addr = tmem + L::kColS + t * kKeys + lane_bits, o_addr = tmem + L::kColO + t * D + lane_bits;
     const int my_token = row / a.group, my_head = row % a.group;
-    uint32_t n = 0;  // blocks taken
+    uint32_t n = 0, taken = 0;  // blocks, segments of this tile
     bool ok = true;
-    while (ok && next()) {
-      const int first_token = (w.pair * 2 + t) * tile_tokens;  // of the tile, within the new tokens
-      if (first_token >= w.s.n) continue;
-      const int token = first_token + my_token;
-      const bool valid = my_token < tile_tokens && token < w.s.n;
+    for (uint32_t segs = 0; ok; ++segs) {
+      const int at = segs % kSegments;
+      ok = wait_inline(&sh.seg_full[at], (segs / kSegments) & 1, abort_flag);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      const Segment& g = sh.seg[at];
+      const int blocks = g.blocks, seg_key0 = g.key0, tokens = g.tokens;
       // Rows without a token copy the range of the tile's last one.
-      const int pos = w.s.len - w.s.n + min(min(token, first_token + tile_tokens - 1), w.s.n - 1);
-      const int lo = gdn::key_lo(a, pos), hi = max(pos + 1, w.s.full);
+      const int pos = g.pos + min(t * tile_tokens + min(my_token, tile_tokens - 1), tokens - 1);
+      const int lo = gdn::key_lo(a, pos), hi = max(pos + 1, g.full);
       float slope = 0.f;
-      if (kMods && a.slopes) slope = a.slopes[w.head * a.group + my_head] * gdn::kLog2e;
+      if (kMods && a.slopes) slope = a.slopes[g.head * a.group + my_head] * gdn::kLog2e;
+      __syncwarp();
+      if (lane == 0) gdn::mbar_arrive(&sh.seg_empty[at]);
+      if (blocks == 0) break;
+      if (t * tile_tokens >= tokens) continue;
       float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
-      for (int blk = w.blk0; blk < w.blk1; ++blk, ++n) {
-        const int key0 = (w.first + blk) * kKeys;
+      for (int j = 0; j < blocks; ++j, ++n) {
+        const int key0 = seg_key0 + j * kKeys;
         ok = wait_inline(&sh.s_full[t], n & 1, abort_flag);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
           ok = false;
@@ -597,13 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float r = m == -INFINITY ? 0.f : gdn::exp2_approx(m - to);
           m = to;
           l2 = __fmul2_rn(l2, make_float2(r, r));
-          if (blk > w.blk0) {
-            ok = wait_inline(&sh.o_full[t], (n - 1) & 1, abort_flag);
-            if (!__all_sync(0xFFFFFFFFu, ok)) {
-              ok = false;
-              break;
-            }
-            gdn::tc_fence_after();
+          if (j > 0) {  // O of the blocks before is complete: S came behind it
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               float x[16];
@@ -617,6 +764,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float ref = m == -INFINITY ? 0.f : m;  // a row that has seen no key yet: weights 2^-inf = 0
         const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), ref2 = make_float2(-ref, -ref);
+        // Weights of 64 keys at a time, so that the first half of P V runs beside
+        // the exponentials of the second.
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t p[32];
@@ -630,58 +779,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             p[i] = gdn::pack_bf162(x);
           }
           tmem_st32_nw(s_addr + 32 * h, p);
+          gdn::tmem_wait_st();
+          gdn::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) gdn::mbar_arrive(&sh.p_full[t][h]);
         }
-        gdn::tmem_wait_st();
-        gdn::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) gdn::mbar_arrive(&sh.p_full[t]);
       }
       if (!ok) break;
-      // ---- epilogue ----
-      ok = wait_inline(&sh.o_full[t], (n - 1) & 1, abort_flag);
-      if (!__all_sync(0xFFFFFFFFu, ok)) {
-        ok = false;
-        break;
-      }
-      gdn::tc_fence_after();
-      const float l = l2.x + l2.y;
-      const bool starts = w.blk0 == 0, ends = w.blk1 == w.blocks;
-      if (starts && ends) {
-        const float inv = 1.f / l;
-        const int64_t out = (static_cast<int64_t>(w.s.first_token) + token) * a.Hq + w.head * a.group + my_head;
-        uint4* dst = reinterpret_cast<uint4*>(a.o + out * D);
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float x[32];
-          gdn::tmem_ld32(o_addr + c, x);
-          if (valid) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[c / 8 + i] =
-                  make_uint4(gdn::pack_bf162(x[8 * i] * inv, x[8 * i + 1] * inv), gdn::pack_bf162(x[8 * i + 2] * inv, x[8 * i + 3] * inv),
-                             gdn::pack_bf162(x[8 * i + 4] * inv, x[8 * i + 5] * inv), gdn::pack_bf162(x[8 * i + 6] * inv, x[8 * i + 7] * inv));
-          }
+      if (taken > 0) {  // the epilogue has taken the last segment's
+        ok = wait_inline(&sh.o_free[t], (taken - 1) & 1, abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          ok = false;
+          break;
         }
-        if (valid && a.lse) a.lse[out] = (m + log2f(l)) / gdn::kLog2e;
-      } else {
-        // One segment of a CTA at most starts an item that it does not end, and
-        // one at most continues one: two slots per CTA.
-        const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (starts ? 1 : 0)) * 2 + t;
-        float4* dst = d.part_o + slot * (D / 4) * kRows + row;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float x[32];
-          gdn::tmem_ld32(o_addr + c, x);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[(c / 4 + i) * kRows] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-        }
-        d.part_ml[slot * kRows + row] = make_float2(m, l);
-        if (starts && t == 0 && row == 0)
-          d.cuts[blockIdx.x] = make_int4(w.b, w.pair, w.head, share_owner(total, eff, w.item0 + w.cost - 1));
       }
-      // The next segment's first P V overwrites O: these loads come first.
-      gdn::tc_fence_before();
+      sh.stat[t][row] = make_float2(m, l2.x + l2.y);
+      ++taken;
+      __syncwarp();
+      if (lane == 0) gdn::mbar_arrive(&sh.stat_full[t]);
     }
     if (!ok) *abort_flag = 1;
   }
@@ -689,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   gdn::tc_fence_after();
   if (tid == 0 && sh.abort) gdn::record_error(a.paged.err_word, GDN_DEVERR_TIMEOUT, 0);
-  if (warp == kAllocWarp) gdn::tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) gdn::tmem_dealloc(tmem, 512);
 }
 
 // Joins the partial results of the items that CTAs of the kernel above cut: the
@@ -710,45 +825,50 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
   const int token = (cut.y * 2 + t) * d.tile_tokens + in_tile;
   if (in_tile >= d.tile_tokens || token >= s.new_tokens) return;
   constexpr int kG = D / 32;  // groups of four dimensions per thread
+  const int group0 = threadIdx.x >> 5;
+  auto slot_of = [&](int i) { return (2 * static_cast<int64_t>(i) + (i == c ? 1 : 0)) * 2 + t; };
   float m = -INFINITY, l = 0.f;
+  for (int i = c; i <= cut.w; ++i) m = fmaxf(m, d.part_ml[slot_of(i) * kRows + row].x);
   float4 o[kG];
 #pragma unroll
   for (int k = 0; k < kG; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // The parts in a fixed order; two in flight.
+#pragma unroll 2
   for (int i = c; i <= cut.w; ++i) {
-    const int64_t slot = (2 * static_cast<int64_t>(i) + (i == c ? 1 : 0)) * 2 + t;
+    const int64_t slot = slot_of(i);
     const float2 ml = d.part_ml[slot * kRows + row];
-    const float top = fmaxf(m, ml.x);
-    const float ra = m == -INFINITY ? 0.f : gdn::exp2_approx(m - top);
-    const float rb = ml.x == -INFINITY ? 0.f : gdn::exp2_approx(ml.x - top);
-    l = l * ra + ml.y * rb;
-    m = top;
+    float4 x[kG];
+#pragma unroll
+    for (int k = 0; k < kG; ++k) x[k] = d.part_o[(slot * (D / 4) + group0 + 8 * k) * kRows + row];
+    const float f = ml.x == -INFINITY ? 0.f : gdn::exp2_approx(ml.x - m);
+    l = fmaf(ml.y, f, l);
 #pragma unroll
     for (int k = 0; k < kG; ++k) {
-      const float4 x = d.part_o[(slot * (D / 4) + (threadIdx.x >> 5) + 8 * k) * kRows + row];
-      o[k].x = o[k].x * ra + x.x * rb;
-      o[k].y = o[k].y * ra + x.y * rb;
-      o[k].z = o[k].z * ra + x.z * rb;
-      o[k].w = o[k].w * ra + x.w * rb;
+      o[k].x = fmaf(x[k].x, f, o[k].x);
+      o[k].y = fmaf(x[k].y, f, o[k].y);
+      o[k].z = fmaf(x[k].z, f, o[k].z);
+      o[k].w = fmaf(x[k].w, f, o[k].w);
     }
   }
   const float inv = 1.f / l;
   const int64_t out = (static_cast<int64_t>(s.first_token) + token) * a.Hq + cut.z * a.group + row % a.group;
 #pragma unroll
   for (int k = 0; k < kG; ++k)
-    reinterpret_cast<uint2*>(a.o + out * D)[(threadIdx.x >> 5) + 8 * k] =
+    reinterpret_cast<uint2*>(a.o + out * D)[group0 + 8 * k] =
         make_uint2(gdn::pack_bf162(o[k].x * inv, o[k].y * inv), gdn::pack_bf162(o[k].z * inv, o[k].w * inv));
   if (a.lse && threadIdx.x < 32) a.lse[out] = (m + log2f(l)) / gdn::kLog2e;
 }
 
+constexpr int kWholeKeys = 8 * kKeys;  // longest sequence whose items are never cut (see launch)
 constexpr size_t kCutBytes = kMaxGrid * sizeof(int4);
 size_t workspace_bytes_of(int D) {
   return kCutBytes + static_cast<size_t>(4) * kMaxGrid * kRows * (sizeof(float2) + D * sizeof(float));
 }
 
 template <int D, bool kMods>
-int launch(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache* cache, void* workspace, int sms, cudaStream_t stream) {
+int launch(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache* cache, const gdn_page_table* table, void* workspace, int sms, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  constexpr int smem = Layout<D>::kBytes + sizeof(Smem<D>) + 1024;
+  constexpr int smem = Layout<D>::kBytes + sizeof(Smem<D>);
   static_assert(smem <= 232448, "shared memory of one CTA");
   int rc = gdn_host::func_attr_once(chunk_attention_kernel<D, kMods>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem,
                                     done);
@@ -757,16 +877,20 @@ int launch(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache* cache, void* w
   const int64_t dims[4] = {D, d.a.group, total_tokens, d.a.Hkv};
   const int64_t strides[3] = {2 * D, 2 * d.a.q_stride, 2 * static_cast<int64_t>(d.a.group) * D};
   if ((rc = gdn_host::encode_map_4d(&q_map, d.a.q, dims, strides, d.a.group, d.tile_tokens)) != GDN_OK) return rc;
-  if ((rc = gdn_host::encode_cache_map(&k_map, cache->k, cache, d.a.box_rows)) != GDN_OK) return rc;
-  if ((rc = gdn_host::encode_cache_map(&v_map, cache->v, cache, d.a.box_rows)) != GDN_OK) return rc;
+  if ((rc = gdn_host::encode_cache_map(&k_map, cache->k, cache, d.a.box_shift)) != GDN_OK) return rc;
+  if ((rc = gdn_host::encode_cache_map(&v_map, cache->v, cache, d.a.box_shift)) != GDN_OK) return rc;
   const int grid = sms < kMaxGrid ? sms : kMaxGrid;
+  // The longest sequence the table can hold has every entry that the others do
+  // not need.  Where even that is a few blocks, the join's launch would cost more
+  // than an even split saves.
+  d.whole = (static_cast<int64_t>(table->num_entries) - table->num_seqs + 1) * cache->page_size <= kWholeKeys;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   d.cuts = reinterpret_cast<int4*>(ws);
   d.part_ml = reinterpret_cast<float2*>(ws + kCutBytes);
   d.part_o = reinterpret_cast<float4*>(ws + kCutBytes + sizeof(float2) * 4 * kMaxGrid * kRows);
   rc = gdn_host::launch_pdl(chunk_attention_kernel<D, kMods>, dim3(grid), dim3(kThreads), smem, stream, d, q_map, k_map,
                             v_map);
-  if (rc != GDN_OK) return rc;
+  if (rc != GDN_OK || d.whole) return rc;
   return gdn_host::launch_pdl(chunk_join_kernel<D>, dim3(grid, 8), dim3(256), 0, stream, d);
 }
 
@@ -795,8 +919,8 @@ extern "C" int gdn_attention_paged(const gdn_bf16* q, int64_t q_token_stride, gd
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool mods = d.a.cap_log2 > 0.f || d.a.slopes;
   if (cache->head_dim == 64)
-    return mods ? launch<64, true>(d, total_tokens, cache, workspace, sms, s)
-                : launch<64, false>(d, total_tokens, cache, workspace, sms, s);
-  return mods ? launch<128, true>(d, total_tokens, cache, workspace, sms, s)
-              : launch<128, false>(d, total_tokens, cache, workspace, sms, s);
+    return mods ? launch<64, true>(d, total_tokens, cache, table, workspace, sms, s)
+                : launch<64, false>(d, total_tokens, cache, table, workspace, sms, s);
+  return mods ? launch<128, true>(d, total_tokens, cache, table, workspace, sms, s)
+              : launch<128, false>(d, total_tokens, cache, table, workspace, sms, s);
 }

@@ -67,7 +67,7 @@ struct AttnArgs {
   const float* slopes;        // [Hq] or nullptr
   const int32_t* full_lens;   // [num_seqs] or nullptr
   int32_t window;             // < 0: none
-  int32_t box_rows;           // tokens per copy of a page
+  int32_t box_shift;          // log2 of the tokens per copy of a page
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -84,6 +84,35 @@ __device__ __forceinline__ float capped(float x, float cap_log2) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(exp2_approx(x) + 1.f));
   return fmaf(-2.f * cap_log2, r, cap_log2);
+}
+
+// A line of `total` units in equal pieces for `eff` CTAs: piece c is [start(c),
+// start(c + 1)).  One 64-bit division per CTA; the rest is in 32 bits.
+struct Shares {
+  int64_t total, q;
+  int r, eff;
+  __device__ __forceinline__ Shares(int64_t units, int64_t most, int grid) {
+    total = units;
+    eff = static_cast<int>(most < 1 ? 1 : most < grid ? most : grid);
+    q = total <= 0xFFFFFFFFll ? static_cast<int64_t>(static_cast<uint32_t>(total) / static_cast<uint32_t>(eff))
+                              : total / eff;
+    r = static_cast<int>(total - q * eff);
+  }
+  __device__ __forceinline__ int64_t start(int c) const { return q * c + r * c / eff; }
+  // The piece that holds unit x.
+  __device__ __forceinline__ int owner(int64_t x) const {
+    int c = min(static_cast<int>(static_cast<float>(x) / static_cast<float>(total) * static_cast<float>(eff)), eff - 1);
+    while (c + 1 < eff && start(c + 1) <= x) ++c;
+    while (start(c) > x) --c;
+    return c;
+  }
+};
+// floor(x / d) for 0 <= x < d * most, without a 64-bit division.
+__device__ __forceinline__ int small_quotient(int64_t x, int d, int most) {
+  int c = min(static_cast<int>(static_cast<float>(x) / static_cast<float>(d)), most - 1);
+  while (static_cast<int64_t>(c + 1) * d <= x) ++c;
+  while (static_cast<int64_t>(c) * d > x) --c;
+  return c;
 }
 
 // Keys that a token at `pos` sees: [lo, hi).
@@ -168,20 +197,19 @@ inline int attention_args(gdn::AttnArgs* a, const gdn_bf16* q, int64_t q_stride,
   a->slopes = options ? options->slopes : nullptr;
   a->full_lens = options ? options->full_lens : nullptr;
   a->window = options ? options->window : -1;
-  a->box_rows = 1;
-  while (a->box_rows < tile_keys && cache->page_size % (2 * a->box_rows) == 0) a->box_rows *= 2;
+  while ((1 << a->box_shift) < tile_keys && cache->page_size % (2 << a->box_shift) == 0) ++a->box_shift;
   return GDN_OK;
 }
 
 // Tensor map of one cache array, {D, heads, slots, pages}, with boxes of 64
-// dimensions of one head of box_rows slots.  An axis of one entry may carry any
+// dimensions of one head of 2^box_shift slots.  An axis of one entry may carry any
 // stride; the map wants a multiple of 16 bytes.
-inline int encode_cache_map(CUtensorMap* map, const gdn_bf16* base, const gdn_kv_cache* c, int box_rows) {
+inline int encode_cache_map(CUtensorMap* map, const gdn_bf16* base, const gdn_kv_cache* c, int box_shift) {
   const int64_t dims[4] = {c->head_dim, c->num_heads, c->page_size, c->num_pages};
   const int64_t strides[3] = {2 * (c->num_heads > 1 ? c->head_stride : c->head_dim),
                               2 * (c->page_size > 1 ? c->token_stride : c->head_dim),
                               2 * (c->num_pages > 1 ? c->page_stride : c->head_dim)};
-  return encode_map_4d(map, base, dims, strides, 1, box_rows);
+  return encode_map_4d(map, base, dims, strides, 1, 1 << box_shift);
 }
 
 }  // namespace gdn_host

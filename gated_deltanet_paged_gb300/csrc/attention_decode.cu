@@ -34,7 +34,7 @@ constexpr int kRows = 16;     // query heads per pass of an item
 // Fixed cost of an item (its queries, the join of the warps, its stores) in
 // blocks, so that shares of many short items weigh the same as shares of long ones.
 constexpr int kItemCost = 2;
-constexpr int kMinShare = 6;  // blocks below which a cut costs more than it saves
+constexpr int kMinShare = 8;  // blocks below which a cut costs more than it saves
 constexpr int kWholeBlocks = 8;  // longest item that is never cut (see launch)
 
 struct DecodeArgs {
@@ -97,7 +97,7 @@ __device__ __forceinline__ bool next_segment(const DecodeArgs& d, Walk& w) {
       w.it = load_item(d.a, ++w.b);
       continue;
     }
-    w.head = static_cast<int>((w.pos - w.base) / w.it.cost);
+    w.head = gdn::small_quotient(w.pos - w.base, w.it.cost, per_seq);
     w.item0 = w.base + static_cast<int64_t>(w.head) * w.it.cost;
     const int64_t stop = min(w.end, w.item0 + w.it.cost);
     w.blk0 = max(0, static_cast<int>(w.pos - w.item0) - kItemCost);
@@ -146,16 +146,6 @@ __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
 }
 
-// The piece [start, end) of the batch's line that CTA c takes, and the CTA that
-// holds line position x.  eff: CTAs that get one.
-__device__ __forceinline__ int64_t share_start(int64_t total, int eff, int c) { return total * c / eff; }
-__device__ __forceinline__ int share_owner(int64_t total, int eff, int64_t x) {
-  int c = static_cast<int>(x * eff / total);
-  while (c + 1 < eff && share_start(total, eff, c + 1) <= x) ++c;
-  while (share_start(total, eff, c) > x) --c;
-  return c;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_attention_kernel(const __grid_constant__ DecodeArgs d, const __grid_constant__ CUtensorMap k_map,
@@ -164,6 +154,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   Smem<D>& sh = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const AttnArgs& a = d.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == kConsumers * 32) {
+    gdn::prefetch_tensormap(&k_map);
+    gdn::prefetch_tensormap(&v_map);
+  }
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       gdn::mbar_init(&sh.full[i], 1);
@@ -178,8 +172,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // ---- this CTA's share of the line ----
   const int per_seq = a.Hkv * d.passes;
   Walk w;
-  int64_t total = 0;
-  int eff = gridDim.x;
+  gdn::Shares shares(0, 1, 1);
   if (d.whole) {
     w.pos = blockIdx.x;
     w.end = static_cast<int64_t>(a.paged.num_seqs) * per_seq;
@@ -205,17 +198,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (lane == 31) sh.scan[warp] = incl;
     __syncthreads();
-    int64_t before = incl - mine;
+    int64_t before = incl - mine, total = 0;
     for (int i = 0; i < kThreads / 32; ++i) {
       if (i < warp) before += sh.scan[i];
       total += sh.scan[i];
     }
     total *= per_seq;
-    const int64_t most = total / kMinShare;
-    eff = static_cast<int>(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
+    shares = gdn::Shares(total, total / kMinShare, gridDim.x);
     const int c = blockIdx.x;
-    const int64_t start = c < eff ? share_start(total, eff, c) : total;
-    const int64_t end = c < eff ? share_start(total, eff, c + 1) : total;
+    const int64_t start = c < shares.eff ? shares.start(c) : total;
+    const int64_t end = c < shares.eff ? shares.start(c + 1) : total;
     // The thread whose sequences hold `start` sets up the walk.
     if (start < end && before * per_seq <= start && start < (before + mine) * per_seq) {
       Walk x;
@@ -246,15 +238,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int stage = n % kStages;
         const int key0 = (w.it.first + blk) * kBlock;
         // The copies of this block: only those that hold a visible key.
-        const int first = max(0, w.it.lo - key0) / a.box_rows;
-        const int last = (min(kBlock, w.it.hi - key0) + a.box_rows - 1) / a.box_rows;
+        const int first = max(0, w.it.lo - key0) >> a.box_shift;
+        const int last = (min(kBlock, w.it.hi - key0) + (1 << a.box_shift) - 1) >> a.box_shift;
         int page[2], slot[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int box = lane + 32 * i;
           page[i] = 0;
           if (box >= first && box < last) {
-            const int key = key0 + box * a.box_rows;
+            const int key = key0 + (box << a.box_shift);
             const int entry = key / a.paged.page_size;
             slot[i] = key - entry * a.paged.page_size;
             page[i] = a.paged.pages[w.it.s.entry + entry];
@@ -266,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         if (lane == 0) {
           if (n >= kStages) ok = gdn::mbar_wait_or_abort(&sh.empty[stage], ((n / kStages) - 1) & 1, &sh.abort);
-          if (ok) gdn::mbar_arrive_expect_tx(&sh.full[stage], (last - first) * a.box_rows * D * 4);
+          if (ok) gdn::mbar_arrive_expect_tx(&sh.full[stage], ((last - first) << a.box_shift) * D * 4);
         }
         ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         if (!ok) break;
@@ -274,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int i = 0; i < 2; ++i) {
           const int box = lane + 32 * i;
           if (box >= first && box < last) {
-            const int at = box * a.box_rows * 128;
+            const int at = (box << a.box_shift) * 128;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
               gdn::tma_load_4d(sh.kv[stage][0] + c * kBlock * 128 + at, &k_map, &sh.full[stage], c * 64, head, slot[i],
@@ -485,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (t == 0) d.part_ml[slot * kRows + r] = make_float2(m[i], l[i]);
         }
         if (starts && lane == 0)
-          d.cuts[blockIdx.x] = make_int4(w.b, head, pass, share_owner(total, eff, w.item0 + w.it.cost - 1));
+          d.cuts[blockIdx.x] = make_int4(w.b, head, pass, shares.owner(w.item0 + w.it.cost - 1));
       }
     }
   }
@@ -537,8 +529,8 @@ int launch(const DecodeArgs& base, const gdn_kv_cache* cache, const gdn_page_tab
   if (rc != GDN_OK) return rc;
   DecodeArgs d = base;
   CUtensorMap k_map, v_map;
-  if ((rc = gdn_host::encode_cache_map(&k_map, cache->k, cache, d.a.box_rows)) != GDN_OK) return rc;
-  if ((rc = gdn_host::encode_cache_map(&v_map, cache->v, cache, d.a.box_rows)) != GDN_OK) return rc;
+  if ((rc = gdn_host::encode_cache_map(&k_map, cache->k, cache, d.a.box_shift)) != GDN_OK) return rc;
+  if ((rc = gdn_host::encode_cache_map(&v_map, cache->v, cache, d.a.box_shift)) != GDN_OK) return rc;
   d.passes = (d.a.group + kRows - 1) / kRows;
   const int64_t items = static_cast<int64_t>(table->num_seqs) * d.a.Hkv * d.passes;
   int grid = 2 * sms < kMaxGrid ? 2 * sms : kMaxGrid;

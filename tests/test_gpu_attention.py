@@ -386,6 +386,27 @@ def test_chunk_equals_decode_and_split_chunks():
     within(dl, ref[1][last.cpu()], ref[3][last.cpu()], "lse of the last token")
 
 
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_outputs_on_any_16_byte_boundary(decode, dim):
+    """o, q, the keys and the values start 16 bytes into their allocations."""
+    new, prefix = ([1, 1], [100, 700]) if decode else ([70, 5], [100, 700])
+    b = Batch(new, prefix, 64, 6, 2, dim, seed=13).fill()
+    want, _ = check_attention(b, decode=decode)
+
+    def shifted(t):
+        raw = torch.empty(t.numel() + 8, dtype=torch.bfloat16, device="cuda")[8:]
+        assert raw.data_ptr() % 32 == 16
+        return raw.view(t.shape).copy_(t)
+
+    o, q, k, v = shifted(b.q), shifted(b.q), shifted(b.k_cache), shifted(b.v_cache)
+    if decode:
+        gdn.gdn_attention_decode_paged(q, k, v, *b.table, o=o)
+    else:
+        gdn.gdn_attention_paged(q, k, v, b.cu, *b.table, o=o)
+    assert torch.equal(o.view(I16), want.view(I16))
+
+
 def test_cache_beyond_32_bit_offsets():
     """A cache of more than 2^32 elements per array: tokens in its last pages."""
     pages, ps, hkv, dim = 4200, 1024, 8, 128

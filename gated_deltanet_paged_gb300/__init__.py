@@ -114,8 +114,8 @@ def library():
                 fn = getattr(lib, name)
                 fn.argtypes = args
                 fn.restype = ctypes.c_int
-            sizes = {"gdn_prefill_workspace_bytes": [i32] * 3, "gdn_attention_workspace_bytes": [i32] * 5,
-                     "gdn_attention_decode_workspace_bytes": [i32] * 4}
+            sizes = {"gdn_prefill_workspace_bytes": [i32] * 3, "gdn_attention_workspace_bytes": [i32] * 7,
+                     "gdn_attention_decode_workspace_bytes": [i32] * 6}
             for name, args in sizes.items():
                 getattr(lib, name).argtypes = args
                 getattr(lib, name).restype = ctypes.c_size_t
@@ -140,9 +140,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _raw_stream(index):
+    """The handle of the current stream of CUDA device ``index``, without building
+    a torch.cuda.Stream (2 us)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _stream(t):
-    # The handle of torch.cuda.current_stream(t.device), without building a Stream (2 us).
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return _raw_stream(t.device.index)
 
 
 def _need(t, dtype, name, ndim=None):
@@ -421,20 +426,22 @@ def gdn_pool_zero_rows(pool, rows, err_word=None):
 # The attention layer: rotary positions, the paged key / value cache, attention
 # ---------------------------------------------------------------------------
 # A call of these at decode sizes lasts a few microseconds on the GPU, so the
-# checks below read each property of a tensor once and leave the wording of an
-# error to the slow path.
-def _heads_arg(t, name, D=None):
-    """A bf16 [T, H, D] tensor with dense heads; the token stride may be padded
-    (a slice of a fused projection).  Returns (T, H, D, token stride)."""
+# checks read each property of a tensor once (get_device() is -1 off the GPU) and
+# leave the wording of an error to the slow path.
+def _heads_arg(t, name, dev, D=None):
+    """A bf16 [T, H, D] tensor with dense heads on CUDA device ``dev``; the token
+    stride may be padded (a slice of a fused projection).  Returns (T, H, D,
+    token stride)."""
     if t is None:
         raise ValueError("%s is required" % name)
     if t.dtype is not torch.bfloat16:
         raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dim() != 3:
+    if t.get_device() != dev or dev < 0:
+        raise ValueError("%s must be a CUDA tensor on the call's device" % name)
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError("%s must have 3 dims" % name)
-    T, H, d = t.shape
+    T, H, d = shape
     s0, s1, s2 = t.stride()
     if (d > 1 and s2 != 1) or (H > 1 and s1 != d) or (T > 1 and s0 < H * d):
         raise ValueError("%s must be [T, H, D] with dense heads" % name)
@@ -443,57 +450,69 @@ def _heads_arg(t, name, D=None):
     return T, H, d, s0 if T > 1 else H * d
 
 
-def _vector(t, dtype, name):
-    """The length of a contiguous 1-d CUDA tensor."""
-    if t is None or t.dtype is not dtype or not t.is_cuda or t.dim() != 1 or not t.is_contiguous():
+def _vector(t, dtype, name, dev):
+    """The length of a contiguous 1-d tensor on CUDA device ``dev``."""
+    if t is None or t.dtype is not dtype or t.get_device() != dev or t.stride() != (1,):
         _need(t, dtype, name, 1)
+        if t.get_device() != dev:
+            raise ValueError("%s must be on the call's device" % name)
     return t.shape[0]
 
 
-def _same_device(device, *others):
-    for x in others:
-        if x is not None and x.device != device:
-            raise ValueError("all tensors must be on %s, got one on %s" % (device, x.device))
-
-
-def _kv_cache_arg(k_cache, v_cache):
-    """(gdn_kv_cache bytes, Hkv, D)."""
+def _kv_cache_arg(k_cache, v_cache, dev):
+    """(gdn_kv_cache bytes, Hkv, D, page size)."""
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if t.dtype is not torch.bfloat16:
             raise TypeError("%s must be %s, got %s" % (n, torch.bfloat16, t.dtype))
-        if not t.is_cuda:
-            raise ValueError("%s must be a CUDA tensor" % n)
+        if t.get_device() != dev:
+            raise ValueError("%s must be a CUDA tensor on the call's device" % n)
     shape, strides = k_cache.shape, k_cache.stride()
     if len(shape) != 4 or (shape[3] > 1 and strides[3] != 1):
         raise ValueError("k_cache must be [num_pages, page_size, Hkv, D] with dense D")
     if v_cache.shape != shape or v_cache.stride() != strides:
         raise ValueError("k_cache and v_cache must have the same shape and strides")
-    return _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), *shape, *strides[:3]), shape[2], shape[3]
+    pages, ps, h, d = shape
+    return _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), pages, ps, h, d, *strides[:3]), h, d, ps
 
 
-def _page_table_arg(page_indices, page_indptr, last_page_len, cu_seqlens, T):
-    """(gdn_page_table bytes, num_seqs), checked against T new tokens."""
+def _page_table_arg(page_indices, page_indptr, last_page_len, cu_seqlens, T, dev):
+    """(gdn_page_table bytes, num_seqs, num_entries), checked against T new tokens."""
     i32 = torch.int32
-    n = _vector(page_indices, i32, "page_indices")
-    S = _vector(last_page_len, i32, "last_page_len")
-    if _vector(page_indptr, i32, "page_indptr") != S + 1:
+    n = _vector(page_indices, i32, "page_indices", dev)
+    S = _vector(last_page_len, i32, "last_page_len", dev)
+    if _vector(page_indptr, i32, "page_indptr", dev) != S + 1:
         raise ValueError("page_indptr must hold one entry more than last_page_len")
     if cu_seqlens is None:
         if T != S:
             raise ValueError("without cu_seqlens every sequence has one new token: got %d tokens, %d sequences" % (T, S))
-    elif _vector(cu_seqlens, i32, "cu_seqlens") != S + 1:
+    elif _vector(cu_seqlens, i32, "cu_seqlens", dev) != S + 1:
         raise ValueError("cu_seqlens must hold one entry more than last_page_len")
-    return _PAGE_TABLE.pack(page_indices.data_ptr(), n, page_indptr.data_ptr(), last_page_len.data_ptr(), S), S
+    return _PAGE_TABLE.pack(page_indices.data_ptr(), n, page_indptr.data_ptr(), last_page_len.data_ptr(), S), S, n
 
 
-def _frequencies_arg(frequencies, D):
+def _frequencies_arg(frequencies, D, dev):
     """rotary_dim of an int64 frequency tensor (None: 0)."""
     if frequencies is None:
         return 0
-    n = _vector(frequencies, torch.int64, "frequencies")
+    n = _vector(frequencies, torch.int64, "frequencies", dev)
     if not 0 < 2 * n <= D:
         raise ValueError("frequencies must hold between 1 and D / 2 entries")
     return 2 * n
+
+
+def _out_arg(t, like, T, H, D, name, dev):
+    """A dense bf16 [T, H, D] output: the caller's, or a new one."""
+    if t is None:
+        if like.is_contiguous():
+            return torch.empty_like(like)
+        return torch.empty((T, H, D), dtype=torch.bfloat16, device=like.device)
+    if _need(t, torch.bfloat16, name, 3).shape != (T, H, D) or t.get_device() != dev:
+        raise ValueError("%s must be [%d, %d, %d] on the call's device" % (name, T, H, D))
+    return t
+
+
+def _err_arg(err_word, dev):
+    return None if err_word is None or _vector(err_word, torch.int32, "err_word", dev) < 1 else err_word.data_ptr()
 
 
 def gdn_rope_frequencies(rotary_dim, base=10000.0, *, factor=1.0, original_len=0, low_turns=1.0, high_turns=32.0,
@@ -516,23 +535,23 @@ def gdn_rope(x, frequencies, positions, *, interleaved=False, inverse=False, amp
     frequencies, and scaled by ``amplitude``; pairs are (i, i + rotary_dim / 2),
     or (2 i, 2 i + 1) with ``interleaved``.  ``inverse`` applies the transposed
     map (the gradient's).  ``out`` may be x itself."""
-    T, H, D, xs = _heads_arg(x, "x")
-    rotary = _frequencies_arg(frequencies, D)
+    dev = x.get_device()
+    T, H, D, xs = _heads_arg(x, "x", dev)
+    rotary = _frequencies_arg(frequencies, D, dev)
     if rotary == 0:
         raise ValueError("frequencies is required")
-    if _vector(positions, torch.int32, "positions") != T:
+    if _vector(positions, torch.int32, "positions", dev) != T:
         raise ValueError("positions must hold one entry per token")
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=x.device)
+        out = _out_arg(None, x, T, H, D, "out", dev)
         ys = H * D
     else:
-        To, Ho, _, ys = _heads_arg(out, "out", D)
+        To, Ho, _, ys = _heads_arg(out, "out", dev, D)
         if (To, Ho) != (T, H):
             raise ValueError("out must have the shape of x")
-    _same_device(x.device, frequencies, positions, out)
-    _check("gdn_rope", library().gdn_rope(x.data_ptr(), xs, out.data_ptr(), ys, positions.data_ptr(),
-                                          frequencies.data_ptr(), T, H, D, rotary, 1 if interleaved else 0,
-                                          1 if inverse else 0, amplitude, _stream(x)))
+    _check("gdn_rope", (_lib or library()).gdn_rope(
+        x.data_ptr(), xs, out.data_ptr(), ys, positions.data_ptr(), frequencies.data_ptr(), T, H, D, rotary,
+        1 if interleaved else 0, 1 if inverse else 0, amplitude, _raw_stream(dev)))
     return out
 
 
@@ -543,80 +562,74 @@ def gdn_kv_append_paged(k, v, k_cache, v_cache, cu_seqlens, page_indices, page_i
     their positions on the way, and rotate the queries q (bf16 [T, Hq, D]) along.
     ``cu_seqlens`` None: one new token per sequence.  Returns the rotated queries
     (None without q); the caches are updated in place."""
-    cache, Hkv, D = _kv_cache_arg(k_cache, v_cache)
-    T, Hk, _, ks = _heads_arg(k, "k", D)
-    Tv, Hv, _, vs = _heads_arg(v, "v", D)
+    dev = k.get_device()
+    cache, Hkv, D, _ = _kv_cache_arg(k_cache, v_cache, dev)
+    T, Hk, _, ks = _heads_arg(k, "k", dev, D)
+    Tv, Hv, _, vs = _heads_arg(v, "v", dev, D)
     if Tv != T or Hk != Hkv or Hv != Hkv:
         raise ValueError("k and v must be [T, Hkv, D]")
-    table, _ = _page_table_arg(page_indices, page_indptr, last_page_len, cu_seqlens, T)
-    rotary = _frequencies_arg(frequencies, D)
+    table, _, _ = _page_table_arg(page_indices, page_indptr, last_page_len, cu_seqlens, T, dev)
+    rotary = _frequencies_arg(frequencies, D, dev)
     qs = Hq = 0
     if q is not None:
-        Tq, Hq, _, qs = _heads_arg(q, "q", D)
+        Tq, Hq, _, qs = _heads_arg(q, "q", dev, D)
         if Tq != T:
             raise ValueError("q must hold as many tokens as k")
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-        elif _need(q_out, torch.bfloat16, "q_out", 3).shape != q.shape:
-            raise ValueError("q_out must have the shape of q")
+        q_out = _out_arg(q_out, q, T, Hq, D, "q_out", dev)
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    _same_device(k.device, v, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, q, q_out,
-                 frequencies, err_word)
-    _check("gdn_kv_append_paged", library().gdn_kv_append_paged(
+    _check("gdn_kv_append_paged", (_lib or library()).gdn_kv_append_paged(
         _ptr(q), qs, _ptr(q_out), k.data_ptr(), ks, v.data_ptr(), vs, _ptr(cu_seqlens), T, Hq, cache, table,
-        _ptr(frequencies), rotary, 1 if interleaved else 0, amplitude, _ptr(_opt(err_word, torch.int32, "err_word")),
-        _stream(k)))
+        _ptr(frequencies), rotary, 1 if interleaved else 0, amplitude, _err_arg(err_word, dev), _raw_stream(dev)))
     return q_out
 
 
-@functools.lru_cache(maxsize=256)
-def gdn_attention_workspace_bytes(num_seqs: int, total_tokens: int, Hq: int, Hkv: int, D: int) -> int:
-    return int(library().gdn_attention_workspace_bytes(num_seqs, total_tokens, Hq, Hkv, D))
+@functools.lru_cache(maxsize=1024)
+def gdn_attention_workspace_bytes(num_seqs: int, total_tokens: int, Hq: int, Hkv: int, D: int, num_entries: int,
+                                  page_size: int) -> int:
+    return int(library().gdn_attention_workspace_bytes(num_seqs, total_tokens, Hq, Hkv, D, num_entries, page_size))
 
 
-@functools.lru_cache(maxsize=256)
-def gdn_attention_decode_workspace_bytes(num_seqs: int, Hq: int, Hkv: int, D: int) -> int:
-    return int(library().gdn_attention_decode_workspace_bytes(num_seqs, Hq, Hkv, D))
+@functools.lru_cache(maxsize=1024)
+def gdn_attention_decode_workspace_bytes(num_seqs: int, Hq: int, Hkv: int, D: int, num_entries: int,
+                                         page_size: int) -> int:
+    return int(library().gdn_attention_decode_workspace_bytes(num_seqs, Hq, Hkv, D, num_entries, page_size))
 
 
 def _attention(decode, q, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, scale, softcap, window,
                slopes, full_lens, o, lse, return_lse, err_word, workspace):
-    cache, Hkv, D = _kv_cache_arg(k_cache, v_cache)
-    T, Hq, _, qs = _heads_arg(q, "q", D)
-    table, S = _page_table_arg(page_indices, page_indptr, last_page_len, cu_seqlens, T)
+    dev = q.get_device()
+    cache, Hkv, D, page_size = _kv_cache_arg(k_cache, v_cache, dev)
+    T, Hq, _, qs = _heads_arg(q, "q", dev, D)
+    table, S, entries = _page_table_arg(page_indices, page_indptr, last_page_len, cu_seqlens, T, dev)
     window = -1 if window is None else int(window)
     options = None
     if softcap or window >= 0 or slopes is not None or full_lens is not None:
-        if slopes is not None and _vector(slopes, torch.float32, "slopes") != Hq:
+        if slopes is not None and _vector(slopes, torch.float32, "slopes", dev) != Hq:
             raise ValueError("slopes must hold one entry per query head")
-        if full_lens is not None and _vector(full_lens, torch.int32, "full_lens") != S:
+        if full_lens is not None and _vector(full_lens, torch.int32, "full_lens", dev) != S:
             raise ValueError("full_lens must hold one entry per sequence")
         options = _ATTENTION_OPTIONS.pack(softcap, _ptr(slopes) or 0, window, _ptr(full_lens) or 0)
-    if o is None:
-        o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    elif _need(o, torch.bfloat16, "o", 3).shape != q.shape:
-        raise ValueError("o must have the shape of q")
+    o = _out_arg(o, q, T, Hq, D, "o", dev)
     if lse is not None:
-        if _need(lse, torch.float32, "lse", 2).shape != (T, Hq):
-            raise ValueError("lse must be [T, Hq]")
+        if _need(lse, torch.float32, "lse", 2).shape != (T, Hq) or lse.get_device() != dev:
+            raise ValueError("lse must be [T, Hq] on the call's device")
     elif return_lse:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    need = (gdn_attention_decode_workspace_bytes(S, Hq, Hkv, D) if decode
-            else gdn_attention_workspace_bytes(S, T, Hq, Hkv, D))
+    need = (gdn_attention_decode_workspace_bytes(S, Hq, Hkv, D, entries, page_size) if decode
+            else gdn_attention_workspace_bytes(S, T, Hq, Hkv, D, entries, page_size))
     if workspace is None:
-        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=q.device)
-    elif _vector(workspace, torch.uint8, "workspace") < need:
+        if need:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    elif _vector(workspace, torch.uint8, "workspace", dev) < need:
         raise ValueError("workspace holds %d bytes, the call needs %d" % (workspace.numel(), need))
-    _same_device(q.device, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, slopes, full_lens, o,
-                 lse, err_word, workspace)
-    tail = (cache, table, scale, options, workspace.data_ptr(), workspace.shape[0],
-            _ptr(_opt(err_word, torch.int32, "err_word")), _stream(q))
+    tail = (cache, table, scale, options, _ptr(workspace), need, _err_arg(err_word, dev), _raw_stream(dev))
+    lib = _lib or library()
     if decode:
-        _check("gdn_attention_decode_paged", library().gdn_attention_decode_paged(
+        _check("gdn_attention_decode_paged", lib.gdn_attention_decode_paged(
             q.data_ptr(), qs, o.data_ptr(), _ptr(lse), Hq, *tail))
     else:
-        _check("gdn_attention_paged", library().gdn_attention_paged(
+        _check("gdn_attention_paged", lib.gdn_attention_paged(
             q.data_ptr(), qs, o.data_ptr(), _ptr(lse), _ptr(cu_seqlens), T, Hq, *tail))
     return (o, lse) if return_lse else o
 
@@ -631,7 +644,7 @@ def gdn_attention_paged(q, k_cache, v_cache, cu_seqlens, page_indices, page_indp
     ``full_lens`` (int32 [num_seqs]: prefix mask, keys below it seen by every new
     token).  ``cu_seqlens`` None: one new token per sequence.  ``workspace``:
     optional uint8 device tensor of at least gdn_attention_workspace_bytes(...)
-    bytes.  Returns o (bf16 [T, Hq, D]), with ``return_lse`` (o, lse), lse the
+    bytes (0 for batches of short sequences).  Returns o (bf16 [T, Hq, D]), with ``return_lse`` (o, lse), lse the
     natural logarithm of the sum of exponentials (fp32 [T, Hq])."""
     return _attention(False, q, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, scale, softcap,
                       window, slopes, full_lens, o, lse, return_lse, err_word, workspace)

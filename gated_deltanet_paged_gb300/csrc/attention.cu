@@ -51,7 +51,7 @@ struct ChunkArgs {
   float4* part_o;       // [2 grid][2 tiles][D / 4][128 rows]
   float2* part_ml;      // [2 grid][2 tiles][128 rows]
   int32_t whole;        // items are not cut: a CTA takes those that begin in its piece
-  int4* cuts;           // [grid]: (sequence, token tile pair, key head, last CTA) of an item cut at this CTA's end, or -1
+  int4* cuts;           // [grid]: (first token, tokens, key head, last CTA) of an item cut at this CTA's end, or -1
 };
 
 struct Seq {
@@ -67,7 +67,7 @@ __device__ __forceinline__ Seq load_seq(const ChunkArgs& d, int b) {
   q.len = s.len;
   q.entry = s.entry;
   q.refused = s.refused;
-  q.full = d.a.full_lens && s.new_tokens ? min(d.a.full_lens[b], s.len) : 0;
+  q.full = d.a.full_lens ? min(d.a.full_lens[b], s.len) : 0;
   q.pairs = (s.new_tokens + 2 * d.tile_tokens - 1) / (2 * d.tile_tokens);
   return q;
 }
@@ -170,6 +170,7 @@ struct Smem {
   uint64_t o_last[2];      // O of a segment is complete
   uint64_t o_free[2];      // ... and has been read
   uint64_t stat_full[2];
+  uint64_t turn[2];        // the other tile's products of a block have been issued
   uint64_t seg_full[kSegments], seg_empty[kSegments];
   int64_t scan[kThreads / 32];
   Walk walk;
@@ -304,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       gdn::mbar_init(&sh.o_last[t], 1);
       gdn::mbar_init(&sh.o_free[t], 4);
       gdn::mbar_init(&sh.stat_full[t], 4);
+      gdn::mbar_init(&sh.turn[t], 1);
     }
     for (int i = 0; i < kSegments; ++i) {
       gdn::mbar_init(&sh.seg_full[i], 1);
@@ -328,16 +330,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   gdn::pdl_launch_dependents();
 
   // ---- this CTA's share of the line ----
-  gdn::Shares shares(0, 1, 1);
+  gdn::Shares<7> shares(0, 1, 1);
   bool idle;
   {
     const int per = (a.paged.num_seqs + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, a.paged.num_seqs), b1 = min(b0 + per, a.paged.num_seqs);
-    int64_t mine = 0;
+    int64_t mine = 0, cost = 0;
+    Seq s = {};
     for (int b = b0; b < b1; ++b) {
-      const Seq s = load_seq(d, b);
+      s = load_seq(d, b);
       if (s.refused && blockIdx.x == 0) gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_TABLE, b);
-      mine += seq_cost(d, s);
+      cost = seq_cost(d, s);
+      mine += cost;
     }
     int64_t incl = mine;
 #pragma unroll
@@ -353,10 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       total += sh.scan[i];
     }
     total *= a.Hkv;
-    shares = gdn::Shares(total, total / kMinShare, gridDim.x);
+    // Whole items need no smallest piece: every one can have a CTA to itself.
+    shares = gdn::Shares<7>(total, total / (d.whole ? kItemCost : kMinShare), gridDim.x);
     const int c = blockIdx.x;
-    const int64_t start = c < shares.eff ? shares.start(c) : total;
-    const int64_t end = c < shares.eff ? shares.start(c + 1) : total;
+    const int64_t start = shares.start(c), end = shares.start(c + 1);
     idle = start >= end;
     // The thread whose sequences hold `start` sets up the walk.
     if (!idle && before * a.Hkv <= start && start < (before + mine) * a.Hkv) {
@@ -365,11 +369,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       x.end = end;
       x.b = b0;
       int64_t base = before * a.Hkv;
-      for (;; ++x.b) {
+      x.s = s;  // one sequence per thread, unless there are more than threads
+      for (; per > 1; ++x.b) {
         x.s = load_seq(d, x.b);
-        const int64_t span = seq_cost(d, x.s) * a.Hkv;
-        if (start < base + span) break;
-        base += span;
+        cost = seq_cost(d, x.s);
+        if (start < base + cost * a.Hkv) break;
+        base += cost * a.Hkv;
       }
       int i = 0;  // the last pair that begins at or before start
       for (int step = x.s.pairs > 1 ? 1 << (31 - __clz(x.s.pairs - 1)) : 0; step; step >>= 1)
@@ -417,6 +422,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pair0 = w.pair * 2 * tile_tokens;  // first token of the item within the sequence's new ones
         const int token = w.s.first_token + pair0;
         const bool two = pair0 + tile_tokens < w.s.n;
+        // Pages of the first block, asked for before anything waits.
+        int page[4], slot[4];
+        auto look_up = [&](int key0) {
+          const int first = max(0, w.lo - key0) >> a.box_shift;
+          const int last = (min(kKeys, w.hi - key0) + box_rows - 1) >> a.box_shift;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int box = lane + 32 * i;
+            if (32 * i < boxes && box >= first && box < last) {
+              const int key = key0 + box * box_rows;
+              const int entry = key / a.paged.page_size;
+              slot[i] = key - entry * a.paged.page_size;
+              page[i] = a.paged.pages[w.s.entry + entry];
+            }
+          }
+        };
+        if (more) look_up((w.first + w.blk0) * kKeys);
         if (segs >= kSegments && !wait(&sh.seg_empty[segs % kSegments], ((segs / kSegments) - 1) & 1)) break;
         if (lane == 0) {
           Segment g = {};
@@ -435,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // and one at most continues one: two partial slots per CTA.
             g.part = starts && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
             if (starts && !ends)
-              d.cuts[blockIdx.x] = make_int4(w.b, w.pair, w.head, shares.owner(w.item0 + w.cost - 1));
+              d.cuts[blockIdx.x] = make_int4(token, g.tokens, w.head, shares.owner(w.item0 + w.cost - 1));
           }
           sh.seg[segs % kSegments] = g;
           gdn::mbar_arrive(&sh.seg_full[segs % kSegments]);
@@ -469,21 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int key0 = (w.first + blk) * kKeys;
           const int first = max(0, w.lo - key0) >> a.box_shift;
           const int last = (min(kKeys, w.hi - key0) + box_rows - 1) >> a.box_shift;
-          int page[4], slot[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int box = lane + 32 * i;
-            if (32 * i < boxes && box >= first && box < last) {
-              const int key = key0 + box * box_rows;
-              const int entry = key / a.paged.page_size;
-              slot[i] = key - entry * a.paged.page_size;
-              page[i] = a.paged.pages[w.s.entry + entry];
-              if (page[i] < 0 || page[i] >= a.paged.num_pages) {
-                gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_ID, w.b);
-                page[i] = a.paged.num_pages;  // outside the map: zeros
-              }
-            }
-          }
+          if (blk > w.blk0) look_up(key0);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++n) {
             const int stage = n % L::kStages;
@@ -500,6 +508,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) {
               const int box = lane + 32 * i;
               if (32 * i < boxes && box >= first && box < last) {
+                if (page[i] < 0 || page[i] >= a.paged.num_pages) {
+                  gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_ID, w.b);
+                  page[i] = a.paged.num_pages;  // outside the map: zeros
+                }
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
                   gdn::tma_load_4d(dst + c * L::kHalf + box * box_rows * 128, map, bar, c * 64, w.head, slot[i], page[i]);
@@ -535,15 +547,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t v_desc = gdn::sdesc(gdn::smem_u32(ring), L::kHalf, 1024);
       const uint32_t s_col = tmem + L::kColS + t * kKeys, o_col = tmem + L::kColO + t * D;
       constexpr uint32_t kStep = L::kTile >> 4;  // a stage, in descriptor units
-      uint32_t n = 0, np = 0, done_segs = 0;     // ring tiles, blocks of this tile, segments of this tile
+      uint32_t np = 0, done_segs = 0, turns = 0;  // blocks and segments of this tile, blocks of both
       uint32_t stage = 0, phase = 0;
       auto advance = [&] {
-        ++n;
         if (++stage == L::kStages) stage = 0, phase ^= 1;
       };
       // S = Q K^T of the ring's current tile, which is released with it.
       auto scores = [&](bool last) {
-        if (!wait(&sh.full[stage], phase)) return;
         gdn::tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -558,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       Segment g;
       for (uint32_t segs = 0; next(segs, g); ++segs) {
-        const bool active = t * tile_tokens < g.tokens;
+        const bool active = t * tile_tokens < g.tokens, two = tile_tokens < g.tokens;
         if (!wait(&sh.q_full, segs & 1)) break;
         if (!active) {
           // Keep in step: release every tile of the segment unread.
@@ -570,6 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           continue;
         }
+        if (!wait(&sh.full[stage], phase)) break;
         scores(g.blocks == 1);
         for (int j = 0; ok && j < g.blocks; ++j) {
           const uint32_t v_stage = stage;
@@ -581,6 +592,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) gdn::tc_mma4_ts(o_col, s_col, 8, v_desc + v_stage * kStep, 128, id_o, j > 0);
           __syncwarp();
           if (!wait(&sh.p_full[t][1], np & 1)) break;
+          // The tiles take turns with the rest of P V and the next S.  Interleaved,
+          // both would end together, and both softmaxes would then run beside an
+          // idle tensor core (measured: two stable rhythms, 3,450 cycles per block
+          // that way and 2,600 when the tiles are half a period apart).
+          if (two && (t == 1 || turns > 0) && !wait(&sh.turn[t], (t == 1 ? turns : turns - 1) & 1)) break;
           gdn::tc_fence_after();
           if (elect_one()) {
             gdn::tc_mma4_ts(o_col, s_col + 32, 8, v_desc + v_stage * kStep + 4 * 128, 128, id_o, 1);
@@ -589,7 +605,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           ++np;
-          if (j + 1 < g.blocks) scores(j + 2 == g.blocks);
+          if (j + 1 < g.blocks) {
+            if (!wait(&sh.full[stage], phase)) break;
+            scores(j + 2 == g.blocks);
+          }
+          if (two) {
+            if (lane == 0) gdn::mbar_arrive(&sh.turn[t ^ 1]);
+            ++turns;
+          }
         }
         ++done_segs;
       }
@@ -740,8 +763,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 4; i < 128; ++i) top[i & 3] = fmaxf(top[i & 3], s[i]);
-        float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        for (int i = 4; i < 124; i += 8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top[k] = gdn::max3(top[k], s[i + 2 * k], s[i + 2 * k + 1]);
+        }
+        float mx = gdn::max3(gdn::max3(top[0], top[1], s[124]), gdn::max3(top[2], s[125], s[126]), fmaxf(top[3], s[127]));
         if (!kMods) mx *= a.scale_log2;
         // The reference moves when a maximum is more than 2^8 above it.
         const bool grow = mx > m + 8.f || (m == -INFINITY && mx > m);
@@ -809,8 +835,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the partial results of the items that CTAs of the kernel above cut: the
 // item that CTA c = blockIdx.x started and did not end has slot 1 of c, then slot
-// 0 of every CTA up to the one that ended it.  blockIdx.y: 32 rows; a thread
-// takes one row and every eighth group of four dimensions.
+// 0 of every CTA up to the one that ended it.  blockIdx.y: 32 rows and half of
+// the dimensions; a thread takes one row and D / 64 groups of four dimensions.
+// Latency-bound: the parts are added in a fixed order, four of them in flight.
+constexpr int kJoinSlices = 16;
 template <int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkArgs d) {
   gdn::pdl_wait();
@@ -819,54 +847,69 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
   const int4 cut = d.cuts[c];
   if (cut.x < 0) return;
   const AttnArgs& a = d.a;
-  const int t = blockIdx.y >> 2, row = (blockIdx.y & 3) * 32 + (threadIdx.x & 31);
-  const gdn::SeqRange s = gdn::seq_range(a.paged, cut.x);
+  const int t = blockIdx.y >> 3, row = (blockIdx.y & 3) * 32 + (threadIdx.x & 31);
   const int in_tile = row / a.group;
-  const int token = (cut.y * 2 + t) * d.tile_tokens + in_tile;
-  if (in_tile >= d.tile_tokens || token >= s.new_tokens) return;
-  constexpr int kG = D / 32;  // groups of four dimensions per thread
-  const int group0 = threadIdx.x >> 5;
-  auto slot_of = [&](int i) { return (2 * static_cast<int64_t>(i) + (i == c ? 1 : 0)) * 2 + t; };
+  const int token = t * d.tile_tokens + in_tile;
+  if (in_tile >= d.tile_tokens || token >= cut.y) return;
+  constexpr int kG = D / 64;  // groups of four dimensions per thread
+  constexpr int kParts = 4;
+  const int group0 = (threadIdx.x >> 5) + 8 * kG * ((blockIdx.y >> 2) & 1);
   float m = -INFINITY, l = 0.f;
-  for (int i = c; i <= cut.w; ++i) m = fmaxf(m, d.part_ml[slot_of(i) * kRows + row].x);
   float4 o[kG];
 #pragma unroll
   for (int k = 0; k < kG; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  // The parts in a fixed order; two in flight.
-#pragma unroll 2
-  for (int i = c; i <= cut.w; ++i) {
-    const int64_t slot = slot_of(i);
-    const float2 ml = d.part_ml[slot * kRows + row];
-    float4 x[kG];
+  for (int i0 = c; i0 <= cut.w; i0 += kParts) {
+    float2 ml[kParts];
+    float4 x[kParts][kG];
 #pragma unroll
-    for (int k = 0; k < kG; ++k) x[k] = d.part_o[(slot * (D / 4) + group0 + 8 * k) * kRows + row];
-    const float f = ml.x == -INFINITY ? 0.f : gdn::exp2_approx(ml.x - m);
-    l = fmaf(ml.y, f, l);
+    for (int p = 0; p < kParts; ++p) {
+      ml[p] = make_float2(-INFINITY, 0.f);
+      const int i = i0 + p;
+      if (i > cut.w) continue;
+      const int64_t slot = (2 * static_cast<int64_t>(i) + (i == c ? 1 : 0)) * 2 + t;
+      ml[p] = d.part_ml[slot * kRows + row];
 #pragma unroll
-    for (int k = 0; k < kG; ++k) {
-      o[k].x = fmaf(x[k].x, f, o[k].x);
-      o[k].y = fmaf(x[k].y, f, o[k].y);
-      o[k].z = fmaf(x[k].z, f, o[k].z);
-      o[k].w = fmaf(x[k].w, f, o[k].w);
+      for (int k = 0; k < kG; ++k) x[p][k] = d.part_o[(slot * (D / 4) + group0 + 8 * k) * kRows + row];
+    }
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      if (ml[p].x == -INFINITY) continue;  // no part, or one in which the row saw no key
+      const float top = fmaxf(m, ml[p].x);
+      const float f = gdn::exp2_approx(m - top), g = gdn::exp2_approx(ml[p].x - top);
+      m = top;
+      l = l * f + ml[p].y * g;
+#pragma unroll
+      for (int k = 0; k < kG; ++k) {
+        o[k].x = o[k].x * f + x[p][k].x * g;
+        o[k].y = o[k].y * f + x[p][k].y * g;
+        o[k].z = o[k].z * f + x[p][k].z * g;
+        o[k].w = o[k].w * f + x[p][k].w * g;
+      }
     }
   }
   const float inv = 1.f / l;
-  const int64_t out = (static_cast<int64_t>(s.first_token) + token) * a.Hq + cut.z * a.group + row % a.group;
+  const int64_t out = (static_cast<int64_t>(cut.x) + token) * a.Hq + cut.z * a.group + row % a.group;
 #pragma unroll
   for (int k = 0; k < kG; ++k)
     reinterpret_cast<uint2*>(a.o + out * D)[group0 + 8 * k] =
         make_uint2(gdn::pack_bf162(o[k].x * inv, o[k].y * inv), gdn::pack_bf162(o[k].z * inv, o[k].w * inv));
-  if (a.lse && threadIdx.x < 32) a.lse[out] = (m + log2f(l)) / gdn::kLog2e;
+  if (a.lse && group0 == 0) a.lse[out] = (m + log2f(l)) / gdn::kLog2e;
 }
 
-constexpr int kWholeKeys = 8 * kKeys;  // longest sequence whose items are never cut (see launch)
+constexpr int kWholeKeys = 8 * kKeys;  // longest sequence whose items are never cut
 constexpr size_t kCutBytes = kMaxGrid * sizeof(int4);
-size_t workspace_bytes_of(int D) {
+// Where even the longest sequence is a few blocks, the join's launch would cost
+// more than an even split saves.
+bool whole_items(int32_t num_seqs, int32_t num_entries, int32_t page_size) {
+  return gdn_host::longest_sequence(num_seqs, num_entries, page_size) <= kWholeKeys;
+}
+size_t workspace_bytes_of(int D, bool whole) {
+  if (whole) return 0;
   return kCutBytes + static_cast<size_t>(4) * kMaxGrid * kRows * (sizeof(float2) + D * sizeof(float));
 }
 
 template <int D, bool kMods>
-int launch(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache* cache, const gdn_page_table* table, void* workspace, int sms, cudaStream_t stream) {
+int launch(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache* cache, void* workspace, int sms, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   constexpr int smem = Layout<D>::kBytes + sizeof(Smem<D>);
   static_assert(smem <= 232448, "shared memory of one CTA");
@@ -880,10 +923,6 @@ int launch(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache* cache, const g
   if ((rc = gdn_host::encode_cache_map(&k_map, cache->k, cache, d.a.box_shift)) != GDN_OK) return rc;
   if ((rc = gdn_host::encode_cache_map(&v_map, cache->v, cache, d.a.box_shift)) != GDN_OK) return rc;
   const int grid = sms < kMaxGrid ? sms : kMaxGrid;
-  // The longest sequence the table can hold has every entry that the others do
-  // not need.  Where even that is a few blocks, the join's launch would cost more
-  // than an even split saves.
-  d.whole = (static_cast<int64_t>(table->num_entries) - table->num_seqs + 1) * cache->page_size <= kWholeKeys;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   d.cuts = reinterpret_cast<int4*>(ws);
   d.part_ml = reinterpret_cast<float2*>(ws + kCutBytes);
@@ -891,15 +930,15 @@ int launch(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache* cache, const g
   rc = gdn_host::launch_pdl(chunk_attention_kernel<D, kMods>, dim3(grid), dim3(kThreads), smem, stream, d, q_map, k_map,
                             v_map);
   if (rc != GDN_OK || d.whole) return rc;
-  return gdn_host::launch_pdl(chunk_join_kernel<D>, dim3(grid, 8), dim3(256), 0, stream, d);
+  return gdn_host::launch_pdl(chunk_join_kernel<D>, dim3(grid, kJoinSlices), dim3(256), 0, stream, d);
 }
 
 }  // namespace
 
 extern "C" size_t gdn_attention_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32_t Hq, int32_t Hkv,
-                                                int32_t D) {
-  if (num_seqs < 0 || total_tokens < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
-  return workspace_bytes_of(D);
+                                                int32_t D, int32_t num_entries, int32_t page_size) {
+  if (num_seqs < 0 || num_entries < 0 || page_size < 1 || total_tokens < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
+  return workspace_bytes_of(D, whole_items(num_seqs, num_entries, page_size));
 }
 
 extern "C" int gdn_attention_paged(const gdn_bf16* q, int64_t q_token_stride, gdn_bf16* o, float* lse,
@@ -908,7 +947,8 @@ extern "C" int gdn_attention_paged(const gdn_bf16* q, int64_t q_token_stride, gd
                                    const gdn_attention_options* options, void* workspace, size_t workspace_bytes,
                                    int32_t* err_word, void* stream) {
   ChunkArgs d = {};
-  const size_t need = cache ? workspace_bytes_of(cache->head_dim) : 0;
+  d.whole = cache && table && whole_items(table->num_seqs, table->num_entries, cache->page_size);
+  const size_t need = cache ? workspace_bytes_of(cache->head_dim, d.whole) : 0;
   int rc = gdn_host::attention_args(&d.a, q, q_token_stride, o, lse, cu_seqlens, total_tokens, Hq, cache, table, scale,
                                     options, workspace, workspace_bytes, need, err_word, kKeys);
   if (rc != GDN_OK || table->num_seqs == 0 || total_tokens == 0) return rc;
@@ -919,8 +959,8 @@ extern "C" int gdn_attention_paged(const gdn_bf16* q, int64_t q_token_stride, gd
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool mods = d.a.cap_log2 > 0.f || d.a.slopes;
   if (cache->head_dim == 64)
-    return mods ? launch<64, true>(d, total_tokens, cache, table, workspace, sms, s)
-                : launch<64, false>(d, total_tokens, cache, table, workspace, sms, s);
-  return mods ? launch<128, true>(d, total_tokens, cache, table, workspace, sms, s)
-              : launch<128, false>(d, total_tokens, cache, table, workspace, sms, s);
+    return mods ? launch<64, true>(d, total_tokens, cache, workspace, sms, s)
+                : launch<64, false>(d, total_tokens, cache, workspace, sms, s);
+  return mods ? launch<128, true>(d, total_tokens, cache, workspace, sms, s)
+              : launch<128, false>(d, total_tokens, cache, workspace, sms, s);
 }

@@ -70,6 +70,12 @@ struct AttnArgs {
   int32_t box_shift;          // log2 of the tokens per copy of a page
 };
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -87,21 +93,28 @@ __device__ __forceinline__ float capped(float x, float cap_log2) {
 }
 
 // A line of `total` units in equal pieces for `eff` CTAs: piece c is [start(c),
-// start(c + 1)).  One 64-bit division per CTA; the rest is in 32 bits.
+// start(c + 1)).  Any monotone boundaries do, so a product in floats replaces the
+// 64-bit division, in steps of 2^shift units (doubles took 3,400 cycles here, with
+// every thread of the CTA at the few FP64 units): this runs at the head of every
+// CTA, where time counts in small calls.  No piece is empty: eff is chosen so
+// that a piece is some steps long at least.
+template <int kShift>
 struct Shares {
-  int64_t total, q;
-  int r, eff;
+  int64_t total;
+  float per;  // steps
+  int eff, shift;
   __device__ __forceinline__ Shares(int64_t units, int64_t most, int grid) {
     total = units;
     eff = static_cast<int>(most < 1 ? 1 : most < grid ? most : grid);
-    q = total <= 0xFFFFFFFFll ? static_cast<int64_t>(static_cast<uint32_t>(total) / static_cast<uint32_t>(eff))
-                              : total / eff;
-    r = static_cast<int>(total - q * eff);
+    shift = units >> (kShift + 31) ? kShift + 14 : kShift;  // steps in 32 bits
+    per = __fdividef(static_cast<float>(static_cast<int>(units >> shift)), static_cast<float>(eff));
   }
-  __device__ __forceinline__ int64_t start(int c) const { return q * c + r * c / eff; }
+  __device__ __forceinline__ int64_t start(int c) const {
+    return c >= eff ? total : min(static_cast<int64_t>(static_cast<int>(per * static_cast<float>(c))) << shift, total);
+  }
   // The piece that holds unit x.
   __device__ __forceinline__ int owner(int64_t x) const {
-    int c = min(static_cast<int>(static_cast<float>(x) / static_cast<float>(total) * static_cast<float>(eff)), eff - 1);
+    int c = min(static_cast<int>(__fdividef(static_cast<float>(static_cast<int>(x >> shift)), per)), eff - 1);
     while (c + 1 < eff && start(c + 1) <= x) ++c;
     while (start(c) > x) --c;
     return c;
@@ -109,7 +122,7 @@ struct Shares {
 };
 // floor(x / d) for 0 <= x < d * most, without a 64-bit division.
 __device__ __forceinline__ int small_quotient(int64_t x, int d, int most) {
-  int c = min(static_cast<int>(static_cast<float>(x) / static_cast<float>(d)), most - 1);
+  int c = min(static_cast<int>(__fdividef(static_cast<float>(x), static_cast<float>(d))), most - 1);
   while (static_cast<int64_t>(c + 1) * d <= x) ++c;
   while (static_cast<int64_t>(c) * d > x) --c;
   return c;
@@ -181,7 +194,7 @@ inline int attention_args(gdn::AttnArgs* a, const gdn_bf16* q, int64_t q_stride,
   if (table->num_seqs == 0 || total_tokens == 0) return GDN_OK;
   if (bad_tokens(q, q_stride, Hq, D) || !o || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
     return GDN_ERR_INVALID_ARGUMENT;
-  if (!workspace || !aligned16(workspace) || workspace_bytes < need) return GDN_ERR_INVALID_ARGUMENT;
+  if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return GDN_ERR_INVALID_ARGUMENT;
   *a = gdn::AttnArgs{};
   a->q = reinterpret_cast<const __nv_bfloat16*>(q);
   a->q_stride = q_stride;
@@ -199,6 +212,12 @@ inline int attention_args(gdn::AttnArgs* a, const gdn_bf16* q, int64_t q_stride,
   a->window = options ? options->window : -1;
   while ((1 << a->box_shift) < tile_keys && cache->page_size % (2 << a->box_shift) == 0) ++a->box_shift;
   return GDN_OK;
+}
+
+// The longest sequence that a table can hold has every entry that the others do
+// not need.
+inline int64_t longest_sequence(int32_t num_seqs, int32_t num_entries, int32_t page_size) {
+  return (static_cast<int64_t>(num_entries) - num_seqs + 1) * page_size;
 }
 
 // Tensor map of one cache array, {D, heads, slots, pages}, with boxes of 64

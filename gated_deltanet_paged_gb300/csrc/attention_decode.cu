@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // ---- this CTA's share of the line ----
   const int per_seq = a.Hkv * d.passes;
   Walk w;
-  gdn::Shares shares(0, 1, 1);
+  gdn::Shares<0> shares(0, 1, 1);
   if (d.whole) {
     w.pos = blockIdx.x;
     w.end = static_cast<int64_t>(a.paged.num_seqs) * per_seq;
@@ -204,10 +204,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       total += sh.scan[i];
     }
     total *= per_seq;
-    shares = gdn::Shares(total, total / kMinShare, gridDim.x);
+    shares = gdn::Shares<0>(total, total / kMinShare, gridDim.x);
     const int c = blockIdx.x;
-    const int64_t start = c < shares.eff ? shares.start(c) : total;
-    const int64_t end = c < shares.eff ? shares.start(c + 1) : total;
+    const int64_t start = shares.start(c), end = shares.start(c + 1);
     // The thread whose sequences hold `start` sets up the walk.
     if (start < end && before * per_seq <= start && start < (before + mine) * per_seq) {
       Walk x;
@@ -516,7 +515,13 @@ __global__ void __launch_bounds__(D) decode_join_kernel(const __grid_constant__ 
 
 constexpr int kMaxGrid = 2 * 160;  // two CTAs per SM
 
-size_t workspace_bytes_of(int D) {
+// Where even the longest sequence is a few blocks, one CTA takes a whole item: the
+// scan of the batch and the join's launch would cost more than the blocks.
+bool whole_items(int32_t num_seqs, int32_t num_entries, int32_t page_size) {
+  return gdn_host::longest_sequence(num_seqs, num_entries, page_size) <= kWholeBlocks * kBlock;
+}
+size_t workspace_bytes_of(int D, bool whole) {
+  if (whole) return 0;
   return static_cast<size_t>(2) * kMaxGrid * kRows * (D * 4 + 8) + kMaxGrid * sizeof(int4);
 }
 
@@ -534,11 +539,6 @@ int launch(const DecodeArgs& base, const gdn_kv_cache* cache, const gdn_page_tab
   d.passes = (d.a.group + kRows - 1) / kRows;
   const int64_t items = static_cast<int64_t>(table->num_seqs) * d.a.Hkv * d.passes;
   int grid = 2 * sms < kMaxGrid ? 2 * sms : kMaxGrid;
-  // The longest sequence the table can hold has every entry that the others do
-  // not need.  Where even that is a few blocks, one CTA takes a whole item: the
-  // scan of the batch and the join's launch would cost more than the blocks.
-  const int64_t longest = (static_cast<int64_t>(table->num_entries) - table->num_seqs + 1) * cache->page_size;
-  d.whole = longest <= kWholeBlocks * kBlock;
   if (d.whole && items < grid) grid = static_cast<int>(items);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   d.cuts = reinterpret_cast<int4*>(ws);
@@ -551,9 +551,10 @@ int launch(const DecodeArgs& base, const gdn_kv_cache* cache, const gdn_page_tab
 
 }  // namespace
 
-extern "C" size_t gdn_attention_decode_workspace_bytes(int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D) {
-  if (num_seqs < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
-  return workspace_bytes_of(D);
+extern "C" size_t gdn_attention_decode_workspace_bytes(int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D,
+                                                       int32_t num_entries, int32_t page_size) {
+  if (num_seqs < 0 || num_entries < 0 || page_size < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
+  return workspace_bytes_of(D, whole_items(num_seqs, num_entries, page_size));
 }
 
 extern "C" int gdn_attention_decode_paged(const gdn_bf16* q, int64_t q_token_stride, gdn_bf16* o, float* lse,
@@ -562,7 +563,8 @@ extern "C" int gdn_attention_decode_paged(const gdn_bf16* q, int64_t q_token_str
                                           size_t workspace_bytes, int32_t* err_word, void* stream) {
   DecodeArgs d = {};
   const int32_t n = table ? table->num_seqs : 0;
-  const size_t need = cache ? workspace_bytes_of(cache->head_dim) : 0;
+  d.whole = cache && table && whole_items(n, table->num_entries, cache->page_size);
+  const size_t need = cache ? workspace_bytes_of(cache->head_dim, d.whole) : 0;
   int rc = gdn_host::attention_args(&d.a, q, q_token_stride, o, lse, nullptr, n, Hq, cache, table, scale, options,
                                     workspace, workspace_bytes, need, err_word, kBlock);
   if (rc != GDN_OK || n == 0) return rc;

@@ -464,9 +464,14 @@ int gdn_attention_decode_paged(const gdn_bf16 *q, int64_t q_token_stride, gdn_bf
                                const gdn_attention_options *options, void *workspace, size_t workspace_bytes,
                                int32_t *err_word, void *stream);
 
-/* Bytes of workspace of the two calls above (0 for invalid arguments). */
-size_t gdn_attention_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32_t Hq, int32_t Hkv, int32_t D);
-size_t gdn_attention_decode_workspace_bytes(int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D);
+/* Bytes of workspace of the two calls above for a page table of num_entries
+ * entries and a cache of page_size (0 also for invalid arguments).  0 where even
+ * the longest sequence that such a table can hold is a few blocks of keys: the
+ * calls then cut nothing, and workspace may be NULL. */
+size_t gdn_attention_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32_t Hq, int32_t Hkv, int32_t D,
+                                     int32_t num_entries, int32_t page_size);
+size_t gdn_attention_decode_workspace_bytes(int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D,
+                                            int32_t num_entries, int32_t page_size);
 
 /* Static text for a status code. */
 const char *gdn_status_string(int status);

@@ -19,7 +19,7 @@ def cache(**kw):
 
 
 def table(**kw):
-    a = dict(page_indices=FAKE, num_entries=4, page_indptr=FAKE, last_page_len=FAKE, num_seqs=2)
+    a = dict(page_indices=FAKE, num_entries=400, page_indptr=FAKE, last_page_len=FAKE, num_seqs=2)
     a.update(kw)
     return gdn._PAGE_TABLE.pack(*[v or 0 for v in a.values()])
 
@@ -112,12 +112,17 @@ def test_unsupported_forms():
 
 def test_workspace_sizes():
     lib = gdn.library()
-    assert lib.gdn_attention_workspace_bytes(2, 100, 4, 2, 128) > 0
-    assert lib.gdn_attention_decode_workspace_bytes(2, 4, 2, 64) > 0
-    for bad in ((-1, 100, 4, 2, 128), (2, -1, 4, 2, 128), (2, 100, 5, 2, 128), (2, 100, 0, 2, 128), (2, 100, 4, 0, 128),
-                (2, 100, 4, 2, 96)):
+    assert lib.gdn_attention_workspace_bytes(2, 100, 4, 2, 128, 1000, 16) > 0
+    assert lib.gdn_attention_decode_workspace_bytes(2, 4, 2, 64, 1000, 16) > 0
+    # a table that holds no long sequence: nothing is cut
+    assert lib.gdn_attention_workspace_bytes(2, 100, 4, 2, 128, 4, 16) == 0
+    assert lib.gdn_attention_decode_workspace_bytes(2, 4, 2, 64, 4, 16) == 0
+    for bad in ((-1, 100, 4, 2, 128, 1000, 16), (2, -1, 4, 2, 128, 1000, 16), (2, 100, 5, 2, 128, 1000, 16),
+                (2, 100, 0, 2, 128, 1000, 16), (2, 100, 4, 0, 128, 1000, 16), (2, 100, 4, 2, 96, 1000, 16),
+                (2, 100, 4, 2, 128, -1, 16), (2, 100, 4, 2, 128, 1000, 0)):
         assert lib.gdn_attention_workspace_bytes(*bad) == 0
-    for bad in ((-1, 4, 2, 128), (2, 5, 2, 128), (2, 4, 0, 128), (2, 4, 2, 80)):
+    for bad in ((-1, 4, 2, 128, 1000, 16), (2, 5, 2, 128, 1000, 16), (2, 4, 0, 128, 1000, 16), (2, 4, 2, 80, 1000, 16),
+                (2, 4, 2, 128, -1, 16), (2, 4, 2, 128, 1000, 0)):
         assert lib.gdn_attention_decode_workspace_bytes(*bad) == 0
 
 

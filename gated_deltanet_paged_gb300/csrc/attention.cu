@@ -24,6 +24,8 @@
 //     where the piece ends (as the decode kernel does); the line's prefix sums
 //     have closed forms, so that every CTA finds its piece from the page table
 //     itself.  A join kernel adds up the cut items.
+#include <type_traits>
+
 #include "attention_common.cuh"
 
 namespace {
@@ -268,9 +270,19 @@ __device__ __forceinline__ void tmem_st32_nw(uint32_t taddr, const uint32_t* r) 
       : "memory");
 }
 
-// kMods: scores are capped or biased (the options that change a score; those
-// that only hide keys cost nothing away from the edges).
-template <int D, bool kMods>
+// How scores become weights.
+//   kPlain: scale and reference in one multiply-add.
+//   kGeneral: a cap or a bias first (the options that change a score; those that
+//     only hide keys cost nothing away from the edges).
+//   kBounded: a cap of at most kBoundedCap bounds the scores on both sides, so that
+//     0 serves as the reference for the whole row: weights within 2^-80 .. 2^80
+//     and their sums over 2^30 keys are far inside fp32 and bf16, and no maximum
+//     is taken.  (A bias only lowers scores, and each row sees its own key, whose
+//     bias is 0.)
+enum Scores { kPlain, kGeneral, kBounded };
+constexpr float kBoundedCap = 80.f;  // in units of log2
+
+template <int D, Scores kScores>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_attention_kernel(const __grid_constant__ ChunkArgs d, const __grid_constant__ CUtensorMap q_map,
                            const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
@@ -725,13 +737,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = g.pos + min(t * tile_tokens + min(my_token, tile_tokens - 1), tokens - 1);
       const int lo = gdn::key_lo(a, pos), hi = max(pos + 1, g.full);
       float slope = 0.f;
-      if (kMods && a.slopes) slope = a.slopes[g.head * a.group + my_head] * gdn::kLog2e;
+      if (kScores != kPlain && a.slopes) slope = a.slopes[g.head * a.group + my_head] * gdn::kLog2e;
       __syncwarp();
       if (lane == 0) gdn::mbar_arrive(&sh.seg_empty[at]);
       if (blocks == 0) break;
       if (t * tile_tokens >= tokens) continue;
-      float m = -INFINITY;
+      float m = kScores == kBounded ? 0.f : -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
+      float2 poly[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) poly[i] = make_float2(a.cap_poly[i], a.cap_poly[i]);
       for (int j = 0; j < blocks; ++j, ++n) {
         const int key0 = seg_key0 + j * kKeys;
         ok = wait_inline(&sh.s_full[t], n & 1, abort_flag);
@@ -742,25 +757,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         gdn::tc_fence_after();
         float s[128];
         tmem_ld128(s_addr, s);
-        if (kMods) {
-          if (a.cap_log2 > 0.f) {
+        const bool edge = __any_sync(0xFFFFFFFFu, key0 < lo || key0 + kKeys > hi);
+        // Options and masks of scores [kFrom, kFrom + kCount), into units of log2.
+        auto modify = [&](auto from_c, auto count_c) {
+          constexpr int kFrom = decltype(from_c)::value, kCount = decltype(count_c)::value;
+          float* const x = s + kFrom;
+          if (kScores != kPlain) {
+            if (a.cap_log2 > 0.f) {
+              // Where the warp's scores stay within the cap (they mostly do), the
+              // polynomial; else the exponential form.
+              float big[4] = {fabsf(x[0]), fabsf(x[1]), fabsf(x[2]), fabsf(x[3])};
 #pragma unroll
-            for (int i = 0; i < 128; ++i) s[i] = gdn::capped(s[i] * a.scale_log2, a.cap_log2);
-          } else {
+              for (int i = 4; i < kCount; ++i) big[i & 3] = fmaxf(big[i & 3], fabsf(x[i]));
+              const float most = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
+              if (__all_sync(0xFFFFFFFFu, most <= a.cap_poly_max)) {
 #pragma unroll
-            for (int i = 0; i < 128; ++i) s[i] *= a.scale_log2;
+                for (int i = 0; i < kCount; i += 2) {
+                  const float2 y = gdn::capped_near(make_float2(x[i], x[i + 1]), poly);
+                  x[i] = y.x;
+                  x[i + 1] = y.y;
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < kCount; ++i) x[i] = gdn::capped(x[i] * a.scale_log2, a.cap_log2);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < kCount; ++i) x[i] *= a.scale_log2;
+            }
+            if (a.slopes) {
+              const float back = static_cast<float>(pos - key0);
+#pragma unroll
+              for (int i = 0; i < kCount; ++i) x[i] = fmaf(-slope, fabsf(back - static_cast<float>(kFrom + i)), x[i]);
+            }
           }
-          if (a.slopes) {
-            const float back = static_cast<float>(pos - key0);
+          if (edge) {
+            const int from = lo - key0, to = hi - key0;
 #pragma unroll
-            for (int i = 0; i < 128; ++i) s[i] = fmaf(-slope, fabsf(back - static_cast<float>(i)), s[i]);
+            for (int i = 0; i < kCount; ++i) x[i] = kFrom + i >= from && kFrom + i < to ? x[i] : -INFINITY;
           }
-        }
-        if (__any_sync(0xFFFFFFFFu, key0 < lo || key0 + kKeys > hi)) {
-          const int from = lo - key0, to = hi - key0;
+        };
+        // Weights of 64 keys at a time, so that the first half of P V runs beside
+        // the exponentials of the second.
+        auto publish = [&](auto half_c, float ref) {
+          constexpr int h = decltype(half_c)::value;
+          const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), ref2 = make_float2(-ref, -ref);
+          uint32_t p[32];
 #pragma unroll
-          for (int i = 0; i < 128; ++i) s[i] = i >= from && i < to ? s[i] : -INFINITY;
+          for (int i = 0; i < 32; ++i) {
+            float2 x = make_float2(s[64 * h + 2 * i], s[64 * h + 2 * i + 1]);
+            if (kScores == kPlain) x = __ffma2_rn(x, scale2, ref2);
+            if (kScores == kGeneral) x = __fadd2_rn(x, ref2);
+            x = make_float2(gdn::exp2_approx(x.x), gdn::exp2_approx(x.y));
+            // fp32 into the sum; bf16, as the values are, into the product.
+            l2 = __fadd2_rn(l2, x);
+            p[i] = gdn::pack_bf162(x);
+          }
+          tmem_st32_nw(s_addr + 32 * h, p);
+          gdn::tmem_wait_st();
+          gdn::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) gdn::mbar_arrive(&sh.p_full[t][h]);
+        };
+        using std::integral_constant;
+        if (kScores == kBounded) {
+          modify(integral_constant<int, 0>(), integral_constant<int, 64>());
+          publish(integral_constant<int, 0>(), 0.f);
+          modify(integral_constant<int, 64>(), integral_constant<int, 64>());
+          publish(integral_constant<int, 1>(), 0.f);
+          continue;
         }
+        modify(integral_constant<int, 0>(), integral_constant<int, 128>());
         float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
         for (int i = 4; i < 124; i += 8) {
@@ -768,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 4; ++k) top[k] = gdn::max3(top[k], s[i + 2 * k], s[i + 2 * k + 1]);
         }
         float mx = gdn::max3(gdn::max3(top[0], top[1], s[124]), gdn::max3(top[2], s[125], s[126]), fmaxf(top[3], s[127]));
-        if (!kMods) mx *= a.scale_log2;
+        if (kScores == kPlain) mx *= a.scale_log2;
         // The reference moves when a maximum is more than 2^8 above it.
         const bool grow = mx > m + 8.f || (m == -INFINITY && mx > m);
         if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -789,27 +856,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;  // a row that has seen no key yet: weights 2^-inf = 0
-        const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), ref2 = make_float2(-ref, -ref);
-        // Weights of 64 keys at a time, so that the first half of P V runs beside
-        // the exponentials of the second.
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t p[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float2 x = make_float2(s[64 * h + 2 * i], s[64 * h + 2 * i + 1]);
-            x = kMods ? __fadd2_rn(x, ref2) : __ffma2_rn(x, scale2, ref2);
-            x = make_float2(gdn::exp2_approx(x.x), gdn::exp2_approx(x.y));
-            // fp32 into the sum; bf16, as the values are, into the product.
-            l2 = __fadd2_rn(l2, x);
-            p[i] = gdn::pack_bf162(x);
-          }
-          tmem_st32_nw(s_addr + 32 * h, p);
-          gdn::tmem_wait_st();
-          gdn::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) gdn::mbar_arrive(&sh.p_full[t][h]);
-        }
+        publish(integral_constant<int, 0>(), ref);
+        publish(integral_constant<int, 1>(), ref);
       }
       if (!ok) break;
       if (taken > 0) {  // the epilogue has taken the last segment's
@@ -908,12 +956,12 @@ size_t workspace_bytes_of(int D, bool whole) {
   return kCutBytes + static_cast<size_t>(4) * kMaxGrid * kRows * (sizeof(float2) + D * sizeof(float));
 }
 
-template <int D, bool kMods>
+template <int D, Scores kScores>
 int launch(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache* cache, void* workspace, int sms, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   constexpr int smem = Layout<D>::kBytes + sizeof(Smem<D>);
   static_assert(smem <= 232448, "shared memory of one CTA");
-  int rc = gdn_host::func_attr_once(chunk_attention_kernel<D, kMods>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem,
+  int rc = gdn_host::func_attr_once(chunk_attention_kernel<D, kScores>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem,
                                     done);
   if (rc != GDN_OK) return rc;
   CUtensorMap q_map, k_map, v_map;
@@ -927,7 +975,7 @@ int launch(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache* cache, void* w
   d.cuts = reinterpret_cast<int4*>(ws);
   d.part_ml = reinterpret_cast<float2*>(ws + kCutBytes);
   d.part_o = reinterpret_cast<float4*>(ws + kCutBytes + sizeof(float2) * 4 * kMaxGrid * kRows);
-  rc = gdn_host::launch_pdl(chunk_attention_kernel<D, kMods>, dim3(grid), dim3(kThreads), smem, stream, d, q_map, k_map,
+  rc = gdn_host::launch_pdl(chunk_attention_kernel<D, kScores>, dim3(grid), dim3(kThreads), smem, stream, d, q_map, k_map,
                             v_map);
   if (rc != GDN_OK || d.whole) return rc;
   return gdn_host::launch_pdl(chunk_join_kernel<D>, dim3(grid, kJoinSlices), dim3(256), 0, stream, d);
@@ -957,10 +1005,16 @@ extern "C" int gdn_attention_paged(const gdn_bf16* q, int64_t q_token_stride, gd
   if (rc != GDN_OK) return rc;
   d.tile_tokens = kRows / d.a.group;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool mods = d.a.cap_log2 > 0.f || d.a.slopes;
-  if (cache->head_dim == 64)
-    return mods ? launch<64, true>(d, total_tokens, cache, workspace, sms, s)
-                : launch<64, false>(d, total_tokens, cache, workspace, sms, s);
-  return mods ? launch<128, true>(d, total_tokens, cache, workspace, sms, s)
-              : launch<128, false>(d, total_tokens, cache, workspace, sms, s);
+  const Scores scores = d.a.cap_log2 > 0.f && d.a.cap_log2 <= kBoundedCap ? kBounded
+                        : d.a.cap_log2 > 0.f || d.a.slopes                ? kGeneral
+                                                                          : kPlain;
+  const auto run = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    switch (scores) {
+      case kPlain: return launch<D, kPlain>(d, total_tokens, cache, workspace, sms, s);
+      case kGeneral: return launch<D, kGeneral>(d, total_tokens, cache, workspace, sms, s);
+      default: return launch<D, kBounded>(d, total_tokens, cache, workspace, sms, s);
+    }
+  };
+  return cache->head_dim == 64 ? run(std::integral_constant<int, 64>()) : run(std::integral_constant<int, 128>());
 }

@@ -168,7 +168,7 @@ def test_chunk_attention(lens, page_size, hq, hkv, dim, layout):
 def _options(name, hq, seqs):
     opts = {}
     if "cap" in name:
-        opts["softcap"] = 12.0
+        opts["softcap"] = 100.0 if "highcap" in name else 12.0
     if "slope" in name:
         opts["slopes"] = torch.tensor([2.0 ** (-8.0 * (h + 1) / hq) for h in range(hq)], device="cuda")
     if "window" in name:
@@ -182,7 +182,7 @@ def _options(name, hq, seqs):
 
 
 OPTIONS = ["cap", "slope", "window0", "window1", "window100", "window5000", "prefix", "cap slope window200", "scale",
-           "cap slope prefix scale"]
+           "cap slope prefix scale", "highcap", "highcap slope window64"]
 
 
 @pytest.mark.parametrize("name", OPTIONS)

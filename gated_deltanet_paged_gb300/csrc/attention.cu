@@ -258,6 +258,55 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&r)[128]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) pin32(r + 32 * i);
 }
+__device__ __forceinline__ void tmem_wait_ld32(float (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  pin32(r);
+}
+__device__ __forceinline__ float max128(const float (&s)[128]) {
+  float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+  for (int i = 4; i < 124; i += 8) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top[k] = gdn::max3(top[k], s[i + 2 * k], s[i + 2 * k + 1]);
+  }
+  return gdn::max3(gdn::max3(top[0], top[1], s[124]), gdn::max3(top[2], s[125], s[126]), fmaxf(top[3], s[127]));
+}
+// Cap and bias of 32 scores, into units of log2; back: distance of the first key.
+__device__ __forceinline__ void modify_scores(const AttnArgs& a, const float2 (&poly)[5], float slope, int back,
+                                              float (&x)[32]) {
+  if (a.cap_log2 > 0.f) {
+    // Where the warp's scores stay within the cap (they mostly do), the
+    // polynomial; else the exponential form.
+    float big[4] = {fabsf(x[0]), fabsf(x[1]), fabsf(x[2]), fabsf(x[3])};
+#pragma unroll
+    for (int i = 4; i < 32; ++i) big[i & 3] = fmaxf(big[i & 3], fabsf(x[i]));
+    const float most = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
+    if (__all_sync(0xFFFFFFFFu, most <= a.cap_poly_max)) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float2 y = gdn::capped_near(make_float2(x[i], x[i + 1]), poly);
+        x[i] = y.x;
+        x[i + 1] = y.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = gdn::capped(x[i] * a.scale_log2, a.cap_log2);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] *= a.scale_log2;
+  }
+  if (a.slopes) {
+    const float from = static_cast<float>(back);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = fmaf(-slope, fabsf(from - static_cast<float>(i)), x[i]);
+  }
+}
+// Scores outside [from, to) are hidden.
+__device__ __forceinline__ void mask_scores(int from, int to, float (&x)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) x[i] = i >= from && i < to ? x[i] : -INFINITY;
+}
 __device__ __forceinline__ void tmem_st32_nw(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -755,109 +804,115 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         gdn::tc_fence_after();
-        float s[128];
-        tmem_ld128(s_addr, s);
         const bool edge = __any_sync(0xFFFFFFFFu, key0 < lo || key0 + kKeys > hi);
-        // Options and masks of scores [kFrom, kFrom + kCount), into units of log2.
-        auto modify = [&](auto from_c, auto count_c) {
-          constexpr int kFrom = decltype(from_c)::value, kCount = decltype(count_c)::value;
-          float* const x = s + kFrom;
-          if (kScores != kPlain) {
-            if (a.cap_log2 > 0.f) {
-              // Where the warp's scores stay within the cap (they mostly do), the
-              // polynomial; else the exponential form.
-              float big[4] = {fabsf(x[0]), fabsf(x[1]), fabsf(x[2]), fabsf(x[3])};
-#pragma unroll
-              for (int i = 4; i < kCount; ++i) big[i & 3] = fmaxf(big[i & 3], fabsf(x[i]));
-              const float most = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
-              if (__all_sync(0xFFFFFFFFu, most <= a.cap_poly_max)) {
-#pragma unroll
-                for (int i = 0; i < kCount; i += 2) {
-                  const float2 y = gdn::capped_near(make_float2(x[i], x[i + 1]), poly);
-                  x[i] = y.x;
-                  x[i + 1] = y.y;
-                }
-              } else {
-#pragma unroll
-                for (int i = 0; i < kCount; ++i) x[i] = gdn::capped(x[i] * a.scale_log2, a.cap_log2);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < kCount; ++i) x[i] *= a.scale_log2;
-            }
-            if (a.slopes) {
-              const float back = static_cast<float>(pos - key0);
-#pragma unroll
-              for (int i = 0; i < kCount; ++i) x[i] = fmaf(-slope, fabsf(back - static_cast<float>(kFrom + i)), x[i]);
-            }
-          }
+        // Plain scores stay in registers from the maximum to the weights, all 128.
+        // The others go through loops of 32, read from TMEM again where needed:
+        // unrolled, their instructions were fetched more slowly than issued (ncu: 1.5
+        // warps per issue waited for one, against 0.4 on the plain path; rolling
+        // took the 64 mixed sequences from 2.13 to 1.73 ms, and 4 x 8,192 plain
+        // tokens from 1.39 to 1.48).
+        float ref = 0.f;
+        float s[kScores == kPlain ? 128 : 1];
+        if constexpr (kScores == kPlain) {
+          tmem_ld128(s_addr, s);
           if (edge) {
-            const int from = lo - key0, to = hi - key0;
 #pragma unroll
-            for (int i = 0; i < kCount; ++i) x[i] = kFrom + i >= from && kFrom + i < to ? x[i] : -INFINITY;
+            for (int i = 0; i < 128; ++i) s[i] = i >= lo - key0 && i < hi - key0 ? s[i] : -INFINITY;
           }
+        }
+        if constexpr (kScores != kBounded) {
+          float mx;
+          if constexpr (kScores == kPlain) {
+            mx = max128(s) * a.scale_log2;
+          } else {
+            // Changed and masked scores go back to TMEM.
+            mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < kKeys; c += 32) {
+              float x[32];
+              gdn::tmem_ld32(s_addr + c, x);
+              modify_scores(a, poly, slope, pos - key0 - c, x);
+              if (edge) mask_scores(lo - key0 - c, hi - key0 - c, x);
+              tmem_st32_nw(s_addr + c, reinterpret_cast<const uint32_t*>(x));
+              float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+              for (int i = 4; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
+              mx = fmaxf(mx, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+            }
+            gdn::tmem_wait_st();
+          }
+          // The reference moves when a maximum is more than 2^8 above it.
+          const bool grow = mx > m + 8.f || (m == -INFINITY && mx > m);
+          if (__any_sync(0xFFFFFFFFu, grow)) {
+            const float to = fmaxf(m, mx);
+            const float r = m == -INFINITY ? 0.f : gdn::exp2_approx(m - to);
+            m = to;
+            l2 = __fmul2_rn(l2, make_float2(r, r));
+            if (j > 0) {  // O of the blocks before is complete: S came behind it
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                float x[16];
+                gdn::tmem_ld16(o_addr + c, x);
+                uint32_t y[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[i] * r);
+                gdn::tmem_st16(o_addr + c, y);
+              }
+            }
+          }
+          ref = m == -INFINITY ? 0.f : m;  // a row that has seen no key yet: weights 2^-inf = 0
+        }
+        // Weights over the first half of their S columns: fp32 into the sum; bf16, as
+        // the values are, into the product.  64 keys at a time, so that the first half
+        // of P V runs beside the exponentials of the second.
+        const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), ref2 = make_float2(-ref, -ref);
+        auto weight = [&](float2 x) {
+          if (kScores == kPlain) x = __ffma2_rn(x, scale2, ref2);
+          if (kScores == kGeneral) x = __fadd2_rn(x, ref2);
+          x = make_float2(gdn::exp2_approx(x.x), gdn::exp2_approx(x.y));
+          l2 = __fadd2_rn(l2, x);
+          return gdn::pack_bf162(x);
         };
-        // Weights of 64 keys at a time, so that the first half of P V runs beside
-        // the exponentials of the second.
-        auto publish = [&](auto half_c, float ref) {
-          constexpr int h = decltype(half_c)::value;
-          const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), ref2 = make_float2(-ref, -ref);
-          uint32_t p[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float2 x = make_float2(s[64 * h + 2 * i], s[64 * h + 2 * i + 1]);
-            if (kScores == kPlain) x = __ffma2_rn(x, scale2, ref2);
-            if (kScores == kGeneral) x = __fadd2_rn(x, ref2);
-            x = make_float2(gdn::exp2_approx(x.x), gdn::exp2_approx(x.y));
-            // fp32 into the sum; bf16, as the values are, into the product.
-            l2 = __fadd2_rn(l2, x);
-            p[i] = gdn::pack_bf162(x);
-          }
-          tmem_st32_nw(s_addr + 32 * h, p);
+        auto publish = [&](int h) {
           gdn::tmem_wait_st();
           gdn::tc_fence_before();
           __syncwarp();
           if (lane == 0) gdn::mbar_arrive(&sh.p_full[t][h]);
         };
-        using std::integral_constant;
-        if (kScores == kBounded) {
-          modify(integral_constant<int, 0>(), integral_constant<int, 64>());
-          publish(integral_constant<int, 0>(), 0.f);
-          modify(integral_constant<int, 64>(), integral_constant<int, 64>());
-          publish(integral_constant<int, 1>(), 0.f);
-          continue;
-        }
-        modify(integral_constant<int, 0>(), integral_constant<int, 128>());
-        float top[4] = {s[0], s[1], s[2], s[3]};
+        if constexpr (kScores == kPlain) {
 #pragma unroll
-        for (int i = 4; i < 124; i += 8) {
+          for (int h = 0; h < 2; ++h) {
+            uint32_t p[32];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) top[k] = gdn::max3(top[k], s[i + 2 * k], s[i + 2 * k + 1]);
-        }
-        float mx = gdn::max3(gdn::max3(top[0], top[1], s[124]), gdn::max3(top[2], s[125], s[126]), fmaxf(top[3], s[127]));
-        if (kScores == kPlain) mx *= a.scale_log2;
-        // The reference moves when a maximum is more than 2^8 above it.
-        const bool grow = mx > m + 8.f || (m == -INFINITY && mx > m);
-        if (__any_sync(0xFFFFFFFFu, grow)) {
-          const float to = fmaxf(m, mx);
-          const float r = m == -INFINITY ? 0.f : gdn::exp2_approx(m - to);
-          m = to;
-          l2 = __fmul2_rn(l2, make_float2(r, r));
-          if (j > 0) {  // O of the blocks before is complete: S came behind it
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              float x[16];
-              gdn::tmem_ld16(o_addr + c, x);
-              uint32_t y[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[i] * r);
-              gdn::tmem_st16(o_addr + c, y);
+            for (int i = 0; i < 32; ++i) p[i] = weight(make_float2(s[64 * h + 2 * i], s[64 * h + 2 * i + 1]));
+            tmem_st32_nw(s_addr + 32 * h, p);
+            publish(h);
+          }
+        } else {
+          auto weights = [&](float (&x)[32], int c) {
+            if (kScores == kBounded) {
+              modify_scores(a, poly, slope, pos - key0 - c, x);
+              if (edge) mask_scores(lo - key0 - c, hi - key0 - c, x);
             }
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[i] = weight(make_float2(x[2 * i], x[2 * i + 1]));
+            gdn::tmem_st16_nw(s_addr + c / 2, p);
+          };
+          // The next 32 scores are on their way meanwhile.
+          float x[32], y[32];
+          tmem_ld32_nw(s_addr, x);
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            tmem_wait_ld32(x);
+            tmem_ld32_nw(s_addr + 64 * h + 32, y);
+            weights(x, 64 * h);
+            tmem_wait_ld32(y);
+            if (h == 0) tmem_ld32_nw(s_addr + 64, x);
+            weights(y, 64 * h + 32);
+            publish(h);
           }
         }
-        const float ref = m == -INFINITY ? 0.f : m;  // a row that has seen no key yet: weights 2^-inf = 0
-        publish(integral_constant<int, 0>(), ref);
-        publish(integral_constant<int, 1>(), ref);
       }
       if (!ok) break;
       if (taken > 0) {  // the epilogue has taken the last segment's

@@ -226,6 +226,23 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8], bool al
                : "memory");
 }
 
+// Four columns of this thread's TMEM lane, waited for.
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+      : "memory");
+}
+
 // 128 fp32 columns of this thread's TMEM lane: four loads in flight, one wait.
 // The registers pass through the wait, so that no use is scheduled before it.
 __device__ __forceinline__ void tmem_ld32_nw(uint32_t taddr, float* r) {
@@ -271,35 +288,33 @@ __device__ __forceinline__ float max128(const float (&s)[128]) {
   }
   return gdn::max3(gdn::max3(top[0], top[1], s[124]), gdn::max3(top[2], s[125], s[126]), fmaxf(top[3], s[127]));
 }
-// Cap and bias of 32 scores, into units of log2; back: distance of the first key.
-__device__ __forceinline__ void modify_scores(const AttnArgs& a, const float2 (&poly)[5], float slope, int back,
-                                              float (&x)[32]) {
-  if (a.cap_log2 > 0.f) {
-    // Where the warp's scores stay within the cap (they mostly do), the
-    // polynomial; else the exponential form.
-    float big[4] = {fabsf(x[0]), fabsf(x[1]), fabsf(x[2]), fabsf(x[3])};
+// Cap of 32 scores in TMEM columns from addr, into units of log2.  Where the
+// warp's scores stay within the cap (they mostly do), the polynomial; else the
+// exponential form, four scores at a time by way of TMEM: it is rarely taken, and
+// its instructions would stand between those of the other (1.73 -> 1.60 ms on the
+// 64 mixed sequences).
+__device__ __forceinline__ void cap_scores(const AttnArgs& a, const float2 (&poly)[5], uint32_t addr, float (&x)[32]) {
+  float big[4] = {fabsf(x[0]), fabsf(x[1]), fabsf(x[2]), fabsf(x[3])};
 #pragma unroll
-    for (int i = 4; i < 32; ++i) big[i & 3] = fmaxf(big[i & 3], fabsf(x[i]));
-    const float most = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
-    if (__all_sync(0xFFFFFFFFu, most <= a.cap_poly_max)) {
+  for (int i = 4; i < 32; ++i) big[i & 3] = fmaxf(big[i & 3], fabsf(x[i]));
+  const float most = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
+  if (__all_sync(0xFFFFFFFFu, most <= a.cap_poly_max)) {
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const float2 y = gdn::capped_near(make_float2(x[i], x[i + 1]), poly);
-        x[i] = y.x;
-        x[i + 1] = y.y;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = gdn::capped(x[i] * a.scale_log2, a.cap_log2);
+    for (int i = 0; i < 32; i += 2) {
+      const float2 y = gdn::capped_near(make_float2(x[i], x[i + 1]), poly);
+      x[i] = y.x;
+      x[i + 1] = y.y;
     }
   } else {
+#pragma unroll 1
+    for (int i = 0; i < 32; i += 4) {
+      uint32_t z[4];
+      tmem_ld4(addr + i, z);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] *= a.scale_log2;
-  }
-  if (a.slopes) {
-    const float from = static_cast<float>(back);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = fmaf(-slope, fabsf(from - static_cast<float>(i)), x[i]);
+      for (int k = 0; k < 4; ++k) z[k] = __float_as_uint(gdn::capped(__uint_as_float(z[k]) * a.scale_log2, a.cap_log2));
+      tmem_st4(addr + i, z);
+    }
+    gdn::tmem_ld32(addr, x);
   }
 }
 // Scores outside [from, to) are hidden.
@@ -321,13 +336,12 @@ __device__ __forceinline__ void tmem_st32_nw(uint32_t taddr, const uint32_t* r) 
 
 // How scores become weights.
 //   kPlain: scale and reference in one multiply-add.
-//   kGeneral: a cap or a bias first (the options that change a score; those that
-//     only hide keys cost nothing away from the edges).
-//   kBounded: a cap of at most kBoundedCap bounds the scores on both sides, so that
-//     0 serves as the reference for the whole row: weights within 2^-80 .. 2^80
-//     and their sums over 2^30 keys are far inside fp32 and bf16, and no maximum
-//     is taken.  (A bias only lowers scores, and each row sees its own key, whose
-//     bias is 0.)
+//   kGeneral: a bias, or any cap, first (the options that change a score; those
+//     that only hide keys cost nothing away from the edges).
+//   kBounded: a cap of at most kBoundedCap, and no bias.  It bounds the scores on
+//     both sides, so that 0 serves as the reference for the whole row: weights
+//     within 2^-80 .. 2^80 and their sums over 2^30 keys are far inside fp32 and
+//     bf16, and no maximum is taken.
 enum Scores { kPlain, kGeneral, kBounded };
 constexpr float kBoundedCap = 80.f;  // in units of log2
 
@@ -786,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = g.pos + min(t * tile_tokens + min(my_token, tile_tokens - 1), tokens - 1);
       const int lo = gdn::key_lo(a, pos), hi = max(pos + 1, g.full);
       float slope = 0.f;
-      if (kScores != kPlain && a.slopes) slope = a.slopes[g.head * a.group + my_head] * gdn::kLog2e;
+      if (kScores == kGeneral && a.slopes) slope = a.slopes[g.head * a.group + my_head] * gdn::kLog2e;
       __syncwarp();
       if (lane == 0) gdn::mbar_arrive(&sh.seg_empty[at]);
       if (blocks == 0) break;
@@ -809,8 +823,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The others go through loops of 32, read from TMEM again where needed:
         // unrolled, their instructions were fetched more slowly than issued (ncu: 1.5
         // warps per issue waited for one, against 0.4 on the plain path; rolling
-        // took the 64 mixed sequences from 2.13 to 1.73 ms, and 4 x 8,192 plain
-        // tokens from 1.39 to 1.48).
+        // took the 64 mixed sequences from 2.13 to 1.73 ms, but would take 4 x 8,192
+        // plain tokens from 1.39 to 1.48).
         float ref = 0.f;
         float s[kScores == kPlain ? 128 : 1];
         if constexpr (kScores == kPlain) {
@@ -831,7 +845,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < kKeys; c += 32) {
               float x[32];
               gdn::tmem_ld32(s_addr + c, x);
-              modify_scores(a, poly, slope, pos - key0 - c, x);
+              if (a.cap_log2 > 0.f) {
+                cap_scores(a, poly, s_addr + c, x);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] *= a.scale_log2;
+              }
+              if (a.slopes) {
+                const float back = static_cast<float>(pos - key0 - c);  // distance of the first key
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = fmaf(-slope, fabsf(back - static_cast<float>(i)), x[i]);
+              }
               if (edge) mask_scores(lo - key0 - c, hi - key0 - c, x);
               tmem_st32_nw(s_addr + c, reinterpret_cast<const uint32_t*>(x));
               float top[4] = {x[0], x[1], x[2], x[3]};
@@ -891,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           auto weights = [&](float (&x)[32], int c) {
             if (kScores == kBounded) {
-              modify_scores(a, poly, slope, pos - key0 - c, x);
+              cap_scores(a, poly, s_addr + c, x);
               if (edge) mask_scores(lo - key0 - c, hi - key0 - c, x);
             }
             uint32_t p[16];
@@ -1060,9 +1084,8 @@ extern "C" int gdn_attention_paged(const gdn_bf16* q, int64_t q_token_stride, gd
   if (rc != GDN_OK) return rc;
   d.tile_tokens = kRows / d.a.group;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const Scores scores = d.a.cap_log2 > 0.f && d.a.cap_log2 <= kBoundedCap ? kBounded
-                        : d.a.cap_log2 > 0.f || d.a.slopes                ? kGeneral
-                                                                          : kPlain;
+  const bool bounded = d.a.cap_log2 > 0.f && d.a.cap_log2 <= kBoundedCap && !d.a.slopes;
+  const Scores scores = bounded ? kBounded : d.a.cap_log2 > 0.f || d.a.slopes ? kGeneral : kPlain;
   const auto run = [&](auto dim) {
     constexpr int D = decltype(dim)::value;
     switch (scores) {

@@ -201,12 +201,6 @@ __device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, cons
   return true;
 }
 
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
 // This warp has read its part of O.
 __device__ __forceinline__ void release(uint64_t* bar, int lane) {
   gdn::tc_fence_before();
@@ -492,28 +486,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t raw_parity = 0, raw_last = 0;  // per stage: parity of its next raw copy; its last copy was one
       bool q_in_flight = false;
       const int boxes = kKeys >> a.box_shift, box_rows = 1 << a.box_shift;
+      const int step_entries = kKeys / a.paged.page_size, step_slots = kKeys % a.paged.page_size;  // of a block
       for (bool more = true; more; ++segs) {
         more = next_segment(d, w);
         const int pair0 = w.pair * 2 * tile_tokens;  // first token of the item within the sequence's new ones
         const int token = w.s.first_token + pair0;
         const bool two = pair0 + tile_tokens < w.s.n;
-        // Pages of the first block, asked for before anything waits.
-        int page[4], slot[4];
-        auto look_up = [&](int key0) {
-          const int first = max(0, w.lo - key0) >> a.box_shift;
-          const int last = (min(kKeys, w.hi - key0) + box_rows - 1) >> a.box_shift;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int box = lane + 32 * i;
-            if (32 * i < boxes && box >= first && box < last) {
-              const int key = key0 + box * box_rows;
-              const int entry = key / a.paged.page_size;
-              slot[i] = key - entry * a.paged.page_size;
-              page[i] = a.paged.pages[w.s.entry + entry];
-            }
+        // Lane i copies box i of every block: where its rows lie follows from block to
+        // block without a division, and their page is asked for a block ahead.  (This
+        // warp's instructions are rarely in the cache: with a lookup of all boxes
+        // per block the products waited for keys.)  A block of more than 32
+        // boxes, from pages of an odd or once even size, looks them up on the spot.
+        int key = (w.first + w.blk0) * kKeys + lane * box_rows;  // first key of this lane's box
+        int entry = key / a.paged.page_size, slot = key - entry * a.paged.page_size;
+        auto visible = [&](int k) { return k + box_rows > w.lo && k < w.hi; };
+        auto page_of = [&](int e) {
+          int p = a.paged.pages[w.s.entry + e];
+          if (p < 0 || p >= a.paged.num_pages) {
+            gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_ID, w.b);
+            p = a.paged.num_pages;  // outside the map: zeros
           }
+          return p;
         };
-        if (more) look_up((w.first + w.blk0) * kKeys);
+        int page = more && lane < boxes && visible(key) ? page_of(entry) : 0;
         if (segs >= kSegments && !wait(&sh.seg_empty[segs % kSegments], ((segs / kSegments) - 1) & 1)) break;
         if (lane == 0) {
           Segment g = {};
@@ -566,7 +561,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int key0 = (w.first + blk) * kKeys;
           const int first = max(0, w.lo - key0) >> a.box_shift;
           const int last = (min(kKeys, w.hi - key0) + box_rows - 1) >> a.box_shift;
-          if (blk > w.blk0) look_up(key0);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++n) {
             const int stage = n % L::kStages;
@@ -579,21 +573,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             raw_parity ^= clear ? 1u << stage : 0u;
             uint8_t* dst = ring + stage * L::kTile;
             const CUtensorMap* map = kv ? &v_map : &k_map;
+            auto copy = [&](int box, int o, int p) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int box = lane + 32 * i;
-              if (32 * i < boxes && box >= first && box < last) {
-                if (page[i] < 0 || page[i] >= a.paged.num_pages) {
-                  gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_ID, w.b);
-                  page[i] = a.paged.num_pages;  // outside the map: zeros
-                }
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                  gdn::tma_load_4d(dst + c * L::kHalf + box * box_rows * 128, map, bar, c * 64, w.head, slot[i], page[i]);
+              for (int c = 0; c < D / 64; ++c)
+                gdn::tma_load_4d(dst + c * L::kHalf + box * box_rows * 128, map, bar, c * 64, w.head, o, p);
+            };
+            if (boxes <= 32) {
+              if (lane < boxes && visible(key)) copy(lane, slot, page);
+            } else {
+#pragma unroll 1
+              for (int box = lane; box < boxes; box += 32) {
+                const int k = key0 + box * box_rows;
+                if (!visible(k)) continue;
+                const int e = k / a.paged.page_size;
+                copy(box, k - e * a.paged.page_size, page_of(e));
               }
             }
             __syncwarp();
           }
+          key += kKeys;
+          entry += step_entries;
+          slot += step_slots;
+          if (slot >= a.paged.page_size) slot -= a.paged.page_size, ++entry;
+          if (boxes <= 32 && lane < boxes && blk + 1 < w.blk1 && visible(key)) page = page_of(entry);
           if (ok && !q_sent) q_sent = send_queries(true);
         }
         if (!ok) break;
@@ -630,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // S = Q K^T of the ring's current tile, which is released with it.
       auto scores = [&](bool last) {
         gdn::tc_fence_after();
-        if (elect_one()) {
+        if (gdn::elect_one()) {
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
             gdn::tc_mma4(s_col, q_desc + c * (L::kHalf >> 4), 2, k_desc + stage * kStep + c * (L::kHalf >> 4), 2, id_s, c);
@@ -664,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j == 0 && done_segs > 0 && !wait(&sh.o_free[t], (done_segs - 1) & 1)) break;
           if (!wait(&sh.p_full[t][0], np & 1)) break;
           gdn::tc_fence_after();
-          if (elect_one()) gdn::tc_mma4_ts(o_col, s_col, 8, v_desc + v_stage * kStep, 128, id_o, j > 0);
+          if (gdn::elect_one()) gdn::tc_mma4_ts(o_col, s_col, 8, v_desc + v_stage * kStep, 128, id_o, j > 0);
           __syncwarp();
           if (!wait(&sh.p_full[t][1], np & 1)) break;
           // The tiles take turns with the rest of P V and the next S.  Interleaved,
@@ -673,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // that way and 2,600 when the tiles are half a period apart).
           if (two && (t == 1 || turns > 0) && !wait(&sh.turn[t], (t == 1 ? turns : turns - 1) & 1)) break;
           gdn::tc_fence_after();
-          if (elect_one()) {
+          if (gdn::elect_one()) {
             gdn::tc_mma4_ts(o_col, s_col + 32, 8, v_desc + v_stage * kStep + 4 * 128, 128, id_o, 1);
             if (j + 1 == g.blocks) gdn::tc_commit(&sh.o_last[t]);
             gdn::tc_commit(&sh.empty[v_stage]);
@@ -693,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) *abort_flag = 1;
       // Every product is complete before TMEM is given back.
-      if (elect_one()) gdn::tc_commit(&sh.done[t]);
+      if (gdn::elect_one()) gdn::tc_commit(&sh.done[t]);
       __syncwarp();
       gdn::mbar_wait(&sh.done[t], 0);
     } else if (warp == kClearWarp) {

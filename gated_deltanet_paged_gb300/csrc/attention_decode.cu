@@ -153,7 +153,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ uint8_t raw[];
   Smem<D>& sh = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const AttnArgs& a = d.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   if (tid == kConsumers * 32) {
     gdn::prefetch_tensormap(&k_map);
     gdn::prefetch_tensormap(&v_map);
@@ -261,21 +262,23 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         if (!ok) break;
+        // One copy after the other from one lane, with the addresses passed along: a
+        // copy per lane instead makes each of them a turn of a divergent loop.
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int box = lane + 32 * i;
-          if (box >= first && box < last) {
-            const int at = (box << a.box_shift) * 128;
+          for (int box = max(first, 32 * i); box < min(last, 32 * i + 32); ++box) {
+            const int p = __shfl_sync(0xFFFFFFFFu, page[i], box & 31), o = __shfl_sync(0xFFFFFFFFu, slot[i], box & 31);
+            if (gdn::elect_one()) {
+              const int at = (box << a.box_shift) * 128;
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-              gdn::tma_load_4d(sh.kv[stage][0] + c * kBlock * 128 + at, &k_map, &sh.full[stage], c * 64, head, slot[i],
-                               page[i]);
-              gdn::tma_load_4d(sh.kv[stage][1] + c * kBlock * 128 + at, &v_map, &sh.full[stage], c * 64, head, slot[i],
-                               page[i]);
+              for (int c = 0; c < D / 64; ++c) {
+                gdn::tma_load_4d(sh.kv[stage][0] + c * kBlock * 128 + at, &k_map, &sh.full[stage], c * 64, head, o, p);
+                gdn::tma_load_4d(sh.kv[stage][1] + c * kBlock * 128 + at, &v_map, &sh.full[stage], c * 64, head, o, p);
+              }
             }
+            __syncwarp();
           }
         }
-        __syncwarp();
       }
     }
     if (!ok) {

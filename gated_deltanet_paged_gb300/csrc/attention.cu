@@ -17,8 +17,9 @@
 //     the other.  S and O of both tiles fill the 512 columns of TMEM (D = 128); the
 //     weights go back over the first half of their S as the A operand of P V.
 //   - Warp roles: two softmax warpgroups (one row per thread, its 128 scores in
-//     registers), one warp that issues the products, one that copies pages by
-//     TMA, one that clears the value rows of keys no row may see.
+//     registers), two warps that issue the products, one that copies keys page by
+//     page by TMA and one that copies values and clears those that no row may see,
+//     and an epilogue warpgroup.
 //   - The batch is one line of (sequence, token tile, key head) items, as long as
 //     their key ranges, and each CTA takes an equal piece of it, cutting items
 //     where the piece ends (as the decode kernel does); the line's prefix sums
@@ -35,9 +36,9 @@ using gdn::AttnArgs;
 constexpr int kRows = 128;   // rows per tile
 constexpr int kKeys = 128;   // keys per block
 // Warps 0-3 and 4-7: softmax of tiles 0 and 1; 8 and 9: products of tiles 0 and
-// 1; 10: segments and copies; 11: clearing; 12-15: epilogue.
+// 1; 10: segments, queries and keys; 11: values; 12-15: epilogue.
 constexpr int kThreads = 512;
-constexpr int kMmaWarp = 8, kLoadWarp = 10, kClearWarp = 11;
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kValueWarp = 11;
 // 65,536 registers: 256 softmax threads hold 128 scores each, the others little.
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 56;
 static_assert(256 * (kSoftmaxRegs + kOtherRegs) == 65536, "register split of the block");
@@ -159,6 +160,83 @@ struct alignas(16) Segment {
   int full;         // prefix mask
   int head;
   int part;         // -1: the whole item; else its partial slot
+  int entry;        // first page table entry of the sequence
+  int seq;
+};
+
+// Copies of one K or V tile after the other by a warp: lane i has box i of every
+// tile.  Where its rows lie follows from tile to tile without a division, and
+// their page is asked for a tile ahead.  (The instructions of these warps are
+// rarely in the cache: with a lookup per tile the products waited for keys.)  A
+// tile of more than 32 boxes, from pages of an odd or once even size, is looked
+// up on the spot.
+template <int D>
+struct TileCopies {
+  const AttnArgs& a;
+  const CUtensorMap* map;
+  int lane, boxes, box_rows, step_entries, step_slots;
+  int lo, hi, head, seq;
+  const int32_t* pages;
+  int key0, entry, slot, page;
+
+  __device__ __forceinline__ TileCopies(const AttnArgs& args, const CUtensorMap* m, int l) : a(args), map(m), lane(l) {
+    boxes = kKeys >> a.box_shift;
+    box_rows = 1 << a.box_shift;
+    step_entries = kKeys / a.paged.page_size;
+    step_slots = kKeys % a.paged.page_size;
+  }
+  __device__ __forceinline__ bool visible(int k) const { return k + box_rows > lo && k < hi; }
+  __device__ __forceinline__ int page_of(int e) const {
+    int p = pages[e];
+    if (p < 0 || p >= a.paged.num_pages) {
+      gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_ID, seq);
+      p = a.paged.num_pages;  // outside the map: zeros
+    }
+    return p;
+  }
+  __device__ __forceinline__ void look_ahead() {
+    if (boxes <= 32 && lane < boxes && visible(key0 + lane * box_rows)) page = page_of(entry);
+  }
+  __device__ __forceinline__ void begin(const Segment& g) {
+    lo = g.lo, hi = g.hi, head = g.head, seq = g.seq;
+    pages = a.paged.pages + g.entry;
+    key0 = g.key0;
+    const int key = key0 + lane * box_rows;
+    entry = key / a.paged.page_size;
+    slot = key - entry * a.paged.page_size;
+    look_ahead();
+  }
+  // Bytes of the boxes that hold a visible key; the others are not copied.
+  __device__ __forceinline__ int bytes() const {
+    const int first = max(0, lo - key0) >> a.box_shift;
+    const int last = (min(kKeys, hi - key0) + box_rows - 1) >> a.box_shift;
+    return (last - first) * box_rows * D * 2;
+  }
+  __device__ __forceinline__ void box(uint8_t* dst, uint64_t* bar, int i, int o, int p) const {
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      gdn::tma_load_4d(dst + c * (kRows * 128) + i * box_rows * 128, map, bar, c * 64, head, o, p);
+  }
+  // The current tile; then on to the next of `more`.
+  __device__ __forceinline__ void copy(uint8_t* dst, uint64_t* bar, bool more) {
+    if (boxes <= 32) {
+      if (lane < boxes && visible(key0 + lane * box_rows)) box(dst, bar, lane, slot, page);
+    } else {
+#pragma unroll 1
+      for (int i = lane; i < boxes; i += 32) {
+        const int k = key0 + i * box_rows;
+        if (!visible(k)) continue;
+        const int e = k / a.paged.page_size;
+        box(dst, bar, i, k - e * a.paged.page_size, page_of(e));
+      }
+    }
+    __syncwarp();
+    key0 += kKeys;
+    entry += step_entries;
+    slot += step_slots;
+    if (slot >= a.paged.page_size) slot -= a.paged.page_size, ++entry;
+    if (more) look_ahead();
+  }
 };
 
 template <int D>
@@ -480,62 +558,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       return g.blocks > 0;
     };
     if (warp == kLoadWarp) {
-      // --------------------------------------------- segments and copies
+      // ------------------------------------ segments, queries and keys
       Walk w = sh.walk;
-      uint32_t n = 0, segs = 0;                // tiles issued, segments announced
-      uint32_t raw_parity = 0, raw_last = 0;  // per stage: parity of its next raw copy; its last copy was one
+      TileCopies<D> keys(a, &k_map, lane);
+      uint32_t n = 0, segs = 0;  // ring tiles (keys are the even ones), segments announced
       bool q_in_flight = false;
-      const int boxes = kKeys >> a.box_shift, box_rows = 1 << a.box_shift;
-      const int step_entries = kKeys / a.paged.page_size, step_slots = kKeys % a.paged.page_size;  // of a block
-      for (bool more = true; more; ++segs) {
-        more = next_segment(d, w);
-        const int pair0 = w.pair * 2 * tile_tokens;  // first token of the item within the sequence's new ones
-        const int token = w.s.first_token + pair0;
-        const bool two = pair0 + tile_tokens < w.s.n;
-        // Lane i copies box i of every block: where its rows lie follows from block to
-        // block without a division, and their page is asked for a block ahead.  (This
-        // warp's instructions are rarely in the cache: with a lookup of all boxes
-        // per block the products waited for keys.)  A block of more than 32
-        // boxes, from pages of an odd or once even size, looks them up on the spot.
-        int key = (w.first + w.blk0) * kKeys + lane * box_rows;  // first key of this lane's box
-        int entry = key / a.paged.page_size, slot = key - entry * a.paged.page_size;
-        auto visible = [&](int k) { return k + box_rows > w.lo && k < w.hi; };
-        auto page_of = [&](int e) {
-          int p = a.paged.pages[w.s.entry + e];
-          if (p < 0 || p >= a.paged.num_pages) {
-            gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_ID, w.b);
-            p = a.paged.num_pages;  // outside the map: zeros
-          }
-          return p;
-        };
-        int page = more && lane < boxes && visible(key) ? page_of(entry) : 0;
+      for (;; ++segs) {
+        const bool more = next_segment(d, w);
         if (segs >= kSegments && !wait(&sh.seg_empty[segs % kSegments], ((segs / kSegments) - 1) & 1)) break;
+        Segment g = {};
+        if (more) {
+          const bool starts = w.blk0 == 0, ends = w.blk1 == w.blocks;
+          const int pair0 = w.pair * 2 * tile_tokens;  // first token of the item within the sequence's new ones
+          g.blocks = w.blk1 - w.blk0;
+          g.key0 = (w.first + w.blk0) * kKeys;
+          g.lo = w.lo;
+          g.hi = w.hi;
+          g.first_token = w.s.first_token + pair0;
+          g.tokens = min(2 * tile_tokens, w.s.n - pair0);
+          g.pos = w.s.len - w.s.n + pair0;
+          g.full = w.s.full;
+          g.head = w.head;
+          // One segment of a CTA at most starts an item that it does not end, and
+          // one at most continues one: two partial slots per CTA.
+          g.part = starts && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
+          g.entry = w.s.entry;
+          g.seq = w.b;
+          if (lane == 0 && starts && !ends)
+            d.cuts[blockIdx.x] = make_int4(g.first_token, g.tokens, g.head, shares.owner(w.item0 + w.cost - 1));
+        }
         if (lane == 0) {
-          Segment g = {};
-          if (more) {
-            const bool starts = w.blk0 == 0, ends = w.blk1 == w.blocks;
-            g.blocks = w.blk1 - w.blk0;
-            g.key0 = (w.first + w.blk0) * kKeys;
-            g.lo = w.lo;
-            g.hi = w.hi;
-            g.first_token = token;
-            g.tokens = min(2 * tile_tokens, w.s.n - pair0);
-            g.pos = w.s.len - w.s.n + pair0;
-            g.full = w.s.full;
-            g.head = w.head;
-            // One segment of a CTA at most starts an item that it does not end,
-            // and one at most continues one: two partial slots per CTA.
-            g.part = starts && ends ? -1 : 2 * static_cast<int>(blockIdx.x) + (starts ? 1 : 0);
-            if (starts && !ends)
-              d.cuts[blockIdx.x] = make_int4(token, g.tokens, w.head, shares.owner(w.item0 + w.cost - 1));
-          }
           sh.seg[segs % kSegments] = g;
           gdn::mbar_arrive(&sh.seg_full[segs % kSegments]);
         }
         __syncwarp();
         if (!more) break;
+        keys.begin(g);
         // The queries go first where their room is free; else behind the first
-        // block's keys and values, which need none that the segment before holds.
+        // block's keys, which need none that the segment before holds.
         auto send_queries = [&](bool must) {
           if (segs > 0) {
             const uint32_t parity = (segs - 1) & 1;
@@ -546,70 +606,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (lane == 0) {
-            const int bytes = a.group * tile_tokens * D * 2;
-            gdn::mbar_arrive_expect_tx(&sh.q_full, two ? 2 * bytes : bytes);
-            for (int t = 0; t < (two ? 2 : 1); ++t)
+            const int bytes = a.group * tile_tokens * D * 2, tiles_used = g.tokens > tile_tokens ? 2 : 1;
+            gdn::mbar_arrive_expect_tx(&sh.q_full, tiles_used * bytes);
+            for (int t = 0; t < tiles_used; ++t)
               for (int c = 0; c < D / 64; ++c)
                 gdn::tma_load_4d(tiles + t * L::kTile + c * L::kHalf, &q_map, &sh.q_full, c * 64, 0,
-                                 token + t * tile_tokens, w.head);
+                                 g.first_token + t * tile_tokens, g.head);
           }
+          __syncwarp();
           q_in_flight = true;
           return true;
         };
         bool q_sent = send_queries(false);
-        for (int blk = w.blk0; ok && blk < w.blk1; ++blk) {
-          const int key0 = (w.first + blk) * kKeys;
-          const int first = max(0, w.lo - key0) >> a.box_shift;
-          const int last = (min(kKeys, w.hi - key0) + box_rows - 1) >> a.box_shift;
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++n) {
-            const int stage = n % L::kStages;
-            const bool clear = kv && (key0 < w.lo || key0 + kKeys > w.hi);
-            uint64_t* bar = clear ? &sh.raw[stage] : &sh.full[stage];
-            if (n >= L::kStages && !wait(&sh.empty[stage], ((n / L::kStages) - 1) & 1)) break;
-            if (lane == 0) gdn::mbar_arrive_expect_tx(bar, (last - first) * box_rows * D * 2);
-            __syncwarp();
-            raw_last = clear ? raw_last | (1u << stage) : raw_last & ~(1u << stage);
-            raw_parity ^= clear ? 1u << stage : 0u;
-            uint8_t* dst = ring + stage * L::kTile;
-            const CUtensorMap* map = kv ? &v_map : &k_map;
-            auto copy = [&](int box, int o, int p) {
-#pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                gdn::tma_load_4d(dst + c * L::kHalf + box * box_rows * 128, map, bar, c * 64, w.head, o, p);
-            };
-            if (boxes <= 32) {
-              if (lane < boxes && visible(key)) copy(lane, slot, page);
-            } else {
-#pragma unroll 1
-              for (int box = lane; box < boxes; box += 32) {
-                const int k = key0 + box * box_rows;
-                if (!visible(k)) continue;
-                const int e = k / a.paged.page_size;
-                copy(box, k - e * a.paged.page_size, page_of(e));
-              }
-            }
-            __syncwarp();
-          }
-          key += kKeys;
-          entry += step_entries;
-          slot += step_slots;
-          if (slot >= a.paged.page_size) slot -= a.paged.page_size, ++entry;
-          if (boxes <= 32 && lane < boxes && blk + 1 < w.blk1 && visible(key)) page = page_of(entry);
-          if (ok && !q_sent) q_sent = send_queries(true);
+        for (int j = 0; j < g.blocks; ++j, n += 2) {
+          const uint32_t stage = n % L::kStages;
+          if (n >= L::kStages && !wait(&sh.empty[stage], ((n / L::kStages) - 1) & 1)) break;
+          if (lane == 0) gdn::mbar_arrive_expect_tx(&sh.full[stage], keys.bytes());
+          __syncwarp();
+          keys.copy(ring + stage * L::kTile, &sh.full[stage], j + 1 < g.blocks);
+          if (!q_sent && !(q_sent = send_queries(true))) break;
         }
         if (!ok) break;
       }
       if (!ok && lane == 0) {
         // Leave no copy in flight behind (bounded waits, as everywhere).
         *abort_flag = 1;
-        for (uint32_t i = n > L::kStages ? n - L::kStages : 0; i < n; ++i) {
-          const int stage = i % L::kStages;
-          if ((raw_last >> stage) & 1)
-            gdn::mbar_wait(&sh.raw[stage], ((raw_parity >> stage) & 1) ^ 1);
-          else
-            gdn::mbar_wait(&sh.full[stage], (i / L::kStages) & 1);
-        }
+        for (uint32_t i = n > 2 * L::kStages ? n - 2 * L::kStages : 0; i < n; i += 2)
+          gdn::mbar_wait(&sh.full[i % L::kStages], (i / L::kStages) & 1);
         if (q_in_flight) gdn::mbar_wait(&sh.q_full, segs & 1);
       }
     } else if (warp < kLoadWarp) {
@@ -698,21 +721,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (gdn::elect_one()) gdn::tc_commit(&sh.done[t]);
       __syncwarp();
       gdn::mbar_wait(&sh.done[t], 0);
-    } else if (warp == kClearWarp) {
-      // ------------------------------ value rows that no row of the item sees
+    } else if (warp == kValueWarp) {
+      // ------------------------------------------------------------- values
       // Slots past the sequence's end or before every window may hold anything,
-      // and 0 * NaN would reach the sum: they become zeros in shared memory.
-      // Their copies complete on `raw`, and this warp completes `full`.
-      uint32_t n = 0, raw_parity = 0;
+      // and 0 * NaN would reach the sum: value rows that no row of the item sees
+      // become zeros in shared memory.  Their tile's copies complete on `raw`, and
+      // this warp completes `full`.
+      TileCopies<D> values(a, &v_map, lane);
+      uint32_t n = 1, raw_parity = 0;  // ring tiles (values are the odd ones); per stage, parity of its next raw copy
       Segment g;
       for (uint32_t segs = 0; ok && next(segs, g); ++segs) {
+        values.begin(g);
         for (int j = 0; j < g.blocks; ++j, n += 2) {
+          const uint32_t stage = n % L::kStages;
           const int key0 = g.key0 + j * kKeys;
-          if (key0 >= g.lo && key0 + kKeys <= g.hi) continue;
-          const uint32_t stage = (n + 1) % L::kStages;  // K, V, K, V, ...
-          if (!wait(&sh.raw[stage], (raw_parity >> stage) & 1)) break;
-          raw_parity ^= 1u << stage;
+          const bool clear = key0 < g.lo || key0 + kKeys > g.hi;
+          uint64_t* bar = clear ? &sh.raw[stage] : &sh.full[stage];
+          if (n >= L::kStages && !wait(&sh.empty[stage], ((n / L::kStages) - 1) & 1)) break;
+          if (lane == 0) gdn::mbar_arrive_expect_tx(bar, values.bytes());
+          __syncwarp();
           uint8_t* dst = ring + stage * L::kTile;
+          values.copy(dst, bar, j + 1 < g.blocks);
+          if (!clear) continue;
+          if (!wait(bar, (raw_parity >> stage) & 1)) break;
+          raw_parity ^= 1u << stage;
           const int from = max(0, g.lo - key0), to = min(kKeys, g.hi - key0);
           for (int i = lane; i < kKeys * D / 8; i += 32) {
             const int row = (i >> 3) & (kKeys - 1);
@@ -723,7 +755,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) gdn::mbar_arrive(&sh.full[stage]);
         }
       }
-      if (!ok) *abort_flag = 1;
+      if (!ok && lane == 0) {
+        *abort_flag = 1;
+        for (uint32_t i = n > 2 * L::kStages ? n - 2 * L::kStages : 1; i < n; i += 2)
+          gdn::mbar_wait(&sh.full[i % L::kStages], (i / L::kStages) & 1);
+      }
     } else {
       // ----------------------------------------------------------- epilogue
       // Reads a segment's O while the softmax warps are on the next one.

@@ -729,31 +729,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       // this warp completes `full`.
       TileCopies<D> values(a, &v_map, lane);
       uint32_t n = 1, raw_parity = 0;  // ring tiles (values are the odd ones); per stage, parity of its next raw copy
+      int pending = -1, from = 0, to = 0;  // stage to be cleared, except rows [from, to)
+      auto clear = [&] {
+        const int at = pending;
+        pending = -1;
+        if (!wait(&sh.raw[at], (raw_parity >> at) & 1)) return;
+        raw_parity ^= 1u << at;
+        uint4* dst = reinterpret_cast<uint4*>(ring + at * L::kTile);
+        for (int i = lane; i < (from + kKeys - to) * 8; i += 32) {
+          const int r = i >> 3, row = r < from ? r : r - from + to;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) dst[(c * kRows + row) * 8 + (i & 7)] = make_uint4(0, 0, 0, 0);
+        }
+        gdn::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) gdn::mbar_arrive(&sh.full[at]);
+      };
       Segment g;
       for (uint32_t segs = 0; ok && next(segs, g); ++segs) {
         values.begin(g);
-        for (int j = 0; j < g.blocks; ++j, n += 2) {
-          const uint32_t stage = n % L::kStages;
+        for (int j = 0; ok && j < g.blocks; ++j, n += 2) {
+          const uint32_t stage = n % L::kStages, parity = ((n / L::kStages) - 1) & 1;
           const int key0 = g.key0 + j * kKeys;
-          const bool clear = key0 < g.lo || key0 + kKeys > g.hi;
-          uint64_t* bar = clear ? &sh.raw[stage] : &sh.full[stage];
-          if (n >= L::kStages && !wait(&sh.empty[stage], ((n / L::kStages) - 1) & 1)) break;
+          const bool partial = key0 < g.lo || key0 + kKeys > g.hi;
+          uint64_t* bar = partial ? &sh.raw[stage] : &sh.full[stage];
+          // A tile that waits to be cleared is cleared behind this tile's copies,
+          // unless there is no room for them yet.
+          if (n >= L::kStages && pending >= 0 && !__all_sync(0xFFFFFFFFu, gdn::mbar_test(&sh.empty[stage], parity))) clear();
+          if (n >= L::kStages && !wait(&sh.empty[stage], parity)) break;
           if (lane == 0) gdn::mbar_arrive_expect_tx(bar, values.bytes());
           __syncwarp();
-          uint8_t* dst = ring + stage * L::kTile;
-          values.copy(dst, bar, j + 1 < g.blocks);
-          if (!clear) continue;
-          if (!wait(bar, (raw_parity >> stage) & 1)) break;
-          raw_parity ^= 1u << stage;
-          const int from = max(0, g.lo - key0), to = min(kKeys, g.hi - key0);
-          for (int i = lane; i < kKeys * D / 8; i += 32) {
-            const int row = (i >> 3) & (kKeys - 1);
-            if (row < from || row >= to) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
-          }
-          gdn::fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) gdn::mbar_arrive(&sh.full[stage]);
+          values.copy(ring + stage * L::kTile, bar, j + 1 < g.blocks);
+          if (pending >= 0) clear();
+          if (partial) pending = stage, from = max(0, g.lo - key0), to = min(kKeys, g.hi - key0);
         }
+        // The last tile of a segment is the one that is partial most often, and the
+        // products are about to wait for it.
+        if (pending >= 0) clear();
       }
       if (!ok && lane == 0) {
         *abort_flag = 1;

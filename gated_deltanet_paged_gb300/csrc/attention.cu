@@ -164,81 +164,6 @@ struct alignas(16) Segment {
   int seq;
 };
 
-// Copies of one K or V tile after the other by a warp: lane i has box i of every
-// tile.  Where its rows lie follows from tile to tile without a division, and
-// their page is asked for a tile ahead.  (The instructions of these warps are
-// rarely in the cache: with a lookup per tile the products waited for keys.)  A
-// tile of more than 32 boxes, from pages of an odd or once even size, is looked
-// up on the spot.
-template <int D>
-struct TileCopies {
-  const AttnArgs& a;
-  const CUtensorMap* map;
-  int lane, boxes, box_rows, step_entries, step_slots;
-  int lo, hi, head, seq;
-  const int32_t* pages;
-  int key0, entry, slot, page;
-
-  __device__ __forceinline__ TileCopies(const AttnArgs& args, const CUtensorMap* m, int l) : a(args), map(m), lane(l) {
-    boxes = kKeys >> a.box_shift;
-    box_rows = 1 << a.box_shift;
-    step_entries = kKeys / a.paged.page_size;
-    step_slots = kKeys % a.paged.page_size;
-  }
-  __device__ __forceinline__ bool visible(int k) const { return k + box_rows > lo && k < hi; }
-  __device__ __forceinline__ int page_of(int e) const {
-    int p = pages[e];
-    if (p < 0 || p >= a.paged.num_pages) {
-      gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_ID, seq);
-      p = a.paged.num_pages;  // outside the map: zeros
-    }
-    return p;
-  }
-  __device__ __forceinline__ void look_ahead() {
-    if (boxes <= 32 && lane < boxes && visible(key0 + lane * box_rows)) page = page_of(entry);
-  }
-  __device__ __forceinline__ void begin(const Segment& g) {
-    lo = g.lo, hi = g.hi, head = g.head, seq = g.seq;
-    pages = a.paged.pages + g.entry;
-    key0 = g.key0;
-    const int key = key0 + lane * box_rows;
-    entry = key / a.paged.page_size;
-    slot = key - entry * a.paged.page_size;
-    look_ahead();
-  }
-  // Bytes of the boxes that hold a visible key; the others are not copied.
-  __device__ __forceinline__ int bytes() const {
-    const int first = max(0, lo - key0) >> a.box_shift;
-    const int last = (min(kKeys, hi - key0) + box_rows - 1) >> a.box_shift;
-    return (last - first) * box_rows * D * 2;
-  }
-  __device__ __forceinline__ void box(uint8_t* dst, uint64_t* bar, int i, int o, int p) const {
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c)
-      gdn::tma_load_4d(dst + c * (kRows * 128) + i * box_rows * 128, map, bar, c * 64, head, o, p);
-  }
-  // The current tile; then on to the next of `more`.
-  __device__ __forceinline__ void copy(uint8_t* dst, uint64_t* bar, bool more) {
-    if (boxes <= 32) {
-      if (lane < boxes && visible(key0 + lane * box_rows)) box(dst, bar, lane, slot, page);
-    } else {
-#pragma unroll 1
-      for (int i = lane; i < boxes; i += 32) {
-        const int k = key0 + i * box_rows;
-        if (!visible(k)) continue;
-        const int e = k / a.paged.page_size;
-        box(dst, bar, i, k - e * a.paged.page_size, page_of(e));
-      }
-    }
-    __syncwarp();
-    key0 += kKeys;
-    entry += step_entries;
-    slot += step_slots;
-    if (slot >= a.paged.page_size) slot -= a.paged.page_size, ++entry;
-    if (more) look_ahead();
-  }
-};
-
 template <int D>
 struct Smem {
   uint64_t full[Layout<D>::kStages];
@@ -560,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLoadWarp) {
       // ------------------------------------ segments, queries and keys
       Walk w = sh.walk;
-      TileCopies<D> keys(a, &k_map, lane);
+      gdn::TileCopies<D, kKeys> keys(a, &k_map, lane);
       uint32_t n = 0, segs = 0;  // ring tiles (keys are the even ones), segments announced
       bool q_in_flight = false;
       for (;; ++segs) {
@@ -593,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (!more) break;
-        keys.begin(g);
+        keys.begin(g.lo, g.hi, g.head, g.seq, g.entry, g.key0);
         // The queries go first where their room is free; else behind the first
         // block's keys, which need none that the segment before holds.
         auto send_queries = [&](bool must) {
@@ -727,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // and 0 * NaN would reach the sum: value rows that no row of the item sees
       // become zeros in shared memory.  Their tile's copies complete on `raw`, and
       // this warp completes `full`.
-      TileCopies<D> values(a, &v_map, lane);
+      gdn::TileCopies<D, kKeys> values(a, &v_map, lane);
       uint32_t n = 1, raw_parity = 0;  // ring tiles (values are the odd ones); per stage, parity of its next raw copy
       int pending = -1, from = 0, to = 0;  // stage to be cleared, except rows [from, to)
       auto clear = [&] {
@@ -747,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       Segment g;
       for (uint32_t segs = 0; ok && next(segs, g); ++segs) {
-        values.begin(g);
+        values.begin(g.lo, g.hi, g.head, g.seq, g.entry, g.key0);
         for (int j = 0; ok && j < g.blocks; ++j, n += 2) {
           const uint32_t stage = n % L::kStages, parity = ((n / L::kStages) - 1) & 1;
           const int key0 = g.key0 + j * kKeys;

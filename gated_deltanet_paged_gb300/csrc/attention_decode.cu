@@ -7,15 +7,15 @@
 // Bound: HBM.  Every key and value is read once, 4 D bytes per (key, head), for
 // 4 D G flops (G query heads per key head), far below the ridge.  What the
 // kernel needs is bytes in flight and equal shares:
-//   - the whole batch is one line of 64-key blocks, (sequence, head) after
+//   - the whole batch is one line of blocks of 8,192 / D keys, (sequence, head) after
 //     (sequence, head), and each CTA takes an equal piece of it, cutting
 //     (sequence, head) items wherever the piece ends.  Every CTA derives its
 //     piece from the page table itself: no planning launch, no host
 //     synchronisation.  A cut item leaves partial results in the workspace, and
 //     a small second kernel joins them in a fixed order.
-//   - a producer warp keeps three 64-key stages of K and V (32 KB each at D =
-//     128) in flight by TMA, page by page; two CTAs per SM.
-//   - four consumer warps take 16 keys of a block each and never wait for one
+//   - two warps keep two blocks of K and V (32 KB each) in flight by TMA, page by
+//     page; two CTAs per SM.
+//   - four consumer warps take a quarter of a block's keys each and never wait for one
 //     another inside an item: mma.sync with the G query heads as the 16 rows
 //     (the matrix work is a tenth of the copy time), private (m, l, o), joined
 //     through shared memory when the item ends.
@@ -26,16 +26,20 @@ namespace {
 using gdn::AttnArgs;
 using gdn::SeqRange;
 
-constexpr int kBlock = 64;    // keys per stage
-constexpr int kStages = 3;
-constexpr int kConsumers = 4;  // warps, 16 keys of a block each
-constexpr int kThreads = (kConsumers + 1) * 32;
+// Keys per stage: 16 KB each of K and V.
+template <int D>
+constexpr int kBlock = 8192 / D;
+// Two stages, so 128 KB on their way per SM: with a third the queues before HBM
+// grow and its rate falls (256 sequences, 8.5 GB: 1.23 ms against 1.17).
+constexpr int kStages = 2;
+constexpr int kConsumers = 4;  // warps, a quarter of a block's keys each
+constexpr int kThreads = (kConsumers + 2) * 32;  // and one warp that copies keys, one that copies values
 constexpr int kRows = 16;     // query heads per pass of an item
 // Fixed cost of an item (its queries, the join of the warps, its stores) in
 // blocks, so that shares of many short items weigh the same as shares of long ones.
 constexpr int kItemCost = 2;
 constexpr int kMinShare = 8;  // blocks below which a cut costs more than it saves
-constexpr int kWholeBlocks = 8;  // longest item that is never cut (see launch)
+constexpr int kWholeKeys = 512;  // longest sequence that is never cut
 
 struct DecodeArgs {
   AttnArgs a;
@@ -54,13 +58,14 @@ struct Item {
   int blocks;
   int cost;        // 0: nothing to do
 };
+template <int D>
 __device__ __forceinline__ Item load_item(const AttnArgs& a, int b) {
   Item it;
   it.s = gdn::seq_range(a.paged, b);
   it.hi = it.s.len;
   it.lo = gdn::key_lo(a, it.s.len - 1);
-  it.first = it.lo / kBlock;
-  it.blocks = (it.hi + kBlock - 1) / kBlock - it.first;
+  it.first = it.lo / kBlock<D>;
+  it.blocks = (it.hi + kBlock<D> - 1) / kBlock<D> - it.first;
   it.cost = it.s.new_tokens ? it.blocks + kItemCost : 0;
   return it;
 }
@@ -75,6 +80,7 @@ struct Walk {
   int blk0, blk1;     // blocks of the item in this segment
   int64_t item0;      // line position of the item
 };
+template <int D>
 __device__ __forceinline__ bool next_segment(const DecodeArgs& d, Walk& w) {
   const int per_seq = d.a.Hkv * d.passes;
   if (d.whole) {
@@ -82,7 +88,7 @@ __device__ __forceinline__ bool next_segment(const DecodeArgs& d, Walk& w) {
       const int id = static_cast<int>(w.pos);
       w.pos += gridDim.x;
       const int b = id / per_seq;
-      if (b != w.b) w.b = b, w.it = load_item(d.a, b);
+      if (b != w.b) w.b = b, w.it = load_item<D>(d.a, b);
       w.head = id - b * per_seq;
       w.blk0 = 0;
       w.blk1 = w.it.blocks;
@@ -94,7 +100,7 @@ __device__ __forceinline__ bool next_segment(const DecodeArgs& d, Walk& w) {
     const int64_t span = static_cast<int64_t>(w.it.cost) * per_seq;
     if (w.pos >= w.base + span) {
       w.base += span;
-      w.it = load_item(d.a, ++w.b);
+      w.it = load_item<D>(d.a, ++w.b);
       continue;
     }
     w.head = gdn::small_quotient(w.pos - w.base, w.it.cost, per_seq);
@@ -110,7 +116,7 @@ __device__ __forceinline__ bool next_segment(const DecodeArgs& d, Walk& w) {
 
 template <int D>
 struct Smem {
-  static constexpr int kTile = kBlock * D * 2;  // one of K, V
+  static constexpr int kTile = kBlock<D> * D * 2;  // one of K, V
   alignas(1024) uint8_t kv[kStages][2][kTile];
   float4 join_o[D / 8][32];  // one warp's partial result, lane by lane
   float4 join_ml[32];        // m, l of its two rows
@@ -161,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      gdn::mbar_init(&sh.full[i], 1);
+      gdn::mbar_init(&sh.full[i], 2);
       gdn::mbar_init(&sh.empty[i], kConsumers);
     }
     sh.abort = 0;
@@ -187,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int b0 = min(tid * per, a.paged.num_seqs), b1 = min(b0 + per, a.paged.num_seqs);
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) {
-      const Item it = load_item(a, b);
+      const Item it = load_item<D>(a, b);
       if (it.s.refused && blockIdx.x == 0) gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_TABLE, b);
       mine += it.cost;
     }
@@ -215,10 +221,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       x.end = end;
       x.base = before * per_seq;
       x.b = b0;
-      x.it = load_item(a, b0);
+      x.it = load_item<D>(a, b0);
       while (start >= x.base + static_cast<int64_t>(x.it.cost) * per_seq) {
         x.base += static_cast<int64_t>(x.it.cost) * per_seq;
-        x.it = load_item(a, ++x.b);
+        x.it = load_item<D>(a, ++x.b);
       }
       sh.walk = x;
     }
@@ -228,67 +234,30 @@ __global__ void __launch_bounds__(kThreads, 2)
     w = sh.walk;
   }
 
-  if (warp == kConsumers) {
-    // ---------------------------------------------------------- producer
+  if (warp >= kConsumers) {
+    // ------------------------------------------------ keys, or values
+    const int kv = warp - kConsumers;
+    gdn::TileCopies<D, kBlock<D>> tiles(a, kv ? &v_map : &k_map, lane);
     int n = 0;  // blocks issued
     bool ok = true;
-    while (ok && next_segment(d, w)) {
-      const int head = w.head / d.passes;
-      for (int blk = w.blk0; ok && blk < w.blk1; ++blk, ++n) {
+    while (ok && next_segment<D>(d, w)) {
+      tiles.begin(w.it.lo, w.it.hi, w.head / d.passes, w.b, w.it.s.entry, (w.it.first + w.blk0) * kBlock<D>);
+      for (int blk = w.blk0; blk < w.blk1; ++blk, ++n) {
         const int stage = n % kStages;
-        const int key0 = (w.it.first + blk) * kBlock;
-        // The copies of this block: only those that hold a visible key.
-        const int first = max(0, w.it.lo - key0) >> a.box_shift;
-        const int last = (min(kBlock, w.it.hi - key0) + (1 << a.box_shift) - 1) >> a.box_shift;
-        int page[2], slot[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int box = lane + 32 * i;
-          page[i] = 0;
-          if (box >= first && box < last) {
-            const int key = key0 + (box << a.box_shift);
-            const int entry = key / a.paged.page_size;
-            slot[i] = key - entry * a.paged.page_size;
-            page[i] = a.paged.pages[w.it.s.entry + entry];
-            if (page[i] < 0 || page[i] >= a.paged.num_pages) {
-              gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_ID, w.b);
-              page[i] = a.paged.num_pages;  // outside the map: zeros
-            }
-          }
-        }
-        if (lane == 0) {
-          if (n >= kStages) ok = gdn::mbar_wait_or_abort(&sh.empty[stage], ((n / kStages) - 1) & 1, &sh.abort);
-          if (ok) gdn::mbar_arrive_expect_tx(&sh.full[stage], ((last - first) << a.box_shift) * D * 4);
-        }
-        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        if (n >= kStages)
+          ok = __all_sync(0xFFFFFFFFu, gdn::mbar_wait_or_abort(&sh.empty[stage], ((n / kStages) - 1) & 1, &sh.abort));
         if (!ok) break;
-        // One copy after the other from one lane, with the addresses passed along: a
-        // copy per lane instead makes each of them a turn of a divergent loop.
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          for (int box = max(first, 32 * i); box < min(last, 32 * i + 32); ++box) {
-            const int p = __shfl_sync(0xFFFFFFFFu, page[i], box & 31), o = __shfl_sync(0xFFFFFFFFu, slot[i], box & 31);
-            if (gdn::elect_one()) {
-              const int at = (box << a.box_shift) * 128;
-#pragma unroll
-              for (int c = 0; c < D / 64; ++c) {
-                gdn::tma_load_4d(sh.kv[stage][0] + c * kBlock * 128 + at, &k_map, &sh.full[stage], c * 64, head, o, p);
-                gdn::tma_load_4d(sh.kv[stage][1] + c * kBlock * 128 + at, &v_map, &sh.full[stage], c * 64, head, o, p);
-              }
-            }
-            __syncwarp();
-          }
-        }
+        if (lane == 0) gdn::mbar_arrive_expect_tx(&sh.full[stage], tiles.bytes());
+        __syncwarp();
+        tiles.copy(sh.kv[stage][kv], &sh.full[stage], blk + 1 < w.blk1);
       }
     }
-    if (!ok) {
+    if (!ok && lane == 0) {
       // Leave no copy in flight behind: the stages that were issued complete by
       // themselves (bounded wait, as everywhere).
-      if (lane == 0) {
-        sh.abort = 1;
-        for (int i = max(0, n - kStages); i < n; ++i) gdn::mbar_wait(&sh.full[i % kStages], (i / kStages) & 1);
-        gdn::record_error(a.paged.err_word, GDN_DEVERR_TIMEOUT, 0);
-      }
+      sh.abort = 1;
+      for (int i = max(0, n - kStages); i < n; ++i) gdn::mbar_wait(&sh.full[i % kStages], (i / kStages) & 1);
+      gdn::record_error(a.paged.err_word, GDN_DEVERR_TIMEOUT, 0);
     }
     return;
   }
@@ -296,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // ------------------------------------------------------------ consumers
   const int g = lane >> 2, t = lane & 3;  // fragment row and column pair
   int n = 0;
-  while (next_segment(d, w)) {
+  while (next_segment<D>(d, w)) {
     const int head = w.head / d.passes, pass = w.head % d.passes;
     const int h0 = head * a.group + pass * kRows;             // first query head of the rows
     const int rows = min(kRows, a.group - pass * kRows);
@@ -329,23 +298,27 @@ __global__ void __launch_bounds__(kThreads, 2)
         sh.abort = 1;
         break;
       }
-      const int key0 = (w.it.first + blk) * kBlock + warp * 16;  // this warp's keys
+      constexpr int kSub = kBlock<D> / 64;  // 16-key groups of this warp
+      const int row0 = warp * 16 * kSub;
+      const int key0 = (w.it.first + blk) * kBlock<D> + row0;  // this warp's keys
       const int lo = w.it.lo - key0, hi = w.it.hi - key0;
-      if (hi > 0 && lo < 16) {
+      if (hi > 0 && lo < 16 * kSub) {
         const uint32_t kt = gdn::smem_u32(sh.kv[stage][0]), vt = gdn::smem_u32(sh.kv[stage][1]);
-        float s[2][4] = {};
+        float s[2 * kSub][4] = {};
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t b[4];
-          const uint32_t r = warp * 16 + (lane >> 4) * 8 + (lane & 7), c = 2 * k + ((lane >> 3) & 1);
-          ldmatrix4(kt + (c >> 3) * (kBlock * 128) + gdn::swz(r, c & 7), b);
-          mma_16816(s[0], q[k], b[0], b[1]);
-          mma_16816(s[1], q[k], b[2], b[3]);
-        }
-        const bool edge = lo > 0 || hi < 16;
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) {
+            uint32_t b[4];
+            const uint32_t r = row0 + 16 * u + (lane >> 4) * 8 + (lane & 7), c = 2 * k + ((lane >> 3) & 1);
+            ldmatrix4(kt + (c >> 3) * (kBlock<D> * 128) + gdn::swz(r, c & 7), b);
+            mma_16816(s[2 * u], q[k], b[0], b[1]);
+            mma_16816(s[2 * u + 1], q[k], b[2], b[3]);
+          }
+        const bool edge = lo > 0 || hi < 16 * kSub;
         float top[2] = {m[0], m[1]};
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2 * kSub; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float x = s[j][i] * a.scale_log2;
@@ -377,34 +350,37 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
         // Weights: fp32 into the sum, bf16 (as the values are) into the product.
-        uint32_t p[4];
+        uint32_t p[kSub][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 2 * kSub; ++j) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             // A row that has seen nothing yet keeps m = -inf; its weights are 0.
             s[j][i] = s[j][i] == -INFINITY ? 0.f : gdn::exp2_approx(s[j][i] - m[i >> 1]);
             l[i >> 1] += s[j][i];
           }
-          p[2 * j] = gdn::pack_bf162(s[j][0], s[j][1]);
-          p[2 * j + 1] = gdn::pack_bf162(s[j][2], s[j][3]);
+          p[j >> 1][2 * (j & 1)] = gdn::pack_bf162(s[j][0], s[j][1]);
+          p[j >> 1][2 * (j & 1) + 1] = gdn::pack_bf162(s[j][2], s[j][3]);
         }
-        // Values of keys outside [lo, hi) are cleared: 0 * NaN would reach the sum.
-        uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-        if (edge) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int key = 2 * t + 8 * i;
-            keep[i] = ((key >= lo && key < hi) ? 0x0000FFFFu : 0u) | ((key + 1 >= lo && key + 1 < hi) ? 0xFFFF0000u : 0u);
+        for (int u = 0; u < kSub; ++u) {
+          // Values of keys outside [lo, hi) are cleared: 0 * NaN would reach the sum.
+          uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int key = 16 * u + 2 * t + 8 * i;
+              keep[i] = ((key >= lo && key < hi) ? 0x0000FFFFu : 0u) | ((key + 1 >= lo && key + 1 < hi) ? 0xFFFF0000u : 0u);
+            }
           }
-        }
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t b[4];
-          const uint32_t r = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), c = 2 * k + (lane >> 4);
-          ldmatrix4_trans(vt + (c >> 3) * (kBlock * 128) + gdn::swz(r, c & 7), b);
-          mma_16816(o[2 * k], p, b[0] & keep[0], b[1] & keep[1]);
-          mma_16816(o[2 * k + 1], p, b[2] & keep[0], b[3] & keep[1]);
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t b[4];
+            const uint32_t r = row0 + 16 * u + ((lane >> 3) & 1) * 8 + (lane & 7), c = 2 * k + (lane >> 4);
+            ldmatrix4_trans(vt + (c >> 3) * (kBlock<D> * 128) + gdn::swz(r, c & 7), b);
+            mma_16816(o[2 * k], p[u], b[0] & keep[0], b[1] & keep[1]);
+            mma_16816(o[2 * k + 1], p[u], b[2] & keep[0], b[3] & keep[1]);
+          }
         }
       }
       __syncwarp();
@@ -521,7 +497,7 @@ constexpr int kMaxGrid = 2 * 160;  // two CTAs per SM
 // Where even the longest sequence is a few blocks, one CTA takes a whole item: the
 // scan of the batch and the join's launch would cost more than the blocks.
 bool whole_items(int32_t num_seqs, int32_t num_entries, int32_t page_size) {
-  return gdn_host::longest_sequence(num_seqs, num_entries, page_size) <= kWholeBlocks * kBlock;
+  return gdn_host::longest_sequence(num_seqs, num_entries, page_size) <= kWholeKeys;
 }
 size_t workspace_bytes_of(int D, bool whole) {
   if (whole) return 0;
@@ -569,7 +545,7 @@ extern "C" int gdn_attention_decode_paged(const gdn_bf16* q, int64_t q_token_str
   d.whole = cache && table && whole_items(n, table->num_entries, cache->page_size);
   const size_t need = cache ? workspace_bytes_of(cache->head_dim, d.whole) : 0;
   int rc = gdn_host::attention_args(&d.a, q, q_token_stride, o, lse, nullptr, n, Hq, cache, table, scale, options,
-                                    workspace, workspace_bytes, need, err_word, kBlock);
+                                    workspace, workspace_bytes, need, err_word, cache && cache->head_dim == 64 ? kBlock<64> : kBlock<128>);
   if (rc != GDN_OK || n == 0) return rc;
   int sms = 0;
   rc = gdn_host::check_device(&sms);

@@ -46,6 +46,7 @@ constexpr int kSegments = 4;  // segments announced ahead
 // Fixed cost of an item (queries, pipeline fill, epilogue) in keys.
 constexpr int kItemCost = 2 * kKeys;
 constexpr int kMinShare = 4 * kKeys;  // keys below which a cut costs more than it saves
+constexpr int kMinBlocks = 2;         // blocks of a piece, where items are cut evenly
 constexpr int kMaxGrid = 160;         // one CTA per SM
 
 struct ChunkArgs {
@@ -106,6 +107,7 @@ struct Walk {
   int64_t pos, end;  // line positions
   int64_t item0;     // of the current item
   int b, pair, head, cost;
+  int last;          // CTA that takes the end of the item; -1: as the line is shared out
   Seq s;
   // The current segment:
   int lo, hi;        // keys that the item's rows see between them
@@ -148,6 +150,30 @@ struct Layout {
   static constexpr int kBytes = (2 + kStages) * kTile;
   static constexpr uint32_t kColS = 0, kColO = 256;    // TMEM columns: S of both tiles, O of both tiles
 };
+
+// Sum over the CTA's threads before this one, and over all.
+template <typename T>
+__device__ __forceinline__ T scan_block(int64_t* scratch64, T mine, T* total) {
+  T* const scratch = reinterpret_cast<T*>(scratch64);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) scratch[warp] = incl;
+  __syncthreads();
+  T before = incl - mine, sum = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) before += scratch[i];
+    sum += scratch[i];
+  }
+  __syncthreads();
+  *total = sum;
+  return before;
+}
 
 // One segment of the CTA's share, as the copying warp announces it to the others.
 struct alignas(16) Segment {
@@ -401,63 +427,102 @@ __global__ void __launch_bounds__(kThreads, 1)
   gdn::pdl_wait();
   gdn::pdl_launch_dependents();
 
-  // ---- this CTA's share of the line ----
+  // ---- this CTA's share ----
   gdn::Shares<7> shares(0, 1, 1);
   bool idle;
   {
+    const int c = blockIdx.x, grid = gridDim.x;
     const int per = (a.paged.num_seqs + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, a.paged.num_seqs), b1 = min(b0 + per, a.paged.num_seqs);
-    int64_t mine = 0, cost = 0;
     Seq s = {};
+    int pairs = 0;
     for (int b = b0; b < b1; ++b) {
       s = load_seq(d, b);
-      if (s.refused && blockIdx.x == 0) gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_TABLE, b);
-      cost = seq_cost(d, s);
-      mine += cost;
+      if (s.refused && c == 0) gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_TABLE, b);
+      pairs = min(pairs + s.pairs, kMaxGrid + 1);  // no more are told apart
     }
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    if (lane == 31) sh.scan[warp] = incl;
-    __syncthreads();
-    int64_t before = incl - mine, total = 0;
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) before += sh.scan[i];
-      total += sh.scan[i];
-    }
-    total *= a.Hkv;
-    // Whole items need no smallest piece: every one can have a CTA to itself.
-    shares = gdn::Shares<7>(total, total / (d.whole ? kItemCost : kMinShare), gridDim.x);
-    const int c = blockIdx.x;
-    const int64_t start = shares.start(c), end = shares.start(c + 1);
-    idle = start >= end;
-    // The thread whose sequences hold `start` sets up the walk.
-    if (!idle && before * a.Hkv <= start && start < (before + mine) * a.Hkv) {
-      Walk x;
-      x.pos = start;
-      x.end = end;
-      x.b = b0;
-      int64_t base = before * a.Hkv;
-      x.s = s;  // one sequence per thread, unless there are more than threads
-      for (; per > 1; ++x.b) {
-        x.s = load_seq(d, x.b);
-        cost = seq_cost(d, x.s);
-        if (start < base + cost * a.Hkv) break;
-        base += cost * a.Hkv;
+    int all_pairs;
+    const int pairs_before = scan_block(sh.scan, pairs, &all_pairs);
+    const int64_t all_items = static_cast<int64_t>(all_pairs) * a.Hkv;
+    if (all_items <= min(grid, kMaxGrid)) {
+      // Few items: each gets CTAs to itself, by its length, and they cut it evenly.
+      // Cutting the line instead gives many a CTA the end of one item and the start
+      // of the next, and an item's fixed cost twice (452 tokens over 2,500: the
+      // CTAs end between 10.6 and 17 us, aligned between 10 and 12).
+      int2* table = reinterpret_cast<int2*>(tiles + 2 * L::kTile);  // pairs; the ring is not in use yet
+      int at = pairs_before;
+      for (int b = b0; b < b1; ++b) {
+        if (per > 1) s = load_seq(d, b);
+        for (int i = 0; i < s.pairs; ++i) table[at++] = make_int2(b, i);
       }
-      int i = 0;  // the last pair that begins at or before start
-      for (int step = x.s.pairs > 1 ? 1 << (31 - __clz(x.s.pairs - 1)) : 0; step; step >>= 1)
-        if (step < x.s.pairs - i && cost_before(d, x.s, i + step) * a.Hkv <= start - base) i += step;
-      x.pair = i;
-      x.cost = pair_cost(d, x.s, i);
-      base += cost_before(d, x.s, i) * a.Hkv;
-      x.head = gdn::small_quotient(start - base, x.cost, a.Hkv);
-      x.item0 = base + static_cast<int64_t>(x.head) * x.cost;
-      if (d.whole && start > x.item0) x.pos = x.item0 + x.cost;
-      sh.walk = x;
+      __syncthreads();
+      Walk x = {};
+      int blocks = 0;
+      const int items = static_cast<int>(all_items);
+      if (tid < items) {
+        const int2 pair = table[tid / a.Hkv];
+        x.b = pair.x, x.pair = pair.y, x.head = tid % a.Hkv;
+        x.s = load_seq(d, x.b);
+        x.cost = pair_cost(d, x.s, x.pair);
+        blocks = (pair_hi(d, x.s, x.pair) + kKeys - 1) / kKeys - pair_lo(d, x.s, x.pair) / kKeys;
+      }
+      int sum, pieces_total;
+      scan_block(sh.scan, x.cost >> 7, &sum);
+      int pieces = tid < items ? 1 : 0;
+      if (tid < items && !d.whole) {
+        pieces += static_cast<int>(__fdividef(static_cast<float>(grid - items) * static_cast<float>(x.cost >> 7),
+                                              static_cast<float>(sum)));
+        pieces = min(pieces, max(1, blocks / kMinBlocks));
+      }
+      const int piece = c - scan_block(sh.scan, pieces, &pieces_total);
+      idle = c >= pieces_total;
+      if (piece >= 0 && piece < pieces) {
+        // As a walk along a line on which the item begins at 0.
+        const int blk0 = blocks * piece / pieces, blk1 = blocks * (piece + 1) / pieces;
+        x.pos = blk0 ? kItemCost + static_cast<int64_t>(blk0) * kKeys : 0;
+        x.end = blk1 < blocks ? kItemCost + static_cast<int64_t>(blk1) * kKeys : x.cost;
+        x.last = c - piece + pieces - 1;
+        sh.walk = x;
+      }
+    } else {
+      int64_t cost = 0, mine = 0, total;
+      for (int b = b0; b < b1; ++b) {
+        if (per > 1) s = load_seq(d, b);
+        cost = seq_cost(d, s);
+        mine += cost;
+      }
+      const int64_t before = scan_block(sh.scan, mine, &total);
+      total *= a.Hkv;
+      // Whole items need no smallest piece: every one can have a CTA to itself.
+      shares = gdn::Shares<7>(total, total / (d.whole ? kItemCost : kMinShare), grid);
+      const int64_t start = shares.start(c), end = shares.start(c + 1);
+      idle = start >= end;
+      // The thread whose sequences hold `start` sets up the walk.
+      if (!idle && before * a.Hkv <= start && start < (before + mine) * a.Hkv) {
+        Walk x;
+        x.pos = start;
+        x.end = end;
+        x.last = -1;
+        x.b = b0;
+        int64_t base = before * a.Hkv;
+        x.s = s;  // one sequence per thread, unless there are more than threads
+        for (; per > 1; ++x.b) {
+          x.s = load_seq(d, x.b);
+          cost = seq_cost(d, x.s);
+          if (start < base + cost * a.Hkv) break;
+          base += cost * a.Hkv;
+        }
+        int i = 0;  // the last pair that begins at or before start
+        for (int step = x.s.pairs > 1 ? 1 << (31 - __clz(x.s.pairs - 1)) : 0; step; step >>= 1)
+          if (step < x.s.pairs - i && cost_before(d, x.s, i + step) * a.Hkv <= start - base) i += step;
+        x.pair = i;
+        x.cost = pair_cost(d, x.s, i);
+        base += cost_before(d, x.s, i) * a.Hkv;
+        x.head = gdn::small_quotient(start - base, x.cost, a.Hkv);
+        x.item0 = base + static_cast<int64_t>(x.head) * x.cost;
+        if (d.whole && start > x.item0) x.pos = x.item0 + x.cost;
+        sh.walk = x;
+      }
     }
     if (tid == 0 && !d.whole) d.cuts[c] = make_int4(-1, 0, 0, 0);
   }
@@ -510,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           g.entry = w.s.entry;
           g.seq = w.b;
           if (lane == 0 && starts && !ends)
-            d.cuts[blockIdx.x] = make_int4(g.first_token, g.tokens, g.head, shares.owner(w.item0 + w.cost - 1));
+            d.cuts[blockIdx.x] = make_int4(g.first_token, g.tokens, g.head, w.last >= 0 ? w.last : shares.owner(w.item0 + w.cost - 1));
         }
         if (lane == 0) {
           sh.seg[segs % kSegments] = g;
@@ -936,66 +1001,86 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partial results of the items that CTAs of the kernel above cut: the
-// item that CTA c = blockIdx.x started and did not end has slot 1 of c, then slot
-// 0 of every CTA up to the one that ended it.  blockIdx.y: 32 rows and half of
-// the dimensions; a thread takes one row and D / 64 groups of four dimensions.
-// Latency-bound: the parts are added in a fixed order, four of them in flight.
+// item that CTA c started and did not end has slot 1 of c, then slot 0 of every
+// CTA up to the one that ended it.  Four blocks per SM share the cut items out
+// between them, in slices of 32 rows and half of the dimensions (a block for every
+// CTA and slice took 4 us to launch, most of them to find nothing); a thread takes
+// one row and D / 64 groups of four dimensions.  Latency-bound: the parts are added
+// in a fixed order, four of them in flight.
 constexpr int kJoinSlices = 16;
+constexpr int kJoinThreads = 256;
+static_assert(kMaxGrid <= kJoinThreads, "one thread per record");
 template <int D>
-__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkArgs d) {
+__global__ void __launch_bounds__(kJoinThreads, 4) chunk_join_kernel(const __grid_constant__ ChunkArgs d, int ctas) {
+  __shared__ int4 cuts[kMaxGrid];
+  __shared__ int owners[kMaxGrid];
+  __shared__ int count[kJoinThreads / 32];
   gdn::pdl_wait();
   gdn::pdl_launch_dependents();
-  const int c = blockIdx.x;
-  const int4 cut = d.cuts[c];
-  if (cut.x < 0) return;
   const AttnArgs& a = d.a;
-  const int t = blockIdx.y >> 3, row = (blockIdx.y & 3) * 32 + (threadIdx.x & 31);
-  const int in_tile = row / a.group;
-  const int token = t * d.tile_tokens + in_tile;
-  if (in_tile >= d.tile_tokens || token >= cut.y) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int4 mine = tid < ctas ? d.cuts[tid] : make_int4(-1, 0, 0, 0);
+  const unsigned found = __ballot_sync(0xFFFFFFFFu, mine.x >= 0);
+  if (lane == 0) count[warp] = __popc(found);
+  __syncthreads();
+  int at = __popc(found & ((1u << lane) - 1)), total = 0;
+  for (int i = 0; i < kJoinThreads / 32; ++i) {
+    if (i < warp) at += count[i];
+    total += count[i];
+  }
+  if (mine.x >= 0) cuts[at] = mine, owners[at] = tid;
+  __syncthreads();
   constexpr int kG = D / 64;  // groups of four dimensions per thread
   constexpr int kParts = 4;
-  const int group0 = (threadIdx.x >> 5) + 8 * kG * ((blockIdx.y >> 2) & 1);
-  float m = -INFINITY, l = 0.f;
-  float4 o[kG];
+  for (int job = blockIdx.x; job < total * kJoinSlices; job += gridDim.x) {
+    const int4 cut = cuts[job / kJoinSlices];
+    const int c = owners[job / kJoinSlices], slice = job % kJoinSlices;
+    const int t = slice >> 3, row = (slice & 3) * 32 + lane;
+    const int in_tile = row / a.group;
+    const int token = t * d.tile_tokens + in_tile;
+    if (in_tile >= d.tile_tokens || token >= cut.y) continue;
+    const int group0 = warp + 8 * kG * ((slice >> 2) & 1);
+    float m = -INFINITY, l = 0.f;
+    float4 o[kG];
 #pragma unroll
-  for (int k = 0; k < kG; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = c; i0 <= cut.w; i0 += kParts) {
-    float2 ml[kParts];
-    float4 x[kParts][kG];
+    for (int k = 0; k < kG; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = c; i0 <= cut.w; i0 += kParts) {
+      float2 ml[kParts];
+      float4 x[kParts][kG];
 #pragma unroll
-    for (int p = 0; p < kParts; ++p) {
-      ml[p] = make_float2(-INFINITY, 0.f);
-      const int i = i0 + p;
-      if (i > cut.w) continue;
-      const int64_t slot = (2 * static_cast<int64_t>(i) + (i == c ? 1 : 0)) * 2 + t;
-      ml[p] = d.part_ml[slot * kRows + row];
+      for (int p = 0; p < kParts; ++p) {
+        ml[p] = make_float2(-INFINITY, 0.f);
+        const int i = i0 + p;
+        if (i > cut.w) continue;
+        const int64_t slot = (2 * static_cast<int64_t>(i) + (i == c ? 1 : 0)) * 2 + t;
+        ml[p] = d.part_ml[slot * kRows + row];
 #pragma unroll
-      for (int k = 0; k < kG; ++k) x[p][k] = d.part_o[(slot * (D / 4) + group0 + 8 * k) * kRows + row];
-    }
+        for (int k = 0; k < kG; ++k) x[p][k] = d.part_o[(slot * (D / 4) + group0 + 8 * k) * kRows + row];
+      }
 #pragma unroll
-    for (int p = 0; p < kParts; ++p) {
-      if (ml[p].x == -INFINITY) continue;  // no part, or one in which the row saw no key
-      const float top = fmaxf(m, ml[p].x);
-      const float f = gdn::exp2_approx(m - top), g = gdn::exp2_approx(ml[p].x - top);
-      m = top;
-      l = l * f + ml[p].y * g;
+      for (int p = 0; p < kParts; ++p) {
+        if (ml[p].x == -INFINITY) continue;  // no part, or one in which the row saw no key
+        const float top = fmaxf(m, ml[p].x);
+        const float f = gdn::exp2_approx(m - top), g = gdn::exp2_approx(ml[p].x - top);
+        m = top;
+        l = l * f + ml[p].y * g;
 #pragma unroll
-      for (int k = 0; k < kG; ++k) {
-        o[k].x = o[k].x * f + x[p][k].x * g;
-        o[k].y = o[k].y * f + x[p][k].y * g;
-        o[k].z = o[k].z * f + x[p][k].z * g;
-        o[k].w = o[k].w * f + x[p][k].w * g;
+        for (int k = 0; k < kG; ++k) {
+          o[k].x = o[k].x * f + x[p][k].x * g;
+          o[k].y = o[k].y * f + x[p][k].y * g;
+          o[k].z = o[k].z * f + x[p][k].z * g;
+          o[k].w = o[k].w * f + x[p][k].w * g;
+        }
       }
     }
-  }
-  const float inv = 1.f / l;
-  const int64_t out = (static_cast<int64_t>(cut.x) + token) * a.Hq + cut.z * a.group + row % a.group;
+    const float inv = 1.f / l;
+    const int64_t out = (static_cast<int64_t>(cut.x) + token) * a.Hq + cut.z * a.group + row % a.group;
 #pragma unroll
-  for (int k = 0; k < kG; ++k)
-    reinterpret_cast<uint2*>(a.o + out * D)[group0 + 8 * k] =
-        make_uint2(gdn::pack_bf162(o[k].x * inv, o[k].y * inv), gdn::pack_bf162(o[k].z * inv, o[k].w * inv));
-  if (a.lse && group0 == 0) a.lse[out] = (m + log2f(l)) / gdn::kLog2e;
+    for (int k = 0; k < kG; ++k)
+      reinterpret_cast<uint2*>(a.o + out * D)[group0 + 8 * k] =
+          make_uint2(gdn::pack_bf162(o[k].x * inv, o[k].y * inv), gdn::pack_bf162(o[k].z * inv, o[k].w * inv));
+    if (a.lse && group0 == 0) a.lse[out] = (m + log2f(l)) / gdn::kLog2e;
+  }
 }
 
 constexpr int kWholeKeys = 8 * kKeys;  // longest sequence whose items are never cut
@@ -1032,7 +1117,7 @@ int launch(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache* cache, void* w
   rc = gdn_host::launch_pdl(chunk_attention_kernel<D, kScores>, dim3(grid), dim3(kThreads), smem, stream, d, q_map, k_map,
                             v_map);
   if (rc != GDN_OK || d.whole) return rc;
-  return gdn_host::launch_pdl(chunk_join_kernel<D>, dim3(grid, kJoinSlices), dim3(256), 0, stream, d);
+  return gdn_host::launch_pdl(chunk_join_kernel<D>, dim3(4 * grid), dim3(kJoinThreads), 0, stream, d, grid);
 }
 
 }  // namespace

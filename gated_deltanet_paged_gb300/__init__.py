@@ -1,9 +1,11 @@
 """Paged Gated Delta-Rule (GDN) prefill and decode for GB300 (sm_103a), and the
 attention layer that runs over the same page table.
 
-Thin ctypes binding over the C ABI in ``include/gdn_paged.h``: each function
-checks tensor dtypes / devices, passes ``data_ptr()`` values and the current
-CUDA stream, and raises on a non-zero status.  Every step of the computation
+Thin binding over the C ABI in ``include/gdn_paged.h``: each function checks
+tensor dtypes / devices, passes ``data_ptr()`` values and the current CUDA
+stream, and raises on a non-zero status.  The recurrent layer's calls go through
+ctypes, the attention layer's through a small extension module
+(csrc/binding.cpp).  Every step of the computation
 runs in the CUDA library ``libgdn_paged.so``; there is no fallback path, and
 calling any of these functions without the library (or without an sm_103a GPU)
 raises.
@@ -13,9 +15,8 @@ Source: "flashinfer.gdn_paged" (docs.flashinfer.ai/api/gdn_paged.html).
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib
 import os
-import struct
 import threading
 
 import torch
@@ -62,13 +63,6 @@ class _PrefillSlots(ctypes.Structure):
 
 class _DecodeSlots(ctypes.Structure):
     _fields_ = [("initial_state_indices", ctypes.c_void_p), ("output_state_indices", ctypes.c_void_p)]
-
-
-# gdn_kv_cache, gdn_page_table and gdn_attention_options of the C header in native
-# layout, packed into bytes (a ctypes.Structure takes a microsecond to fill).
-_KV_CACHE = struct.Struct("@PPiiiiqqq")
-_PAGE_TABLE = struct.Struct("@PiPPi4x")
-_ATTENTION_OPTIONS = struct.Struct("@f4xPi4xP")
 
 
 def library():
@@ -425,94 +419,17 @@ def gdn_pool_zero_rows(pool, rows, err_word=None):
 # ---------------------------------------------------------------------------
 # The attention layer: rotary positions, the paged key / value cache, attention
 # ---------------------------------------------------------------------------
-# A call of these at decode sizes lasts a few microseconds on the GPU, so the
-# checks read each property of a tensor once (get_device() is -1 off the GPU) and
-# leave the wording of an error to the slow path.
-def _heads_arg(t, name, dev, D=None):
-    """A bf16 [T, H, D] tensor with dense heads on CUDA device ``dev``; the token
-    stride may be padded (a slice of a fused projection).  Returns (T, H, D,
-    token stride)."""
-    if t is None:
-        raise ValueError("%s is required" % name)
-    if t.dtype is not torch.bfloat16:
-        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
-    if t.get_device() != dev or dev < 0:
-        raise ValueError("%s must be a CUDA tensor on the call's device" % name)
-    shape = t.shape
-    if len(shape) != 3:
-        raise ValueError("%s must have 3 dims" % name)
-    T, H, d = shape
-    s0, s1, s2 = t.stride()
-    if (d > 1 and s2 != 1) or (H > 1 and s1 != d) or (T > 1 and s0 < H * d):
-        raise ValueError("%s must be [T, H, D] with dense heads" % name)
-    if D is not None and d != D:
-        raise ValueError("%s must have %d dimensions per head, got %d" % (name, D, d))
-    return T, H, d, s0 if T > 1 else H * d
+_calls = None
 
 
-def _vector(t, dtype, name, dev):
-    """The length of a contiguous 1-d tensor on CUDA device ``dev``."""
-    if t is None or t.dtype is not dtype or t.get_device() != dev or t.stride() != (1,):
-        _need(t, dtype, name, 1)
-        if t.get_device() != dev:
-            raise ValueError("%s must be on the call's device" % name)
-    return t.shape[0]
-
-
-def _kv_cache_arg(k_cache, v_cache, dev):
-    """(gdn_kv_cache bytes, Hkv, D, page size)."""
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype is not torch.bfloat16:
-            raise TypeError("%s must be %s, got %s" % (n, torch.bfloat16, t.dtype))
-        if t.get_device() != dev:
-            raise ValueError("%s must be a CUDA tensor on the call's device" % n)
-    shape, strides = k_cache.shape, k_cache.stride()
-    if len(shape) != 4 or (shape[3] > 1 and strides[3] != 1):
-        raise ValueError("k_cache must be [num_pages, page_size, Hkv, D] with dense D")
-    if v_cache.shape != shape or v_cache.stride() != strides:
-        raise ValueError("k_cache and v_cache must have the same shape and strides")
-    pages, ps, h, d = shape
-    return _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), pages, ps, h, d, *strides[:3]), h, d, ps
-
-
-def _page_table_arg(page_indices, page_indptr, last_page_len, cu_seqlens, T, dev):
-    """(gdn_page_table bytes, num_seqs, num_entries), checked against T new tokens."""
-    i32 = torch.int32
-    n = _vector(page_indices, i32, "page_indices", dev)
-    S = _vector(last_page_len, i32, "last_page_len", dev)
-    if _vector(page_indptr, i32, "page_indptr", dev) != S + 1:
-        raise ValueError("page_indptr must hold one entry more than last_page_len")
-    if cu_seqlens is None:
-        if T != S:
-            raise ValueError("without cu_seqlens every sequence has one new token: got %d tokens, %d sequences" % (T, S))
-    elif _vector(cu_seqlens, i32, "cu_seqlens", dev) != S + 1:
-        raise ValueError("cu_seqlens must hold one entry more than last_page_len")
-    return _PAGE_TABLE.pack(page_indices.data_ptr(), n, page_indptr.data_ptr(), last_page_len.data_ptr(), S), S, n
-
-
-def _frequencies_arg(frequencies, D, dev):
-    """rotary_dim of an int64 frequency tensor (None: 0)."""
-    if frequencies is None:
-        return 0
-    n = _vector(frequencies, torch.int64, "frequencies", dev)
-    if not 0 < 2 * n <= D:
-        raise ValueError("frequencies must hold between 1 and D / 2 entries")
-    return 2 * n
-
-
-def _out_arg(t, like, T, H, D, name, dev):
-    """A dense bf16 [T, H, D] output: the caller's, or a new one."""
-    if t is None:
-        if like.is_contiguous():
-            return torch.empty_like(like)
-        return torch.empty((T, H, D), dtype=torch.bfloat16, device=like.device)
-    if _need(t, torch.bfloat16, name, 3).shape != (T, H, D) or t.get_device() != dev:
-        raise ValueError("%s must be [%d, %d, %d] on the call's device" % (name, T, H, D))
-    return t
-
-
-def _err_arg(err_word, dev):
-    return None if err_word is None or _vector(err_word, torch.int32, "err_word", dev) < 1 else err_word.data_ptr()
+def _load_calls():
+    """The module _attention (csrc/binding.cpp), which links to libgdn_paged.so."""
+    global _calls
+    library()  # builds both where the sources are newer
+    module = importlib.import_module(__name__ + "._attention")
+    module.set_error(GdnError)
+    _calls = module
+    return module
 
 
 def gdn_rope_frequencies(rotary_dim, base=10000.0, *, factor=1.0, original_len=0, low_turns=1.0, high_turns=32.0,
@@ -535,24 +452,7 @@ def gdn_rope(x, frequencies, positions, *, interleaved=False, inverse=False, amp
     frequencies, and scaled by ``amplitude``; pairs are (i, i + rotary_dim / 2),
     or (2 i, 2 i + 1) with ``interleaved``.  ``inverse`` applies the transposed
     map (the gradient's).  ``out`` may be x itself."""
-    dev = x.get_device()
-    T, H, D, xs = _heads_arg(x, "x", dev)
-    rotary = _frequencies_arg(frequencies, D, dev)
-    if rotary == 0:
-        raise ValueError("frequencies is required")
-    if _vector(positions, torch.int32, "positions", dev) != T:
-        raise ValueError("positions must hold one entry per token")
-    if out is None:
-        out = _out_arg(None, x, T, H, D, "out", dev)
-        ys = H * D
-    else:
-        To, Ho, _, ys = _heads_arg(out, "out", dev, D)
-        if (To, Ho) != (T, H):
-            raise ValueError("out must have the shape of x")
-    _check("gdn_rope", (_lib or library()).gdn_rope(
-        x.data_ptr(), xs, out.data_ptr(), ys, positions.data_ptr(), frequencies.data_ptr(), T, H, D, rotary,
-        1 if interleaved else 0, 1 if inverse else 0, amplitude, _raw_stream(dev)))
-    return out
+    return (_calls or _load_calls()).rope(x, frequencies, positions, interleaved, inverse, amplitude, out)
 
 
 def gdn_kv_append_paged(k, v, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, *, q=None,
@@ -562,76 +462,18 @@ def gdn_kv_append_paged(k, v, k_cache, v_cache, cu_seqlens, page_indices, page_i
     their positions on the way, and rotate the queries q (bf16 [T, Hq, D]) along.
     ``cu_seqlens`` None: one new token per sequence.  Returns the rotated queries
     (None without q); the caches are updated in place."""
-    dev = k.get_device()
-    cache, Hkv, D, _ = _kv_cache_arg(k_cache, v_cache, dev)
-    T, Hk, _, ks = _heads_arg(k, "k", dev, D)
-    Tv, Hv, _, vs = _heads_arg(v, "v", dev, D)
-    if Tv != T or Hk != Hkv or Hv != Hkv:
-        raise ValueError("k and v must be [T, Hkv, D]")
-    table, _, _ = _page_table_arg(page_indices, page_indptr, last_page_len, cu_seqlens, T, dev)
-    rotary = _frequencies_arg(frequencies, D, dev)
-    qs = Hq = 0
-    if q is not None:
-        Tq, Hq, _, qs = _heads_arg(q, "q", dev, D)
-        if Tq != T:
-            raise ValueError("q must hold as many tokens as k")
-        q_out = _out_arg(q_out, q, T, Hq, D, "q_out", dev)
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    _check("gdn_kv_append_paged", (_lib or library()).gdn_kv_append_paged(
-        _ptr(q), qs, _ptr(q_out), k.data_ptr(), ks, v.data_ptr(), vs, _ptr(cu_seqlens), T, Hq, cache, table,
-        _ptr(frequencies), rotary, 1 if interleaved else 0, amplitude, _err_arg(err_word, dev), _raw_stream(dev)))
-    return q_out
+    return (_calls or _load_calls()).kv_append(k, v, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, q,
+                                          frequencies, interleaved, amplitude, q_out, err_word)
 
 
-@functools.lru_cache(maxsize=1024)
 def gdn_attention_workspace_bytes(num_seqs: int, total_tokens: int, Hq: int, Hkv: int, D: int, num_entries: int,
                                   page_size: int) -> int:
     return int(library().gdn_attention_workspace_bytes(num_seqs, total_tokens, Hq, Hkv, D, num_entries, page_size))
 
 
-@functools.lru_cache(maxsize=1024)
 def gdn_attention_decode_workspace_bytes(num_seqs: int, Hq: int, Hkv: int, D: int, num_entries: int,
                                          page_size: int) -> int:
     return int(library().gdn_attention_decode_workspace_bytes(num_seqs, Hq, Hkv, D, num_entries, page_size))
-
-
-def _attention(decode, q, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, scale, softcap, window,
-               slopes, full_lens, o, lse, return_lse, err_word, workspace):
-    dev = q.get_device()
-    cache, Hkv, D, page_size = _kv_cache_arg(k_cache, v_cache, dev)
-    T, Hq, _, qs = _heads_arg(q, "q", dev, D)
-    table, S, entries = _page_table_arg(page_indices, page_indptr, last_page_len, cu_seqlens, T, dev)
-    window = -1 if window is None else int(window)
-    options = None
-    if softcap or window >= 0 or slopes is not None or full_lens is not None:
-        if slopes is not None and _vector(slopes, torch.float32, "slopes", dev) != Hq:
-            raise ValueError("slopes must hold one entry per query head")
-        if full_lens is not None and _vector(full_lens, torch.int32, "full_lens", dev) != S:
-            raise ValueError("full_lens must hold one entry per sequence")
-        options = _ATTENTION_OPTIONS.pack(softcap, _ptr(slopes) or 0, window, _ptr(full_lens) or 0)
-    o = _out_arg(o, q, T, Hq, D, "o", dev)
-    if lse is not None:
-        if _need(lse, torch.float32, "lse", 2).shape != (T, Hq) or lse.get_device() != dev:
-            raise ValueError("lse must be [T, Hq] on the call's device")
-    elif return_lse:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    need = (gdn_attention_decode_workspace_bytes(S, Hq, Hkv, D, entries, page_size) if decode
-            else gdn_attention_workspace_bytes(S, T, Hq, Hkv, D, entries, page_size))
-    if workspace is None:
-        if need:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
-    elif _vector(workspace, torch.uint8, "workspace", dev) < need:
-        raise ValueError("workspace holds %d bytes, the call needs %d" % (workspace.numel(), need))
-    tail = (cache, table, scale, options, _ptr(workspace), need, _err_arg(err_word, dev), _raw_stream(dev))
-    lib = _lib or library()
-    if decode:
-        _check("gdn_attention_decode_paged", lib.gdn_attention_decode_paged(
-            q.data_ptr(), qs, o.data_ptr(), _ptr(lse), Hq, *tail))
-    else:
-        _check("gdn_attention_paged", lib.gdn_attention_paged(
-            q.data_ptr(), qs, o.data_ptr(), _ptr(lse), _ptr(cu_seqlens), T, Hq, *tail))
-    return (o, lse) if return_lse else o
 
 
 def gdn_attention_paged(q, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, *, scale=0.0,
@@ -646,8 +488,9 @@ def gdn_attention_paged(q, k_cache, v_cache, cu_seqlens, page_indices, page_indp
     optional uint8 device tensor of at least gdn_attention_workspace_bytes(...)
     bytes (0 for batches of short sequences).  Returns o (bf16 [T, Hq, D]), with ``return_lse`` (o, lse), lse the
     natural logarithm of the sum of exponentials (fp32 [T, Hq])."""
-    return _attention(False, q, k_cache, v_cache, cu_seqlens, page_indices, page_indptr, last_page_len, scale, softcap,
-                      window, slopes, full_lens, o, lse, return_lse, err_word, workspace)
+    return (_calls or _load_calls()).attention(False, q, k_cache, v_cache, cu_seqlens, page_indices, page_indptr,
+                                          last_page_len, scale, softcap, window, slopes, full_lens, o, lse, return_lse,
+                                          err_word, workspace)
 
 
 def gdn_attention_decode_paged(q, k_cache, v_cache, page_indices, page_indptr, last_page_len, *, scale=0.0,
@@ -656,5 +499,5 @@ def gdn_attention_decode_paged(q, k_cache, v_cache, page_indices, page_indptr, l
     """The single-token form of gdn_attention_paged: q is [num_seqs, Hq, D], the
     last token of every sequence; the rest as there (``workspace``:
     gdn_attention_decode_workspace_bytes)."""
-    return _attention(True, q, k_cache, v_cache, None, page_indices, page_indptr, last_page_len, scale, softcap, window,
-                      slopes, full_lens, o, lse, return_lse, err_word, workspace)
+    return (_calls or _load_calls()).attention(True, q, k_cache, v_cache, None, page_indices, page_indptr, last_page_len, scale,
+                                          softcap, window, slopes, full_lens, o, lse, return_lse, err_word, workspace)

@@ -8,6 +8,22 @@ import torch
 
 import gated_deltanet_paged_gb300 as gdn
 
+P, I32, I64, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+
+
+class KVCache(ctypes.Structure):  # gdn_kv_cache
+    _fields_ = [("k", P), ("v", P), ("num_pages", I32), ("page_size", I32), ("num_heads", I32), ("head_dim", I32),
+                ("page_stride", I64), ("token_stride", I64), ("head_stride", I64)]
+
+
+class PageTable(ctypes.Structure):  # gdn_page_table
+    _fields_ = [("page_indices", P), ("num_entries", I32), ("page_indptr", P), ("last_page_len", P), ("num_seqs", I32)]
+
+
+class AttentionOptions(ctypes.Structure):  # gdn_attention_options
+    _fields_ = [("softcap", F32), ("slopes", P), ("window", I32), ("full_lens", P)]
+
+
 FAKE = 0x10000  # aligned, never dereferenced: every call below ends in a host check
 
 
@@ -15,19 +31,19 @@ def cache(**kw):
     a = dict(k=FAKE, v=FAKE, num_pages=4, page_size=16, num_heads=2, head_dim=128, page_stride=16 * 256,
              token_stride=256, head_stride=128)
     a.update(kw)
-    return gdn._KV_CACHE.pack(*[v or 0 for v in a.values()])
+    return ctypes.byref(KVCache(*a.values()))
 
 
 def table(**kw):
     a = dict(page_indices=FAKE, num_entries=400, page_indptr=FAKE, last_page_len=FAKE, num_seqs=2)
     a.update(kw)
-    return gdn._PAGE_TABLE.pack(*[v or 0 for v in a.values()])
+    return ctypes.byref(PageTable(*a.values()))
 
 
 def options(**kw):
     a = dict(softcap=0.0, slopes=None, window=-1, full_lens=None)
     a.update(kw)
-    return gdn._ATTENTION_OPTIONS.pack(*[v or 0 for v in a.values()])
+    return ctypes.byref(AttentionOptions(*a.values()))
 
 
 def rope(**kw):
@@ -175,3 +191,7 @@ def test_binding_checks_tensors():
         gdn.gdn_attention_paged(x, c, c, p, p, p, p)
     with pytest.raises(ValueError):
         gdn.gdn_kv_append_paged(x, x, c, c, p, p, p, p)
+    with pytest.raises(TypeError):
+        gdn.gdn_rope([1], f, p)
+    with pytest.raises(ValueError):
+        gdn.gdn_attention_decode_paged(None, c, c, p, p, p)

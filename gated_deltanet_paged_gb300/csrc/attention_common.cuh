@@ -313,6 +313,7 @@ inline int attention_args(gdn::AttnArgs* a, const gdn_bf16* q, int64_t q_stride,
   a->Hkv = Hkv;
   a->group = Hq / Hkv;
   const float s = scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(D));
+  if (!(s <= 3.0e38f) || (cap > 0.f && !(2.f * s / cap * gdn::kLog2e <= 3.0e38f))) return GDN_ERR_INVALID_ARGUMENT;
   a->cap_log2 = cap > 0.f ? cap * gdn::kLog2e : 0.f;
   // tanh(u) / u for |u| <= 0.75 as a polynomial in u^2, fitted by least squares on
   // Chebyshev nodes reweighted towards the minimax error (5.7e-07 relative), with

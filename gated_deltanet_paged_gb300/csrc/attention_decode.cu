@@ -463,32 +463,46 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // Joins the partial results of the items that CTAs of the kernel above cut: block
 // c takes the item that CTA c started and did not end (slot 2 c + 1, then slot 0
-// of every CTA up to the one that ended it), one thread per dimension.
+// of every CTA up to the one that ended it).  A thread takes one dimension of
+// every fourth row; the parts are added in a fixed order, four of them in flight.
+constexpr int kJoinRows = 4;
 template <int D>
-__global__ void __launch_bounds__(D) decode_join_kernel(const __grid_constant__ DecodeArgs d) {
+__global__ void __launch_bounds__(kJoinRows* D) decode_join_kernel(const __grid_constant__ DecodeArgs d) {
   gdn::pdl_wait();
   gdn::pdl_launch_dependents();
-  const int c = blockIdx.x;
+  const int c = blockIdx.x, dim = threadIdx.x % D;
   const int4 cut = d.cuts[c];
   if (cut.x < 0) return;
   const AttnArgs& a = d.a;
   const int rows = min(kRows, a.group - cut.z * kRows);
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+  constexpr int kParts = 4;
+  for (int r = threadIdx.x / D; r < rows; r += kJoinRows) {
     float m = -INFINITY, l = 0.f, o = 0.f;
-    for (int i = c; i <= cut.w; ++i) {
-      const int64_t at = (2 * static_cast<int64_t>(i) + (i == c ? 1 : 0)) * kRows + r;
-      const float2 ml = d.part_ml[at];
-      const float x = d.part_o[at * D + threadIdx.x];
-      const float top = fmaxf(m, ml.x);
-      const float ra = m == -INFINITY ? 0.f : gdn::exp2_approx(m - top);
-      const float rb = ml.x == -INFINITY ? 0.f : gdn::exp2_approx(ml.x - top);
-      o = o * ra + x * rb;
-      l = l * ra + ml.y * rb;
-      m = top;
+    for (int i0 = c; i0 <= cut.w; i0 += kParts) {
+      float2 ml[kParts];
+      float x[kParts];
+#pragma unroll
+      for (int p = 0; p < kParts; ++p) {
+        ml[p] = make_float2(-INFINITY, 0.f);
+        const int i = i0 + p;
+        if (i > cut.w) continue;
+        const int64_t at = (2 * static_cast<int64_t>(i) + (i == c ? 1 : 0)) * kRows + r;
+        ml[p] = d.part_ml[at];
+        x[p] = d.part_o[at * D + dim];
+      }
+#pragma unroll
+      for (int p = 0; p < kParts; ++p) {
+        if (ml[p].x == -INFINITY) continue;  // no part
+        const float top = fmaxf(m, ml[p].x);
+        const float f = gdn::exp2_approx(m - top), g = gdn::exp2_approx(ml[p].x - top);
+        m = top;
+        o = o * f + x[p] * g;
+        l = l * f + ml[p].y * g;
+      }
     }
     const int64_t row = static_cast<int64_t>(cut.x) * a.Hq + cut.y * a.group + cut.z * kRows + r;
-    a.o[row * D + threadIdx.x] = __float2bfloat16(o / l);
-    if (a.lse && threadIdx.x == 0) a.lse[row] = (m + log2f(l)) / gdn::kLog2e;
+    a.o[row * D + dim] = __float2bfloat16(o / l);
+    if (a.lse && dim == 0) a.lse[row] = (m + log2f(l)) / gdn::kLog2e;
   }
 }
 
@@ -525,7 +539,7 @@ int launch(const DecodeArgs& base, const gdn_kv_cache* cache, const gdn_page_tab
   d.part_o = reinterpret_cast<float*>(ws + kMaxGrid * sizeof(int4) + sizeof(float2) * 2 * kMaxGrid * kRows);
   rc = gdn_host::launch_pdl(decode_attention_kernel<D>, dim3(grid), dim3(kThreads), smem, stream, d, k_map, v_map);
   if (rc != GDN_OK || d.whole) return rc;
-  return gdn_host::launch_pdl(decode_join_kernel<D>, dim3(grid, 4), dim3(D), 0, stream, d);
+  return gdn_host::launch_pdl(decode_join_kernel<D>, dim3(grid), dim3(kJoinRows * D), 0, stream, d);
 }
 
 }  // namespace

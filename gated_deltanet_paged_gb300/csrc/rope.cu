@@ -156,6 +156,49 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const RotateArgs a)
   const int t = static_cast<int>(id / a.slices), slice = static_cast<int>(id % a.slices);
   if (t >= a.T) return;
 
+  const int heads = a.Hq + 2 * a.Hkv;
+  const int total = heads * a.units;
+  const int stride = a.slices * 32;
+  const int rotated = a.half / W;  // units that rotate; the rest are copied
+  // Where unit `unit` of a head keeps its two pieces.
+  auto offsets = [&](int unit, int* first, int* second) {
+    if (unit < rotated && !a.interleaved) {
+      *first = unit * W;
+      *second = a.half + *first;
+    } else {
+      *first = unit * 2 * W;  // rotated units end at 2 * half, so copied ones follow on
+      *second = *first + W;
+    }
+  };
+  Piece<W> pa[kBatch], pb[kBatch];
+  auto load = [&](int u0) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int u = u0 + j * stride;
+      if (u >= total) continue;
+      const int h = u / a.units;
+      int first, second;
+      offsets(u - h * a.units, &first, &second);
+      const __nv_bfloat16* src;
+      if (h < a.Hq)
+        src = a.q + t * a.q_stride + static_cast<int64_t>(h) * a.D;
+      else if (h < a.Hq + a.Hkv)
+        src = a.k + t * a.k_stride + static_cast<int64_t>(h - a.Hq) * a.D;
+      else
+        src = a.v + t * a.v_stride + static_cast<int64_t>(h - a.Hq - a.Hkv) * a.D;
+      pa[j] = load_piece<W>(src + first);
+      pb[j] = load_piece<W>(src + second);
+    }
+  };
+  // The first heads and the frequencies are asked for before the position: finding
+  // that takes up to four loads that wait for one another.
+  int u0 = slice * 32 + lane;
+  load(u0);
+  int64_t freq[kMaxPairs / 32];
+#pragma unroll
+  for (int i = 0; i < kMaxPairs / 32; ++i)
+    if (lane + 32 * i < a.half) freq[i] = a.freq[lane + 32 * i];
+
   int position;
   int64_t slot = -1;  // element offset of the token's cache slot
   if (a.positions) {
@@ -179,63 +222,41 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const RotateArgs a)
   }
 
   float2* cs = cs_all[warp];
-  for (int i = lane; i < a.half; i += 32) {
-    const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(position)) * static_cast<uint64_t>(a.freq[i]);
+#pragma unroll
+  for (int i = 0; i < kMaxPairs / 32; ++i) {
+    if (lane + 32 * i >= a.half) break;
+    const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(position)) * static_cast<uint64_t>(freq[i]);
     const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
     float sn, cn;
     sincospif(half_turns, &sn, &cn);
-    cs[i] = make_float2(cn * a.amplitude, sn * a.amplitude * a.sign);
+    cs[lane + 32 * i] = make_float2(cn * a.amplitude, sn * a.amplitude * a.sign);
   }
   __syncwarp();
 
-  const int heads = a.Hq + 2 * a.Hkv;
-  const int total = heads * a.units;
-  const int stride = a.slices * 32;
-  const int rotated = a.half / W;  // units that rotate; the rest are copied
-  for (int u0 = slice * 32 + lane; u0 < total; u0 += kBatch * stride) {
-    Piece<W> pa[kBatch], pb[kBatch];
-    __nv_bfloat16* dst[kBatch];
-    int off_b[kBatch], pair[kBatch];
+  while (u0 < total) {
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      dst[j] = nullptr;
       const int u = u0 + j * stride;
       if (u >= total) continue;
       const int h = u / a.units, unit = u - h * a.units;
-      const __nv_bfloat16* src;
+      int first, second;
+      offsets(unit, &first, &second);
+      __nv_bfloat16* dst;
       bool turns = unit < rotated;
       if (h < a.Hq) {
-        src = a.q + t * a.q_stride + static_cast<int64_t>(h) * a.D;
-        dst[j] = a.q_out + t * a.q_out_stride + static_cast<int64_t>(h) * a.D;
+        dst = a.q_out + t * a.q_out_stride + static_cast<int64_t>(h) * a.D;
       } else {
-        const bool is_v = h >= a.Hq + a.Hkv;
-        const int g = h - a.Hq - (is_v ? a.Hkv : 0);
         if (slot < 0) continue;
-        src = (is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) + static_cast<int64_t>(g) * a.D;
-        dst[j] = (is_v ? a.v_cache : a.k_cache) + slot + g * a.head_stride;
+        const bool is_v = h >= a.Hq + a.Hkv;
+        dst = (is_v ? a.v_cache : a.k_cache) + slot + (h - a.Hq - (is_v ? a.Hkv : 0)) * a.head_stride;
         turns = turns && !is_v;
       }
-      int first, second;
-      if (unit < rotated && !a.interleaved) {
-        first = unit * W;
-        second = a.half + first;
-      } else {
-        first = unit * 2 * W;  // rotated units end at 2 * half, so copied ones follow on
-        second = first + W;
-      }
-      pair[j] = turns ? unit * W : -1;
-      dst[j] += first;
-      off_b[j] = second - first;
-      pa[j] = load_piece<W>(src + first);
-      pb[j] = load_piece<W>(src + second);
+      if (turns) rotate<W>(pa[j], pb[j], cs + unit * W, a.interleaved != 0);
+      store_piece<W>(dst + first, pa[j]);
+      store_piece<W>(dst + second, pb[j]);
     }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      if (!dst[j]) continue;
-      if (pair[j] >= 0) rotate<W>(pa[j], pb[j], cs + pair[j], a.interleaved != 0);
-      store_piece<W>(dst[j], pa[j]);
-      store_piece<W>(dst[j] + off_b[j], pb[j]);
-    }
+    u0 += kBatch * stride;
+    load(u0);
   }
 }
 

@@ -19,6 +19,8 @@
 //     another inside an item: mma.sync with the G query heads as the 16 rows
 //     (the matrix work is a tenth of the copy time), private (m, l, o), joined
 //     through shared memory when the item ends.
+#include <algorithm>
+
 #include "attention_common.cuh"
 
 namespace {
@@ -118,8 +120,8 @@ template <int D>
 struct Smem {
   static constexpr int kTile = kBlock<D> * D * 2;  // one of K, V
   alignas(1024) uint8_t kv[kStages][2][kTile];
-  float4 join_o[D / 8][32];  // one warp's partial result, lane by lane
-  float4 join_ml[32];        // m, l of its two rows
+  float4 join_o[kConsumers][D / 8][32];  // the warps' partial results, lane by lane
+  float4 join_ml[kConsumers][32];        // m, l of their two rows
   uint64_t full[kStages];
   uint64_t empty[kStages];
   int64_t scan[kThreads / 32 + 1];
@@ -387,87 +389,86 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane == 0) gdn::mbar_arrive(&sh.empty[stage]);
     }
 
-    // ---- join the four warps into warp 0, one after the other (one buffer:
-    // a second would cost the third stage its place beside a second CTA) ----
+    // ---- join the four warps: each takes a quarter of the dimensions of all ----
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
       l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
     }
-    for (int from = 1; from < kConsumers; ++from) {
-      if (warp == from) {
+    consumers_sync();  // the last item's results have been read
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) sh.join_o[i][lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-        sh.join_ml[lane] = make_float4(m[0], m[1], l[0], l[1]);
-      }
-      if (tid == 0) sh.stop = *static_cast<volatile int*>(&sh.abort);  // one reading for all warps
-      consumers_sync();
-      if (warp == 0) {
-        const float4 ml = sh.join_ml[lane];
-        const float mb[2] = {ml.x, ml.y}, lb[2] = {ml.z, ml.w};
-        float ra[2], rb[2];
+    for (int i = 0; i < D / 8; ++i) sh.join_o[warp][i][lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+    sh.join_ml[warp][lane] = make_float4(m[0], m[1], l[0], l[1]);
+    if (tid == 0) sh.stop = *static_cast<volatile int*>(&sh.abort);  // one reading for all warps
+    consumers_sync();
+    if (sh.stop) return;
+    float f[kConsumers][2];
+    {
+      float4 ml[kConsumers];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float top = fmaxf(m[i], mb[i]);
-          ra[i] = m[i] == -INFINITY ? 0.f : gdn::exp2_approx(m[i] - top);
-          rb[i] = mb[i] == -INFINITY ? 0.f : gdn::exp2_approx(mb[i] - top);
-          l[i] = l[i] * ra[i] + lb[i] * rb[i];
-          m[i] = top;
-        }
+      for (int v = 0; v < kConsumers; ++v) ml[v] = sh.join_ml[v][lane];
+      m[0] = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+      m[1] = fmaxf(fmaxf(ml[0].y, ml[1].y), fmaxf(ml[2].y, ml[3].y));
+      l[0] = l[1] = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const float4 x = sh.join_o[i][lane];
-          o[i][0] = o[i][0] * ra[0] + x.x * rb[0];
-          o[i][1] = o[i][1] * ra[0] + x.y * rb[0];
-          o[i][2] = o[i][2] * ra[1] + x.z * rb[1];
-          o[i][3] = o[i][3] * ra[1] + x.w * rb[1];
-        }
-      }
-      const int stop = sh.stop;
-      consumers_sync();
-      if (stop) return;
-    }
-    if (warp == 0) {
-      const bool starts = w.blk0 == 0, ends = w.blk1 == w.it.blocks;
-      if (starts && ends) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = g + 8 * i;
-          if (r >= rows) continue;
-          const float inv = 1.f / l[i];
-          const int64_t row = static_cast<int64_t>(w.b) * a.Hq + h0 + r;
-          uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + row * D);
-#pragma unroll
-          for (int k = 0; k < D / 8; ++k) dst[k * 4 + t] = gdn::pack_bf162(o[k][2 * i] * inv, o[k][2 * i + 1] * inv);
-          if (a.lse && t == 0) a.lse[row] = (m[i] + log2f(l[i])) / gdn::kLog2e;
-        }
-      } else {
-        // One segment of a CTA at most starts an item that it does not end, and
-        // one at most continues one: two slots per CTA.
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (starts ? 1 : 0);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = g + 8 * i;
-          if (r >= rows) continue;
-          float2* dst = reinterpret_cast<float2*>(d.part_o + (slot * kRows + r) * D);
-#pragma unroll
-          for (int k = 0; k < D / 8; ++k) dst[k * 4 + t] = make_float2(o[k][2 * i], o[k][2 * i + 1]);
-          if (t == 0) d.part_ml[slot * kRows + r] = make_float2(m[i], l[i]);
-        }
-        if (starts && lane == 0)
-          d.cuts[blockIdx.x] = make_int4(w.b, head, pass, shares.owner(w.item0 + w.it.cost - 1));
+      for (int v = 0; v < kConsumers; ++v) {
+        f[v][0] = ml[v].x == -INFINITY ? 0.f : gdn::exp2_approx(ml[v].x - m[0]);
+        f[v][1] = ml[v].y == -INFINITY ? 0.f : gdn::exp2_approx(ml[v].y - m[1]);
+        l[0] = fmaf(ml[v].z, f[v][0], l[0]);
+        l[1] = fmaf(ml[v].w, f[v][1], l[1]);
       }
     }
+    const bool starts = w.blk0 == 0, ends = w.blk1 == w.it.blocks;
+    // One segment of a CTA at most starts an item that it does not end, and one at
+    // most continues one: two slots per CTA.
+    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (starts ? 1 : 0);
+    const int64_t row0 = static_cast<int64_t>(w.b) * a.Hq + h0;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+      const int at = warp * (D / 32) + k;
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int v = 0; v < kConsumers; ++v) {
+        const float4 y = sh.join_o[v][at][lane];
+        x[0] = fmaf(y.x, f[v][0], x[0]);
+        x[1] = fmaf(y.y, f[v][0], x[1]);
+        x[2] = fmaf(y.z, f[v][1], x[2]);
+        x[3] = fmaf(y.w, f[v][1], x[3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = g + 8 * i;
+        if (r >= rows) continue;
+        if (starts && ends)
+          reinterpret_cast<uint32_t*>(a.o + (row0 + r) * D)[at * 4 + t] =
+              gdn::pack_bf162(x[2 * i] / l[i], x[2 * i + 1] / l[i]);
+        else
+          reinterpret_cast<float2*>(d.part_o + (slot * kRows + r) * D)[at * 4 + t] = make_float2(x[2 * i], x[2 * i + 1]);
+      }
+    }
+    if (warp == 0 && t == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = g + 8 * i;
+        if (r >= rows) continue;
+        if (!(starts && ends))
+          d.part_ml[slot * kRows + r] = make_float2(m[i], l[i]);
+        else if (a.lse)
+          a.lse[row0 + r] = (m[i] + log2f(l[i])) / gdn::kLog2e;
+      }
+    }
+    if (tid == 0 && starts && !ends)
+      d.cuts[blockIdx.x] = make_int4(w.b, head, pass, shares.owner(w.item0 + w.it.cost - 1));
   }
 }
 
 // Joins the partial results of the items that CTAs of the kernel above cut: block
 // c takes the item that CTA c started and did not end (slot 2 c + 1, then slot 0
-// of every CTA up to the one that ended it).  A thread takes one dimension of
-// every fourth row; the parts are added in a fixed order, four of them in flight.
-constexpr int kJoinRows = 4;
+// of every CTA up to the one that ended it).  A thread takes one dimension of a
+// row, or of some where the rows are more than 1,024 / D; the parts are added in a
+// fixed order, four of them in flight.
 template <int D>
-__global__ void __launch_bounds__(kJoinRows* D) decode_join_kernel(const __grid_constant__ DecodeArgs d) {
+__global__ void __launch_bounds__(1024) decode_join_kernel(const __grid_constant__ DecodeArgs d) {
   gdn::pdl_wait();
   gdn::pdl_launch_dependents();
   const int c = blockIdx.x, dim = threadIdx.x % D;
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(kJoinRows* D) decode_join_kernel(const __grid_
   const AttnArgs& a = d.a;
   const int rows = min(kRows, a.group - cut.z * kRows);
   constexpr int kParts = 4;
-  for (int r = threadIdx.x / D; r < rows; r += kJoinRows) {
+  for (int r = threadIdx.x / D; r < rows; r += blockDim.x / D) {
     float m = -INFINITY, l = 0.f, o = 0.f;
     for (int i0 = c; i0 <= cut.w; i0 += kParts) {
       float2 ml[kParts];
@@ -539,7 +540,7 @@ int launch(const DecodeArgs& base, const gdn_kv_cache* cache, const gdn_page_tab
   d.part_o = reinterpret_cast<float*>(ws + kMaxGrid * sizeof(int4) + sizeof(float2) * 2 * kMaxGrid * kRows);
   rc = gdn_host::launch_pdl(decode_attention_kernel<D>, dim3(grid), dim3(kThreads), smem, stream, d, k_map, v_map);
   if (rc != GDN_OK || d.whole) return rc;
-  return gdn_host::launch_pdl(decode_join_kernel<D>, dim3(grid), dim3(kJoinRows * D), 0, stream, d);
+  return gdn_host::launch_pdl(decode_join_kernel<D>, dim3(grid), dim3(D * std::min(std::min(d.a.group, kRows), 1024 / D)), 0, stream, d);
 }
 
 }  // namespace

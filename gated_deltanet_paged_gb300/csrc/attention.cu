@@ -359,13 +359,15 @@ __device__ __forceinline__ void tmem_st32_nw(uint32_t taddr, const uint32_t* r) 
 
 // How scores become weights.
 //   kPlain: scale and reference in one multiply-add.
+//   kBiased: a bias that is linear in the key (no prefix mask: every visible key is
+//     behind the token) first.
 //   kGeneral: a bias, or any cap, first (the options that change a score; those
 //     that only hide keys cost nothing away from the edges).
 //   kBounded: a cap of at most kBoundedCap, and no bias.  It bounds the scores on
 //     both sides, so that 0 serves as the reference for the whole row: weights
 //     within 2^-80 .. 2^80 and their sums over 2^30 keys are far inside fp32 and
 //     bf16, and no maximum is taken.
-enum Scores { kPlain, kGeneral, kBounded };
+enum Scores { kPlain, kBiased, kGeneral, kBounded };
 constexpr float kBoundedCap = 80.f;  // in units of log2
 
 template <int D, Scores kScores>
@@ -840,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = g.pos + min(t * tile_tokens + min(my_token, tile_tokens - 1), tokens - 1);
       const int lo = gdn::key_lo(a, pos), hi = max(pos + 1, g.full);
       float slope = 0.f;
-      if (kScores == kGeneral && a.slopes) slope = a.slopes[g.head * a.group + my_head] * gdn::kLog2e;
+      if ((kScores == kGeneral || kScores == kBiased) && a.slopes) slope = a.slopes[g.head * a.group + my_head] * gdn::kLog2e;
       __syncwarp();
       if (lane == 0) gdn::mbar_arrive(&sh.seg_empty[at]);
       if (blocks == 0) break;
@@ -859,16 +861,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         gdn::tc_fence_after();
         const bool edge = __any_sync(0xFFFFFFFFu, key0 < lo || key0 + kKeys > hi);
-        // Plain scores stay in registers from the maximum to the weights, all 128.
+        // Plain and biased scores stay in registers from the maximum to the weights, all 128.
         // The others go through loops of 32, read from TMEM again where needed:
         // unrolled, their instructions were fetched more slowly than issued (ncu: 1.5
         // warps per issue waited for one, against 0.4 on the plain path; rolling
         // took the 64 mixed sequences from 2.13 to 1.73 ms, but would take 4 x 8,192
         // plain tokens from 1.39 to 1.48).
         float ref = 0.f;
-        float s[kScores == kPlain ? 128 : 1];
-        if constexpr (kScores == kPlain) {
+        constexpr bool kInRegisters = kScores == kPlain || kScores == kBiased;
+        float s[kInRegisters ? 128 : 1];
+        if constexpr (kInRegisters) {
           tmem_ld128(s_addr, s);
+          if constexpr (kScores == kBiased) {
+            // The bias of keys i and i + 1, and its step to the next two.
+            const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), step = make_float2(2.f * slope, 2.f * slope);
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) {
+              const float first = slope * static_cast<float>(key0 + c - pos);
+              float2 bias = make_float2(first, first + slope);
+#pragma unroll
+              for (int i = c; i < c + 32; i += 2) {
+                const float2 x = __ffma2_rn(make_float2(s[i], s[i + 1]), scale2, bias);
+                s[i] = x.x;
+                s[i + 1] = x.y;
+                bias = __fadd2_rn(bias, step);
+              }
+            }
+          }
           if (edge) {
 #pragma unroll
             for (int i = 0; i < 128; ++i) s[i] = i >= lo - key0 && i < hi - key0 ? s[i] : -INFINITY;
@@ -876,8 +895,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if constexpr (kScores != kBounded) {
           float mx;
-          if constexpr (kScores == kPlain) {
-            mx = max128(s) * a.scale_log2;
+          if constexpr (kInRegisters) {
+            mx = max128(s);
+            if (kScores == kPlain) mx *= a.scale_log2;
           } else {
             // Changed and masked scores go back to TMEM.
             mx = -INFINITY;
@@ -932,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), ref2 = make_float2(-ref, -ref);
         auto weight = [&](float2 x) {
           if (kScores == kPlain) x = __ffma2_rn(x, scale2, ref2);
-          if (kScores == kGeneral) x = __fadd2_rn(x, ref2);
+          if (kScores == kGeneral || kScores == kBiased) x = __fadd2_rn(x, ref2);
           x = make_float2(gdn::exp2_approx(x.x), gdn::exp2_approx(x.y));
           l2 = __fadd2_rn(l2, x);
           return gdn::pack_bf162(x);
@@ -943,7 +963,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) gdn::mbar_arrive(&sh.p_full[t][h]);
         };
-        if constexpr (kScores == kPlain) {
+        if constexpr (kInRegisters) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t p[32];
@@ -1145,11 +1165,13 @@ extern "C" int gdn_attention_paged(const gdn_bf16* q, int64_t q_token_stride, gd
   d.tile_tokens = kRows / d.a.group;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bounded = d.a.cap_log2 > 0.f && d.a.cap_log2 <= kBoundedCap && !d.a.slopes;
-  const Scores scores = bounded ? kBounded : d.a.cap_log2 > 0.f || d.a.slopes ? kGeneral : kPlain;
+  const bool linear = d.a.slopes && d.a.cap_log2 == 0.f && !d.a.full_lens;
+  const Scores scores = bounded ? kBounded : linear ? kBiased : d.a.cap_log2 > 0.f || d.a.slopes ? kGeneral : kPlain;
   const auto run = [&](auto dim) {
     constexpr int D = decltype(dim)::value;
     switch (scores) {
       case kPlain: return launch<D, kPlain>(d, total_tokens, cache, workspace, sms, s);
+      case kBiased: return launch<D, kBiased>(d, total_tokens, cache, workspace, sms, s);
       case kGeneral: return launch<D, kGeneral>(d, total_tokens, cache, workspace, sms, s);
       default: return launch<D, kBounded>(d, total_tokens, cache, workspace, sms, s);
     }

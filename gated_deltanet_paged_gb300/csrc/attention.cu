@@ -46,6 +46,7 @@ constexpr int kSegments = 4;  // segments announced ahead
 // Fixed cost of an item (queries, pipeline fill, epilogue) in keys.
 constexpr int kItemCost = 2 * kKeys;
 constexpr int kMinShare = 4 * kKeys;  // keys below which a cut costs more than it saves
+constexpr int kCrossing = 3;          // what a CTA's second segment costs, in blocks
 constexpr int kMinBlocks = 2;         // blocks of a piece, where items are cut evenly
 constexpr int kMaxGrid = 160;         // one CTA per SM
 
@@ -179,7 +180,7 @@ __device__ __forceinline__ T scan_block(int64_t* scratch64, T mine, T* total) {
 struct alignas(16) Segment {
   int blocks;       // in this segment; 0: no more segments
   int key0;         // first key of the first block
-  int lo, hi;       // keys that the item's rows see between them
+  int lo, hi;       // keys that are copied
   int first_token;  // row of the item's first token in q and o
   int tokens;       // of the item
   int pos;          // position of its first token
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- this CTA's share ----
   gdn::Shares<7> shares(0, 1, 1);
-  bool idle;
+  bool idle = true;
   {
     const int c = blockIdx.x, grid = gridDim.x;
     const int per = (a.paged.num_seqs + kThreads - 1) / kThreads;
@@ -446,7 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int all_pairs;
     const int pairs_before = scan_block(sh.scan, pairs, &all_pairs);
     const int64_t all_items = static_cast<int64_t>(all_pairs) * a.Hkv;
-    if (all_items <= min(grid, kMaxGrid)) {
+    bool aligned = all_items <= min(grid, kMaxGrid);
+    if (aligned) {
       // Few items: each gets CTAs to itself, by its length, and they cut it evenly.
       // Cutting the line instead gives many a CTA the end of one item and the start
       // of the next, and an item's fixed cost twice (452 tokens over 2,500: the
@@ -469,16 +471,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         blocks = (pair_hi(d, x.s, x.pair) + kKeys - 1) / kKeys - pair_lo(d, x.s, x.pair) / kKeys;
       }
       int sum, pieces_total;
-      scan_block(sh.scan, x.cost >> 7, &sum);
+      scan_block(sh.scan, x.cost / kKeys, &sum);
       int pieces = tid < items ? 1 : 0;
       if (tid < items && !d.whole) {
-        pieces += static_cast<int>(__fdividef(static_cast<float>(grid - items) * static_cast<float>(x.cost >> 7),
+        pieces += static_cast<int>(__fdividef(static_cast<float>(grid - items) * static_cast<float>(x.cost / kKeys),
                                               static_cast<float>(sum)));
         pieces = min(pieces, max(1, blocks / kMinBlocks));
       }
       const int piece = c - scan_block(sh.scan, pieces, &pieces_total);
+      // Unless a piece is longer than a share of the line and the cost of a second
+      // segment (512 tokens over 131,072 are 64 items: 128 of 152 CTAs would work).
+      const bool longer = pieces && x.cost / pieces > (sum / grid + kCrossing) * kKeys;
+      aligned = d.whole || !__syncthreads_or(longer);
       idle = c >= pieces_total;
-      if (piece >= 0 && piece < pieces) {
+      if (aligned && piece >= 0 && piece < pieces) {
         // As a walk along a line on which the item begins at 0.
         const int blk0 = blocks * piece / pieces, blk1 = blocks * (piece + 1) / pieces;
         x.pos = blk0 ? kItemCost + static_cast<int64_t>(blk0) * kKeys : 0;
@@ -486,7 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         x.last = c - piece + pieces - 1;
         sh.walk = x;
       }
-    } else {
+    }
+    if (!aligned) {
       int64_t cost = 0, mine = 0, total;
       for (int b = b0; b < b1; ++b) {
         if (per > 1) s = load_seq(d, b);
@@ -565,7 +572,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           g.blocks = w.blk1 - w.blk0;
           g.key0 = (w.first + w.blk0) * kKeys;
           g.lo = w.lo;
-          g.hi = w.hi;
+          // To the end of the last block, as far as the sequence goes: those tokens'
+          // weights are 0 and their values finite, so that only blocks which a
+          // sequence ends in, or a window begins in, have values to clear.
+          g.hi = min(w.s.len, (w.hi + kKeys - 1) / kKeys * kKeys);
           g.first_token = w.s.first_token + pair0;
           g.tokens = min(2 * tile_tokens, w.s.n - pair0);
           g.pos = w.s.len - w.s.n + pair0;
@@ -716,48 +726,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kValueWarp) {
       // ------------------------------------------------------------- values
       // Slots past the sequence's end or before every window may hold anything,
-      // and 0 * NaN would reach the sum: value rows that no row of the item sees
-      // become zeros in shared memory.  Their tile's copies complete on `raw`, and
-      // this warp completes `full`.
+      // and 0 * NaN would reach the sum: their value rows become zeros in shared
+      // memory.  The tile's copies complete on `raw`, and this warp completes `full`.
       gdn::TileCopies<D, kKeys> values(a, &v_map, lane);
       uint32_t n = 1, raw_parity = 0;  // ring tiles (values are the odd ones); per stage, parity of its next raw copy
-      int pending = -1, from = 0, to = 0;  // stage to be cleared, except rows [from, to)
-      auto clear = [&] {
-        const int at = pending;
-        pending = -1;
-        if (!wait(&sh.raw[at], (raw_parity >> at) & 1)) return;
-        raw_parity ^= 1u << at;
-        uint4* dst = reinterpret_cast<uint4*>(ring + at * L::kTile);
-        for (int i = lane; i < (from + kKeys - to) * 8; i += 32) {
-          const int r = i >> 3, row = r < from ? r : r - from + to;
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) dst[(c * kRows + row) * 8 + (i & 7)] = make_uint4(0, 0, 0, 0);
-        }
-        gdn::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) gdn::mbar_arrive(&sh.full[at]);
-      };
       Segment g;
       for (uint32_t segs = 0; ok && next(segs, g); ++segs) {
         values.begin(g.lo, g.hi, g.head, g.seq, g.entry, g.key0);
-        for (int j = 0; ok && j < g.blocks; ++j, n += 2) {
-          const uint32_t stage = n % L::kStages, parity = ((n / L::kStages) - 1) & 1;
+        for (int j = 0; j < g.blocks; ++j, n += 2) {
+          const uint32_t stage = n % L::kStages;
           const int key0 = g.key0 + j * kKeys;
           const bool partial = key0 < g.lo || key0 + kKeys > g.hi;
           uint64_t* bar = partial ? &sh.raw[stage] : &sh.full[stage];
-          // A tile that waits to be cleared is cleared behind this tile's copies,
-          // unless there is no room for them yet.
-          if (n >= L::kStages && pending >= 0 && !__all_sync(0xFFFFFFFFu, gdn::mbar_test(&sh.empty[stage], parity))) clear();
-          if (n >= L::kStages && !wait(&sh.empty[stage], parity)) break;
+          if (n >= L::kStages && !wait(&sh.empty[stage], ((n / L::kStages) - 1) & 1)) break;
           if (lane == 0) gdn::mbar_arrive_expect_tx(bar, values.bytes());
           __syncwarp();
           values.copy(ring + stage * L::kTile, bar, j + 1 < g.blocks);
-          if (pending >= 0) clear();
-          if (partial) pending = stage, from = max(0, g.lo - key0), to = min(kKeys, g.hi - key0);
+          if (!partial) continue;
+          if (!wait(bar, (raw_parity >> stage) & 1)) break;
+          raw_parity ^= 1u << stage;
+          const int from = max(0, g.lo - key0), to = min(kKeys, g.hi - key0);
+          uint4* dst = reinterpret_cast<uint4*>(ring + stage * L::kTile);
+          for (int i = lane; i < (from + kKeys - to) * 8; i += 32) {
+            const int r = i >> 3, row = r < from ? r : r - from + to;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) dst[(c * kRows + row) * 8 + (i & 7)] = make_uint4(0, 0, 0, 0);
+          }
+          gdn::fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) gdn::mbar_arrive(&sh.full[stage]);
         }
-        // The last tile of a segment is the one that is partial most often, and the
-        // products are about to wait for it.
-        if (pending >= 0) clear();
       }
       if (!ok && lane == 0) {
         *abort_flag = 1;

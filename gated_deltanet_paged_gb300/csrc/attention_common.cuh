@@ -207,19 +207,7 @@ struct TileCopies {
   }
   // The current tile; then on to the next of `more`.
   __device__ __forceinline__ void copy(uint8_t* dst, uint64_t* bar, bool more) {
-    if (boxes <= 4) {
-      // One lane issues, at 16 cycles a copy; a copy per lane, each with addresses of
-      // its own, takes 55, and over pages of 64 tokens and more the decode of 256
-      // sequences 1.23 ms instead of 1.18.
-      int o[4], p[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = __shfl_sync(0xFFFFFFFFu, slot, i), p[i] = __shfl_sync(0xFFFFFFFFu, page, i);
-      if (elect_one()) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i < boxes && visible(key0 + i * box_rows)) box(dst, bar, i, o[i], p[i]);
-      }
-    } else if (boxes <= 32) {
+    if (boxes <= 32) {
       if (lane < boxes && visible(key0 + lane * box_rows)) box(dst, bar, lane, slot, page);
     } else {
 #pragma unroll 1

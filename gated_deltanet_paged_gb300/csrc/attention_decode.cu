@@ -19,8 +19,6 @@
 //     another inside an item: mma.sync with the G query heads as the 16 rows
 //     (the matrix work is a tenth of the copy time), private (m, l, o), joined
 //     through shared memory when the item ends.
-#include <algorithm>
-
 #include "attention_common.cuh"
 
 namespace {
@@ -36,20 +34,20 @@ constexpr int kBlock = 8192 / D;
 constexpr int kStages = 2;
 constexpr int kConsumers = 4;  // warps, a quarter of a block's keys each
 constexpr int kThreads = (kConsumers + 2) * 32;  // and one warp that copies keys, one that copies values
-constexpr int kRows = 16;     // query heads per pass of an item
+constexpr int kRows = 16;     // query heads of a key head at most (see gdn_attention_decode_paged)
 // Fixed cost of an item (its queries, the join of the warps, its stores) in
 // blocks, so that shares of many short items weigh the same as shares of long ones.
 constexpr int kItemCost = 2;
 constexpr int kMinShare = 8;  // blocks below which a cut costs more than it saves
+constexpr int kMaxGrid = 2 * 160;  // two CTAs per SM
 constexpr int kWholeKeys = 512;  // longest sequence that is never cut
 
 struct DecodeArgs {
   AttnArgs a;
   float* part_o;     // [2 grid][kRows][D]
   float2* part_ml;   // [2 grid][kRows]
-  int4* cuts;        // [grid]: (sequence, head, row pass, last CTA) of an item cut at this CTA's end, or -1
+  int4* cuts;        // [grid]: (sequence, head, last CTA) of an item cut at this CTA's end, or -1
   int32_t whole;     // items are not cut
-  int32_t passes;    // ceil(group / kRows): an item is (sequence, head, pass)
 };
 
 // The key range of sequence b's token in blocks, and its cost.
@@ -77,14 +75,14 @@ struct Walk {
   int64_t pos, end;   // units of the batch's line (whole: item numbers)
   int64_t base;       // line position of sequence b
   int b;
-  int head;           // (head, pass) number within the sequence
+  int head;
   Item it;
   int blk0, blk1;     // blocks of the item in this segment
   int64_t item0;      // line position of the item
 };
 template <int D>
 __device__ __forceinline__ bool next_segment(const DecodeArgs& d, Walk& w) {
-  const int per_seq = d.a.Hkv * d.passes;
+  const int per_seq = d.a.Hkv;
   if (d.whole) {
     while (w.pos < w.end) {
       const int id = static_cast<int>(w.pos);
@@ -179,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   gdn::pdl_launch_dependents();
 
   // ---- this CTA's share of the line ----
-  const int per_seq = a.Hkv * d.passes;
+  const int per_seq = a.Hkv;
   Walk w;
   gdn::Shares<0> shares(0, 1, 1);
   if (d.whole) {
@@ -243,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     int n = 0;  // blocks issued
     bool ok = true;
     while (ok && next_segment<D>(d, w)) {
-      tiles.begin(w.it.lo, w.it.hi, w.head / d.passes, w.b, w.it.s.entry, (w.it.first + w.blk0) * kBlock<D>);
+      tiles.begin(w.it.lo, w.it.hi, w.head, w.b, w.it.s.entry, (w.it.first + w.blk0) * kBlock<D>);
       for (int blk = w.blk0; blk < w.blk1; ++blk, ++n) {
         const int stage = n % kStages;
         if (n >= kStages)
@@ -268,9 +266,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int g = lane >> 2, t = lane & 3;  // fragment row and column pair
   int n = 0;
   while (next_segment<D>(d, w)) {
-    const int head = w.head / d.passes, pass = w.head % d.passes;
-    const int h0 = head * a.group + pass * kRows;             // first query head of the rows
-    const int rows = min(kRows, a.group - pass * kRows);
+    const int h0 = w.head * a.group;  // first query head of the rows
+    const int rows = a.group;
     // Queries as A fragments; rows past the group are zero.
     uint32_t q[D / 16][4];
     {
@@ -458,56 +455,111 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     if (tid == 0 && starts && !ends)
-      d.cuts[blockIdx.x] = make_int4(w.b, head, pass, shares.owner(w.item0 + w.it.cost - 1));
+      d.cuts[blockIdx.x] = make_int4(w.b, w.head, shares.owner(w.item0 + w.it.cost - 1), 0);
   }
 }
 
-// Joins the partial results of the items that CTAs of the kernel above cut: block
-// c takes the item that CTA c started and did not end (slot 2 c + 1, then slot 0
-// of every CTA up to the one that ended it).  A thread takes one dimension of a
-// row, or of some where the rows are more than 1,024 / D; the parts are added in a
-// fixed order, four of them in flight.
-template <int D>
-__global__ void __launch_bounds__(1024) decode_join_kernel(const __grid_constant__ DecodeArgs d) {
+// Joins the partial results of the items that CTAs of the kernel above cut: the
+// item that CTA c started and did not end has slot 2 c + 1, then slot 0 of every
+// CTA up to the one that ended it.  A thread takes one dimension of a row and every
+// kGroups-th part, four of them in flight; the groups add up in a fixed order.
+//   kGroups 1, many items, most cut in two: block c takes CTA c's cut, all rows at
+//     once (61 sequences: the call takes 15.6 us, shared out as below 17.1).
+//   kGroups 8, few items cut into many parts: the blocks share the rows of all cuts
+//     out between them (4 sequences of 65,536 on one key head, 76 parts: 57 us with
+//     one group, 33 with eight).
+constexpr int kJoinThreads = 1024;
+template <int D, int kGroups>
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeArgs d, int ctas) {
+  __shared__ int4 cuts[kGroups > 1 ? kMaxGrid : 1];  // with the CTA that made the cut
+  __shared__ int count[kJoinThreads / 32];
+  __shared__ float2 group_ml[kJoinThreads / D];
+  __shared__ float group_o[kGroups > 1 ? kJoinThreads : 1];
   gdn::pdl_wait();
   gdn::pdl_launch_dependents();
-  const int c = blockIdx.x, dim = threadIdx.x % D;
-  const int4 cut = d.cuts[c];
-  if (cut.x < 0) return;
   const AttnArgs& a = d.a;
-  const int rows = min(kRows, a.group - cut.z * kRows);
+  const int tid = threadIdx.x, dim = tid % D, unit = tid / D, group = unit % kGroups;
+  const int per_job = blockDim.x / D / kGroups;  // rows
+  const int slices = (a.group + per_job - 1) / per_job;
+  int job = blockIdx.x, jobs = 0, stride = gridDim.x;
+  if constexpr (kGroups > 1) {
+    // The cut items in the order of their CTAs, the same in every block.
+    int4 mine = tid < ctas ? d.cuts[tid] : make_int4(-1, 0, 0, 0);
+    mine.w = tid;
+    const unsigned here = __ballot_sync(0xFFFFFFFFu, mine.x >= 0);
+    if ((tid & 31) == 0) count[tid >> 5] = __popc(here);
+    __syncthreads();
+    int at = __popc(here & ((1u << (tid & 31)) - 1)), found = 0;
+    for (int i = 0; i < blockDim.x / 32; ++i) {
+      if (i < tid >> 5) at += count[i];
+      found += count[i];
+    }
+    if (mine.x >= 0) cuts[at] = mine;
+    __syncthreads();
+    jobs = found * slices;
+  } else {
+    if (d.cuts[job].x < 0) return;
+    job = 0, jobs = slices, stride = 1;
+  }
   constexpr int kParts = 4;
-  for (int r = threadIdx.x / D; r < rows; r += blockDim.x / D) {
+  for (; job < jobs; job += stride) {
+    int4 cut;
+    if constexpr (kGroups > 1) {
+      cut = cuts[job / slices];
+    } else {
+      cut = d.cuts[blockIdx.x];
+      cut.w = blockIdx.x;
+    }
+    const int r = job % slices * per_job + unit / kGroups;
     float m = -INFINITY, l = 0.f, o = 0.f;
-    for (int i0 = c; i0 <= cut.w; i0 += kParts) {
-      float2 ml[kParts];
-      float x[kParts];
+    if (r < a.group) {
+      for (int i0 = cut.w + group; i0 <= cut.z; i0 += kParts * kGroups) {
+        float2 ml[kParts];
+        float x[kParts];
 #pragma unroll
-      for (int p = 0; p < kParts; ++p) {
-        ml[p] = make_float2(-INFINITY, 0.f);
-        const int i = i0 + p;
-        if (i > cut.w) continue;
-        const int64_t at = (2 * static_cast<int64_t>(i) + (i == c ? 1 : 0)) * kRows + r;
-        ml[p] = d.part_ml[at];
-        x[p] = d.part_o[at * D + dim];
-      }
+        for (int p = 0; p < kParts; ++p) {
+          ml[p] = make_float2(-INFINITY, 0.f);
+          const int i = i0 + p * kGroups;
+          if (i > cut.z) continue;
+          const int64_t at = (2 * static_cast<int64_t>(i) + (i == cut.w ? 1 : 0)) * kRows + r;
+          ml[p] = d.part_ml[at];
+          x[p] = d.part_o[at * D + dim];
+        }
 #pragma unroll
-      for (int p = 0; p < kParts; ++p) {
-        if (ml[p].x == -INFINITY) continue;  // no part
-        const float top = fmaxf(m, ml[p].x);
-        const float f = gdn::exp2_approx(m - top), g = gdn::exp2_approx(ml[p].x - top);
-        m = top;
-        o = o * f + x[p] * g;
-        l = l * f + ml[p].y * g;
+        for (int p = 0; p < kParts; ++p) {
+          if (ml[p].x == -INFINITY) continue;  // no part
+          const float top = fmaxf(m, ml[p].x);
+          const float f = gdn::exp2_approx(m - top), g = gdn::exp2_approx(ml[p].x - top);
+          m = top;
+          o = o * f + x[p] * g;
+          l = l * f + ml[p].y * g;
+        }
       }
     }
-    const int64_t row = static_cast<int64_t>(cut.x) * a.Hq + cut.y * a.group + cut.z * kRows + r;
-    a.o[row * D + dim] = __float2bfloat16(o / l);
-    if (a.lse && dim == 0) a.lse[row] = (m + log2f(l)) / gdn::kLog2e;
+    if constexpr (kGroups > 1) {
+      __syncthreads();  // the last job's values have been read
+      group_o[tid] = o;
+      if (dim == 0) group_ml[unit] = make_float2(m, l);
+      __syncthreads();
+      if (group == 0) {
+        for (int i = 1; i < kGroups; ++i) {
+          const float2 ml = group_ml[unit + i];
+          if (ml.x == -INFINITY) continue;
+          const float top = fmaxf(m, ml.x);
+          const float f = gdn::exp2_approx(m - top), g = gdn::exp2_approx(ml.x - top);
+          m = top;
+          o = o * f + group_o[tid + i * D] * g;
+          l = l * f + ml.y * g;
+        }
+      }
+    }
+    if (group == 0 && r < a.group) {
+      const int64_t row = static_cast<int64_t>(cut.x) * a.Hq + cut.y * a.group + r;
+      a.o[row * D + dim] = __float2bfloat16(o / l);
+      if (a.lse && dim == 0) a.lse[row] = (m + log2f(l)) / gdn::kLog2e;
+    }
   }
 }
-
-constexpr int kMaxGrid = 2 * 160;  // two CTAs per SM
 
 // Where even the longest sequence is a few blocks, one CTA takes a whole item: the
 // scan of the batch and the join's launch would cost more than the blocks.
@@ -530,8 +582,7 @@ int launch(const DecodeArgs& base, const gdn_kv_cache* cache, const gdn_page_tab
   CUtensorMap k_map, v_map;
   if ((rc = gdn_host::encode_cache_map(&k_map, cache->k, cache, d.a.box_shift)) != GDN_OK) return rc;
   if ((rc = gdn_host::encode_cache_map(&v_map, cache->v, cache, d.a.box_shift)) != GDN_OK) return rc;
-  d.passes = (d.a.group + kRows - 1) / kRows;
-  const int64_t items = static_cast<int64_t>(table->num_seqs) * d.a.Hkv * d.passes;
+  const int64_t items = static_cast<int64_t>(table->num_seqs) * d.a.Hkv;
   int grid = 2 * sms < kMaxGrid ? 2 * sms : kMaxGrid;
   if (d.whole && items < grid) grid = static_cast<int>(items);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -540,13 +591,22 @@ int launch(const DecodeArgs& base, const gdn_kv_cache* cache, const gdn_page_tab
   d.part_o = reinterpret_cast<float*>(ws + kMaxGrid * sizeof(int4) + sizeof(float2) * 2 * kMaxGrid * kRows);
   rc = gdn_host::launch_pdl(decode_attention_kernel<D>, dim3(grid), dim3(kThreads), smem, stream, d, k_map, v_map);
   if (rc != GDN_OK || d.whole) return rc;
-  return gdn_host::launch_pdl(decode_join_kernel<D>, dim3(grid), dim3(D * std::min(std::min(d.a.group, kRows), 1024 / D)), 0, stream, d);
+  if (items * 8 > grid) {
+    const int rows = d.a.group * D > kJoinThreads ? kJoinThreads / D : d.a.group;
+    return gdn_host::launch_pdl(decode_join_kernel<D, 1>, dim3(grid), dim3(rows * D), 0, stream, d, grid);
+  }
+  const int per_job = kJoinThreads / D / 8;
+  const int64_t jobs = items * ((d.a.group + per_job - 1) / per_job);
+  const int blocks = jobs < grid ? static_cast<int>(jobs) : grid;
+  return gdn_host::launch_pdl(decode_join_kernel<D, 8>, dim3(blocks), dim3(kJoinThreads), 0, stream, d, grid);
 }
 
 }  // namespace
 
 extern "C" size_t gdn_attention_decode_workspace_bytes(int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D,
                                                        int32_t num_entries, int32_t page_size) {
+  if (Hkv >= 1 && Hq / Hkv > kRows)  // see gdn_attention_decode_paged
+    return gdn_attention_workspace_bytes(num_seqs, num_seqs, Hq, Hkv, D, num_entries, page_size);
   if (num_seqs < 0 || num_entries < 0 || page_size < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
   return workspace_bytes_of(D, whole_items(num_seqs, num_entries, page_size));
 }
@@ -555,6 +615,13 @@ extern "C" int gdn_attention_decode_paged(const gdn_bf16* q, int64_t q_token_str
                                           int32_t Hq, const gdn_kv_cache* cache, const gdn_page_table* table,
                                           float scale, const gdn_attention_options* options, void* workspace,
                                           size_t workspace_bytes, int32_t* err_word, void* stream) {
+  // More query heads per key head than this kernel's rows would read the cache once
+  // for every sixteen; the chunk kernel has 128 rows (64 sequences of 8,192, 17 / 64
+  // / 128 query heads on one key head: 87 / 160 / 229 us here, 58 / 59 / 61 there;
+  // 16: 53 here, 58 there).
+  if (cache && cache->num_heads >= 1 && Hq / cache->num_heads > kRows)
+    return gdn_attention_paged(q, q_token_stride, o, lse, nullptr, table ? table->num_seqs : 0, Hq, cache, table, scale,
+                               options, workspace, workspace_bytes, err_word, stream);
   DecodeArgs d = {};
   const int32_t n = table ? table->num_seqs : 0;
   d.whole = cache && table && whole_items(n, table->num_entries, cache->page_size);

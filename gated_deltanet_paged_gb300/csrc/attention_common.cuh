@@ -233,8 +233,9 @@ namespace gdn_host {
 
 // Checks of a page table and a cache that need no device data.
 inline int check_paged(const gdn_kv_cache* c, const gdn_page_table* t, const int32_t* cu_seqlens, int32_t total_tokens) {
-  if (!c || !t || !c->k || !c->v || !t->page_indices || !t->page_indptr || !t->last_page_len)
-    return GDN_ERR_INVALID_ARGUMENT;
+  if (!c || !t || !c->k || !c->v || !t->page_indptr) return GDN_ERR_INVALID_ARGUMENT;
+  // An array without entries may be NULL, as an empty tensor's pointer is.
+  if ((!t->page_indices && t->num_entries != 0) || (!t->last_page_len && t->num_seqs != 0)) return GDN_ERR_INVALID_ARGUMENT;
   if (t->num_seqs < 0 || t->num_entries < 0 || total_tokens < 0 || c->num_pages < 1 || c->page_size < 1 ||
       c->num_heads < 1 || c->head_dim < 8 || c->head_dim % 8 != 0)
     return GDN_ERR_INVALID_ARGUMENT;

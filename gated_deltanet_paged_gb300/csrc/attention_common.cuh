@@ -318,13 +318,16 @@ inline int attention_args(gdn::AttnArgs* a, const gdn_bf16* q, int64_t q_stride,
   a->scale_log2 = cap > 0.f ? 2.f * s / cap * gdn::kLog2e : s * gdn::kLog2e;
   a->slopes = options ? options->slopes : nullptr;
   a->full_lens = options ? options->full_lens : nullptr;
-  a->window = options ? options->window : -1;
+  // No sequence has 2^30 tokens, so that a larger window hides nothing; the kernels
+  // add to distances in 32 bits.
+  a->window = options && options->window < (1 << 30) ? options->window : -1;
   while ((1 << a->box_shift) < tile_keys && cache->page_size % (2 << a->box_shift) == 0) ++a->box_shift;
   return GDN_OK;
 }
 
 // The longest sequence that a table can hold has every entry that the others do
-// not need.
+// not need, where each has a page.  Beside sequences without any it can be longer:
+// the calls are right all the same, but leave it whole.
 inline int64_t longest_sequence(int32_t num_seqs, int32_t num_entries, int32_t page_size) {
   return (static_cast<int64_t>(num_entries) - num_seqs + 1) * page_size;
 }

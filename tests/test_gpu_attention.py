@@ -193,6 +193,16 @@ def test_chunk_options(name, hq, hkv, dim, page_size):
         check_attention(b, **_options(name, hq, len(b.new)))
 
 
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("window", [2**30 - 1, 2**30, 2**31 - 1])
+def test_windows_beyond_any_sequence_hide_nothing(decode, window):
+    new, prefix = ([1] * 3, [20, 1500, 0]) if decode else ([200, 3, 65], [20, 1500, 0])
+    b = Batch(new, prefix, 64, 32, 8, 128, seed=22).fill()
+    o, lse = check_attention(b, decode=decode, window=window)
+    o2, lse2 = check_attention(b, decode=decode)
+    assert torch.equal(o.view(I16), o2.view(I16)) and torch.equal(lse, lse2)
+
+
 def test_single_row_groups_of_every_size():
     """Every number of query heads per key head up to the largest."""
     for g in (1, 2, 3, 5, 9, 16, 17, 31, 43, 64, 65, 100, 128):
@@ -211,6 +221,7 @@ SHARED = {
     "few items of unlike lengths": ([40, 64, 1], [5000, 90, 700]),
     "items longer than a share of the line": ([750], [4000]),
     "many items, some long": ([900, 1, 300], [300, 2500, 1100]),
+    "a long one beside sequences without pages": ([0] * 60 + [40] + [0] * 9, [0] * 60 + [3000] + [0] * 9),
 }
 
 

@@ -101,6 +101,8 @@ def attention_f64(batch, *, scale=0.0, softcap=0.0, window=-1, slopes=None, full
     g = batch.hq // batch.hkv
     scale = scale if scale > 0 else batch.dim**-0.5
     for b, (n, p) in enumerate(zip(batch.new, batch.prefix)):
+        if n == 0:
+            continue
         q = batch.q[t : t + n].double().cpu().transpose(0, 1)
         k = batch.k[b].double().transpose(0, 1).repeat_interleave(g, 0)
         v = batch.v[b].double().transpose(0, 1).repeat_interleave(g, 0)

@@ -31,9 +31,10 @@
 // prompts of 8,192 1.33 ms, 1,650 TFLOP/s, 0.89 of a library matrix product's best;
 // the tensor pipe is active for 80% of the cycles, and what is left are the turns of
 // the two tiles and the items' ends.  512 tokens over 131,072 625 us, 1,760 TFLOP/s;
-// 16 over 131,072 97 us, 5.5 TB/s.  With a cap of 30 1,090 TFLOP/s: two softmax
-// warps per scheduler do not hide the latency of its instructions (issue 46%, no
-// pipe above 50%).  The shortest calls, 9 us, are launch and one block's latency.
+// 16 over 131,072 97 us, 5.5 TB/s.  With a cap of 30 1,160 TFLOP/s: the
+// softmax takes longer than the products (heads of 64, with half of them, take nine
+// tenths of the time), at 0.5 instructions per cycle; four warps per scheduler
+// instead of two, half a row each, issue no more.  The shortest calls, 9 us, are launch and one block's latency.
 #include <type_traits>
 
 #include "attention_common.cuh"
@@ -339,23 +340,26 @@ __device__ __forceinline__ float max128(const float (&s)[128]) {
   return gdn::max3(gdn::max3(top[0], top[1], s[124]), gdn::max3(top[2], s[125], s[126]), fmaxf(top[3], s[127]));
 }
 // Cap of 32 scores in TMEM columns from addr, into units of log2.  Where the
-// warp's scores stay within the cap (they mostly do), the polynomial; else the
-// exponential form, four scores at a time by way of TMEM: it is rarely taken, and
-// its instructions would stand between those of the other (1.73 -> 1.60 ms on the
-// 64 mixed sequences).
+// warp's scores stay within the cap (they mostly do), the polynomial, which is
+// evaluated beside the maximum that decides it (64 mixed sequences 1.50 -> 1.46 ms).
+// Else the exponential form, four scores at a time by way of TMEM: it is rarely
+// taken, and its instructions would stand between those of the other (1.73 -> 1.60 ms).
 __device__ __forceinline__ void cap_scores(const AttnArgs& a, const float2 (&poly)[5], uint32_t addr, float (&x)[32]) {
-  float big[4] = {fabsf(x[0]), fabsf(x[1]), fabsf(x[2]), fabsf(x[3])};
+  float big[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-  for (int i = 4; i < 32; ++i) big[i & 3] = fmaxf(big[i & 3], fabsf(x[i]));
-  const float most = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
-  if (__all_sync(0xFFFFFFFFu, most <= a.cap_poly_max)) {
+  for (int i = 4; i < 28; i += 8) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const float2 y = gdn::capped_near(make_float2(x[i], x[i + 1]), poly);
-      x[i] = y.x;
-      x[i + 1] = y.y;
-    }
-  } else {
+    for (int k = 0; k < 4; ++k) big[k] = gdn::max3_abs(big[k], x[i + 2 * k], x[i + 2 * k + 1]);
+  }
+  const float most = gdn::max3_abs(gdn::max3_abs(big[0], x[28], x[29]), gdn::max3_abs(big[1], x[30], x[31]),
+                                   gdn::max3_abs(big[2], big[3], 0.f));
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float2 y = gdn::capped_near(make_float2(x[i], x[i + 1]), poly);
+    x[i] = y.x;
+    x[i + 1] = y.y;
+  }
+  if (!__all_sync(0xFFFFFFFFu, most <= a.cap_poly_max)) {
 #pragma unroll 1
     for (int i = 0; i < 32; i += 4) {
       uint32_t z[4];
@@ -1168,6 +1172,13 @@ int launch(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache* cache, void* w
   int rc = gdn_host::func_attr_once(chunk_attention_kernel<D, kScores>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem,
                                     done);
   if (rc != GDN_OK) return rc;
+  // The register split would wait for ever in a block that holds fewer.
+  static const bool fits = [] {
+    cudaFuncAttributes attr;
+    return cudaFuncGetAttributes(&attr, chunk_attention_kernel<D, kScores>) == cudaSuccess &&
+           attr.numRegs * kThreads >= 256 * (kSoftmaxRegs + kOtherRegs);
+  }();
+  if (!fits) return GDN_ERR_CUDA;
   CUtensorMap q_map, k_map, v_map;
   const int64_t dims[4] = {D, d.a.group, total_tokens, d.a.Hkv};
   const int64_t strides[3] = {2 * D, 2 * d.a.q_stride, 2 * static_cast<int64_t>(d.a.group) * D};

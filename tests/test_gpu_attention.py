@@ -182,7 +182,7 @@ def _options(name, hq, seqs):
 
 
 OPTIONS = ["cap", "slope", "window0", "window1", "window100", "window5000", "prefix", "cap slope window200", "scale",
-           "cap slope prefix scale", "highcap", "highcap slope window64"]
+           "cap slope prefix scale", "highcap", "highcap slope window64", "cap window100", "cap prefix", "cap window0"]
 
 
 @pytest.mark.parametrize("name", OPTIONS)
@@ -230,6 +230,18 @@ SHARED = {
 def test_every_way_of_sharing_out(name, window):
     b = Batch(*SHARED[name], 64, 32, 8, 128, seed=21).fill()
     check_attention(b, window=window)
+
+
+@pytest.mark.parametrize("name", list(SHARED))
+def test_every_way_of_sharing_out_under_a_cap(name):
+    b = Batch(*SHARED[name], 64, 32, 8, 64, seed=23, q_scale=3.0).fill()
+    check_attention(b, softcap=20.0, window=900)
+
+
+@pytest.mark.parametrize("g", [1, 3, 16, 43, 100, 128])
+def test_groups_under_a_cap(g):
+    b = Batch([3, 150, 0, 1], [70, 300, 9, 0], 32, g, 1, 128, seed=g, q_scale=4.0).fill()
+    check_attention(b, softcap=6.0)
 
 
 # -------------------------------------------------------------------- decode

@@ -179,7 +179,10 @@ struct Layout {
   static constexpr uint32_t kColS = 0, kColO = 256;    // TMEM columns: S of both tiles, O of both tiles
 };
 
-// Sum over the CTA's threads before this one, and over all.
+// Sum over the CTA's threads before this one, and over all.  Two sums go as one:
+// one of less than kFlag, and that of a flag above it.
+constexpr int kFlag = 1 << 20;
+static_assert(kThreads * (kMaxGrid + 1) < kFlag && kThreads < (1 << 11), "sums of both parts");
 template <typename T>
 __device__ __forceinline__ T scan_block(int64_t* scratch64, T mine, T* total) {
   T* const scratch = reinterpret_cast<T*>(scratch64);
@@ -420,28 +423,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) gdn::record_error(a.paged.err_word, GDN_DEVERR_TIMEOUT, 0);
     return;
   }
-  if (tid == 0) {
-    for (int i = 0; i < L::kStages; ++i) {
-      gdn::mbar_init(&sh.full[i], 1);
-      gdn::mbar_init(&sh.empty[i], 2);
-      gdn::mbar_init(&sh.raw[i], 1);
-    }
+  // Forty barriers, by several warps.
+  if (tid < L::kStages) {
+    gdn::mbar_init(&sh.full[tid], 1);
+    gdn::mbar_init(&sh.empty[tid], 2);
+    gdn::mbar_init(&sh.raw[tid], 1);
+    gdn::fence_mbar_init();
+  } else if (tid >= 32 && tid < 34) {
+    const int t = tid - 32;
+    gdn::mbar_init(&sh.done[t], 1);
+    gdn::mbar_init(&sh.s_full[t], 1);
+    gdn::mbar_init(&sh.p_full[t][0], 4);
+    gdn::mbar_init(&sh.p_full[t][1], 4);
+    gdn::mbar_init(&sh.o_last[t], 1);
+    gdn::mbar_init(&sh.o_free[t], 4);
+    gdn::mbar_init(&sh.stat_full[t], 4);
+    gdn::mbar_init(&sh.turn[t], 1);
+    gdn::fence_mbar_init();
+  } else if (tid >= 64 && tid < 64 + kSegments) {
+    gdn::mbar_init(&sh.seg_full[tid - 64], 1);
+    gdn::mbar_init(&sh.seg_empty[tid - 64], kThreads / 32 - 1);
+    gdn::fence_mbar_init();
+  } else if (tid == 96) {
     gdn::mbar_init(&sh.q_full, 1);
     gdn::mbar_init(&sh.q_empty, 2);
-    for (int t = 0; t < 2; ++t) {
-      gdn::mbar_init(&sh.done[t], 1);
-      gdn::mbar_init(&sh.s_full[t], 1);
-      gdn::mbar_init(&sh.p_full[t][0], 4);
-      gdn::mbar_init(&sh.p_full[t][1], 4);
-      gdn::mbar_init(&sh.o_last[t], 1);
-      gdn::mbar_init(&sh.o_free[t], 4);
-      gdn::mbar_init(&sh.stat_full[t], 4);
-      gdn::mbar_init(&sh.turn[t], 1);
-    }
-    for (int i = 0; i < kSegments; ++i) {
-      gdn::mbar_init(&sh.seg_full[i], 1);
-      gdn::mbar_init(&sh.seg_empty[i], kThreads / 32 - 1);
-    }
     sh.abort = 0;
     gdn::fence_mbar_init();
   }
@@ -476,10 +481,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       pairs = min(pairs + s.pairs, kMaxGrid + 1);  // no more are told apart
       is_long = is_long || (s.pairs && s.len > kWholeKeys);
     }
-    const bool whole = d.whole || !__syncthreads_or(is_long);
-    int all_pairs;
-    const int pairs_before = scan_block(sh.scan, pairs, &all_pairs);
-    const int64_t all_items = static_cast<int64_t>(all_pairs) * a.Hkv;
+    // Pairs, and in the upper bits threads with a long sequence.
+    int all;
+    const int pairs_before = scan_block(sh.scan, pairs + (is_long ? kFlag : 0), &all) % kFlag;
+    const bool whole = d.whole || all < kFlag;
+    const int64_t all_items = static_cast<int64_t>(all % kFlag) * a.Hkv;
     bool aligned = all_items <= min(grid, kMaxGrid);
     if (aligned && whole) {
       // A CTA for every item.
@@ -529,11 +535,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                               static_cast<float>(sum)));
         pieces = min(pieces, max(1, blocks / kMinBlocks));
       }
-      const int piece = c - scan_block(sh.scan, pieces, &pieces_total);
       // Unless a piece is longer than a share of the line and the cost of a second
       // segment (512 tokens over 131,072 are 64 items: 128 of 152 CTAs would work).
       const bool longer = pieces && x.cost / pieces > (sum / grid + kCrossing) * kKeys;
-      aligned = !__syncthreads_or(longer);
+      const int piece = c - scan_block(sh.scan, pieces + (longer ? kFlag : 0), &pieces_total) % kFlag;
+      aligned = pieces_total < kFlag;
       idle = c >= pieces_total;
       if (aligned && piece >= 0 && piece < pieces) {
         // As a walk along a line on which the item begins at 0.

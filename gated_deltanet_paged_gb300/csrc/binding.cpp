@@ -4,7 +4,7 @@
 // At decode sizes these calls last 2 to 10 microseconds on the GPU.  Checked from
 // Python and made through ctypes each took 11 to 25 us of host time, most of it
 // in property lookups and in allocating outputs between launches; here the same
-// checks, the allocations and the C call take 4 to 6.  Every function checks
+// checks, the allocations and the C call take 4 to 7.  Every function checks
 // types, shapes and devices, makes one call of include/gdn_paged.h on the current
 // stream, and raises on a non-zero status.
 #include <Python.h>

@@ -347,7 +347,7 @@ __device__ __forceinline__ float max128(const float (&s)[128]) {
 // evaluated beside the maximum that decides it (64 mixed sequences 1.50 -> 1.46 ms).
 // Else the exponential form, four scores at a time by way of TMEM: it is rarely
 // taken, and its instructions would stand between those of the other (1.73 -> 1.60 ms).
-__device__ __forceinline__ void cap_scores(const AttnArgs& a, const float2 (&poly)[5], uint32_t addr, float (&x)[32]) {
+__device__ __forceinline__ void cap_scores(const AttnArgs& a, const gdn::CapPoly& poly, uint32_t addr, float (&x)[32]) {
   float big[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
   for (int i = 4; i < 28; i += 8) {
@@ -362,13 +362,13 @@ __device__ __forceinline__ void cap_scores(const AttnArgs& a, const float2 (&pol
     x[i] = y.x;
     x[i + 1] = y.y;
   }
-  if (!__all_sync(0xFFFFFFFFu, most <= a.cap_poly_max)) {
+  if (!__all_sync(0xFFFFFFFFu, most <= a.cap_near)) {
 #pragma unroll 1
     for (int i = 0; i < 32; i += 4) {
       uint32_t z[4];
       tmem_ld4(addr + i, z);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) z[k] = __float_as_uint(gdn::capped(__uint_as_float(z[k]) * a.scale_log2, a.cap_log2));
+      for (int k = 0; k < 4; ++k) z[k] = __float_as_uint(gdn::capped(__uint_as_float(z[k]), a));
       tmem_st4(addr + i, z);
     }
     gdn::tmem_ld32(addr, x);
@@ -905,9 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t * tile_tokens >= tokens) continue;
       float m = kScores == kBounded ? 0.f : -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
-      float2 poly[5];
-#pragma unroll
-      for (int i = 0; i < 5; ++i) poly[i] = make_float2(a.cap_poly[i], a.cap_poly[i]);
+      const gdn::CapPoly poly(a);
       for (int j = 0; j < blocks; ++j, ++n) {
         const int key0 = seg_key0 + j * kKeys;
         ok = wait_inline(&sh.s_full[t], n & 1, abort_flag);

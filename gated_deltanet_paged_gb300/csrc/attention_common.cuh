@@ -62,10 +62,11 @@ struct AttnArgs {
   float* lse;  // nullptr: not wanted
   PagedTokens paged;
   int32_t Hq, Hkv, group;
-  float scale_log2;           // scale * log2(e); with a cap: 2 scale log2(e) / cap, the tanh's argument
+  float scale_log2;           // scale * log2(e)
   float cap_log2;             // cap * log2(e), 0: no cap
-  float cap_poly[5];          // cap * tanh(s * scale / cap) * log2(e) / s as a polynomial in s^2 ...
-  float cap_poly_max;         // ... for |s| up to this (0: not used)
+  float cap_unit;             // scale / cap: the tanh's argument is u = score * cap_unit
+  float cap_poly[5];          // log2(e) * scale * tanh(u) / u as a polynomial in score^2 ...
+  float cap_near;             // ... for scores up to this
   const float* slopes;        // [Hq] or nullptr
   const int32_t* full_lens;   // [num_seqs] or nullptr
   int32_t window;             // < 0: none
@@ -96,14 +97,59 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// cap * tanh(s * scale / cap) in units of log2: tanh(z) = 1 - 2 / (e^(2 z) + 1),
-// with x = 2 z log2(e).  Off by about 2^-23 of the cap, and exact at the ends
-// (e^(2 z) overflows to infinity or vanishes); the hardware tanh is off by
-// 2^-11 of it, a weight error of 1 percent under a cap of 30.
-__device__ __forceinline__ float capped(float x, float cap_log2) {
+// cap * tanh(u), u = s * scale / cap, in units of log2.
+//   |u| <= 0.75: s * scale * log2(e) * (tanh(u) / u), the quotient as a polynomial in
+//     u^2 (kCapPoly).  Its error is relative to the score, 5.7e-7, so that a cap
+//     far above the scores leaves them as they are.
+//   else: cap * (1 - 2 / (e^(2 u) + 1)), off by about 2^-23 of the cap, which is 2^-22
+//     of the result there, and exact at the ends (e^(2 u) overflows to infinity or
+//     vanishes).
+// The hardware tanh is off by 2^-11 of the cap, a weight error of 1 percent under
+// one of 30.
+constexpr float kCapNear = 0.75f;
+// tanh(u) / u for |u| <= 0.75 as a polynomial in u^2, fitted by least squares on
+// Chebyshev nodes reweighted towards the minimax error (5.7e-07 relative).
+constexpr double kCapPoly[5] = {0.9999994349237419, -0.3332825153150915, 0.1325898321214035, -0.05005630243018433, 0.0129296321851392};
+
+// |s| <= cap_near, two scores on the FMA pipe alone: six operations a pair, where the
+// exponential form takes three trips a score through the special function unit.
+// (Seven, with u^2 instead of s^2 as the variable: 4 x 8,192 tokens 1.97 ms, 1.87 so.)
+struct CapPoly {
+  float2 c[5];
+  __device__ __forceinline__ explicit CapPoly(const AttnArgs& a) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) c[i] = make_float2(a.cap_poly[i], a.cap_poly[i]);
+  }
+};
+__device__ __forceinline__ float2 capped_near(float2 s, const CapPoly& p) {
+  const float2 t = __fmul2_rn(s, s);
+  float2 h = __ffma2_rn(p.c[4], t, p.c[3]);
+  h = __ffma2_rn(h, t, p.c[2]);
+  h = __ffma2_rn(h, t, p.c[1]);
+  h = __ffma2_rn(h, t, p.c[0]);
+  return __fmul2_rn(s, h);
+}
+// The same for one score, rounding by rounding: a score has the same bits whichever
+// of these functions took it, so that what decides between them shows nowhere.
+__device__ __forceinline__ float capped_near(float s, const AttnArgs& a) {
+  const float t = __fmul_rn(s, s);
+  float h = fmaf(a.cap_poly[4], t, a.cap_poly[3]);
+  h = fmaf(h, t, a.cap_poly[2]);
+  h = fmaf(h, t, a.cap_poly[1]);
+  h = fmaf(h, t, a.cap_poly[0]);
+  return __fmul_rn(s, h);
+}
+// Any score.
+__device__ __forceinline__ float capped(float s, const AttnArgs& a) {
+  const float u = s * a.cap_unit, t = u * u;
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(exp2_approx(x) + 1.f));
-  return fmaf(-2.f * cap_log2, r, cap_log2);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(exp2_approx(u * (2.f * kLog2e)) + 1.f));
+  float x = fmaf(-2.f * a.cap_log2, r, a.cap_log2);
+  constexpr float c0 = kCapPoly[0], c1 = kCapPoly[1], c2 = kCapPoly[2], c3 = kCapPoly[3], c4 = kCapPoly[4];
+  const float h = fmaf(fmaf(fmaf(fmaf(c4, t, c3), t, c2), t, c1), t, c0);
+  if (fabsf(u) <= kCapNear) x = s * a.scale_log2 * h;
+  if (fabsf(s) <= a.cap_near) x = capped_near(s, a);
+  return x;
 }
 
 // A line of `total` units in equal pieces for `eff` CTAs: piece c is [start(c),
@@ -140,18 +186,6 @@ __device__ __forceinline__ int small_quotient(int64_t x, int d, int most) {
   while (static_cast<int64_t>(c + 1) * d <= x) ++c;
   while (static_cast<int64_t>(c) * d > x) --c;
   return c;
-}
-
-// The same for two scores within the polynomial's range, on the FMA pipe alone:
-// six operations a score, where capped() takes three trips through the special
-// function unit and the exponential that follows a fourth.
-__device__ __forceinline__ float2 capped_near(float2 s, const float2 (&poly)[5]) {
-  const float2 t = __fmul2_rn(s, s);
-  float2 h = __ffma2_rn(poly[4], t, poly[3]);
-  h = __ffma2_rn(h, t, poly[2]);
-  h = __ffma2_rn(h, t, poly[1]);
-  h = __ffma2_rn(h, t, poly[0]);
-  return __fmul2_rn(s, h);
 }
 
 // Keys that a token at `pos` sees: [lo, hi).
@@ -309,19 +343,27 @@ inline int attention_args(gdn::AttnArgs* a, const gdn_bf16* q, int64_t q_stride,
   a->group = Hq / Hkv;
   const float s = scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(D));
   if (!(s <= 3.0e38f) || (cap > 0.f && !(2.f * s / cap * gdn::kLog2e <= 3.0e38f))) return GDN_ERR_INVALID_ARGUMENT;
-  a->cap_log2 = cap > 0.f ? cap * gdn::kLog2e : 0.f;
-  // tanh(u) / u for |u| <= 0.75 as a polynomial in u^2, fitted by least squares on
-  // Chebyshev nodes reweighted towards the minimax error (5.7e-07 relative), with
-  // u = s * k and the cap folded into the coefficients.  Where k^9 would leave
-  // the normal numbers of fp32, the kernels use the exponential form.
-  constexpr double kPoly[5] = {0.9999994349237419, -0.3332825153150915, 0.1325898321214035, -0.05005630243018433, 0.0129296321851392};
-  const double k = cap > 0.f ? static_cast<double>(s) / cap : 0.0;
-  if (k >= 1e-4 && k <= 1e3) {
-    double scaled = k * cap * 1.4426950408889634;
-    for (int i = 0; i < 5; ++i, scaled *= k * k) a->cap_poly[i] = static_cast<float>(kPoly[i] * scaled);
-    a->cap_poly_max = static_cast<float>(0.75 / k);
+  a->scale_log2 = s * gdn::kLog2e;
+  if (cap > 0.f) {
+    a->cap_log2 = cap * gdn::kLog2e;
+    a->cap_unit = s / cap;
+    // The polynomial in the score has the powers of cap_unit in its coefficients.
+    // Those that leave the normal numbers (scale / cap below about 4e-5) are left out,
+    // and it is used up to where they would weigh 2^-24 of the whole.
+    constexpr double kUpTo[5] = {4e-4, 0.025, 0.1, 0.2, (1.0 - 1e-6) * gdn::kCapNear};
+    const double k = static_cast<double>(s) / cap;
+    double c[5], power = s * 1.4426950408889634;
+    bool fits = true;
+    for (int i = 0; i < 5; ++i, power *= k * k) {
+      c[i] = gdn::kCapPoly[i] * power;
+      fits = fits && fabs(c[i]) < 1e38;
+    }
+    int top = 4;
+    while (top > 0 && fabs(c[top]) < 1.2e-38) --top;
+    for (int i = 0; i <= top && fits; ++i) a->cap_poly[i] = static_cast<float>(c[i]);
+    // Scores whose squares are finite.
+    a->cap_near = fits ? static_cast<float>(fmin(kUpTo[top] / k, 1e19)) : -1.f;
   }
-  a->scale_log2 = cap > 0.f ? 2.f * s / cap * gdn::kLog2e : s * gdn::kLog2e;
   a->slopes = options ? options->slopes : nullptr;
   a->full_lens = options ? options->full_lens : nullptr;
   // No sequence has 2^30 tokens, so that a larger window hides nothing; the kernels

@@ -326,12 +326,32 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         const bool edge = lo > 0 || hi < 16 * kSub;
         float top[2] = {m[0], m[1]};
+        if (a.cap_log2 > 0.f) {
+          float most = 0.f;
+#pragma unroll
+          for (int j = 0; j < 2 * kSub; ++j) most = gdn::max3_abs(gdn::max3_abs(most, s[j][0], s[j][1]), s[j][2], s[j][3]);
+          if (__all_sync(0xFFFFFFFFu, most <= a.cap_near)) {
+#pragma unroll
+            for (int j = 0; j < 2 * kSub; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[j][i] = gdn::capped_near(s[j][i], a);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2 * kSub; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[j][i] = gdn::capped(s[j][i], a);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2 * kSub; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[j][i] *= a.scale_log2;
+        }
 #pragma unroll
         for (int j = 0; j < 2 * kSub; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float x = s[j][i] * a.scale_log2;
-            if (a.cap_log2 > 0.f) x = gdn::capped(x, a.cap_log2);
+            float x = s[j][i];
             const int key = j * 8 + 2 * t + (i & 1);
             if (a.slopes) x = fmaf(-slope[i >> 1], static_cast<float>(w.it.s.len - 1 - (key0 + key)), x);
             if (edge && (key < lo || key >= hi)) x = -INFINITY;

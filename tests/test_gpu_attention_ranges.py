@@ -1,0 +1,48 @@
+"""Attention at the ends of its options' ranges, on the GPU against the definition
+in 64 bits: soft caps from far below the scores to far above them, and what
+unread slots may change (nothing).  Tolerances as derived in attention_util.py."""
+import pytest
+import torch
+
+import gated_deltanet_paged_gb300 as gdn
+from attention_util import Batch, check_attention
+
+pytestmark = pytest.mark.gpu
+
+I16 = torch.int16
+
+
+def _batch(decode, dim, q_scale, seed=41):
+    new, prefix = ([1] * 4, [700, 0, 63, 2000]) if decode else ([140, 3, 0, 64], [700, 0, 63, 300])
+    return Batch(new, prefix, 64, 8, 2, dim, seed=seed, q_scale=q_scale).fill()
+
+
+# The capped score tends to the score itself as the cap grows: a form with an error
+# that is a fixed part of the cap loses every score under a large one.
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("cap", [5e-5, 0.01, 1.0, 50.0, 60.0, 884.0, 1e3, 1e4, 1e5, 1e6, 1e8, 1e30, 3e38])
+def test_caps_of_every_size(decode, cap):
+    for dim, q_scale in ((128, 1.0), (64, 40.0)):
+        check_attention(_batch(decode, dim, q_scale), decode=decode, softcap=cap)
+
+
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("cap", [2.0, 900.0, 1e6, 1e30])
+def test_caps_with_a_bias(decode, cap):
+    slopes = torch.tensor([2.0 ** -(h + 1) for h in range(8)], device="cuda")
+    check_attention(_batch(decode, 128, 20.0), decode=decode, softcap=cap, slopes=slopes)
+
+
+@pytest.mark.parametrize("decode", [False, True])
+def test_slots_past_the_end_change_no_bit_under_a_cap(decode):
+    """The last page's slots past the sequence's end are copied along with the
+    tokens: their scores may be anything, and decide nothing."""
+    first = None
+    for junk in (0.0, float("nan"), 3.0, 1e30, float("inf")):
+        b = _batch(decode, 128, 2.0)
+        b.k_cache.fill_(junk)
+        b.v_cache.fill_(junk)
+        o, lse = check_attention(b.fill(), decode=decode, softcap=30.0)
+        if first is None:
+            first = o.clone(), lse.clone()
+        assert torch.equal(o.view(I16), first[0].view(I16)) and torch.equal(lse, first[1]), "slots hold %r" % junk

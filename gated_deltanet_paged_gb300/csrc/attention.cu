@@ -232,6 +232,7 @@ struct Smem {
   uint64_t o_last[2];      // O of a segment is complete
   uint64_t o_free[2];      // ... and has been read
   uint64_t stat_full[2];
+  uint64_t mid[2];         // the first half of P V of a block is complete (kCapped)
   uint64_t turn[2];        // the other tile's products of a block have been issued
   uint64_t seg_full[kSegments], seg_empty[kSegments];
   int64_t scan[kThreads / 32];
@@ -342,20 +343,32 @@ __device__ __forceinline__ float max128(const float (&s)[128]) {
   }
   return gdn::max3(gdn::max3(top[0], top[1], s[124]), gdn::max3(top[2], s[125], s[126]), fmaxf(top[3], s[127]));
 }
-// Cap of 32 scores in TMEM columns from addr, into units of log2.  Where the
-// warp's scores stay within the cap (they mostly do), the polynomial, which is
-// evaluated beside the maximum that decides it (64 mixed sequences 1.50 -> 1.46 ms).
-// Else the exponential form, four scores at a time by way of TMEM: it is rarely
-// taken, and its instructions would stand between those of the other (1.73 -> 1.60 ms).
-__device__ __forceinline__ void cap_scores(const AttnArgs& a, const gdn::CapPoly& poly, uint32_t addr, float (&x)[32]) {
+// The largest of 32 values either way, and of `top`.
+__device__ __forceinline__ float largest32(const float (&x)[32], float top) {
   float big[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
   for (int i = 4; i < 28; i += 8) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) big[k] = gdn::max3_abs(big[k], x[i + 2 * k], x[i + 2 * k + 1]);
   }
-  const float most = gdn::max3_abs(gdn::max3_abs(big[0], x[28], x[29]), gdn::max3_abs(big[1], x[30], x[31]),
-                                   gdn::max3_abs(big[2], big[3], 0.f));
+  return gdn::max3_abs(gdn::max3_abs(big[0], x[28], x[29]), gdn::max3_abs(big[1], x[30], x[31]),
+                       gdn::max3_abs(big[2], big[3], top));
+}
+__device__ __forceinline__ float max32(const float (&x)[32]) {
+  float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+  for (int i = 4; i < 28; i += 8) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top[k] = gdn::max3(top[k], x[i + 2 * k], x[i + 2 * k + 1]);
+  }
+  return gdn::max3(gdn::max3(top[0], x[28], x[29]), gdn::max3(top[1], x[30], x[31]), fmaxf(top[2], top[3]));
+}
+// Cap of 32 scores in TMEM columns from addr, into units of log2.  Where the warp's
+// scores stay within the cap (they mostly do), the polynomial, which is evaluated
+// beside the maximum that decides it.  Else any form, four scores at a time by way of
+// TMEM: it is rarely taken, and its instructions would stand between the others.
+__device__ __forceinline__ void cap_scores(const AttnArgs& a, const gdn::CapPoly& poly, uint32_t addr, float (&x)[32]) {
+  const float most = largest32(x, 0.f);
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
     const float2 y = gdn::capped_near(make_float2(x[i], x[i + 1]), poly);
@@ -375,9 +388,9 @@ __device__ __forceinline__ void cap_scores(const AttnArgs& a, const gdn::CapPoly
   }
 }
 // Scores outside [from, to) are hidden.
-__device__ __forceinline__ void mask_scores(int from, int to, float (&x)[32]) {
+__device__ __forceinline__ void hide(int from, int to, float as, float (&x)[32]) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) x[i] = i >= from && i < to ? x[i] : -INFINITY;
+  for (int i = 0; i < 32; ++i) x[i] = i >= from && i < to ? x[i] : as;
 }
 __device__ __forceinline__ void tmem_st32_nw(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -397,12 +410,17 @@ __device__ __forceinline__ void tmem_st32_nw(uint32_t taddr, const uint32_t* r) 
 //     behind the token) first.
 //   kGeneral: a bias, or any cap, first (the options that change a score; those
 //     that only hide keys cost nothing away from the edges).
-//   kBounded: a cap of at most kBoundedCap, and no bias.  It bounds the scores on
-//     both sides, so that 0 serves as the reference for the whole row: weights
-//     within 2^-80 .. 2^80 and their sums over 2^30 keys are far inside fp32 and
-//     bf16, and no maximum is taken.
-enum Scores { kPlain, kBiased, kGeneral, kBounded };
-constexpr float kBoundedCap = 80.f;  // in units of log2
+//   kCapped: a cap and no bias.  Small scores take the cap's polynomial straight to the
+//     weights, without a maximum, 32 keys at a time.
+enum Scores { kPlain, kBiased, kGeneral, kCapped };
+// kCapped's reference is set kAbove over the largest score that a row has, or at
+// kAbove to begin with, and moves in the first block with a score of more than kOver
+// over it, either way (the cap alone would bound the weights too, but by 2^80 at 55:
+// times large values they would leave fp32).  So weights stay below 2^16, and the
+// largest of a row is 2^-48 at least.  Moving is slow, and leaves the tiles out of step
+// for a while: 64 mixed sequences take 1.54 ms, with no distance above the largest
+// score and 16 or 24 over that 1.65 and 1.73.
+constexpr float kAbove = 16.f, kOver = 16.f;
 
 template <int D, Scores kScores>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -439,6 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     gdn::mbar_init(&sh.o_free[t], 4);
     gdn::mbar_init(&sh.stat_full[t], 4);
     gdn::mbar_init(&sh.turn[t], 1);
+    gdn::mbar_init(&sh.mid[t], 1);
     gdn::fence_mbar_init();
   } else if (tid >= 64 && tid < 64 + kSegments) {
     gdn::mbar_init(&sh.seg_full[tid - 64], 1);
@@ -749,7 +768,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j == 0 && done_segs > 0 && !wait(&sh.o_free[t], (done_segs - 1) & 1)) break;
           if (!wait(&sh.p_full[t][0], np & 1)) break;
           gdn::tc_fence_after();
-          if (gdn::elect_one()) gdn::tc_mma4_ts(o_col, s_col, 8, v_desc + v_stage * kStep, 128, id_o, j > 0);
+          if (gdn::elect_one()) {
+            gdn::tc_mma4_ts(o_col, s_col, 8, v_desc + v_stage * kStep, 128, id_o, j > 0);
+            if (kScores == kCapped) gdn::tc_commit(&sh.mid[t]);
+          }
           __syncwarp();
           if (!wait(&sh.p_full[t][1], np & 1)) break;
           // The tiles take turns with the rest of P V and the next S.  Interleaved,
@@ -893,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait_inline(&sh.seg_full[at], (segs / kSegments) & 1, abort_flag);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       const Segment& g = sh.seg[at];
-      const int blocks = g.blocks, seg_key0 = g.key0, tokens = g.tokens;
+      const int blocks = g.blocks, seg_key0 = g.key0, tokens = g.tokens, seg_lo = g.lo, seg_hi = g.hi;
       // Rows without a token copy the range of the tile's last one.
       const int pos = g.pos + min(t * tile_tokens + min(my_token, tile_tokens - 1), tokens - 1);
       const int lo = gdn::key_lo(a, pos), hi = max(pos + 1, g.full);
@@ -903,9 +925,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) gdn::mbar_arrive(&sh.seg_empty[at]);
       if (blocks == 0) break;
       if (t * tile_tokens >= tokens) continue;
-      float m = kScores == kBounded ? 0.f : -INFINITY;
+      float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       const gdn::CapPoly poly(a);
+      const float inv_scale = 1.f / a.scale_log2;
       for (int j = 0; j < blocks; ++j, ++n) {
         const int key0 = seg_key0 + j * kKeys;
         ok = wait_inline(&sh.s_full[t], n & 1, abort_flag);
@@ -921,7 +944,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // warps per issue waited for one, against 0.4 on the plain path; rolling
         // took the 64 mixed sequences from 2.13 to 1.73 ms, but would take 4 x 8,192
         // plain tokens from 1.39 to 1.48).
-        float ref = 0.f;
         constexpr bool kInRegisters = kScores == kPlain || kScores == kBiased;
         float s[kInRegisters ? 128 : 1];
         if constexpr (kInRegisters) {
@@ -947,7 +969,117 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 128; ++i) s[i] = i >= lo - key0 && i < hi - key0 ? s[i] : -INFINITY;
           }
         }
-        if constexpr (kScores != kBounded) {
+        auto publish = [&](int h) {
+          gdn::tmem_wait_st();
+          gdn::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) gdn::mbar_arrive(&sh.p_full[t][h]);
+        };
+        // The reference moves from m (-inf: none yet) to `to`; with O already there
+        // (`summed`) to what it holds.
+        auto move = [&](float to, bool summed) -> float {
+          const float r = m == -INFINITY ? 0.f : gdn::exp2_approx(m - to);
+          m = to;
+          l2 = __fmul2_rn(l2, make_float2(r, r));
+#pragma unroll 1
+          for (int c = 0; c < D && summed; c += 16) {
+            float x[16];
+            gdn::tmem_ld16(o_addr + c, x);
+            uint32_t y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[i] * r);
+            gdn::tmem_st16(o_addr + c, y);
+          }
+          return r;
+        };
+        if constexpr (kScores == kCapped) {
+          auto weights = [&](const float (&z)[32], int c) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 w = make_float2(gdn::exp2_approx(z[i]), gdn::exp2_approx(z[i + 1]));
+              l2 = __fadd2_rn(l2, w);
+              p[i / 2] = gdn::pack_bf162(w);
+            }
+            gdn::tmem_st16_nw(s_addr + c / 2, p);
+          };
+          // 32 keys at a time, the next 32 scores on their way meanwhile.
+          float x[32], y[32];
+          const float ref = m == -INFINITY ? kAbove : m;
+          const float limit = fminf(a.cap_near, (ref + kOver) * inv_scale);
+          const float2 minus = make_float2(-ref, -ref);
+          auto small = [&](float (&z)[32], int c) {
+            const float most = largest32(z, 0.f);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 u = gdn::capped_near(make_float2(z[i], z[i + 1]), poly, minus);
+              z[i] = u.x, z[i + 1] = u.y;
+            }
+            if (!__all_sync(0xFFFFFFFFu, most <= limit)) return false;
+            if (edge) hide(lo - key0 - c, hi - key0 - c, -INFINITY, z);
+            weights(z, c);
+            return true;
+          };
+          int c = 0;  // keys done
+          // Not where slots are junk (past the sequence's end, or before every window):
+          // they would take part in the choice.
+          if (key0 >= seg_lo && key0 + kKeys <= seg_hi) {
+            tmem_ld32_nw(s_addr, x);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              tmem_wait_ld32(x);
+              tmem_ld32_nw(s_addr + 64 * h + 32, y);
+              if (!small(x, 64 * h)) break;
+              c += 32;
+              tmem_wait_ld32(y);
+              if (h == 0) tmem_ld32_nw(s_addr + 64, x);
+              if (!small(y, 64 * h + 32)) break;
+              c += 32;
+              publish(h);
+            }
+            if (c < kKeys) {  // no load is left on its way
+              tmem_wait_ld32(x);
+              pin32(y);
+            }
+          }
+          if (c > 0 && m == -INFINITY && lo < key0 + c && hi > key0) m = kAbove;
+          // The rest of a block with a score that is not small.
+#pragma unroll 1
+          for (; c < kKeys; c += 32) {
+            float z[32];
+            gdn::tmem_ld32(s_addr + c, z);
+            cap_scores(a, poly, s_addr + c, z);
+            if (edge) hide(lo - key0 - c, hi - key0 - c, -INFINITY, z);
+            const float mx = ceilf(max32(z)) + kAbove;
+            if (__any_sync(0xFFFFFFFFu, mx > m)) {
+              // O is complete up to this half: S came behind the blocks before, and the
+              // first half's product is waited for.
+              if (c >= 64) ok = __all_sync(0xFFFFFFFFu, wait_inline(&sh.mid[t], n & 1, abort_flag));
+              if (!ok) break;
+              gdn::tc_fence_after();
+              const float r = move(fmaxf(m, mx), j > 0 || c >= 64);
+              if (c & 32) {
+                // The half's first 32 weights have been written: by a power of two, exactly.
+                float w[16];
+                uint32_t v[16];
+                gdn::tmem_wait_st();
+                gdn::tmem_ld16(s_addr + c / 2 - 16, w);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float2 f = gdn::unpack_bf162(__float_as_uint(w[i]));
+                  v[i] = gdn::pack_bf162(f.x * r, f.y * r);
+                }
+                gdn::tmem_st16(s_addr + c / 2 - 16, v);
+              }
+            }
+            const float by = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] -= by;
+            weights(z, c);
+            if (c & 32) publish(c > 64);
+          }
+          if (!ok) break;
+        } else {
           float mx;
           if constexpr (kInRegisters) {
             mx = max128(s);
@@ -970,7 +1102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = fmaf(-slope, fabsf(back - static_cast<float>(i)), x[i]);
               }
-              if (edge) mask_scores(lo - key0 - c, hi - key0 - c, x);
+              if (edge) hide(lo - key0 - c, hi - key0 - c, -INFINITY, x);
               tmem_st32_nw(s_addr + c, reinterpret_cast<const uint32_t*>(x));
               float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -979,76 +1111,51 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             gdn::tmem_wait_st();
           }
-          // The reference moves when a maximum is more than 2^8 above it.
+          // The reference moves when a maximum is more than 2^8 above it.  O of the blocks
+          // before is complete: S came behind it.
           const bool grow = mx > m + 8.f || (m == -INFINITY && mx > m);
-          if (__any_sync(0xFFFFFFFFu, grow)) {
-            const float to = fmaxf(m, mx);
-            const float r = m == -INFINITY ? 0.f : gdn::exp2_approx(m - to);
-            m = to;
-            l2 = __fmul2_rn(l2, make_float2(r, r));
-            if (j > 0) {  // O of the blocks before is complete: S came behind it
-#pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                float x[16];
-                gdn::tmem_ld16(o_addr + c, x);
-                uint32_t y[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[i] * r);
-                gdn::tmem_st16(o_addr + c, y);
-              }
-            }
-          }
-          ref = m == -INFINITY ? 0.f : m;  // a row that has seen no key yet: weights 2^-inf = 0
-        }
-        // Weights over the first half of their S columns: fp32 into the sum; bf16, as
-        // the values are, into the product.  64 keys at a time, so that the first half
-        // of P V runs beside the exponentials of the second.
-        const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), ref2 = make_float2(-ref, -ref);
-        auto weight = [&](float2 x) {
-          if (kScores == kPlain) x = __ffma2_rn(x, scale2, ref2);
-          if (kScores == kGeneral || kScores == kBiased) x = __fadd2_rn(x, ref2);
-          x = make_float2(gdn::exp2_approx(x.x), gdn::exp2_approx(x.y));
-          l2 = __fadd2_rn(l2, x);
-          return gdn::pack_bf162(x);
-        };
-        auto publish = [&](int h) {
-          gdn::tmem_wait_st();
-          gdn::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) gdn::mbar_arrive(&sh.p_full[t][h]);
-        };
-        if constexpr (kInRegisters) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t p[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) p[i] = weight(make_float2(s[64 * h + 2 * i], s[64 * h + 2 * i + 1]));
-            tmem_st32_nw(s_addr + 32 * h, p);
-            publish(h);
-          }
-        } else {
-          auto weights = [&](float (&x)[32], int c) {
-            if (kScores == kBounded) {
-              cap_scores(a, poly, s_addr + c, x);
-              if (edge) mask_scores(lo - key0 - c, hi - key0 - c, x);
-            }
-            uint32_t p[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) p[i] = weight(make_float2(x[2 * i], x[2 * i + 1]));
-            gdn::tmem_st16_nw(s_addr + c / 2, p);
+          if (__any_sync(0xFFFFFFFFu, grow)) move(fmaxf(m, mx), j > 0);
+          const float ref = m == -INFINITY ? 0.f : m;  // a row that has seen no key yet: weights 2^-inf = 0
+          // Weights over the first half of their S columns: fp32 into the sum; bf16, as
+          // the values are, into the product.  64 keys at a time, so that the first half
+          // of P V runs beside the exponentials of the second.
+          const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), ref2 = make_float2(-ref, -ref);
+          auto weight = [&](float2 x) {
+            if (kScores == kPlain) x = __ffma2_rn(x, scale2, ref2);
+            if (kScores == kGeneral || kScores == kBiased) x = __fadd2_rn(x, ref2);
+            x = make_float2(gdn::exp2_approx(x.x), gdn::exp2_approx(x.y));
+            l2 = __fadd2_rn(l2, x);
+            return gdn::pack_bf162(x);
           };
-          // The next 32 scores are on their way meanwhile.
-          float x[32], y[32];
-          tmem_ld32_nw(s_addr, x);
+          if constexpr (kInRegisters) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t p[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) p[i] = weight(make_float2(s[64 * h + 2 * i], s[64 * h + 2 * i + 1]));
+              tmem_st32_nw(s_addr + 32 * h, p);
+              publish(h);
+            }
+          } else {
+            auto weights = [&](float (&x)[32], int c) {
+              uint32_t p[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) p[i] = weight(make_float2(x[2 * i], x[2 * i + 1]));
+              gdn::tmem_st16_nw(s_addr + c / 2, p);
+            };
+            // The next 32 scores are on their way meanwhile.
+            float x[32], y[32];
+            tmem_ld32_nw(s_addr, x);
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            tmem_wait_ld32(x);
-            tmem_ld32_nw(s_addr + 64 * h + 32, y);
-            weights(x, 64 * h);
-            tmem_wait_ld32(y);
-            if (h == 0) tmem_ld32_nw(s_addr + 64, x);
-            weights(y, 64 * h + 32);
-            publish(h);
+            for (int h = 0; h < 2; ++h) {
+              tmem_wait_ld32(x);
+              tmem_ld32_nw(s_addr + 64 * h + 32, y);
+              weights(x, 64 * h);
+              tmem_wait_ld32(y);
+              if (h == 0) tmem_ld32_nw(s_addr + 64, x);
+              weights(y, 64 * h + 32);
+              publish(h);
+            }
           }
         }
       }
@@ -1224,16 +1331,16 @@ extern "C" int gdn_attention_paged(const gdn_bf16* q, int64_t q_token_stride, gd
   if (rc != GDN_OK) return rc;
   d.tile_tokens = kRows / d.a.group;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool bounded = d.a.cap_log2 > 0.f && d.a.cap_log2 <= kBoundedCap && !d.a.slopes;
+  const bool capped = d.a.cap_log2 > 0.f && !d.a.slopes;
   const bool linear = d.a.slopes && d.a.cap_log2 == 0.f && !d.a.full_lens;
-  const Scores scores = bounded ? kBounded : linear ? kBiased : d.a.cap_log2 > 0.f || d.a.slopes ? kGeneral : kPlain;
+  const Scores scores = capped ? kCapped : linear ? kBiased : d.a.slopes ? kGeneral : kPlain;
   const auto run = [&](auto dim) {
     constexpr int D = decltype(dim)::value;
     switch (scores) {
       case kPlain: return launch<D, kPlain>(d, total_tokens, cache, workspace, sms, s);
       case kBiased: return launch<D, kBiased>(d, total_tokens, cache, workspace, sms, s);
       case kGeneral: return launch<D, kGeneral>(d, total_tokens, cache, workspace, sms, s);
-      default: return launch<D, kBounded>(d, total_tokens, cache, workspace, sms, s);
+      default: return launch<D, kCapped>(d, total_tokens, cache, workspace, sms, s);
     }
   };
   return cache->head_dim == 64 ? run(std::integral_constant<int, 64>()) : run(std::integral_constant<int, 128>());

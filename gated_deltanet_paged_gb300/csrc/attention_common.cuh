@@ -121,13 +121,17 @@ struct CapPoly {
     for (int i = 0; i < 5; ++i) c[i] = make_float2(a.cap_poly[i], a.cap_poly[i]);
   }
 };
-__device__ __forceinline__ float2 capped_near(float2 s, const CapPoly& p) {
+__device__ __forceinline__ float2 near_quotient(float2 s, const CapPoly& p) {
   const float2 t = __fmul2_rn(s, s);
   float2 h = __ffma2_rn(p.c[4], t, p.c[3]);
   h = __ffma2_rn(h, t, p.c[2]);
   h = __ffma2_rn(h, t, p.c[1]);
-  h = __ffma2_rn(h, t, p.c[0]);
-  return __fmul2_rn(s, h);
+  return __ffma2_rn(h, t, p.c[0]);
+}
+__device__ __forceinline__ float2 capped_near(float2 s, const CapPoly& p) { return __fmul2_rn(s, near_quotient(s, p)); }
+// ... and less a reference, at no further cost.
+__device__ __forceinline__ float2 capped_near(float2 s, const CapPoly& p, float2 minus) {
+  return __ffma2_rn(s, near_quotient(s, p), minus);
 }
 // The same for one score, rounding by rounding: a score has the same bits whichever
 // of these functions took it, so that what decides between them shows nowhere.

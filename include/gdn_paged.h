@@ -449,7 +449,9 @@ int gdn_kv_append_paged(const gdn_bf16 *q, int64_t q_token_stride, gdn_bf16 *q_o
  * scale <= 0 selects 1 / sqrt(D).  D is 64 or 128 and Hq / Hkv at most 128.
  * Slots past a sequence's end and keys outside every token's window are not
  * read into any sum, whatever they hold; the keys and values of a sequence's
- * own tokens inside the window have to be finite.
+ * own tokens inside the window have to be finite.  The sum over the values is
+ * taken in fp32 with weights below 2^8, under a softcap without slopes between
+ * 2^-48 and 2^16: values between 2^-70 and 2^90 in size keep their precision.
  * workspace: device memory, 16-byte aligned, of at least
  * gdn_attention_workspace_bytes(...) bytes; it needs no initialisation. */
 int gdn_attention_paged(const gdn_bf16 *q, int64_t q_token_stride, gdn_bf16 *o, float *lse,

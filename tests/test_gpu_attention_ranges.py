@@ -46,3 +46,22 @@ def test_slots_past_the_end_change_no_bit_under_a_cap(decode):
         if first is None:
             first = o.clone(), lse.clone()
         assert torch.equal(o.view(I16), first[0].view(I16)) and torch.equal(lse, first[1]), "slots hold %r" % junk
+
+
+# Scores at either end of the cap, and values near either end of bf16's range: the
+# weights have to be taken relative to the row's largest score, as without a cap
+# (weights of 2^80, or 2^-80, times such values leave fp32).
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("cap", [5.0, 30.0, 55.0, 70.0])
+@pytest.mark.parametrize("size", [2.0**-100, 2.0**100])
+@pytest.mark.parametrize("sign", [-1.0, 0.0, 1.0])
+@pytest.mark.parametrize("window", [-1, 130])
+def test_values_of_every_size_under_a_cap(decode, cap, size, sign, window):
+    """sign: where all scores lie, far beyond the cap; 0: on both sides."""
+    new, prefix = ([1] * 3, [700, 5, 2000]) if decode else ([300, 3, 64], [700, 0, 1300])
+    b = Batch(new, prefix, 64, 8, 2, 64, seed=43, q_scale=100.0)
+    if sign:
+        b.q[:] = b.q.abs()
+        b.k = [sign * k.abs() for k in b.k]
+    b.v = [(v.float() * size).bfloat16() for v in b.v]
+    check_attention(b.fill(), decode=decode, softcap=cap, window=window)

@@ -71,6 +71,8 @@ struct AttnArgs {
   const int32_t* full_lens;   // [num_seqs] or nullptr
   int32_t window;             // < 0: none
   int32_t box_shift;          // log2 of the tokens per copy of a page
+  uint32_t wait_ns;           // limit of the waits
+  int32_t debug_stall;        // test hook (gdn_debug_set_wait_stall): a wait that runs out
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -83,6 +85,23 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
   float r;
   asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+// Bounded wait of a whole warp: its lanes go on, or give up, together (a lane that
+// gave up alone would leave the others at the next instruction that takes all 32).
+// It gives up after limit_ns, or when *abort is set (nullptr: never).
+__device__ __forceinline__ bool warp_wait_more(uint64_t* bar, uint32_t parity, const volatile int* abort, uint32_t limit_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    const bool there = mbar_try_wait_suspend(bar, parity);
+    if (__all_sync(0xFFFFFFFFu, there)) return true;
+    const bool out = (abort && *abort != 0) || globaltimer_ns() - t0 > limit_ns;
+    if (__any_sync(0xFFFFFFFFu, out)) return false;
+  }
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort, uint32_t limit_ns) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  return warp_wait_more(bar, parity, abort, limit_ns);
 }
 
 // One lane of a converged warp.
@@ -373,6 +392,8 @@ inline int attention_args(gdn::AttnArgs* a, const gdn_bf16* q, int64_t q_stride,
   // No sequence has 2^30 tokens, so that a larger window hides nothing; the kernels
   // add to distances in 32 bits.
   a->window = options && options->window < (1 << 30) ? options->window : -1;
+  a->debug_stall = debug_wait_stall();
+  a->wait_ns = a->debug_stall ? 1000000u : 2000000000u;
   while ((1 << a->box_shift) < tile_keys && cache->page_size % (2 << a->box_shift) == 0) ++a->box_shift;
   return GDN_OK;
 }

@@ -482,6 +482,9 @@ __device__ __forceinline__ float2 unpack_bf162(uint32_t u) {
 // ---------------------------------------------------------------------------
 namespace gdn_host {
 
+// gdn_debug_set_wait_stall's switch.
+bool debug_wait_stall();
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // GDN_OK if the current device is an sm_103 part, else GDN_ERR_UNSUPPORTED

@@ -1068,6 +1068,7 @@ void fill_common(PrefillArgs& a, const float* g, const float* beta, gdn_bf16* o,
 }  // namespace
 
 extern "C" void gdn_debug_set_wait_stall(int32_t enable) { g_debug_stall.store(enable != 0 ? 1 : 0); }
+bool gdn_host::debug_wait_stall() { return g_debug_stall.load(std::memory_order_relaxed) != 0; }
 
 extern "C" size_t gdn_prefill_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32_t H) {
   if (num_seqs < 0 || total_tokens < 0 || H < 1) return 0;

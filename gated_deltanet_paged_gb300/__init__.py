@@ -126,8 +126,8 @@ def gdn_debug_set_wait_stall(enable: bool) -> None:
     state-chain kernel of each later prefill call makes its first wait on a
     barrier that nothing completes; the wait gives up after about 1 ms, before
     any copy or tensor-core operation is issued, and the call records
-    GDN_DEVERR_TIMEOUT in err_word and writes nothing.  In a single-token
-    attention call the warps that take keys and values wait so."""
+    GDN_DEVERR_TIMEOUT in err_word and writes nothing.  In the
+    attention calls the warps that take the scores (keys and values) wait so."""
     library().gdn_debug_set_wait_stall(1 if enable else 0)
 
 

@@ -235,6 +235,7 @@ struct Smem {
   uint64_t mid[2];         // the first half of P V of a block is complete (kCapped)
   uint64_t turn[2];        // the other tile's products of a block have been issued
   uint64_t seg_full[kSegments], seg_empty[kSegments];
+  uint64_t never;          // the test hook's barrier, never completed
   int64_t scan[kThreads / 32];
   Walk walk;
   Segment seg[kSegments];
@@ -250,16 +251,6 @@ __device__ __forceinline__ void regs_inc() {
 template <int kRegs>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
-// A bounded wait, in line: with a function call in the kernel the register split
-// below cannot be allocated.
-__device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, const volatile int* abort) {
-  if (gdn::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = gdn::globaltimer_ns();
-  while (!gdn::mbar_try_wait_suspend(bar, parity))
-    if (*abort || gdn::globaltimer_ns() - t0 > 2000000000ull) return false;
-  return true;
 }
 
 // This warp has read its part of O.
@@ -466,6 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (tid == 96) {
     gdn::mbar_init(&sh.q_full, 1);
     gdn::mbar_init(&sh.q_empty, 2);
+    gdn::mbar_init(&sh.never, 1);
     sh.abort = 0;
     gdn::fence_mbar_init();
   }
@@ -624,7 +616,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 8) {
     regs_dec<kOtherRegs>();
     bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && wait_inline(bar, parity, abort_flag); };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && gdn::warp_wait(bar, parity, abort_flag, a.wait_ns); };
+    // What has to end before the CTA does, whatever the others do.
+    auto last = [&](uint64_t* bar, uint32_t parity) { return gdn::warp_wait(bar, parity, nullptr, 2000000000u); };
     // Segment i as announced; false when there is none or a wait ran out.
     auto next = [&](uint32_t i, Segment& g) {
       if (!wait(&sh.seg_full[i % kSegments], (i / kSegments) & 1)) return false;
@@ -638,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Walk w = sh.walk;
       gdn::TileCopies<D, kKeys> keys(a, &k_map, lane);
       uint32_t n = 0, segs = 0;  // ring tiles (keys are the even ones), segments announced
-      bool q_in_flight = false;
+      uint32_t queries = 0;      // sent
       for (;; ++segs) {
         const bool more = next_segment(d, w);
         if (segs >= kSegments && !wait(&sh.seg_empty[segs % kSegments], ((segs / kSegments) - 1) & 1)) break;
@@ -693,31 +687,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  g.first_token + t * tile_tokens, g.head);
           }
           __syncwarp();
-          q_in_flight = true;
+          ++queries;
           return true;
         };
         bool q_sent = send_queries(false);
-        for (int j = 0; j < g.blocks; ++j, n += 2) {
+        for (int j = 0; j < g.blocks; ++j) {
           const uint32_t stage = n % L::kStages;
           if (n >= L::kStages && !wait(&sh.empty[stage], ((n / L::kStages) - 1) & 1)) break;
           if (lane == 0) gdn::mbar_arrive_expect_tx(&sh.full[stage], keys.bytes());
           __syncwarp();
           keys.copy(ring + stage * L::kTile, &sh.full[stage], j + 1 < g.blocks);
+          n += 2;
           if (!q_sent && !(q_sent = send_queries(true))) break;
         }
         if (!ok) break;
       }
-      if (!ok && lane == 0) {
-        // Leave no copy in flight behind (bounded waits, as everywhere).
-        *abort_flag = 1;
-        for (uint32_t i = n > 2 * L::kStages ? n - 2 * L::kStages : 0; i < n; i += 2)
-          gdn::mbar_wait(&sh.full[i % L::kStages], (i / L::kStages) & 1);
-        if (q_in_flight) gdn::mbar_wait(&sh.q_full, segs & 1);
-      }
+      if (!ok) *abort_flag = 1;
+      // Leave no copy in flight behind, whoever gave up (bounded waits, as everywhere).
+      ok = !queries || last(&sh.q_full, (queries - 1) & 1);
+#pragma unroll 1
+      for (uint32_t i = n > L::kStages ? n - L::kStages : 0; i < n; i += 2)
+        ok = last(&sh.full[i % L::kStages], (i / L::kStages) & 1) && ok;
+      if (!ok) *abort_flag = 1;
     } else if (warp < kLoadWarp) {
       // ----------------------------------------------------------- products
-      // One warp per tile.  A warp's products run in the order of their issue, so
-      // S of the next block may overwrite the weights that P V before it reads.
+      // One warp per tile, of which one elected lane does it all: there is no other
+      // to disagree with when a wait runs out.  (Lane 0 instead of an elected one: 4 x
+      // 8,192 tokens 1.60 ms instead of 1.32.  All lanes with a vote at each wait:
+      // 1.36.)  Its products run in the order of their issue, so S of the next block
+      // may overwrite the weights that P V before it reads.
       const int t = warp - kMmaWarp;
       const uint32_t id_s = gdn::idesc_f16(kRows, kKeys, true, true, false, false);
       const uint32_t id_o = gdn::idesc_f16(kRows, D, true, true, false, true);
@@ -734,75 +732,72 @@ __global__ void __launch_bounds__(kThreads, 1)
       // S = Q K^T of the ring's current tile, which is released with it.
       auto scores = [&](bool last) {
         gdn::tc_fence_after();
-        if (gdn::elect_one()) {
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            gdn::tc_mma4(s_col, q_desc + c * (L::kHalf >> 4), 2, k_desc + stage * kStep + c * (L::kHalf >> 4), 2, id_s, c);
-          gdn::tc_commit(&sh.s_full[t]);
-          gdn::tc_commit(&sh.empty[stage]);
-          if (last) gdn::tc_commit(&sh.q_empty);
-        }
-        __syncwarp();
+        for (int c = 0; c < D / 64; ++c)
+          gdn::tc_mma4(s_col, q_desc + c * (L::kHalf >> 4), 2, k_desc + stage * kStep + c * (L::kHalf >> 4), 2, id_s, c);
+        gdn::tc_commit(&sh.s_full[t]);
+        gdn::tc_commit(&sh.empty[stage]);
+        if (last) gdn::tc_commit(&sh.q_empty);
         advance();
       };
-      Segment g;
-      for (uint32_t segs = 0; next(segs, g); ++segs) {
-        const bool active = t * tile_tokens < g.tokens, two = tile_tokens < g.tokens;
-        if (!wait(&sh.q_full, segs & 1)) break;
-        if (!active) {
-          // Keep in step: release every tile of the segment unread.
-          if (lane == 0) gdn::mbar_arrive(&sh.q_empty);
-          for (int i = 0; ok && i < 2 * g.blocks; ++i) {
-            if (!wait(&sh.full[stage], phase)) break;
-            if (lane == 0) gdn::mbar_arrive(&sh.empty[stage]);
-            advance();
+      if (gdn::elect_one()) {
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && gdn::lane_wait(bar, parity, abort_flag, a.wait_ns); };
+        for (uint32_t segs = 0;; ++segs) {
+          if (!wait(&sh.seg_full[segs % kSegments], (segs / kSegments) & 1)) break;
+          const Segment g = sh.seg[segs % kSegments];
+          gdn::mbar_arrive(&sh.seg_empty[segs % kSegments]);
+          if (g.blocks <= 0) break;
+          const bool active = t * tile_tokens < g.tokens, two = tile_tokens < g.tokens;
+          if (!wait(&sh.q_full, segs & 1)) break;
+          if (!active) {
+            // Keep in step: release every tile of the segment unread.
+            gdn::mbar_arrive(&sh.q_empty);
+            for (int i = 0; ok && i < 2 * g.blocks; ++i) {
+              if (!wait(&sh.full[stage], phase)) break;
+              gdn::mbar_arrive(&sh.empty[stage]);
+              advance();
+            }
+            continue;
           }
-          continue;
-        }
-        if (!wait(&sh.full[stage], phase)) break;
-        scores(g.blocks == 1);
-        for (int j = 0; ok && j < g.blocks; ++j) {
-          const uint32_t v_stage = stage;
           if (!wait(&sh.full[stage], phase)) break;
-          advance();
-          if (j == 0 && done_segs > 0 && !wait(&sh.o_free[t], (done_segs - 1) & 1)) break;
-          if (!wait(&sh.p_full[t][0], np & 1)) break;
-          gdn::tc_fence_after();
-          if (gdn::elect_one()) {
+          scores(g.blocks == 1);
+          for (int j = 0; ok && j < g.blocks; ++j) {
+            const uint32_t v_stage = stage;
+            if (!wait(&sh.full[stage], phase)) break;
+            advance();
+            if (j == 0 && done_segs > 0 && !wait(&sh.o_free[t], (done_segs - 1) & 1)) break;
+            if (!wait(&sh.p_full[t][0], np & 1)) break;
+            gdn::tc_fence_after();
             gdn::tc_mma4_ts(o_col, s_col, 8, v_desc + v_stage * kStep, 128, id_o, j > 0);
             if (kScores == kCapped) gdn::tc_commit(&sh.mid[t]);
-          }
-          __syncwarp();
-          if (!wait(&sh.p_full[t][1], np & 1)) break;
-          // The tiles take turns with the rest of P V and the next S.  Interleaved,
-          // both would end together, and both softmaxes would then run beside an
-          // idle tensor core (measured: two stable rhythms, 3,450 cycles per block
-          // that way and 2,600 when the tiles are half a period apart).
-          if (two && (t == 1 || turns > 0) && !wait(&sh.turn[t], (t == 1 ? turns : turns - 1) & 1)) break;
-          gdn::tc_fence_after();
-          if (gdn::elect_one()) {
+            if (!wait(&sh.p_full[t][1], np & 1)) break;
+            // The tiles take turns with the rest of P V and the next S.  Interleaved,
+            // both would end together, and both softmaxes would then run beside an
+            // idle tensor core (measured: two stable rhythms, 3,450 cycles per block
+            // that way and 2,600 when the tiles are half a period apart).
+            if (two && (t == 1 || turns > 0) && !wait(&sh.turn[t], (t == 1 ? turns : turns - 1) & 1)) break;
+            gdn::tc_fence_after();
             gdn::tc_mma4_ts(o_col, s_col + 32, 8, v_desc + v_stage * kStep + 4 * 128, 128, id_o, 1);
             if (j + 1 == g.blocks) gdn::tc_commit(&sh.o_last[t]);
             gdn::tc_commit(&sh.empty[v_stage]);
+            ++np;
+            if (j + 1 < g.blocks) {
+              if (!wait(&sh.full[stage], phase)) break;
+              scores(j + 2 == g.blocks);
+            }
+            if (two) {
+              gdn::mbar_arrive(&sh.turn[t ^ 1]);
+              ++turns;
+            }
           }
-          __syncwarp();
-          ++np;
-          if (j + 1 < g.blocks) {
-            if (!wait(&sh.full[stage], phase)) break;
-            scores(j + 2 == g.blocks);
-          }
-          if (two) {
-            if (lane == 0) gdn::mbar_arrive(&sh.turn[t ^ 1]);
-            ++turns;
-          }
+          ++done_segs;
         }
-        ++done_segs;
+        if (!ok) *abort_flag = 1;
+        // Every product is complete before TMEM is given back.
+        gdn::tc_commit(&sh.done[t]);
       }
-      if (!ok) *abort_flag = 1;
-      // Every product is complete before TMEM is given back.
-      if (gdn::elect_one()) gdn::tc_commit(&sh.done[t]);
       __syncwarp();
-      gdn::mbar_wait(&sh.done[t], 0);
+      if (!last(&sh.done[t], 0)) *abort_flag = 1;
     } else if (warp == kValueWarp) {
       // ------------------------------------------------------------- values
       // Slots past the sequence's end or before every window may hold anything,
@@ -810,6 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // memory.  The tile's copies complete on `raw`, and this warp completes `full`.
       gdn::TileCopies<D, kKeys> values(a, &v_map, lane);
       uint32_t n = 1, raw_parity = 0;  // ring tiles (values are the odd ones); per stage, parity of its next raw copy
+      int uncleared = -1;              // stage of a raw copy that was not waited for to the end
       Segment g;
       for (uint32_t segs = 0; ok && next(segs, g); ++segs) {
         values.begin(g.lo, g.hi, g.head, g.seq, g.entry, g.key0);
@@ -823,7 +819,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           values.copy(ring + stage * L::kTile, bar, j + 1 < g.blocks);
           if (!partial) continue;
-          if (!wait(bar, (raw_parity >> stage) & 1)) break;
+          if (!wait(bar, (raw_parity >> stage) & 1)) {
+            uncleared = static_cast<int>(stage);
+            break;
+          }
           raw_parity ^= 1u << stage;
           const int from = max(0, g.lo - key0), to = min(kKeys, g.hi - key0);
           uint4* dst = reinterpret_cast<uint4*>(ring + stage * L::kTile);
@@ -837,11 +836,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) gdn::mbar_arrive(&sh.full[stage]);
         }
       }
-      if (!ok && lane == 0) {
-        *abort_flag = 1;
-        for (uint32_t i = n > 2 * L::kStages ? n - 2 * L::kStages : 1; i < n; i += 2)
-          gdn::mbar_wait(&sh.full[i % L::kStages], (i / L::kStages) & 1);
-      }
+      if (!ok) *abort_flag = 1;
+      ok = uncleared < 0 || last(&sh.raw[uncleared], (raw_parity >> uncleared) & 1);
+#pragma unroll 1
+      for (uint32_t i = n > L::kStages ? n - L::kStages : 1; i < n; i += 2)
+        ok = last(&sh.full[i % L::kStages], (i / L::kStages) & 1) && ok;
+      if (!ok) *abort_flag = 1;
     } else {
       // ----------------------------------------------------------- epilogue
       // Reads a segment's O while the softmax warps are on the next one.
@@ -910,10 +910,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int my_token = row / a.group, my_head = row % a.group;
     uint32_t n = 0, taken = 0;  // blocks, segments of this tile
     bool ok = true;
-    for (uint32_t segs = 0; ok; ++segs) {
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = gdn::warp_wait(bar, parity, abort_flag, a.wait_ns); };
+    for (uint32_t segs = 0;; ++segs) {
       const int at = segs % kSegments;
-      ok = wait_inline(&sh.seg_full[at], (segs / kSegments) & 1, abort_flag);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      if (!wait(&sh.seg_full[at], (segs / kSegments) & 1)) break;
       const Segment& g = sh.seg[at];
       const int blocks = g.blocks, seg_key0 = g.key0, tokens = g.tokens, seg_lo = g.lo, seg_hi = g.hi;
       // Rows without a token copy the range of the tile's last one.
@@ -925,17 +925,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) gdn::mbar_arrive(&sh.seg_empty[at]);
       if (blocks == 0) break;
       if (t * tile_tokens >= tokens) continue;
+      if (a.debug_stall && !wait(&sh.never, 0)) break;
       float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       const gdn::CapPoly poly(a);
       const float inv_scale = 1.f / a.scale_log2;
       for (int j = 0; j < blocks; ++j, ++n) {
         const int key0 = seg_key0 + j * kKeys;
-        ok = wait_inline(&sh.s_full[t], n & 1, abort_flag);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xFFFFFFFFu, gdn::lane_wait(&sh.s_full[t], n & 1, abort_flag, a.wait_ns));
+        if (!ok) break;
         gdn::tc_fence_after();
         const bool edge = __any_sync(0xFFFFFFFFu, key0 < lo || key0 + kKeys > hi);
         // Plain and biased scores stay in registers from the maximum to the weights, all 128.
@@ -1054,8 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (__any_sync(0xFFFFFFFFu, mx > m)) {
               // O is complete up to this half: S came behind the blocks before, and the
               // first half's product is waited for.
-              if (c >= 64) ok = __all_sync(0xFFFFFFFFu, wait_inline(&sh.mid[t], n & 1, abort_flag));
-              if (!ok) break;
+              if (c >= 64 && !wait(&sh.mid[t], n & 1)) break;
               gdn::tc_fence_after();
               const float r = move(fmaxf(m, mx), j > 0 || c >= 64);
               if (c & 32) {
@@ -1160,13 +1157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      if (taken > 0) {  // the epilogue has taken the last segment's
-        ok = wait_inline(&sh.o_free[t], (taken - 1) & 1, abort_flag);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          ok = false;
-          break;
-        }
-      }
+      if (taken > 0 && !wait(&sh.o_free[t], (taken - 1) & 1)) break;  // the epilogue has taken the last segment's
       sh.stat[t][row] = make_float2(m, l2.x + l2.y);
       ++taken;
       __syncwarp();
@@ -1177,7 +1168,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   gdn::tc_fence_before();
   __syncthreads();
   gdn::tc_fence_after();
-  if (tid == 0 && sh.abort) gdn::record_error(a.paged.err_word, GDN_DEVERR_TIMEOUT, 0);
+  if (tid == 0 && sh.abort) {
+    gdn::record_error(a.paged.err_word, GDN_DEVERR_TIMEOUT, 0);
+    if (!d.whole) d.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);  // nothing to join
+  }
+  __syncwarp();
   if (warp == kMmaWarp) gdn::tmem_dealloc(tmem, 512);
 }
 

@@ -89,6 +89,8 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 
 // Bounded wait of a whole warp: its lanes go on, or give up, together (a lane that
 // gave up alone would leave the others at the next instruction that takes all 32).
+// In line: with a function call in the chunk kernel its register split cannot be
+// allocated.
 // It gives up after limit_ns, or when *abort is set (nullptr: never).
 __device__ __forceinline__ bool warp_wait_more(uint64_t* bar, uint32_t parity, const volatile int* abort, uint32_t limit_ns) {
   const uint64_t t0 = globaltimer_ns();
@@ -102,6 +104,15 @@ __device__ __forceinline__ bool warp_wait_more(uint64_t* bar, uint32_t parity, c
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort, uint32_t limit_ns) {
   if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
   return warp_wait_more(bar, parity, abort, limit_ns);
+}
+
+// The same of one lane, which alone goes on or takes a vote after it.
+__device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity, const volatile int* abort, uint32_t limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_suspend(bar, parity))
+    if (*abort || globaltimer_ns() - t0 > limit_ns) return false;
+  return true;
 }
 
 // One lane of a converged warp.

@@ -327,9 +327,10 @@ size_t gdn_prefill_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32
  * process first waits on a barrier that nothing completes; the wait gives up
  * after about 1 ms, before the kernel has issued any copy or tensor-core
  * operation, and the kernel records GDN_DEVERR_TIMEOUT in err_word and
- * returns: the call writes no output and no pool row.  In the single-token
- * attention calls the warps that take keys and values wait so; the copies on
- * their way complete, and the call records the same error and writes no output.
+ * returns: the call writes no output and no pool row.  In the attention calls
+ * the warps that take the scores (for single tokens: keys and values) wait so;
+ * the copies and products on their way complete, and the call records the same
+ * error and writes no output.
  * Disabled by default; enable 0 disables it again.  Not for production use. */
 void gdn_debug_set_wait_stall(int32_t enable);
 

@@ -37,3 +37,24 @@ def test_decode_wait_that_runs_out_is_reported(name, dim):
     assert int(err.item()) >> 24 == TIMEOUT
     assert (o == 7.0).all() and (lse == 7.0).all()
     check_attention(b, decode=True)
+
+
+# A CTA per item; items cut evenly among CTAs; equal pieces of the batch; tokens for
+# one of the two tiles only, and a window that has a first block of values cleared.
+CHUNKS = {"one block": ([20], [0]), "whole items": ([300, 0, 64], [0, 7, 900]), "cut items": ([40], [9000]),
+          "pieces of the batch": ([2000, 700, 1], [0, 3000, 5000])}
+
+
+@pytest.mark.parametrize("opts", [{}, {"softcap": 20.0}, {"window": 333}])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("name", list(CHUNKS))
+def test_chunk_wait_that_runs_out_is_reported(name, dim, opts):
+    b = Batch(*CHUNKS[name], 64, 8, 2, dim, seed=52).fill()
+    o = torch.full_like(b.q, 7.0)
+    lse = torch.full(b.q.shape[:2], 7.0, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    _stalled(lambda: gdn.gdn_attention_paged(b.q, b.k_cache, b.v_cache, b.cu, *b.table, o=o, lse=lse, err_word=err,
+                                             **opts))
+    assert int(err.item()) >> 24 == TIMEOUT
+    assert (o == 7.0).all() and (lse == 7.0).all()
+    check_attention(b, **opts)

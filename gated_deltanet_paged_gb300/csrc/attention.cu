@@ -944,21 +944,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         // plain tokens from 1.39 to 1.48).
         constexpr bool kInRegisters = kScores == kPlain || kScores == kBiased;
         float s[kInRegisters ? 128 : 1];
+        const float first_bias = slope * static_cast<float>(key0 - pos);  // kBiased: of the block's first key
         if constexpr (kInRegisters) {
           tmem_ld128(s_addr, s);
           if constexpr (kScores == kBiased) {
-            // The bias of keys i and i + 1, and its step to the next two.
-            const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), step = make_float2(2.f * slope, 2.f * slope);
+            // The bias of key i of the block less that of its first, from two products of
+            // the slope and a whole number, each rounded once (a running sum would add a
+            // rounding for every two keys, each of the bias's own size where the first
+            // key's is not taken out).
+            const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
+            float per_key = slope;
+            asm volatile("" : "+f"(per_key));  // not computed ahead of the blocks: there are no registers for it
+            float2 within8[4];
 #pragma unroll
-            for (int c = 0; c < 128; c += 32) {
-              const float first = slope * static_cast<float>(key0 + c - pos);
-              float2 bias = make_float2(first, first + slope);
+            for (int i = 0; i < 4; ++i) within8[i] = make_float2(per_key * (2 * i), per_key * (2 * i + 1));
 #pragma unroll
-              for (int i = c; i < c + 32; i += 2) {
-                const float2 x = __ffma2_rn(make_float2(s[i], s[i + 1]), scale2, bias);
-                s[i] = x.x;
-                s[i + 1] = x.y;
-                bias = __fadd2_rn(bias, step);
+            for (int c = 0; c < 128; c += 8) {
+              const float2 eights = make_float2(per_key * c, per_key * c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int k = c + 2 * i;
+                const float2 x = __ffma2_rn(make_float2(s[k], s[k + 1]), scale2, __fadd2_rn(eights, within8[i]));
+                s[k] = x.x;
+                s[k + 1] = x.y;
               }
             }
           }
@@ -1081,6 +1089,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (kInRegisters) {
             mx = max128(s);
             if (kScores == kPlain) mx *= a.scale_log2;
+            if (kScores == kBiased) mx += first_bias;
           } else {
             // Changed and masked scores go back to TMEM.
             mx = -INFINITY;
@@ -1112,7 +1121,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // before is complete: S came behind it.
           const bool grow = mx > m + 8.f || (m == -INFINITY && mx > m);
           if (__any_sync(0xFFFFFFFFu, grow)) move(fmaxf(m, mx), j > 0);
-          const float ref = m == -INFINITY ? 0.f : m;  // a row that has seen no key yet: weights 2^-inf = 0
+          float ref = m == -INFINITY ? 0.f : m;  // a row that has seen no key yet: weights 2^-inf = 0
+          if (kScores == kBiased) ref -= first_bias;
           // Weights over the first half of their S columns: fp32 into the sum; bf16, as
           // the values are, into the product.  64 keys at a time, so that the first half
           // of P V runs beside the exponentials of the second.

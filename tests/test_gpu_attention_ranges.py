@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import gated_deltanet_paged_gb300 as gdn
-from attention_util import Batch, check_attention
+from attention_util import Batch, check_attention, within
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,30 @@ def test_values_of_every_size_under_a_cap(decode, cap, size, sign, window):
         b.k = [sign * k.abs() for k in b.k]
     b.v = [(v.float() * size).bfloat16() for v in b.v]
     check_attention(b.fill(), decode=decode, softcap=cap, window=window)
+
+
+@pytest.mark.parametrize("slope", [0.25, 0.125, 0.3])
+def test_bias_that_grows_with_the_distance(slope):
+    """Negative slopes far from the token: the largest weights belong to the first
+    keys, whose bias is 10^5 times the difference between neighbours.  What the 128
+    keys of a block have in common is rounded once for all of them, and the rest at
+    the size of slope * 128, so that the tolerance is that of small scores (zero keys
+    make every score the bias alone; the values tell neighbours apart)."""
+    p, n, ps, dim = 1500000, 3, 1024, 64
+    pages = -(-(p + n) // ps)
+    k = torch.zeros(pages, ps, 1, dim, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    sign = torch.tensor([1.0 if j % 32 < 4 else -1.0 for j in range(ps)])
+    v[0] = sign.bfloat16().cuda()[:, None, None]
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    slopes = torch.tensor([-slope, -slope / 2], device="cuda")
+    q = torch.randn(n, 2, dim, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    o, lse = gdn.gdn_attention_paged(q, k, v, i32(0, n), torch.arange(pages, dtype=torch.int32, device="cuda"),
+                                     i32(0, pages), i32(p + n - (pages - 1) * ps), slopes=slopes, return_lse=True)
+    j = torch.arange(ps, dtype=torch.float64)  # keys beyond have weights below e^-60
+    for h in range(2):
+        x = -slopes[h].double().cpu() * (torch.arange(p, p + n, dtype=torch.float64)[:, None] - j)
+        want_lse = torch.logsumexp(x, -1)
+        want = (torch.exp(x - want_lse[:, None]) @ sign.double())[:, None].expand(n, dim)
+        within(lse[:, h], want_lse, 2.0**-19 * (16 + want_lse.abs()), "lse")
+        within(o[:, h], want, 2.0**-8 * (want.abs() + 1) + 2.0**-14, "o")

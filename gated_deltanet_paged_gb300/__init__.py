@@ -75,7 +75,7 @@ def library():
             from . import build as _build
             if not _build.up_to_date():
                 try:
-                    _build.build()
+                    _build.build_library()
                 except Exception as e:  # no silent fallback: the CUDA library is the product
                     raise RuntimeError("libgdn_paged.so is missing or stale and could not be built: %s" % e)
             lib = ctypes.CDLL(LIB_PATH)
@@ -426,7 +426,14 @@ _calls = None
 def _load_calls():
     """The module _attention (csrc/binding.cpp), which links to libgdn_paged.so."""
     global _calls
-    library()  # builds both where the sources are newer
+    library()
+    from . import build as _build
+
+    with _lock:
+        try:
+            _build.build_binding()  # where it is missing, older than its source, or another torch's
+        except Exception as e:
+            raise RuntimeError("the binding of the attention calls could not be built: %s" % e)
     module = importlib.import_module(__name__ + "._attention")
     module.set_error(GdnError)
     _calls = module

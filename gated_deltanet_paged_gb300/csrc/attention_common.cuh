@@ -410,8 +410,8 @@ inline int attention_args(gdn::AttnArgs* a, const gdn_bf16* q, int64_t q_stride,
 }
 
 // The longest sequence that a table can hold has every entry that the others do
-// not need, where each has a page.  Beside sequences without any it can be longer:
-// the calls are right all the same, but leave it whole.
+// not need, where each has a page.  Beside sequences without any it can be longer
+// (the calls are right all the same).
 inline int64_t longest_sequence(int32_t num_seqs, int32_t num_entries, int32_t page_size) {
   return (static_cast<int64_t>(num_entries) - num_seqs + 1) * page_size;
 }

@@ -67,7 +67,10 @@ constexpr int kMinShare = 4 * kKeys;
 constexpr int kCrossing = 8;
 // Blocks of a piece, where items are cut evenly: 16 + 4,000 take 20.8 / 16.7 / 18.8 us
 // with pieces of 1 / 2 / 5 blocks.
+// (With one, a last piece could begin past the end of its item on the line, which is
+// shorter than its blocks by the keys that a window hides in the first.)
 constexpr int kMinBlocks = 2;
+static_assert(kMinBlocks >= 2, "no piece of an evenly cut item is empty");
 // Items are not cut if no sequence is longer: 1,000 tokens take 19 us, cut 28;
 // 8 x (64 + 400) 16 us, cut 20.  Of 4,000 keys they are: 16 + 4,000 take 17 us,
 // whole 42.

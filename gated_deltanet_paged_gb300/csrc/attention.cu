@@ -28,13 +28,16 @@
 //     CTAs to itself instead; where sequences are short, none is cut.
 //
 // Measured at 32 query heads on 8 key heads of 128 (4 D flops per visible pair): 4
-// prompts of 8,192 1.33 ms, 1,650 TFLOP/s, 0.89 of a library matrix product's best;
-// the tensor pipe is active for 80% of the cycles, and what is left are the turns of
-// the two tiles and the items' ends.  512 tokens over 131,072 625 us, 1,760 TFLOP/s;
-// 16 over 131,072 97 us, 5.5 TB/s.  With a cap of 30 1,160 TFLOP/s: the
-// softmax takes longer than the products (heads of 64, with half of them, take nine
-// tenths of the time), at 0.5 instructions per cycle; four warps per scheduler
-// instead of two, half a row each, issue no more.  The shortest calls, 9 us, are launch and one block's latency.
+// prompts of 8,192 1.32 to 1.36 ms in short runs, 1,620 to 1,660 TFLOP/s, and 1.55 ms
+// (1,420) in long ones under the power limit, where a library matrix product falls
+// from 1,852 to 1,725; the tensor pipe is active for 80% of the cycles, and what is
+// left are the turns of the two tiles and the items' ends.  512 tokens over 131,072
+// 610 us, 1,810 TFLOP/s; 16 over 131,072 95 us, 5.6 TB/s.  Heads of 64 1.08 ms (1,020
+// TFLOP/s), a distance bias 1.69 ms (1,300), a cap of 30 1.86 ms (1,180): there the
+// softmax takes longer than the products, at 0.5 instructions per cycle; four warps
+// per scheduler instead of two, half a row each, issue no more.  Windows of 128 /
+// 1,024 / 4,096 222 / 478 / 1,072 us: an item of one or two blocks is mostly its own
+// fixed cost.  The shortest calls, 9 us, are launch and one block's latency.
 #include <type_traits>
 
 #include "attention_common.cuh"
@@ -1127,8 +1130,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           float ref = m == -INFINITY ? 0.f : m;  // a row that has seen no key yet: weights 2^-inf = 0
           if (kScores == kBiased) ref -= first_bias;
           // Weights over the first half of their S columns: fp32 into the sum; bf16, as
-          // the values are, into the product.  64 keys at a time, so that the first half
-          // of P V runs beside the exponentials of the second.
+          // the values are, into the product (the tensor core takes both operands in one
+          // type; outputs differ from 64 bits by 0.0020 to 0.0023 of their norm, where
+          // rounding the exact ones to bf16 gives 0.0017).  64 keys at a time, so that
+          // the first half of P V runs beside the exponentials of the second.
           const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), ref2 = make_float2(-ref, -ref);
           auto weight = [&](float2 x) {
             if (kScores == kPlain) x = __ffma2_rn(x, scale2, ref2);

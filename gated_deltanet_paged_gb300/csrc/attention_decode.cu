@@ -21,9 +21,10 @@
 //     through shared memory when the item ends.
 //
 // Measured: 256 sequences of up to 32,768 tokens, 4 key heads of 128 (8.5 GB) 1.17 to
-// 1.20 ms, 7.1 to 7.3 TB/s; 4 of 65,600, 8 key heads (1.07 GB) 158 us, 6.8 TB/s (a plain
-// copy: 6.7).  61 sequences of up to 9,000 (65 MB) 15.5 us: launch, the shares and the
-// join are 7 of them; 2 short sequences 5.3 us are launch and latency alone.
+// 1.20 ms, 7.1 to 7.3 TB/s; 4 of 65,600, 8 key heads (1.07 GB) 157 us, 6.8 TB/s (a plain
+// copy: 6.7).  61 sequences of up to 9,000 (65 MB) 15.7 us, under a cap 16.8: launch, the
+// shares and the join are 7 of them; 2 short sequences 5.3 us are launch and latency
+// alone.
 #include "attention_common.cuh"
 
 namespace {

@@ -405,8 +405,8 @@ __device__ __forceinline__ void tmem_st32_nw(uint32_t taddr, const uint32_t* r) 
 //   kPlain: scale and reference in one multiply-add.
 //   kBiased: a bias that is linear in the key (no prefix mask: every visible key is
 //     behind the token) first.
-//   kGeneral: a bias, or any cap, first (the options that change a score; those
-//     that only hide keys cost nothing away from the edges).
+//   kGeneral: a bias beside a cap or a prefix mask, both first (the options that change
+//     a score; those that only hide keys cost nothing away from the edges).
 //   kCapped: a cap and no bias.  Small scores take the cap's polynomial straight to the
 //     weights, without a maximum, 32 keys at a time.
 enum Scores { kPlain, kBiased, kGeneral, kCapped };
@@ -946,8 +946,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The others go through loops of 32, read from TMEM again where needed:
         // unrolled, their instructions were fetched more slowly than issued (ncu: 1.5
         // warps per issue waited for one, against 0.4 on the plain path; rolling
-        // took the 64 mixed sequences from 2.13 to 1.73 ms, but would take 4 x 8,192
-        // plain tokens from 1.39 to 1.48).
+        // took the 64 mixed sequences, under a cap on the general path, from 2.13 to 1.73
+        // ms, but would take 4 x 8,192 plain tokens from 1.39 to 1.48).
         constexpr bool kInRegisters = kScores == kPlain || kScores == kBiased;
         float s[kInRegisters ? 128 : 1];
         const float first_bias = slope * static_cast<float>(key0 - pos);  // kBiased: of the block's first key

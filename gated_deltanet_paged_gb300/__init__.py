@@ -35,6 +35,11 @@ __all__ = [
     "gdn_kv_append_paged",
     "gdn_attention_paged",
     "gdn_attention_decode_paged",
+    "gdn_qk_norm_rope",
+    "gdn_kv_append_paged_fp8",
+    "gdn_kv_read_paged_fp8",
+    "gdn_attention_paged_fp8",
+    "gdn_attention_decode_paged_fp8",
     "gdn_attention_workspace_bytes",
     "gdn_attention_decode_workspace_bytes",
     "gdn_status_string",
@@ -103,6 +108,11 @@ def library():
                 "gdn_kv_append_paged": [P, i64, P, P, i64, P, i64, P, i32, i32, P, P, P, i32, i32, f32, P, P],
                 "gdn_attention_paged": [P, i64, P, P, P, i32, i32, P, P, f32, P, P, sz, P, P],
                 "gdn_attention_decode_paged": [P, i64, P, P, i32, P, P, f32, P, P, sz, P, P],
+                "gdn_qk_norm_rope": [P, i64, P, i64, P, i64, P, i64, P, P, P, i32, i32, i32, i32, i32, i32, f32, P],
+                "gdn_kv_append_paged_fp8": [P, i64, P, P, i64, P, i64, P, i32, i32, P, P, P, P, i32, i32, f32, P, P],
+                "gdn_kv_read_paged_fp8": [P, P, P, i32, P, P, P, P],
+                "gdn_attention_paged_fp8": [P, i64, P, P, P, i32, i32, P, P, f32, P, P, sz, P, P],
+                "gdn_attention_decode_paged_fp8": [P, i64, P, P, i32, P, P, f32, P, P, sz, P, P],
             }
             for name, args in sig.items():
                 fn = getattr(lib, name)
@@ -509,3 +519,62 @@ def gdn_attention_decode_paged(q, k_cache, v_cache, page_indices, page_indptr, l
     gdn_attention_decode_workspace_bytes)."""
     return (_calls or _load_calls()).attention(True, q, k_cache, v_cache, None, page_indices, page_indptr, last_page_len, scale,
                                           softcap, window, slopes, full_lens, o, lse, return_lse, err_word, workspace)
+
+
+# ---------------------------------------------------------------------------
+# The attention layer's cache in 8 bits.  k_cache and v_cache are float8_e4m3fn
+# [num_pages, page_size, Hkv, D] (D 64 or 128, page_size a multiple of 16, any order
+# of pages, slots and heads), k_scales and v_scales float8_e8m0fnu [num_pages,
+# page_size / 16, Hkv]: a power of two for every 16 tokens of a page and head.
+# ---------------------------------------------------------------------------
+def gdn_qk_norm_rope(q, k, q_weight, k_weight, frequencies=None, positions=None, *, eps=1e-6, weight_offset=0.0,
+                     interleaved=False, amplitude=1.0, q_out=None, k_out=None):
+    """Norm of every query and key head, x / sqrt(mean(x^2) + eps) times
+    (weight_offset + weight), and the rotation of gdn_rope, in one pass with one
+    rounding.  q: bf16 [T, Hq, D], k: bf16 [T, Hkv, D] or None, token strides free, D
+    at most 256; q_weight, k_weight: bf16 [D] (k_weight None without k).  Without
+    ``frequencies`` nothing is rotated, and ``positions`` (int32 [T]) is not needed.
+    ``q_out`` and ``k_out`` may be q and k.  Returns (q_out, k_out), k_out None without k."""
+    return (_calls or _load_calls()).qk_norm_rope(q, k, q_weight, k_weight, frequencies, positions, eps, weight_offset,
+                                             interleaved, amplitude, q_out, k_out)
+
+
+def gdn_kv_append_paged_fp8(k, v, k_cache, v_cache, k_scales, v_scales, cu_seqlens, page_indices, page_indptr,
+                            last_page_len, *, q=None, q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0,
+                            frequencies=None, interleaved=False, amplitude=1.0, q_out=None, err_word=None):
+    """gdn_kv_append_paged into an 8-bit cache.  With ``q_weight`` and ``k_weight``
+    (both, also without q) queries and keys take the norm of gdn_qk_norm_rope before
+    their rotation.  The scale of a group of 16 tokens is the least power of two that
+    brings its new values to 448; where earlier tokens of the sequence are in the
+    group it does not fall, and where it grows their codes are rounded to it.
+    Returns the queries (None without q); caches and scales are updated in place."""
+    return (_calls or _load_calls()).kv_append8(k, v, k_cache, v_cache, k_scales, v_scales, cu_seqlens, page_indices,
+                                           page_indptr, last_page_len, q, q_weight, k_weight, eps, weight_offset,
+                                           frequencies, interleaved, amplitude, q_out, err_word)
+
+
+def gdn_kv_read_paged_fp8(k_cache, v_cache, k_scales, v_scales, cu_seqlens, total_tokens, page_indices, page_indptr,
+                          last_page_len, *, k_out=None, v_out=None, err_word=None):
+    """Keys and values of every sequence's last tokens (as many as ``cu_seqlens``
+    says, one each where it is None; ``total_tokens`` in all) out of an 8-bit cache:
+    (k, v), bf16 [total_tokens, Hkv, D], exactly what the codes stand for."""
+    return (_calls or _load_calls()).kv_read8(k_cache, v_cache, k_scales, v_scales, cu_seqlens, total_tokens, page_indices,
+                                         page_indptr, last_page_len, k_out, v_out, err_word)
+
+
+def gdn_attention_paged_fp8(q, k_cache, v_cache, k_scales, v_scales, cu_seqlens, page_indices, page_indptr,
+                            last_page_len, *, scale=0.0, softcap=0.0, window=-1, slopes=None, full_lens=None, o=None,
+                            lse=None, return_lse=False, err_word=None, workspace=None):
+    """gdn_attention_paged over an 8-bit cache: the same options, outputs and workspace."""
+    return (_calls or _load_calls()).attention8(False, q, k_cache, v_cache, k_scales, v_scales, cu_seqlens, page_indices,
+                                           page_indptr, last_page_len, scale, softcap, window, slopes, full_lens, o,
+                                           lse, return_lse, err_word, workspace)
+
+
+def gdn_attention_decode_paged_fp8(q, k_cache, v_cache, k_scales, v_scales, page_indices, page_indptr, last_page_len,
+                                   *, scale=0.0, softcap=0.0, window=-1, slopes=None, full_lens=None, o=None,
+                                   lse=None, return_lse=False, err_word=None, workspace=None):
+    """gdn_attention_decode_paged over an 8-bit cache."""
+    return (_calls or _load_calls()).attention8(True, q, k_cache, v_cache, k_scales, v_scales, None, page_indices,
+                                           page_indptr, last_page_len, scale, softcap, window, slopes, full_lens, o,
+                                           lse, return_lse, err_word, workspace)

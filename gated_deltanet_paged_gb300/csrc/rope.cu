@@ -20,15 +20,18 @@
 // token each of 256 sequences 4.7 us, 4 tokens 2.2 us, which are launch and latency.
 #include <math.h>
 
-#include "attention_common.cuh"
+#include "rotate.cuh"
 
 namespace {
 
+using gdn::kMaxPairs;
 using gdn::PagedTokens;
+using gdn::Piece;
 using gdn::SeqRange;
+using gdn_host::bad_rotation;
+using gdn_host::bf;
 
 constexpr int kWarps = 4;
-constexpr int kMaxPairs = 256;  // rotary_dim <= 512
 
 // One kernel serves both calls: the heads of a token are Hq rotated query
 // heads (src q, dst q_out), then Hkv rotated keys and Hkv copied values, both
@@ -53,100 +56,6 @@ struct RotateArgs {
   float sign;           // -1: inverse
   float amplitude;
 };
-
-template <int W>
-struct Piece {  // W bf16 elements
-  uint32_t r[W >= 2 ? W / 2 : 1];
-};
-template <int W>
-__device__ __forceinline__ Piece<W> load_piece(const __nv_bfloat16* p) {
-  Piece<W> x;
-  if constexpr (W == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    x.r[0] = u.x, x.r[1] = u.y, x.r[2] = u.z, x.r[3] = u.w;
-  } else if constexpr (W == 4) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    x.r[0] = u.x, x.r[1] = u.y;
-  } else if constexpr (W == 2) {
-    x.r[0] = *reinterpret_cast<const uint32_t*>(p);
-  } else {
-    x.r[0] = *reinterpret_cast<const uint16_t*>(p);
-  }
-  return x;
-}
-template <int W>
-__device__ __forceinline__ void store_piece(__nv_bfloat16* p, const Piece<W>& x) {
-  if constexpr (W == 8)
-    *reinterpret_cast<uint4*>(p) = make_uint4(x.r[0], x.r[1], x.r[2], x.r[3]);
-  else if constexpr (W == 4)
-    *reinterpret_cast<uint2*>(p) = make_uint2(x.r[0], x.r[1]);
-  else if constexpr (W == 2)
-    *reinterpret_cast<uint32_t*>(p) = x.r[0];
-  else
-    *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(x.r[0]);
-}
-template <int W>
-__device__ __forceinline__ float get(const Piece<W>& x, int i) {
-  return __uint_as_float((i & 1) ? (x.r[i >> 1] & 0xFFFF0000u) : (x.r[i >> 1] << 16));
-}
-template <int W>
-__device__ __forceinline__ Piece<W> pack(const float (&f)[W]) {
-  Piece<W> x;
-  if constexpr (W == 1) {
-    x.r[0] = gdn::pack_bf162(f[0], 0.f) & 0xFFFFu;
-  } else {
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) x.r[i] = gdn::pack_bf162(f[2 * i], f[2 * i + 1]);
-  }
-  return x;
-}
-
-// The pair of pieces (a, b) rotated by cs[0 .. W): the halves of W pairs where
-// the layout keeps them apart, 2 W consecutive elements where it interleaves
-// them.  fp32 throughout, one rounding per result.
-template <int W>
-__device__ __forceinline__ void rotate(Piece<W>& a, Piece<W>& b, const float2* cs, bool interleaved) {
-  float x[W], y[W];
-  if (interleaved) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      // Pair i is elements 2 i and 2 i + 1 of the 2 W.
-      const float e = 2 * i < W ? get<W>(a, (2 * i) % W) : get<W>(b, (2 * i) % W);
-      const float o = 2 * i + 1 < W ? get<W>(a, (2 * i + 1) % W) : get<W>(b, (2 * i + 1) % W);
-      const float2 c = cs[i];
-      const float re = e * c.x - o * c.y, im = e * c.y + o * c.x;
-      if (2 * i < W) x[(2 * i) % W] = re; else y[(2 * i) % W] = re;
-      if (2 * i + 1 < W) x[(2 * i + 1) % W] = im; else y[(2 * i + 1) % W] = im;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float e = get<W>(a, i), o = get<W>(b, i);
-      const float2 c = cs[i];
-      x[i] = e * c.x - o * c.y;
-      y[i] = e * c.y + o * c.x;
-    }
-  }
-  a = pack<W>(x);
-  b = pack<W>(y);
-}
-
-// The sequence of token t: the last b with cu_seqlens[b] <= t, by a 32-way
-// search of the warp (sequences without new tokens share their start with the
-// next one, so the last is the one that holds t).
-__device__ __forceinline__ int find_sequence(const int32_t* cu, int num_seqs, int t) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = num_seqs;  // the answer is in [lo, lo + n)
-  while (n > 1) {
-    const int step = (n + 31) / 32;
-    const int at = lo + lane * step;
-    const bool below = at < lo + n && cu[at] <= t;
-    const int k = max(__popc(__ballot_sync(0xFFFFFFFFu, below)) - 1, 0);
-    n = min(step, lo + n - (lo + k * step));
-    lo += k * step;
-  }
-  return lo;
-}
 
 constexpr int kBatch = 4;  // heads in flight per lane
 
@@ -190,8 +99,8 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const RotateArgs a)
         src = a.k + t * a.k_stride + static_cast<int64_t>(h - a.Hq) * a.D;
       else
         src = a.v + t * a.v_stride + static_cast<int64_t>(h - a.Hq - a.Hkv) * a.D;
-      pa[j] = load_piece<W>(src + first);
-      pb[j] = load_piece<W>(src + second);
+      pa[j] = gdn::load_piece<W>(src + first);
+      pb[j] = gdn::load_piece<W>(src + second);
     }
   };
   // The first heads and the frequencies are asked for before the position: finding
@@ -208,7 +117,7 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const RotateArgs a)
   if (a.positions) {
     position = a.positions[t];
   } else {
-    const int b = a.paged.cu_seqlens ? find_sequence(a.paged.cu_seqlens, a.paged.num_seqs, t) : t;
+    const int b = a.paged.cu_seqlens ? gdn::find_sequence(a.paged.cu_seqlens, a.paged.num_seqs, t) : t;
     const SeqRange s = gdn::seq_range(a.paged, b);
     const int i = t - s.first_token;
     if (s.refused) {
@@ -229,11 +138,7 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const RotateArgs a)
 #pragma unroll
   for (int i = 0; i < kMaxPairs / 32; ++i) {
     if (lane + 32 * i >= a.half) break;
-    const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(position)) * static_cast<uint64_t>(freq[i]);
-    const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
-    float sn, cn;
-    sincospif(half_turns, &sn, &cn);
-    cs[lane + 32 * i] = make_float2(cn * a.amplitude, sn * a.amplitude * a.sign);
+    cs[lane + 32 * i] = gdn::pair_turn(position, freq[i], a.amplitude, a.sign);
   }
   __syncwarp();
 
@@ -255,9 +160,9 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const RotateArgs a)
         dst = (is_v ? a.v_cache : a.k_cache) + slot + (h - a.Hq - (is_v ? a.Hkv : 0)) * a.head_stride;
         turns = turns && !is_v;
       }
-      if (turns) rotate<W>(pa[j], pb[j], cs + unit * W, a.interleaved != 0);
-      store_piece<W>(dst + first, pa[j]);
-      store_piece<W>(dst + second, pb[j]);
+      if (turns) gdn::rotate<W>(pa[j], pb[j], cs + unit * W, a.interleaved != 0);
+      gdn::store_piece<W>(dst + first, pa[j]);
+      gdn::store_piece<W>(dst + second, pb[j]);
     }
     u0 += kBatch * stride;
     load(u0);
@@ -265,9 +170,7 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const RotateArgs a)
 }
 
 int launch_rotate(RotateArgs a, cudaStream_t stream) {
-  // The widest piece that divides the rotated halves and the copied rest.
-  int W = 8;
-  while (a.half % W != 0 || (a.D / 2 - a.half) % W != 0) W >>= 1;
+  const int W = gdn_host::piece_width(a.half, a.D);
   a.units = a.D / (2 * W);
   const int64_t iterations = (static_cast<int64_t>(a.Hq + 2 * a.Hkv) * a.units + 31) / 32;
   // One warp per token where that fills the GPU (it evaluates the sines once
@@ -289,15 +192,6 @@ int launch_rotate(RotateArgs a, cudaStream_t stream) {
     default: return gdn_host::launch_pdl(rotate_kernel<1>, grid, block, 0, stream, a);
   }
 }
-
-bool bad_rotation(const int64_t* frequencies, int32_t rotary_dim, int32_t D, float amplitude) {
-  if (!frequencies) return rotary_dim != 0;
-  return rotary_dim <= 0 || rotary_dim % 2 != 0 || rotary_dim > D || rotary_dim / 2 > kMaxPairs ||
-         (reinterpret_cast<uintptr_t>(frequencies) & 7u) != 0 || !isfinite(amplitude);
-}
-
-const __nv_bfloat16* bf(const gdn_bf16* p) { return reinterpret_cast<const __nv_bfloat16*>(p); }
-__nv_bfloat16* bf(gdn_bf16* p) { return reinterpret_cast<__nv_bfloat16*>(p); }
 
 }  // namespace
 

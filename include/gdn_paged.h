@@ -478,6 +478,105 @@ size_t gdn_attention_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int
 size_t gdn_attention_decode_workspace_bytes(int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D,
                                             int32_t num_entries, int32_t page_size);
 
+/* ------------------------------------------------------------------------
+ * The attention layer's cache in 8 bits.
+ *
+ * Keys and values are held as e4m3 codes (a sign, four exponent and three
+ * mantissa bits; 448 the largest, 0x7F and 0xFF NaN) with a scale for every
+ * group of GDN_FP8_GROUP consecutive tokens of a page and head: a code c under
+ * the scale byte s stands for c * 2^(s - 127) (an e8m0 number).  A power of two
+ * costs no precision, since e4m3 has the same significant bits whatever the
+ * scale, and multiplying by it is exact.  The conventions above hold here too:
+ * the same page table, refusals and error word; strides of the codes are
+ * multiples of 16.
+ * ------------------------------------------------------------------------ */
+#define GDN_FP8_GROUP 16
+
+/* Codes [num_pages, page_size, Hkv, D] with dense D, D 64 or 128, page_size a
+ * multiple of 16; scales [num_pages, page_size / 16, Hkv].  Keys and values have
+ * the same strides, and so have their scales; an order of axes as one likes,
+ * and views into one allocation. */
+typedef struct {
+    uint8_t *k;
+    uint8_t *v;
+    uint8_t *k_scales;
+    uint8_t *v_scales;
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t num_heads;          /* Hkv */
+    int32_t head_dim;           /* D */
+    int64_t page_stride;        /* codes between pages */
+    int64_t token_stride;       /* ... the slots of a page */
+    int64_t head_stride;        /* ... heads */
+    int64_t scale_page_stride;  /* scales between pages */
+    int64_t scale_group_stride; /* ... the groups of a page */
+    int64_t scale_head_stride;  /* ... heads */
+} gdn_kv_cache_fp8;
+
+/* Norm of every query and key head before its rotation:
+ *   y = x / sqrt(mean(x^2) + eps) * (weight_offset + weight)
+ * with one weight per dimension (bf16 [D], 16-byte aligned), the same for every
+ * head of a kind; weight_offset is 1 where weights are stored around zero.  eps
+ * is positive and finite. */
+typedef struct {
+    const gdn_bf16 *q_weight;
+    const gdn_bf16 *k_weight;
+    float eps;
+    float weight_offset;
+} gdn_qk_norm;
+
+/* Norm and rotation of queries and keys in one pass, in fp32 with one rounding
+ * at the end: q_out, k_out = the rotation (as by gdn_rope; none where
+ * frequencies is NULL, and positions may be NULL then) of the heads' norms.  k,
+ * k_out and k_weight are NULL together with Hkv 0.  q, k and the outputs are
+ * [T, H, D] with token strides; an output may be its input (same pointer and
+ * stride), otherwise nothing overlaps.  D is a multiple of 8, at most 256.
+ * Elements up to 2^60 in size keep their precision. */
+int gdn_qk_norm_rope(const gdn_bf16 *q, int64_t q_token_stride, gdn_bf16 *q_out, int64_t q_out_token_stride,
+                     const gdn_bf16 *k, int64_t k_token_stride, gdn_bf16 *k_out, int64_t k_out_token_stride,
+                     const gdn_qk_norm *norm, const int32_t *positions, const int64_t *frequencies,
+                     int32_t total_tokens, int32_t Hq, int32_t Hkv, int32_t D, int32_t rotary_dim,
+                     int32_t interleaved, float amplitude, void *stream);
+
+/* Append, as gdn_kv_append_paged, to a cache in 8 bits: queries and keys take
+ * their norm first (norm NULL: none) and then the rotation, and keys and values
+ * are rounded to nearest (ties to even) as they are written.  The scale of a
+ * group is the least power of two, between 2^-112 and 2^119, that brings its
+ * new tokens to 448 at most; where earlier tokens of the sequence are in the
+ * group already it is not less than it was, and where it grows, their codes are
+ * rounded to it.  Whatever else a group's slots and its scale held is not read.
+ * Infinities are stored as the largest number, NaN as NaN; neither has a say in
+ * the scale of its group but that an infinity raises it to 2^119.  No two
+ * sequences of a call write to one page. */
+int gdn_kv_append_paged_fp8(const gdn_bf16 *q, int64_t q_token_stride, gdn_bf16 *q_out, const gdn_bf16 *k,
+                            int64_t k_token_stride, const gdn_bf16 *v, int64_t v_token_stride,
+                            const int32_t *cu_seqlens, int32_t total_tokens, int32_t Hq,
+                            const gdn_kv_cache_fp8 *cache, const gdn_page_table *table, const gdn_qk_norm *norm,
+                            const int64_t *frequencies, int32_t rotary_dim, int32_t interleaved, float amplitude,
+                            int32_t *err_word, void *stream);
+
+/* Reads keys and values back: row t of k_out and v_out (bf16 [total_tokens, Hkv,
+ * D], dense, not overlapping) receives what is cached for new token t (with
+ * n_b = len_b: for every token of the sequence).  Exact: bf16 holds every value
+ * that an append writes.  Rows of refused sequences and of no sequence stay as
+ * they were; on a page id out of range a row reads as zeros. */
+int gdn_kv_read_paged_fp8(const gdn_kv_cache_fp8 *cache, const gdn_page_table *table, const int32_t *cu_seqlens,
+                          int32_t total_tokens, gdn_bf16 *k_out, gdn_bf16 *v_out, int32_t *err_word, void *stream);
+
+/* gdn_attention_paged and gdn_attention_decode_paged over a cache in 8 bits:
+ * the same definition, options and workspace (the same ..._workspace_bytes), on
+ * the values that the codes stand for.  Scales have to be as an append writes
+ * them, 2^-112 to 2^119, in every group that a token sees. */
+int gdn_attention_paged_fp8(const gdn_bf16 *q, int64_t q_token_stride, gdn_bf16 *o, float *lse,
+                            const int32_t *cu_seqlens, int32_t total_tokens, int32_t Hq,
+                            const gdn_kv_cache_fp8 *cache, const gdn_page_table *table, float scale,
+                            const gdn_attention_options *options, void *workspace, size_t workspace_bytes,
+                            int32_t *err_word, void *stream);
+int gdn_attention_decode_paged_fp8(const gdn_bf16 *q, int64_t q_token_stride, gdn_bf16 *o, float *lse, int32_t Hq,
+                                   const gdn_kv_cache_fp8 *cache, const gdn_page_table *table, float scale,
+                                   const gdn_attention_options *options, void *workspace, size_t workspace_bytes,
+                                   int32_t *err_word, void *stream);
+
 /* Static text for a status code. */
 const char *gdn_status_string(int status);
 

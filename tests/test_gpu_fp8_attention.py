@@ -1,0 +1,122 @@
+"""Paged attention over the 8-bit cache on the GPU against its definition in 64 bits."""
+import pytest
+import torch
+
+import gated_deltanet_paged_gb300 as gdn
+from fp8_util import Batch8, check_attention8
+
+pytestmark = pytest.mark.gpu
+
+I16 = torch.int16
+SHAPES = [(8, 2, 128), (3, 1, 64), (1, 1, 128), (16, 1, 64), (5, 5, 128), (40, 2, 64), (34, 2, 128)]
+CHUNKS = {"ragged": ([100, 37, 0, 1, 65], [0, 64, 7, 63, 1]), "one": ([1], [0]), "long": ([300, 2], [1000, 129]),
+          "ends": ([127, 128, 129, 1], [1, 0, 127, 255]), "deep": ([3, 140], [5000, 2600])}
+
+
+def options(name, hq, new, prefix):
+    slopes = torch.tensor([2.0 ** (-4 * (h + 1) / hq) for h in range(hq)], device="cuda")
+    full = torch.tensor([p + n // 2 for n, p in zip(new, prefix)], dtype=torch.int32, device="cuda")
+    return {"plain": {}, "capped": {"softcap": 5.0}, "window": {"window": 50}, "slopes": {"slopes": slopes},
+            "prefix": {"full_lens": full}, "both": {"softcap": 20.0, "slopes": slopes, "window": 130},
+            "scale": {"scale": 0.3, "softcap": 30.0, "full_lens": full}}[name]
+
+
+@pytest.mark.parametrize("lens", CHUNKS)
+@pytest.mark.parametrize("page_size,layout", [(16, "nhd"), (48, "hnd"), (896, "fused")])
+@pytest.mark.parametrize("hq,hkv,dim", SHAPES[:4])
+def test_chunk(lens, page_size, layout, hq, hkv, dim):
+    new, prefix = CHUNKS[lens]
+    b = Batch8(new, prefix, page_size, hq, hkv, dim, layout=layout, seed=page_size + dim, q_pad=1, padded=layout == "hnd").fill()
+    check_attention8(b)
+
+
+@pytest.mark.parametrize("opts", ["capped", "window", "slopes", "prefix", "both", "scale"])
+@pytest.mark.parametrize("lens", ["ragged", "long", "deep"])
+@pytest.mark.parametrize("hq,hkv,dim", [SHAPES[0], SHAPES[5], SHAPES[1]])
+def test_chunk_options(opts, lens, hq, hkv, dim):
+    new, prefix = CHUNKS[lens]
+    b = Batch8(new, prefix, 64, hq, hkv, dim, seed=len(opts), q_scale=2.0, layout="hnd").fill()
+    check_attention8(b, **options(opts, hq, new, prefix))
+
+
+ONES = {"short": [1, 2, 15, 16, 17, 101], "mixed": [1, 130, 4100, 700, 33], "long": [9000, 64]}
+
+
+@pytest.mark.parametrize("lens", ONES)
+@pytest.mark.parametrize("page_size,layout", [(16, "fused"), (48, "nhd"), (1024, "hnd")])
+@pytest.mark.parametrize("hq,hkv,dim", SHAPES)
+def test_decode(lens, page_size, layout, hq, hkv, dim):
+    lengths = ONES[lens]
+    b = Batch8([1] * len(lengths), [n - 1 for n in lengths], page_size, hq, hkv, dim, layout=layout, seed=page_size + hq,
+               q_pad=1, padded=layout == "nhd").fill()
+    check_attention8(b, decode=True)
+
+
+@pytest.mark.parametrize("opts", ["capped", "window", "slopes", "prefix", "both", "scale"])
+@pytest.mark.parametrize("lens", ["mixed", "long"])
+@pytest.mark.parametrize("hq,hkv,dim", [SHAPES[0], SHAPES[5], SHAPES[6], SHAPES[1]])
+def test_decode_options(opts, lens, hq, hkv, dim):
+    lengths = ONES[lens]
+    new, prefix = [1] * len(lengths), [n - 1 for n in lengths]
+    b = Batch8(new, prefix, 64, hq, hkv, dim, seed=len(opts), q_scale=2.0).fill()
+    check_attention8(b, decode=True, **options(opts, hq, new, prefix))
+
+
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("spread", [1, 40, 100])
+def test_scales_far_apart(decode, spread):
+    """Groups whose scales differ by up to 2^99: a group of large values takes the whole
+    softmax or the whole sum, and the others' share is still right."""
+    new, prefix = ([1] * 4, [40, 300, 15, 1500]) if decode else ([20, 200, 1], [40, 10, 700])
+    b = Batch8(new, prefix, 32, 8, 2, 128, seed=spread, spread=spread)
+    for name in "kv":  # keys small enough for scores that are finite numbers of any size
+        for i, (c, e) in enumerate(b.codes[name]):
+            e -= spread if name == "k" else spread // 2
+            value = c.double() * torch.exp2(e.double()).repeat_interleave(16, 0)[: len(c), :, None]
+            getattr(b, name)[i] = value
+    b.fill()
+    check_attention8(b, decode=decode)
+
+
+def test_chunk_is_what_the_16_bit_cache_gives():
+    """Read back into a 16-bit cache, the same attention gives the same outputs within the
+    rounding of weights and outputs (2^-8 each of a weighted sum of values)."""
+    new, prefix = [300, 1, 90], [100, 500, 0]
+    b = Batch8(new, prefix, 64, 8, 2, 128, seed=11).fill()
+    o8 = gdn.gdn_attention_paged_fp8(b.q, *b.cache, b.cu, *b.table)
+    total = [n + p for n, p in zip(new, prefix)]
+    cu = torch.tensor([0, 400, 901, 991], dtype=torch.int32, device="cuda")
+    k, v = gdn.gdn_kv_read_paged_fp8(*b.cache, cu, sum(total), *b.table)
+    kc = torch.zeros(*b.k_cache.shape, dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    gdn.gdn_kv_append_paged(k, v, kc, vc, cu, *b.table)
+    o16 = gdn.gdn_attention_paged(b.q, kc, vc, b.cu, *b.table)
+    big = float(v.abs().max())
+    assert (o8.float() - o16.float()).abs().max() <= 4 * 2.0**-8 * big
+
+
+@pytest.mark.parametrize("decode", [False, True])
+def test_reports_and_skips(decode):
+    """A refused sequence's outputs stay as they were, a bad page reads as zeros; both are
+    reported, and the others' outputs are what they are without."""
+    new, prefix = [1] * 4 if decode else [5, 20, 3, 7], [30, 200, 16, 900]
+    good = Batch8(new, prefix, 16, 4, 2, 64, seed=6).fill()
+    call = (lambda b, **kw: gdn.gdn_attention_decode_paged_fp8(b.q, *b.cache, *b.table, **kw)) if decode else (
+        lambda b, **kw: gdn.gdn_attention_paged_fp8(b.q, *b.cache, b.cu, *b.table, **kw))
+    ref = call(good)
+    rows = torch.ones(sum(new), dtype=torch.bool)
+    rows[new[0] : new[0] + new[1]] = False
+    for what in ("length", "page"):
+        b = Batch8(new, prefix, 16, 4, 2, 64, seed=6).fill()
+        if what == "length":
+            b.last[1] = 0
+        else:
+            b.indices[b.indptr[1].item() + 3] = -5
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        o = torch.full_like(ref, 7.0)
+        call(b, o=o, err_word=err)
+        assert int(err.item()) == ((2 if what == "length" else 1) << 24 | 1)
+        assert torch.isfinite(o.float()).all()
+        within = (o[rows].float() - ref[rows].float()).abs().max()
+        assert within <= 2.0**-7 * ref.float().abs().max()
+        assert (o[~rows] == 7.0).all() == (what == "length")

@@ -53,9 +53,37 @@ __device__ __forceinline__ Piece<W> pack(const float (&f)[W]) {
   return x;
 }
 
-// The halves x, y of W pairs, turned by cs[0 .. W) in fp32: element i of both where
-// the layout keeps the halves apart, 2 W consecutive elements where it interleaves
-// them.
+// The pair of pieces (a, b) rotated by cs[0 .. W): the halves of W pairs where
+// the layout keeps them apart, 2 W consecutive elements where it interleaves
+// them.  fp32 throughout, one rounding per result.
+template <int W>
+__device__ __forceinline__ void rotate(Piece<W>& a, Piece<W>& b, const float2* cs, bool interleaved) {
+  float x[W], y[W];
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      // Pair i is elements 2 i and 2 i + 1 of the 2 W.
+      const float e = 2 * i < W ? get<W>(a, (2 * i) % W) : get<W>(b, (2 * i) % W);
+      const float o = 2 * i + 1 < W ? get<W>(a, (2 * i + 1) % W) : get<W>(b, (2 * i + 1) % W);
+      const float2 c = cs[i];
+      const float re = e * c.x - o * c.y, im = e * c.y + o * c.x;
+      if (2 * i < W) x[(2 * i) % W] = re; else y[(2 * i) % W] = re;
+      if (2 * i + 1 < W) x[(2 * i + 1) % W] = im; else y[(2 * i + 1) % W] = im;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float e = get<W>(a, i), o = get<W>(b, i);
+      const float2 c = cs[i];
+      x[i] = e * c.x - o * c.y;
+      y[i] = e * c.y + o * c.x;
+    }
+  }
+  a = pack<W>(x);
+  b = pack<W>(y);
+}
+
+// The same of pairs that are in fp32 already.
 template <int W, typename Cs>
 __device__ __forceinline__ void turn(float (&x)[W], float (&y)[W], const Cs& cs, bool interleaved) {
   if (interleaved) {
@@ -82,17 +110,6 @@ __device__ __forceinline__ void turn(float (&x)[W], float (&y)[W], const Cs& cs,
     }
   }
 }
-// The same of bf16 pieces: one rounding per result.
-template <int W>
-__device__ __forceinline__ void rotate(Piece<W>& a, Piece<W>& b, const float2* cs, bool interleaved) {
-  float x[W], y[W];
-#pragma unroll
-  for (int i = 0; i < W; ++i) x[i] = get<W>(a, i), y[i] = get<W>(b, i);
-  turn<W>(x, y, [&](int i) { return cs[i]; }, interleaved);
-  a = pack<W>(x);
-  b = pack<W>(y);
-}
-
 // The sequence of token t: the last b with cu_seqlens[b] <= t, by a 32-way
 // search of the warp (sequences without new tokens share their start with the
 // next one, so the last is the one that holds t).

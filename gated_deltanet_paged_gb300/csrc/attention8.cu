@@ -97,11 +97,3 @@ extern "C" int gdn_attention_paged_fp8(const gdn_bf16* q, int64_t q_token_stride
   return attend(q, q_token_stride, o, lse, cu_seqlens, total_tokens, Hq, cache, table, scale, options, workspace, workspace_bytes,
                 cache && table ? gdn_attention_workspace_bytes(table->num_seqs, total_tokens, Hq, cache->num_heads, cache->head_dim, table->num_entries, cache->page_size) : 0, err_word, stream);
 }
-
-extern "C" int gdn_attention_decode_paged_fp8(const gdn_bf16* q, int64_t q_token_stride, gdn_bf16* o, float* lse,
-                                              int32_t Hq, const gdn_kv_cache_fp8* cache, const gdn_page_table* table,
-                                              float scale, const gdn_attention_options* options, void* workspace, size_t workspace_bytes,
-                                              int32_t* err_word, void* stream) {
-  return attend(q, q_token_stride, o, lse, nullptr, table ? table->num_seqs : 0, Hq, cache, table, scale, options, workspace, workspace_bytes,
-                cache && table ? gdn_attention_decode_workspace_bytes(table->num_seqs, Hq, cache->num_heads, cache->head_dim, table->num_entries, cache->page_size) : 0, err_word, stream);
-}

@@ -230,8 +230,9 @@ __device__ __forceinline__ int key_lo(const AttnArgs& a, int pos) { return a.win
 // their page is asked for a tile ahead.  (The instructions of these warps are
 // rarely in the cache: with a lookup per tile the products waited for keys.)  A
 // tile of more than 32 boxes, from pages of an odd or once even size, is looked
-// up on the spot.
-template <int D, int kKeys>
+// up on the spot.  A row of kElem bytes a dimension goes in columns of 128 bytes, or
+// in one of 64.
+template <int D, int kKeys, int kElem = 2>
 struct TileCopies {
   const AttnArgs& a;
   const CUtensorMap* map;
@@ -272,12 +273,13 @@ struct TileCopies {
   __device__ __forceinline__ int bytes() const {
     const int first = max(0, lo - key0) >> a.box_shift;
     const int last = (min(kKeys, hi - key0) + box_rows - 1) >> a.box_shift;
-    return (last - first) * box_rows * D * 2;
+    return (last - first) * box_rows * D * kElem;
   }
   __device__ __forceinline__ void box(uint8_t* dst, uint64_t* bar, int i, int o, int p) const {
+    constexpr int kRowBytes = D * kElem < 128 ? D * kElem : 128;
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c)
-      tma_load_4d(dst + c * (kKeys * 128) + i * box_rows * 128, map, bar, c * 64, head, o, p);
+    for (int c = 0; c < D * kElem / kRowBytes; ++c)
+      tma_load_4d(dst + c * (kKeys * kRowBytes) + i * box_rows * kRowBytes, map, bar, c * (kRowBytes / kElem), head, o, p);
   }
   // The current tile; then on to the next of `more`.
   __device__ __forceinline__ void copy(uint8_t* dst, uint64_t* bar, bool more) {

@@ -73,6 +73,15 @@ inline int check_paged8(const gdn_kv_cache_fp8* c, const gdn_page_table* t, cons
   return GDN_OK;
 }
 
+// Tensor map of one array of codes, {D, heads, slots, pages}, with boxes of 2^box_shift
+// slots of one head.
+inline int encode_codes_map(CUtensorMap* map, const uint8_t* base, const gdn_kv_cache_fp8* c, int box_shift) {
+  const int64_t dims[4] = {c->head_dim, c->num_heads, c->page_size, c->num_pages};
+  const int64_t strides[3] = {c->num_heads > 1 ? c->head_stride : c->head_dim, c->page_size > 1 ? c->token_stride : c->head_dim,
+                              c->num_pages > 1 ? c->page_stride : c->head_dim};
+  return encode_bytes_map_4d(map, base, dims, strides, 1, 1 << box_shift);
+}
+
 inline gdn::Cache8 cache8(const gdn_kv_cache_fp8* c) {
   return gdn::Cache8{{c->k, c->v},      {c->k_scales, c->v_scales}, c->page_stride,        c->token_stride,
                      c->head_stride, c->scale_page_stride,       c->scale_group_stride, c->scale_head_stride};

@@ -107,6 +107,21 @@ int encode_map_4d(CUtensorMap* map, const void* base, const int64_t (&d)[4], con
   return r == CUDA_SUCCESS ? GDN_OK : GDN_ERR_CUDA;
 }
 
+int encode_bytes_map_4d(CUtensorMap* map, const void* base, const int64_t (&d)[4], const int64_t (&s)[3], int box1,
+                        int box2) {
+  auto fn = encode_fn();
+  if (!fn) return GDN_ERR_CUDA;
+  cuuint64_t dims[4], strides[3];
+  for (int i = 0; i < 4; ++i) dims[i] = static_cast<cuuint64_t>(d[i]);
+  for (int i = 0; i < 3; ++i) strides[i] = static_cast<cuuint64_t>(s[i]);
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(d[0]), static_cast<cuuint32_t>(box1), static_cast<cuuint32_t>(box2), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, d[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GDN_OK : GDN_ERR_CUDA;
+}
+
 }  // namespace gdn_host
 
 extern "C" const char* gdn_status_string(int status) {

@@ -502,6 +502,10 @@ int encode_tiles_map_f16(CUtensorMap* map, const void* base, int64_t rows, int64
 // dims 1-3) with a box of 64 x box1 x box2 x 1 elements and 128-byte swizzle.
 int encode_map_4d(CUtensorMap* map, const void* base, const int64_t (&dims)[4], const int64_t (&strides)[3], int box1,
                   int box2);
+// Encode a 4-D map of bytes, 64 or 128 of them innermost, with a box of all of those x
+// box1 x box2 x 1 and a swizzle over as many bytes.
+int encode_bytes_map_4d(CUtensorMap* map, const void* base, const int64_t (&dims)[4], const int64_t (&strides)[3],
+                        int box1, int box2);
 int encode_tokens_map_32(CUtensorMap* map, const void* base, int64_t T, int64_t H, int64_t D);  // 64B swizzle
 
 inline int launch_status() { return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }

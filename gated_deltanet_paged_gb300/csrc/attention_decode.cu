@@ -32,6 +32,8 @@ namespace {
 // Keys per stage: 16 KB each of K and V.
 template <int D>
 constexpr int kBlock = kTileBytes / (2 * D);
+constexpr int kConsumers = 4;
+constexpr int kThreads = threads_of(kConsumers);
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -53,12 +55,100 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The end of an item's segment in the consumer warps: m, l and o of their two rows each
+// (g and g + 8, in the fragment layout of the products) become the CTA's, a result or
+// a part of one.  false: a wait ran out.
+template <int D>
+__device__ __forceinline__ bool end_segment(const DecodeArgs& d, Smem<kConsumers, D / 8, 1>& sh, const Walk& w,
+                                            const gdn::Shares<0>& shares, int rows, float (&m)[2], float (&l)[2],
+                                            const float (&o)[D / 8][4]) {
+  const AttnArgs& a = d.a;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  const int g = lane >> 2, t = lane & 3;
+  const int h0 = w.head * a.group;
+  // ---- join the four warps: each takes a quarter of the dimensions of all ----
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
+    l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
+  }
+  consumers_sync<kConsumers>();  // the last item's results have been read
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) sh.join_o[warp][i][lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+  sh.join_ml[warp][0][lane] = make_float4(m[0], m[1], l[0], l[1]);
+  if (tid == 0) sh.stop = *static_cast<volatile int*>(&sh.abort);  // one reading for all warps
+  consumers_sync<kConsumers>();
+  if (sh.stop) {
+    if (tid == 0) gdn::record_error(a.paged.err_word, GDN_DEVERR_TIMEOUT, 0);
+    return false;
+  }
+  float f[kConsumers][2];
+  {
+    float4 ml[kConsumers];
+#pragma unroll
+    for (int v = 0; v < kConsumers; ++v) ml[v] = sh.join_ml[v][0][lane];
+    m[0] = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+    m[1] = fmaxf(fmaxf(ml[0].y, ml[1].y), fmaxf(ml[2].y, ml[3].y));
+    l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int v = 0; v < kConsumers; ++v) {
+      f[v][0] = ml[v].x == -INFINITY ? 0.f : gdn::exp2_approx(ml[v].x - m[0]);
+      f[v][1] = ml[v].y == -INFINITY ? 0.f : gdn::exp2_approx(ml[v].y - m[1]);
+      l[0] = fmaf(ml[v].z, f[v][0], l[0]);
+      l[1] = fmaf(ml[v].w, f[v][1], l[1]);
+    }
+  }
+  const bool starts = w.blk0 == 0, ends = w.blk1 == w.it.blocks;
+  // One segment of a CTA at most starts an item that it does not end, and one at
+  // most continues one: two slots per CTA.
+  const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (starts ? 1 : 0);
+  const int64_t row0 = static_cast<int64_t>(w.b) * a.Hq + h0;
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) {
+    const int at = warp * (D / 32) + k;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int v = 0; v < kConsumers; ++v) {
+      const float4 y = sh.join_o[v][at][lane];
+      x[0] = fmaf(y.x, f[v][0], x[0]);
+      x[1] = fmaf(y.y, f[v][0], x[1]);
+      x[2] = fmaf(y.z, f[v][1], x[2]);
+      x[3] = fmaf(y.w, f[v][1], x[3]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = g + 8 * i;
+      if (r >= rows) continue;
+      if (starts && ends)
+        reinterpret_cast<uint32_t*>(a.o + (row0 + r) * D)[at * 4 + t] =
+            gdn::pack_bf162(x[2 * i] / l[i], x[2 * i + 1] / l[i]);
+      else
+        reinterpret_cast<float2*>(d.part_o + (slot * kRows + r) * D)[at * 4 + t] = make_float2(x[2 * i], x[2 * i + 1]);
+    }
+  }
+  if (warp == 0 && t == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = g + 8 * i;
+      if (r >= rows) continue;
+      if (!(starts && ends))
+        d.part_ml[slot * kRows + r] = make_float2(m[i], l[i]);
+      else if (a.lse)
+        a.lse[row0 + r] = (m[i] + log2f(l[i])) / gdn::kLog2e;
+    }
+  }
+  if (tid == 0 && starts && !ends)
+    d.cuts[blockIdx.x] = make_int4(w.b, w.head, shares.owner(w.item0 + w.it.cost - 1), 0);
+  return true;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_attention_kernel(const __grid_constant__ DecodeArgs d, const __grid_constant__ CUtensorMap k_map,
                             const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ uint8_t raw[];
-  Smem<D>& sh = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  Smem<kConsumers, D / 8, 1>& sh = *reinterpret_cast<Smem<kConsumers, D / 8, 1>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const AttnArgs& a = d.a;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
@@ -262,7 +352,7 @@ template <int D>
 int launch(const DecodeArgs& base, const gdn_kv_cache* cache, const gdn_page_table* table, void* workspace, int sms,
            cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  constexpr int smem = sizeof(Smem<D>) + 1024;
+  constexpr int smem = sizeof(Smem<kConsumers, D / 8, 1>) + 1024;
   int rc = gdn_host::func_attr_once(decode_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem, done);
   if (rc != GDN_OK) return rc;
   DecodeArgs d = base;

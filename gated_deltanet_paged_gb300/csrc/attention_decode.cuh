@@ -13,8 +13,9 @@ using gdn::SeqRange;
 // Two stages, so 128 KB on their way per SM: with a third the queues before HBM
 // grow and its rate falls (256 sequences, 8.5 GB: 1.23 ms against 1.17).
 constexpr int kStages = 2;
-constexpr int kConsumers = 4;  // warps, a quarter of a block's keys each
-constexpr int kThreads = (kConsumers + 2) * 32;  // and one warp that copies keys, one that copies values
+// Consumer warps, each with its part of a block's keys, beside one warp that copies keys
+// and one that copies values.
+constexpr int threads_of(int consumers) { return (consumers + 2) * 32; }
 constexpr int kRows = 16;     // query heads of a key head at most (see gdn_attention_decode_paged)
 constexpr int kTileBytes = 16384;
 // Fixed cost of an item (its queries, the join of the warps, its stores) in
@@ -101,16 +102,18 @@ __device__ __forceinline__ bool next_segment(const DecodeArgs& d, Walk& w) {
   return false;
 }
 
-template <int D>
+// kTiles: the join's tiles of a warp, a float4 a lane; kPairs: pairs of rows whose maximum
+// and sum a lane has.
+template <int kConsumers, int kTiles, int kPairs>
 struct Smem {
   static constexpr int kTile = kTileBytes;  // one of K, V
   alignas(1024) uint8_t kv[kStages][2][kTile];
-  float4 join_o[kConsumers][D / 8][32];  // the warps' partial results, lane by lane
-  float4 join_ml[kConsumers][32];        // m, l of their two rows
+  float4 join_o[kConsumers][kTiles][32];  // the warps' partial results, lane by lane
+  float4 join_ml[kConsumers][kPairs][32];  // m, l of two rows
   uint64_t full[kStages];
   uint64_t empty[kStages];
   uint64_t never;  // the test hook's barrier, never completed
-  int64_t scan[kThreads / 32 + 1];
+  int64_t scan[kConsumers + 3];
   Walk walk;
   int abort;
   int stop;
@@ -126,13 +129,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
   return wait_more(bar, parity, abort, limit_ns);
 }
 
+template <int kConsumers>
 __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
 }
 
 // This CTA's share of the line; false: none.  All threads take it together.
-template <int kBlock, typename S>
-__device__ __forceinline__ bool take_share(const DecodeArgs& d, S& sh, Walk& w, gdn::Shares<0>& shares) {
+template <int kBlock, int kConsumers, int kTiles, int kPairs>
+__device__ __forceinline__ bool take_share(const DecodeArgs& d, Smem<kConsumers, kTiles, kPairs>& sh, Walk& w, gdn::Shares<0>& shares) {
+  constexpr int kThreads = threads_of(kConsumers);
   const AttnArgs& a = d.a;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
@@ -190,93 +195,6 @@ __device__ __forceinline__ bool take_share(const DecodeArgs& d, S& sh, Walk& w, 
     if (start >= end) return false;
     w = sh.walk;
   }
-  return true;
-}
-
-// The end of an item's segment in the consumer warps: m, l and o of their two rows each
-// (g and g + 8, in the fragment layout of the products) become the CTA's, a result or
-// a part of one.  false: a wait ran out.
-template <int D, typename S>
-__device__ __forceinline__ bool end_segment(const DecodeArgs& d, S& sh, const Walk& w, const gdn::Shares<0>& shares, int rows,
-                                            float (&m)[2], float (&l)[2], const float (&o)[D / 8][4]) {
-  const AttnArgs& a = d.a;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
-  const int g = lane >> 2, t = lane & 3;
-  const int h0 = w.head * a.group;
-  // ---- join the four warps: each takes a quarter of the dimensions of all ----
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
-    l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
-  }
-  consumers_sync();  // the last item's results have been read
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) sh.join_o[warp][i][lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-  sh.join_ml[warp][lane] = make_float4(m[0], m[1], l[0], l[1]);
-  if (tid == 0) sh.stop = *static_cast<volatile int*>(&sh.abort);  // one reading for all warps
-  consumers_sync();
-  if (sh.stop) {
-    if (tid == 0) gdn::record_error(a.paged.err_word, GDN_DEVERR_TIMEOUT, 0);
-    return false;
-  }
-  float f[kConsumers][2];
-  {
-    float4 ml[kConsumers];
-#pragma unroll
-    for (int v = 0; v < kConsumers; ++v) ml[v] = sh.join_ml[v][lane];
-    m[0] = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
-    m[1] = fmaxf(fmaxf(ml[0].y, ml[1].y), fmaxf(ml[2].y, ml[3].y));
-    l[0] = l[1] = 0.f;
-#pragma unroll
-    for (int v = 0; v < kConsumers; ++v) {
-      f[v][0] = ml[v].x == -INFINITY ? 0.f : gdn::exp2_approx(ml[v].x - m[0]);
-      f[v][1] = ml[v].y == -INFINITY ? 0.f : gdn::exp2_approx(ml[v].y - m[1]);
-      l[0] = fmaf(ml[v].z, f[v][0], l[0]);
-      l[1] = fmaf(ml[v].w, f[v][1], l[1]);
-    }
-  }
-  const bool starts = w.blk0 == 0, ends = w.blk1 == w.it.blocks;
-  // One segment of a CTA at most starts an item that it does not end, and one at
-  // most continues one: two slots per CTA.
-  const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (starts ? 1 : 0);
-  const int64_t row0 = static_cast<int64_t>(w.b) * a.Hq + h0;
-#pragma unroll
-  for (int k = 0; k < D / 32; ++k) {
-    const int at = warp * (D / 32) + k;
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int v = 0; v < kConsumers; ++v) {
-      const float4 y = sh.join_o[v][at][lane];
-      x[0] = fmaf(y.x, f[v][0], x[0]);
-      x[1] = fmaf(y.y, f[v][0], x[1]);
-      x[2] = fmaf(y.z, f[v][1], x[2]);
-      x[3] = fmaf(y.w, f[v][1], x[3]);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = g + 8 * i;
-      if (r >= rows) continue;
-      if (starts && ends)
-        reinterpret_cast<uint32_t*>(a.o + (row0 + r) * D)[at * 4 + t] =
-            gdn::pack_bf162(x[2 * i] / l[i], x[2 * i + 1] / l[i]);
-      else
-        reinterpret_cast<float2*>(d.part_o + (slot * kRows + r) * D)[at * 4 + t] = make_float2(x[2 * i], x[2 * i + 1]);
-    }
-  }
-  if (warp == 0 && t == 0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = g + 8 * i;
-      if (r >= rows) continue;
-      if (!(starts && ends))
-        d.part_ml[slot * kRows + r] = make_float2(m[i], l[i]);
-      else if (a.lse)
-        a.lse[row0 + r] = (m[i] + log2f(l[i])) / gdn::kLog2e;
-    }
-  }
-  if (tid == 0 && starts && !ends)
-    d.cuts[blockIdx.x] = make_int4(w.b, w.head, shares.owner(w.item0 + w.it.cost - 1), 0);
   return true;
 }
 

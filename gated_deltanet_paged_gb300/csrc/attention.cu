@@ -57,7 +57,7 @@ int launch(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache* cache, void* w
   if ((rc = gdn_host::encode_cache_map(&k_map, cache->k, cache, d.a.box_shift)) != GDN_OK) return rc;
   if ((rc = gdn_host::encode_cache_map(&v_map, cache->v, cache, d.a.box_shift)) != GDN_OK) return rc;
   const auto kernel = chunk_attention_kernel<D, kScores>;
-  return launch_chunk<D>(kernel, d, total_tokens, Registers<false>::kSum, done, workspace, sms, stream,
+  return launch_chunk<D, false>(kernel, d, total_tokens, done, workspace, sms, stream,
                          [&](dim3 grid, dim3 block, int smem, const CUtensorMap& q_map) {
                            return gdn_host::launch_pdl(kernel, grid, block, smem, stream, d, q_map, k_map, v_map);
                          });

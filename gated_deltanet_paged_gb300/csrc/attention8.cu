@@ -1,14 +1,12 @@
 // attention8.cu -- softmax attention of a chunk of new tokens over the 8-bit cache.
 //
 // The kernel is that of attention.cu, but for the way of keys and values into shared
-// memory: the four epilogue warps read codes by ordinary loads, a tile ahead in
-// registers, turn them into bf16 (exactly: a code has 4 significant bits and its scale is
-// a power of two) and store them in the layout that the copies by TMA have there.  The
-// products, the softmax and the outputs are bit for bit those over a 16-bit cache that
-// holds the same values.
+// memory: tiles of codes come by TMA into two tiles of their own, and the four epilogue
+// warps turn them into bf16 (exactly: a code has 4 significant bits and its scale is a
+// power of two) in the layout that the copies have there.  The products, the softmax and
+// the outputs are bit for bit those over a 16-bit cache that holds the same values.
 //
-// Bound: the tensor cores, as there; shared memory sees the same traffic.  The
-// conversion is 5 instructions for two codes in warps of its own.
+// Bound: the tensor cores, as there.
 #include "attention_chunk.cuh"
 
 namespace {
@@ -16,17 +14,22 @@ namespace {
 template <int D, Scores kScores>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_attention8_kernel(const __grid_constant__ ChunkArgs d, const __grid_constant__ CUtensorMap q_map,
+                            const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                             const __grid_constant__ gdn::Cache8 codes) {
-  chunk_attention<D, kScores, true>(d, q_map, q_map, q_map, codes);
+  chunk_attention<D, kScores, true>(d, q_map, k_map, v_map, codes);
 }
 
 template <int D, Scores kScores>
-int launch(ChunkArgs d, int32_t total_tokens, const gdn::Cache8& codes, void* workspace, int sms, cudaStream_t stream) {
+int launch(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache_fp8* cache, void* workspace, int sms, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
+  CUtensorMap k_map, v_map;
+  int rc;
+  if ((rc = gdn_host::encode_codes_map(&k_map, cache->k, cache, d.a.box_shift)) != GDN_OK) return rc;
+  if ((rc = gdn_host::encode_codes_map(&v_map, cache->v, cache, d.a.box_shift)) != GDN_OK) return rc;
   const auto kernel = chunk_attention8_kernel<D, kScores>;
-  return launch_chunk<D>(kernel, d, total_tokens, Registers<true>::kSum, done, workspace, sms, stream,
+  return launch_chunk<D, true>(kernel, d, total_tokens, done, workspace, sms, stream,
                          [&](dim3 grid, dim3 block, int smem, const CUtensorMap& q_map) {
-                           return gdn_host::launch_pdl(kernel, grid, block, smem, stream, d, q_map, codes);
+                           return gdn_host::launch_pdl(kernel, grid, block, smem, stream, d, q_map, k_map, v_map, gdn_host::cache8(cache));
                          });
 }
 
@@ -50,9 +53,8 @@ extern "C" int gdn_attention_paged_fp8(const gdn_bf16* q, int64_t q_token_stride
   rc = gdn_host::check_device(&sms);
   if (rc != GDN_OK) return rc;
   d.tile_tokens = kRows / d.a.group;
-  const gdn::Cache8 codes = gdn_host::cache8(cache);
   return by_scores(d.a, cache->head_dim, [&](auto dim, auto scores) {
-    return launch<decltype(dim)::value, decltype(scores)::value>(d, total_tokens, codes, workspace, sms,
+    return launch<decltype(dim)::value, decltype(scores)::value>(d, total_tokens, cache, workspace, sms,
                                                                 static_cast<cudaStream_t>(stream));
   });
 }

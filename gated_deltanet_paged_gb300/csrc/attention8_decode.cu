@@ -53,44 +53,6 @@ struct Smem8 : Smem<kConsumers<NT>, NT * D / 16, NT> {
   float scale[kStages][2][kGroups];  // the keys' scales, and the exponents of the values'
 };
 
-// Scale bytes of one block after the other, a group's by a lane, asked for a block ahead.
-template <int kBlockKeys>
-struct ScaleCopies {
-  const AttnArgs& a;
-  const uint8_t* scales;
-  int64_t page_stride, group_stride, head_stride;
-  int lane, lo, hi, key, entry, slot;
-  const int32_t* pages;
-  int64_t head_at;
-  uint32_t byte;
-
-  __device__ __forceinline__ ScaleCopies(const Decode8Args& d, int kv, int l)
-      : a(d.d.a), scales(d.cache.scales[kv]), page_stride(d.cache.scale_page), group_stride(d.cache.scale_group),
-        head_stride(d.cache.scale_head), lane(l) {}
-  __device__ __forceinline__ void look_ahead() {
-    byte = 127;
-    if (lane >= kBlockKeys / gdn::kGroup || key + gdn::kGroup <= lo || key >= hi) return;
-    const int p = pages[entry];
-    if (p >= 0 && p < a.paged.num_pages)  // else its codes are zeros, reported by the copies
-      byte = scales[p * page_stride + (slot / gdn::kGroup) * group_stride + head_at];
-  }
-  __device__ __forceinline__ void begin(int from, int to, int head, int table_entry, int first) {
-    lo = from, hi = to, head_at = head * head_stride;
-    pages = a.paged.pages + table_entry;
-    key = first + lane * gdn::kGroup;
-    entry = key / a.paged.page_size;
-    slot = key - entry * a.paged.page_size;
-    look_ahead();
-  }
-  __device__ __forceinline__ void next(bool more) {
-    key += kBlockKeys;
-    entry += kBlockKeys / a.paged.page_size;
-    slot += kBlockKeys % a.paged.page_size;
-    if (slot >= a.paged.page_size) slot -= a.paged.page_size, ++entry;
-    if (more) look_ahead();
-  }
-};
-
 // Two 16 x 16 blocks of bytes, transposed: lane 4 g + t gets bytes 4 t .. 4 t + 3 of column
 // g (r[0]) and g + 8 (r[1]) of the first, whose rows are at the addresses of lanes 0 to
 // 15; r[2], r[3] of the second.
@@ -100,11 +62,6 @@ __device__ __forceinline__ void ldmatrix2_bytes_trans(uint32_t addr, uint32_t (&
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 x;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr) : "memory");
-  return x;
-}
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -112,13 +69,6 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Byte offset of 16-byte chunk c of key r of a tile: swizzled over 128 or 64 bytes.
-template <int D>
-__device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
-  if constexpr (D == 128) return gdn::swz(r, c);
-  return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-}
-
 // Four bytes' two rows, transposed as an 8 x 8 tile of 16-bit numbers.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t r;
@@ -254,7 +204,7 @@ __global__ void __launch_bounds__(threads_of(kConsumers<NT>), 2)
     // ------------------------------------------------ keys, or values
     const int kv = warp - kWarps;
     gdn::TileCopies<D, kBlock<D>, 1> tiles(a, kv ? &v_map : &k_map, lane);
-    ScaleCopies<kBlock<D>> scales(d8, kv, lane);
+    gdn::ScaleCopies<kBlock<D>> scales(a, d8.cache, kv, lane);
     int n = 0;  // blocks issued
     bool ok = true;
     while (ok && next_segment<kBlock<D>>(d, w)) {
@@ -356,8 +306,8 @@ __global__ void __launch_bounds__(threads_of(kConsumers<NT>), 2)
         for (int u = 0; u < kSub; ++u)
 #pragma unroll
           for (int c = 0; c < D / 64; ++c) {
-            const uint4 x = lds128(kt + chunk_at<D>(row0 + 16 * u + key, 4 * c + t));
-            const uint4 y = lds128(kt + chunk_at<D>(row0 + 16 * u + key + 2, 4 * c + t));
+            const uint4 x = gdn::lds128(kt + gdn::chunk_at<D>(row0 + 16 * u + key, 4 * c + t));
+            const uint4 y = gdn::lds128(kt + gdn::chunk_at<D>(row0 + 16 * u + key + 2, 4 * c + t));
             const uint32_t upper[4] = {x.x, x.y, x.z, x.w}, lower[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -480,7 +430,7 @@ __global__ void __launch_bounds__(threads_of(kConsumers<NT>), 2)
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) {
             uint32_t x[4];
-            ldmatrix2_bytes_trans(vt + chunk_at<D>(row0 + 16 * u + (lane & 15), 2 * k + (lane >> 4)), x);
+            ldmatrix2_bytes_trans(vt + gdn::chunk_at<D>(row0 + 16 * u + (lane & 15), 2 * k + (lane >> 4)), x);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               uint32_t y[4];

@@ -18,11 +18,10 @@ constexpr int kKeys = 128;   // keys per block
 constexpr int kThreads = 512;
 constexpr int kMmaWarp = 8, kLoadWarp = 10, kValueWarp = 11, kEpilogueWarp = 12;
 // 65,536 registers: 256 softmax threads hold 128 scores each, the others little; but
-// where the cache is in 8 bits, the epilogue's warps convert it and have a tile of codes
-// on its way.
+// where the cache is in 8 bits, the epilogue's warps convert it.
 template <bool kCodes>
 struct Registers {
-  static constexpr int kSoftmax = kCodes ? 176 : 200, kIssue = 56, kEpilogue = kCodes ? 104 : 56;
+  static constexpr int kSoftmax = kCodes ? 184 : 200, kIssue = 56, kEpilogue = kCodes ? 88 : 56;
   static constexpr int kSum = 128 * (2 * kSoftmax + kIssue + kEpilogue);
   static_assert(kSum == 65536, "register split of the block");
 };
@@ -145,14 +144,17 @@ __device__ __forceinline__ bool next_segment(const ChunkArgs& d, Walk& w) {
   }
   return false;
 }
-template <int D>
+template <int D, bool kCodes>
 struct Layout {
   static constexpr int kHalf = kRows * 128;            // 64 dimensions of 128 rows
   static constexpr int kTile = kRows * D * 2;          // a Q, K or V tile
   // Ring of K and V tiles: with a fifth at D = 128 nothing is faster (4 x 8,192
   // tokens 1.36 ms either way, 64 x 512 228 us against 224).
-  static constexpr int kStages = D == 128 ? 4 : 8;
-  static constexpr int kBytes = (2 + kStages) * kTile;
+  static constexpr int kStages = D == 64 ? 8 : kCodes ? 3 : 4;
+  // Ring of tiles of codes behind it: as many bytes ahead as the ring has without.
+  static constexpr int kCodeTile = kKeys * D;
+  static constexpr int kCodeStages = !kCodes ? 0 : D == 64 ? 6 : 4;
+  static constexpr int kBytes = (2 + kStages) * kTile + kCodeStages * kCodeTile;
   static constexpr uint32_t kColS = 0, kColO = 256;    // TMEM columns: S of both tiles, O of both tiles
 };
 
@@ -198,11 +200,12 @@ struct alignas(16) Segment {
   int seq;
 };
 
-template <int D>
+template <int D, bool kCodes>
 struct Smem {
-  uint64_t full[Layout<D>::kStages];
-  uint64_t empty[Layout<D>::kStages];
-  uint64_t raw[Layout<D>::kStages];  // copies of values that are to be cleared before they are `full`
+  using L = Layout<D, kCodes>;
+  uint64_t full[L::kStages];
+  uint64_t empty[L::kStages];
+  uint64_t raw[L::kStages];  // copies of values that are to be cleared before they are `full`
   uint64_t q_full, q_empty, done[2];
   uint64_t s_full[2];      // S is there, and the O of the blocks before is complete
   uint64_t p_full[2][2];   // [tile][half]: 64 keys' weights are there
@@ -219,7 +222,13 @@ struct Smem {
   float2 stat[2][kRows];  // [tile][row]: reference and sum of a segment
   uint32_t tmem;
   int abort;
+  // Of an 8-bit cache: the copies of a tile of codes, and its groups' scales.
+  static constexpr int kCodeStages = kCodes ? L::kCodeStages : 1;
+  uint64_t code_full[kCodeStages], code_empty[kCodeStages];
+  uint32_t code_scale[kCodeStages][kKeys / gdn::kGroup];  // bytes
 };
+template <int D, bool kCodes>
+constexpr int kSmemBytes = Layout<D, kCodes>::kBytes + sizeof(Smem<D, kCodes>);
 
 template <int kRegs>
 __device__ __forceinline__ void regs_inc() {
@@ -372,100 +381,60 @@ __device__ __forceinline__ void tmem_st32_nw(uint32_t taddr, const uint32_t* r) 
       : "memory");
 }
 
-// Tiles of 128 keys or values from the 8-bit cache by four warps: D / 16 lanes take a row,
-// 16 codes each, and write them as bf16 in the layout that the copies of a 16-bit cache
-// have.  A value is its code times its scale, exactly, so that everything behind is the
-// same.  Keys and values of a block lie at the same offsets, which are looked up, with
-// both scales, a block ahead: lane i < 8 has those of the block's group i.
+// A tile of 128 keys or values from the 8-bit cache, as the copies left it at `codes`, to
+// bf16 at `tile`, in the layout that the copies of a 16-bit cache have: four warps, of
+// which D / 16 lanes take a row, 16 codes each.  A value is its code times its scale,
+// exactly, so that everything behind is the same.  Rows outside [from, to) become zeros.
 template <int D>
-struct CodeTiles {
-  static constexpr int kLanes = D / 16, kRowsOfWarp = 32 / kLanes, kRowsOfStep = 4 * kRowsOfWarp;
-  static constexpr int kSteps = kKeys / kRowsOfStep;
-  const AttnArgs& a;
-  const gdn::Cache8& c;
-  int lane, row;              // row of step 0
-  const int32_t* pages;
-  int lo, hi, head, seq, key; // key: of this lane's group, in the block that was looked up last
-  int64_t at, next_at;        // offset of this lane's group in the block in use and in the next; -1: none
-  uint32_t scales, next_scales;  // its bytes, keys' and values'
-  int first;                  // key of row 0 of the tile whose codes are in x
-  uint4 x[kSteps];
-
-  __device__ __forceinline__ CodeTiles(const AttnArgs& args, const gdn::Cache8& cache, int l, int warp)
-      : a(args), c(cache), lane(l), row(warp * kRowsOfWarp + l / kLanes) {}
-  __device__ __forceinline__ void look_up() {
-    next_at = -1;
-    next_scales = 0;
-    if (lane < kKeys / gdn::kGroup && key + gdn::kGroup > lo && key < hi) {
-      const int entry = key / a.paged.page_size, slot = key - entry * a.paged.page_size;
-      const int p = pages[entry];
-      if (p >= 0 && p < a.paged.num_pages) {
-        next_at = p * c.page_stride + slot * c.token_stride + head * c.head_stride;
-        const int64_t s = p * c.scale_page + slot / gdn::kGroup * c.scale_group + head * c.scale_head;
-        next_scales = c.scales[0][s] | c.scales[1][s] << 8;
-      } else {
-        gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_ID, seq);
+__device__ __forceinline__ void convert_tile(uint32_t codes, const uint32_t* scales, uint8_t* tile, int warp, int lane, int from,
+                                             int to) {
+  constexpr int kLanes = D / 16, kRowsOfWarp = 32 / kLanes, kRowsOfStep = 4 * kRowsOfWarp;
+  const int row = warp * kRowsOfWarp + lane / kLanes, chunk = lane % kLanes;
+  // Lanes of the second 64 dimensions write their two chunks in the other order: all
+  // eight of a row then meet different banks.
+  const bool swap = chunk >= 4;
+  uint8_t* const dst = tile + (chunk >> 2) * (kRows * 128);
+  // Rolled, as little code as gives two rows in flight: the kernel's instructions are
+  // fetched more slowly than issued (unrolled, 4 x 8,192 tokens took 3.5 ms).
+  constexpr int kBatch = 2;
+#pragma unroll 1
+  for (int i0 = 0; i0 < kKeys / kRowsOfStep; i0 += kBatch) {
+    uint4 x[kBatch];
+    uint32_t byte[kBatch], odd = 0;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = (i0 + i) * kRowsOfStep + row;
+      x[i] = gdn::lds128(codes + gdn::chunk_at<D>(r, chunk));
+      byte[i] = scales[r / gdn::kGroup];
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = (i0 + i) * kRowsOfStep + row;
+      if (r < from || r >= to) x[i] = make_uint4(0, 0, 0, 0);
+      if (swap) x[i] = make_uint4(x[i].z, x[i].w, x[i].x, x[i].y);
+      odd |= gdn::e4m3_odd(x[i].x) | gdn::e4m3_odd(x[i].y) | gdn::e4m3_odd(x[i].z) | gdn::e4m3_odd(x[i].w);
+      if (byte[i] > gdn::kFastScaleMost) odd = 0x80u;
+    }
+    const bool slow = (odd & 0x80808080u) != 0;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = (i0 + i) * kRowsOfStep + row;
+      const uint32_t f = gdn::fast_scale(byte[i]);
+      uint2 a0 = gdn::e4m3_to_bf16_fast(x[i].x, f), a1 = gdn::e4m3_to_bf16_fast(x[i].y, f);
+      uint2 b0 = gdn::e4m3_to_bf16_fast(x[i].z, f), b1 = gdn::e4m3_to_bf16_fast(x[i].w, f);
+      if (slow) {
+        const float scale = gdn::scale_of(byte[i]);
+        a0 = gdn::e4m3_to_bf16(x[i].x, make_float2(scale, scale));
+        a1 = gdn::e4m3_to_bf16(x[i].y, make_float2(scale, scale));
+        b0 = gdn::e4m3_to_bf16(x[i].z, make_float2(scale, scale));
+        b1 = gdn::e4m3_to_bf16(x[i].w, make_float2(scale, scale));
       }
-    }
-    key += kKeys;
-  }
-  __device__ __forceinline__ int group_of(int step) const { return (step * kRowsOfStep + row) / gdn::kGroup; }
-  // The codes of a step's row in a tile from key `tile` on, asked for.
-  __device__ __forceinline__ uint4 load(int step, int kv, int64_t offsets, int tile) const {
-    const int r = step * kRowsOfStep + row;
-    const int64_t group = __shfl_sync(0xFFFFFFFFu, offsets, group_of(step));
-    uint4 y = make_uint4(0, 0, 0, 0);
-    if (group >= 0 && tile + r >= lo && tile + r < hi)
-      y = *reinterpret_cast<const uint4*>(c.codes[kv] + group + r % gdn::kGroup * c.token_stride + lane % kLanes * 16);
-    return y;
-  }
-  __device__ __forceinline__ void begin(const Segment& g) {
-    lo = g.lo, hi = g.hi, head = g.head, seq = g.seq, first = g.key0;
-    pages = a.paged.pages + g.entry;
-    key = first + lane * gdn::kGroup;
-    look_up();
-    at = next_at;
-    scales = next_scales;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) x[i] = load(i, 0, at, first);
-  }
-  // Tile t of the segment (keys are the even ones) as bf16 to `tile`, the next one's codes
-  // asked for on the way.
-  __device__ __forceinline__ void convert(uint8_t* tile, int t, int blocks) {
-    const int kv = t & 1;
-    const bool more = t + 1 < 2 * blocks;
-    if (kv == 0) {
-      next_at = -1;
-      if (t + 2 < 2 * blocks) look_up();
-    }
-    const int64_t then_at = kv ? next_at : at;
-    const int then_first = kv ? first + kKeys : first;
-    const int chunk = lane % kLanes;
-    // Lanes of the second 64 dimensions write their two chunks in the other order: all
-    // eight of a row then meet different banks.
-    const int swap = chunk >> 2;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const uint4 y = x[i];
-      if (more) x[i] = load(i, kv ^ 1, then_at, then_first);
-      const uint32_t bytes = __shfl_sync(0xFFFFFFFFu, scales, group_of(i));
-      const float f = gdn::scale_of((bytes >> (8 * kv)) & 0xFFu);
-      const float2 scale = make_float2(f, f);
-      const uint2 a0 = gdn::e4m3_to_bf16(swap ? y.z : y.x, scale), a1 = gdn::e4m3_to_bf16(swap ? y.w : y.y, scale);
-      const uint2 b0 = gdn::e4m3_to_bf16(swap ? y.x : y.z, scale), b1 = gdn::e4m3_to_bf16(swap ? y.y : y.w, scale);
-      const int r = i * kRowsOfStep + row;
-      uint8_t* dst = tile + (chunk >> 2) * (kRows * 128);
-      const int c0 = (chunk & 3) * 2 + swap;
+      const int c0 = (chunk & 3) * 2 + (swap ? 1 : 0);
       *reinterpret_cast<uint4*>(dst + gdn::swz(r, c0)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
       *reinterpret_cast<uint4*>(dst + gdn::swz(r, c0 ^ 1)) = make_uint4(b0.x, b0.y, b1.x, b1.y);
     }
-    if (kv) {
-      at = next_at;
-      scales = next_scales;
-      first += kKeys;
-    }
   }
-};
+}
 
 // How scores become weights.
 //   kPlain: scale and reference in one multiply-add.
@@ -485,16 +454,17 @@ enum Scores { kPlain, kBiased, kGeneral, kCapped };
 // score and 16 or 24 over that 1.65 and 1.73.
 constexpr float kAbove = 16.f, kOver = 16.f;
 
-// kCodes: the cache is in 8 bits, read through `codes` and not the key and value maps.
+// kCodes: the cache is in 8 bits, and `codes` says where its scales are.
 template <int D, Scores kScores, bool kCodes>
 __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtensorMap& q_map, const CUtensorMap& k_map,
                                                 const CUtensorMap& v_map, const gdn::Cache8& codes) {
-  using L = Layout<D>;
+  using L = Layout<D, kCodes>;
   using R = Registers<kCodes>;
   // Dynamic shared memory starts behind the 1 KB that the system keeps, on a
   // 1,024-byte boundary as the swizzle needs; there is no room to round up.
   extern __shared__ __align__(1024) uint8_t tiles[];
-  Smem<D>& sh = *reinterpret_cast<Smem<D>*>(tiles + L::kBytes);
+  uint8_t* const code_ring = tiles + (2 + L::kStages) * L::kTile;
+  Smem<D, kCodes>& sh = *reinterpret_cast<Smem<D, kCodes>*>(tiles + L::kBytes);
   uint8_t* ring = tiles + 2 * L::kTile;
   const AttnArgs& a = d.a;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -525,7 +495,11 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
     gdn::fence_mbar_init();
   } else if (tid >= 64 && tid < 64 + kSegments) {
     gdn::mbar_init(&sh.seg_full[tid - 64], 1);
-    gdn::mbar_init(&sh.seg_empty[tid - 64], kThreads / 32 - (kCodes ? 2 : 1));
+    gdn::mbar_init(&sh.seg_empty[tid - 64], kThreads / 32 - 1);
+    gdn::fence_mbar_init();
+  } else if (kCodes && tid >= 128 && tid < 128 + sh.kCodeStages) {
+    gdn::mbar_init(&sh.code_full[tid - 128], 1);
+    gdn::mbar_init(&sh.code_empty[tid - 128], 4);
     gdn::fence_mbar_init();
   } else if (tid == 96) {
     gdn::mbar_init(&sh.q_full, 1);
@@ -539,10 +513,8 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
     for (int i = tid; i < 2 * L::kTile / 16; i += kThreads) reinterpret_cast<uint4*>(tiles)[i] = make_uint4(0, 0, 0, 0);
   if (tid == kLoadWarp * 32) {
     gdn::prefetch_tensormap(&q_map);
-    if constexpr (!kCodes) {
-      gdn::prefetch_tensormap(&k_map);
-      gdn::prefetch_tensormap(&v_map);
-    }
+    gdn::prefetch_tensormap(&k_map);
+    gdn::prefetch_tensormap(&v_map);
   }
   if (warp == kMmaWarp) {
     gdn::tmem_alloc(&sh.tmem, 512);
@@ -704,6 +676,21 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
       if (lane == 0) gdn::mbar_arrive(&sh.seg_empty[i % kSegments]);
       return g.blocks > 0;
     };
+    // Copies in flight, and their barriers.
+    constexpr uint32_t kCopies = kCodes ? sh.kCodeStages : L::kStages;
+    uint64_t* const copied = kCodes ? sh.code_full : sh.full;
+    // Tile n of codes with its scales; false: a wait ran out.
+    auto send_codes = [&](auto& tile, auto& scale, uint32_t n, bool more) {
+      const uint32_t at = n % kCopies;
+      if (n >= kCopies && !wait(&sh.code_empty[at], ((n / kCopies) - 1) & 1)) return false;
+      if (lane < kKeys / gdn::kGroup) sh.code_scale[at][lane] = scale.byte;
+      __syncwarp();
+      if (lane == 0) gdn::mbar_arrive_expect_tx(&sh.code_full[at], tile.bytes());
+      __syncwarp();
+      tile.copy(code_ring + at * L::kCodeTile, &sh.code_full[at], more);
+      scale.next(more);
+      return true;
+    };
     auto epilogue = [&] {
       // ----------------------------------------------------------- epilogue
       // Reads a segment's O while the softmax warps are on the next one.
@@ -764,15 +751,12 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
       if constexpr (!kCodes) {
         for (uint32_t segs = 0; ok && next(segs, g); ++segs) write(g);
       } else {
-        // These warps supply keys and values as well: codes of the next tile are on their
-        // way while those of this one are converted, and a segment's results are written
+        // These warps convert keys and values as well, and a segment's results are written
         // between the tiles of the next as soon as they are there.
-        CodeTiles<D> tiles(a, codes, lane, warp & 3);
         Segment done;
         bool pending = false;
         uint32_t n = 0;  // ring tiles
         for (uint32_t segs = 0; ok && next(segs, g); ++segs) {
-          tiles.begin(g);
           for (int i = 0; ok && i < 2 * g.blocks; ++i, ++n) {
             if (pending) {
               // At the latest where the next tile's room depends on it.
@@ -788,12 +772,18 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
                 pending = false;
               }
             }
-            const uint32_t stage = n % L::kStages;
+            const uint32_t stage = n % L::kStages, at = n % kCopies;
+            const int key0 = g.key0 + (i >> 1) * kKeys;
+            if (!wait(&sh.code_full[at], (n / kCopies) & 1)) break;
             if (n >= L::kStages && !wait(&sh.empty[stage], ((n / L::kStages) - 1) & 1)) break;
-            tiles.convert(ring + stage * L::kTile, i, g.blocks);
+            convert_tile<D>(gdn::smem_u32(code_ring + at * L::kCodeTile), sh.code_scale[at], ring + stage * L::kTile, warp & 3,
+                            lane, g.lo - key0, g.hi - key0);
             gdn::fence_proxy_async();
             __syncwarp();
-            if (lane == 0) gdn::mbar_arrive(&sh.full[stage]);
+            if (lane == 0) {
+              gdn::mbar_arrive(&sh.full[stage]);
+              gdn::mbar_arrive(&sh.code_empty[at]);
+            }
           }
           if (ok && pending) write(done);
           done = g;
@@ -809,7 +799,8 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
     } else if (warp == kLoadWarp) {
       // ------------------------------------ segments, queries and keys
       Walk w = sh.walk;
-      gdn::TileCopies<D, kKeys> keys(a, &k_map, lane);
+      gdn::TileCopies<D, kKeys, kCodes ? 1 : 2> keys(a, &k_map, lane);
+      gdn::ScaleCopies<kKeys> key_scales(a, codes, 0, lane);
       uint32_t n = 0, segs = 0;  // ring tiles (keys are the even ones), segments announced
       uint32_t queries = 0;      // sent
       for (;; ++segs) {
@@ -845,7 +836,8 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
         }
         __syncwarp();
         if (!more) break;
-        if constexpr (!kCodes) keys.begin(g.lo, g.hi, g.head, g.seq, g.entry, g.key0);
+        keys.begin(g.lo, g.hi, g.head, g.seq, g.entry, g.key0);
+        if constexpr (kCodes) key_scales.begin(g.lo, g.hi, g.head, g.entry, g.key0);
         // The queries go first where their room is free; else behind the first
         // block's keys, which need none that the segment before holds.
         auto send_queries = [&](bool must) {
@@ -869,13 +861,17 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
           ++queries;
           return true;
         };
-        bool q_sent = send_queries(kCodes);
-        for (int j = 0; !kCodes && j < g.blocks; ++j) {
-          const uint32_t stage = n % L::kStages;
-          if (n >= L::kStages && !wait(&sh.empty[stage], ((n / L::kStages) - 1) & 1)) break;
-          if (lane == 0) gdn::mbar_arrive_expect_tx(&sh.full[stage], keys.bytes());
-          __syncwarp();
-          keys.copy(ring + stage * L::kTile, &sh.full[stage], j + 1 < g.blocks);
+        bool q_sent = send_queries(false);
+        for (int j = 0; j < g.blocks; ++j) {
+          if constexpr (kCodes) {
+            if (!send_codes(keys, key_scales, n, j + 1 < g.blocks)) break;
+          } else {
+            const uint32_t stage = n % L::kStages;
+            if (n >= L::kStages && !wait(&sh.empty[stage], ((n / L::kStages) - 1) & 1)) break;
+            if (lane == 0) gdn::mbar_arrive_expect_tx(&sh.full[stage], keys.bytes());
+            __syncwarp();
+            keys.copy(ring + stage * L::kTile, &sh.full[stage], j + 1 < g.blocks);
+          }
           n += 2;
           if (!q_sent && !(q_sent = send_queries(true))) break;
         }
@@ -885,8 +881,7 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
       // Leave no copy in flight behind, whoever gave up (bounded waits, as everywhere).
       ok = !queries || last(&sh.q_full, (queries - 1) & 1);
 #pragma unroll 1
-      for (uint32_t i = n > L::kStages ? n - L::kStages : 0; i < n; i += 2)
-        ok = last(&sh.full[i % L::kStages], (i / L::kStages) & 1) && ok;
+      for (uint32_t i = n > kCopies ? n - kCopies : 0; i < n; i += 2) ok = last(&copied[i % kCopies], (i / kCopies) & 1) && ok;
       if (!ok) *abort_flag = 1;
     } else if (warp < kLoadWarp) {
       // ----------------------------------------------------------- products
@@ -978,7 +973,21 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
       __syncwarp();
       if (!last(&sh.done[t], 0)) *abort_flag = 1;
     } else if (kCodes && warp == kValueWarp) {
-      // nothing: the epilogue's warps supply keys and values
+      // ---------------------------------------------------- codes of values
+      gdn::TileCopies<D, kKeys, 1> values(a, &v_map, lane);
+      gdn::ScaleCopies<kKeys> scales(a, codes, 1, lane);
+      uint32_t n = 1;
+      Segment g;
+      for (uint32_t segs = 0; ok && next(segs, g); ++segs) {
+        values.begin(g.lo, g.hi, g.head, g.seq, g.entry, g.key0);
+        scales.begin(g.lo, g.hi, g.head, g.entry, g.key0);
+        for (int j = 0; j < g.blocks && send_codes(values, scales, n, j + 1 < g.blocks); ++j) n += 2;
+      }
+      if (!ok) *abort_flag = 1;
+      ok = true;
+#pragma unroll 1
+      for (uint32_t i = n > kCopies ? n - kCopies : 1; i < n; i += 2) ok = last(&copied[i % kCopies], (i / kCopies) & 1) && ok;
+      if (!ok) *abort_flag = 1;
     } else if (warp == kValueWarp) {
       // ------------------------------------------------------------- values
       // Slots past the sequence's end or before every window may hold anything,
@@ -1414,17 +1423,17 @@ size_t workspace_bytes_of(int D, bool whole) {
 }
 
 // queue(kernel, smem): launches it.
-template <int D, typename Kernel, typename Queue>
-int launch_chunk(Kernel kernel, ChunkArgs& d, int32_t total_tokens, int regs, std::atomic<uint64_t>& done, void* workspace,
+template <int D, bool kCodes, typename Kernel, typename Queue>
+int launch_chunk(Kernel kernel, ChunkArgs& d, int32_t total_tokens, std::atomic<uint64_t>& done, void* workspace,
                  int sms, cudaStream_t stream, const Queue& queue) {
-  constexpr int smem = Layout<D>::kBytes + sizeof(Smem<D>);
+  constexpr int smem = kSmemBytes<D, kCodes>;
   static_assert(smem <= 232448, "shared memory of one CTA");
   int rc = gdn_host::func_attr_once(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem, done);
   if (rc != GDN_OK) return rc;
   // The register split would wait for ever in a block that holds fewer.
   static const bool fits = [&] {
     cudaFuncAttributes attr;
-    return cudaFuncGetAttributes(&attr, kernel) == cudaSuccess && attr.numRegs * kThreads >= regs;
+    return cudaFuncGetAttributes(&attr, kernel) == cudaSuccess && attr.numRegs * kThreads >= Registers<kCodes>::kSum;
   }();
   if (!fits) return GDN_ERR_CUDA;
   CUtensorMap q_map;

@@ -43,12 +43,84 @@ __device__ __forceinline__ uint2 e4m3_to_bf16(uint32_t four, float2 scale) {
   e4m3_to_half4(four, a, b);
   return make_uint2(pack_bf162(__fmul2_rn(half2_to_float2(a), scale)), pack_bf162(__fmul2_rn(half2_to_float2(b), scale)));
 }
+// The same without conversions, which pass through the unit of the exponentials and are
+// in their way: a code's bits, moved to where a bf16 has its sign and the low end of
+// its exponent, are the value times 2^-120 (subnormal codes are subnormal there too),
+// and one product takes that and the scale.  Not for NaN, nor for scales above 2^7.
+constexpr uint32_t kFastScaleMost = 127 + 7;
+__device__ __forceinline__ uint32_t fast_scale(uint32_t byte) {  // 2^(byte - 127 + 120), twice
+  return (byte + 120u) * 0x00800080u;
+}
+__device__ __forceinline__ uint2 e4m3_to_bf16_fast(uint32_t four, uint32_t scale) {
+  // A byte below copies of its sign, moved up by four bits.
+  uint32_t a, b;
+  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(four));
+  asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(b) : "r"(four));
+  a = (a << 4) & 0x87F087F0u;
+  b = (b << 4) & 0x87F087F0u;
+  uint2 r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(a), "r"(scale));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(b), "r"(scale));
+  return r;
+}
+// Bit 7 of a byte is set where its code is NaN.
+__device__ __forceinline__ uint32_t e4m3_odd(uint32_t four) { return (four & 0x7F7F7F7Fu) + 0x01010101u; }
 // Rounded to nearest, ties to even; beyond 448 (infinities too) to 448; NaN stays NaN.
 __device__ __forceinline__ uint32_t to_e4m3(float a, float b) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(a), "f"(b));
   return r;
 }
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 x;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr) : "memory");
+  return x;
+}
+// Byte offset of 16-byte chunk c of key r of a tile: swizzled over 128 or 64 bytes.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
+  if constexpr (D == 128) return swz(r, c);
+  return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// Scale bytes of one block after the other, a group's by a lane, asked for a block ahead.
+template <int kBlockKeys>
+struct ScaleCopies {
+  const AttnArgs& a;
+  const uint8_t* scales;
+  int64_t page_stride, group_stride, head_stride;
+  int lane, lo, hi, key, entry, slot;
+  const int32_t* pages;
+  int64_t head_at;
+  uint32_t byte;
+
+  __device__ __forceinline__ ScaleCopies(const AttnArgs& args, const Cache8& c, int kv, int l)
+      : a(args), scales(c.scales[kv]), page_stride(c.scale_page), group_stride(c.scale_group), head_stride(c.scale_head),
+        lane(l) {}
+  __device__ __forceinline__ void look_ahead() {
+    byte = 127;
+    if (lane >= kBlockKeys / kGroup || key + kGroup <= lo || key >= hi) return;
+    const int p = pages[entry];
+    if (p >= 0 && p < a.paged.num_pages)  // else its codes are zeros, reported by the copies
+      byte = scales[p * page_stride + (slot / kGroup) * group_stride + head_at];
+  }
+  __device__ __forceinline__ void begin(int from, int to, int head, int table_entry, int first) {
+    lo = from, hi = to, head_at = head * head_stride;
+    pages = a.paged.pages + table_entry;
+    key = first + lane * kGroup;
+    entry = key / a.paged.page_size;
+    slot = key - entry * a.paged.page_size;
+    look_ahead();
+  }
+  __device__ __forceinline__ void next(bool more) {
+    key += kBlockKeys;
+    entry += kBlockKeys / a.paged.page_size;
+    slot += kBlockKeys % a.paged.page_size;
+    if (slot >= a.paged.page_size) slot -= a.paged.page_size, ++entry;
+    if (more) look_ahead();
+  }
+};
 
 }  // namespace gdn
 

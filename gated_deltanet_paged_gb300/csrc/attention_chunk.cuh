@@ -225,7 +225,7 @@ struct Smem {
   // Of an 8-bit cache: the copies of a tile of codes, and its groups' scales.
   static constexpr int kCodeStages = kCodes ? L::kCodeStages : 1;
   uint64_t code_full[kCodeStages], code_empty[kCodeStages];
-  uint32_t code_scale[kCodeStages][kKeys / gdn::kGroup];  // bytes
+  float code_scale[kCodeStages][kKeys / gdn::kGroup];
 };
 template <int D, bool kCodes>
 constexpr int kSmemBytes = Layout<D, kCodes>::kBytes + sizeof(Smem<D, kCodes>);
@@ -386,7 +386,7 @@ __device__ __forceinline__ void tmem_st32_nw(uint32_t taddr, const uint32_t* r) 
 // which D / 16 lanes take a row, 16 codes each.  A value is its code times its scale,
 // exactly, so that everything behind is the same.  Rows outside [from, to) become zeros.
 template <int D>
-__device__ __forceinline__ void convert_tile(uint32_t codes, const uint32_t* scales, uint8_t* tile, int warp, int lane, int from,
+__device__ __forceinline__ void convert_tile(uint32_t codes, const float* scales, uint8_t* tile, int warp, int lane, int from,
                                              int to) {
   constexpr int kLanes = D / 16, kRowsOfWarp = 32 / kLanes, kRowsOfStep = 4 * kRowsOfWarp;
   const int row = warp * kRowsOfWarp + lane / kLanes, chunk = lane % kLanes;
@@ -395,40 +395,28 @@ __device__ __forceinline__ void convert_tile(uint32_t codes, const uint32_t* sca
   const bool swap = chunk >= 4;
   uint8_t* const dst = tile + (chunk >> 2) * (kRows * 128);
   // Rolled, as little code as gives two rows in flight: the kernel's instructions are
-  // fetched more slowly than issued (unrolled, 4 x 8,192 tokens took 3.5 ms).
+  // fetched more slowly than issued (unrolled, 4 x 8,192 tokens take 2.3 ms, with four
+  // rows in flight 2.1, with a conversion in integers, which needs a second path for
+  // NaN and for large scales, 2.0 and unrolled 3.5; so 1.8).
   constexpr int kBatch = 2;
 #pragma unroll 1
   for (int i0 = 0; i0 < kKeys / kRowsOfStep; i0 += kBatch) {
     uint4 x[kBatch];
-    uint32_t byte[kBatch], odd = 0;
+    float scale[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int r = (i0 + i) * kRowsOfStep + row;
       x[i] = gdn::lds128(codes + gdn::chunk_at<D>(r, chunk));
-      byte[i] = scales[r / gdn::kGroup];
+      scale[i] = scales[r / gdn::kGroup];
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int r = (i0 + i) * kRowsOfStep + row;
       if (r < from || r >= to) x[i] = make_uint4(0, 0, 0, 0);
       if (swap) x[i] = make_uint4(x[i].z, x[i].w, x[i].x, x[i].y);
-      odd |= gdn::e4m3_odd(x[i].x) | gdn::e4m3_odd(x[i].y) | gdn::e4m3_odd(x[i].z) | gdn::e4m3_odd(x[i].w);
-      if (byte[i] > gdn::kFastScaleMost) odd = 0x80u;
-    }
-    const bool slow = (odd & 0x80808080u) != 0;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = (i0 + i) * kRowsOfStep + row;
-      const uint32_t f = gdn::fast_scale(byte[i]);
-      uint2 a0 = gdn::e4m3_to_bf16_fast(x[i].x, f), a1 = gdn::e4m3_to_bf16_fast(x[i].y, f);
-      uint2 b0 = gdn::e4m3_to_bf16_fast(x[i].z, f), b1 = gdn::e4m3_to_bf16_fast(x[i].w, f);
-      if (slow) {
-        const float scale = gdn::scale_of(byte[i]);
-        a0 = gdn::e4m3_to_bf16(x[i].x, make_float2(scale, scale));
-        a1 = gdn::e4m3_to_bf16(x[i].y, make_float2(scale, scale));
-        b0 = gdn::e4m3_to_bf16(x[i].z, make_float2(scale, scale));
-        b1 = gdn::e4m3_to_bf16(x[i].w, make_float2(scale, scale));
-      }
+      const float2 f = make_float2(scale[i], scale[i]);
+      const uint2 a0 = gdn::e4m3_to_bf16(x[i].x, f), a1 = gdn::e4m3_to_bf16(x[i].y, f);
+      const uint2 b0 = gdn::e4m3_to_bf16(x[i].z, f), b1 = gdn::e4m3_to_bf16(x[i].w, f);
       const int c0 = (chunk & 3) * 2 + (swap ? 1 : 0);
       *reinterpret_cast<uint4*>(dst + gdn::swz(r, c0)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
       *reinterpret_cast<uint4*>(dst + gdn::swz(r, c0 ^ 1)) = make_uint4(b0.x, b0.y, b1.x, b1.y);
@@ -683,7 +671,7 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
     auto send_codes = [&](auto& tile, auto& scale, uint32_t n, bool more) {
       const uint32_t at = n % kCopies;
       if (n >= kCopies && !wait(&sh.code_empty[at], ((n / kCopies) - 1) & 1)) return false;
-      if (lane < kKeys / gdn::kGroup) sh.code_scale[at][lane] = scale.byte;
+      if (lane < kKeys / gdn::kGroup) sh.code_scale[at][lane] = gdn::scale_of(scale.byte);
       __syncwarp();
       if (lane == 0) gdn::mbar_arrive_expect_tx(&sh.code_full[at], tile.bytes());
       __syncwarp();

@@ -43,28 +43,6 @@ __device__ __forceinline__ uint2 e4m3_to_bf16(uint32_t four, float2 scale) {
   e4m3_to_half4(four, a, b);
   return make_uint2(pack_bf162(__fmul2_rn(half2_to_float2(a), scale)), pack_bf162(__fmul2_rn(half2_to_float2(b), scale)));
 }
-// The same without conversions, which pass through the unit of the exponentials and are
-// in their way: a code's bits, moved to where a bf16 has its sign and the low end of
-// its exponent, are the value times 2^-120 (subnormal codes are subnormal there too),
-// and one product takes that and the scale.  Not for NaN, nor for scales above 2^7.
-constexpr uint32_t kFastScaleMost = 127 + 7;
-__device__ __forceinline__ uint32_t fast_scale(uint32_t byte) {  // 2^(byte - 127 + 120), twice
-  return (byte + 120u) * 0x00800080u;
-}
-__device__ __forceinline__ uint2 e4m3_to_bf16_fast(uint32_t four, uint32_t scale) {
-  // A byte below copies of its sign, moved up by four bits.
-  uint32_t a, b;
-  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(four));
-  asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(b) : "r"(four));
-  a = (a << 4) & 0x87F087F0u;
-  b = (b << 4) & 0x87F087F0u;
-  uint2 r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(a), "r"(scale));
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(b), "r"(scale));
-  return r;
-}
-// Bit 7 of a byte is set where its code is NaN.
-__device__ __forceinline__ uint32_t e4m3_odd(uint32_t four) { return (four & 0x7F7F7F7Fu) + 0x01010101u; }
 // Rounded to nearest, ties to even; beyond 448 (infinities too) to 448; NaN stays NaN.
 __device__ __forceinline__ uint32_t to_e4m3(float a, float b) {
   uint16_t r;

@@ -342,8 +342,10 @@ __device__ __forceinline__ float max32(const float (&x)[32]) {
 }
 // Cap of 32 scores in TMEM columns from addr, into units of log2.  Where the warp's
 // scores stay within the cap (they mostly do), the polynomial, which is evaluated
-// beside the maximum that decides it.  Else any form, four scores at a time by way of
-// TMEM: it is rarely taken, and its instructions would stand between the others.
+// beside the maximum that decides it.  Else any form for the groups of four columns that
+// hold a score beyond, read from TMEM once more, one group after the other: its
+// instructions would stand between the others.  (For all eight groups: 64 mixed
+// sequences, 16 heads, a cap of 30 and scores of up to 6 times their deviation, 4.6 ms.)
 __device__ __forceinline__ void cap_scores(const AttnArgs& a, const gdn::CapPoly& poly, uint32_t addr, float (&x)[32]) {
   const float most = largest32(x, 0.f);
 #pragma unroll
@@ -353,15 +355,26 @@ __device__ __forceinline__ void cap_scores(const AttnArgs& a, const gdn::CapPoly
     x[i + 1] = y.y;
   }
   if (!__all_sync(0xFFFFFFFFu, most <= a.cap_near)) {
+    uint32_t groups = 0;
+    {
+      float s[32];
+      gdn::tmem_ld32(addr, s);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (!(gdn::max3_abs(gdn::max3_abs(s[4 * k], s[4 * k + 1], s[4 * k + 2]), s[4 * k + 3], 0.f) <= a.cap_near)) groups |= 1u << k;
+    }
+    groups = __reduce_or_sync(0xFFFFFFFFu, groups);
 #pragma unroll 1
-    for (int i = 0; i < 32; i += 4) {
+    for (; groups; groups &= groups - 1) {
+      const int group = __ffs(groups) - 1;
       uint32_t z[4];
-      tmem_ld4(addr + i, z);
+      tmem_ld4(addr + 4 * group, z);
 #pragma unroll
       for (int k = 0; k < 4; ++k) z[k] = __float_as_uint(gdn::capped(__uint_as_float(z[k]), a));
-      tmem_st4(addr + i, z);
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (group == k / 4) x[k] = __uint_as_float(z[k % 4]);
     }
-    gdn::tmem_ld32(addr, x);
   }
 }
 // Scores outside [from, to) are hidden.
@@ -1134,9 +1147,9 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
           };
           // 32 keys at a time, the next 32 scores on their way meanwhile.
           float x[32], y[32];
-          const float ref = m == -INFINITY ? kAbove : m;
-          const float limit = fminf(a.cap_near, (ref + kOver) * inv_scale);
-          const float2 minus = make_float2(-ref, -ref);
+          float ref = m == -INFINITY ? kAbove : m;
+          float limit = fminf(a.cap_near, (ref + kOver) * inv_scale);
+          float2 minus = make_float2(-ref, -ref);
           auto small = [&](float (&z)[32], int c) {
             const float most = largest32(z, 0.f);
 #pragma unroll
@@ -1149,62 +1162,72 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
             weights(z, c);
             return true;
           };
-          int c = 0;  // keys done
           // Not where slots are junk (past the sequence's end, or before every window):
           // they would take part in the choice.
-          if (key0 >= seg_lo && key0 + kKeys <= seg_hi) {
-            tmem_ld32_nw(s_addr, x);
+          bool fast = key0 >= seg_lo && key0 + kKeys <= seg_hi;
+          if (fast) tmem_ld32_nw(s_addr, x);
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < 2; ++h) {
+            int c = 64 * h;  // keys done
+            if (fast) {
               tmem_wait_ld32(x);
-              tmem_ld32_nw(s_addr + 64 * h + 32, y);
-              if (!small(x, 64 * h)) break;
-              c += 32;
+              tmem_ld32_nw(s_addr + c + 32, y);
+              fast = small(x, c);
+              if (fast) c += 32;
               tmem_wait_ld32(y);
-              if (h == 0) tmem_ld32_nw(s_addr + 64, x);
-              if (!small(y, 64 * h + 32)) break;
-              c += 32;
-              publish(h);
-            }
-            if (c < kKeys) {  // no load is left on its way
-              tmem_wait_ld32(x);
-              pin32(y);
-            }
-          }
-          if (c > 0 && m == -INFINITY && lo < key0 + c && hi > key0) m = kAbove;
-          // The rest of a block with a score that is not small.
-#pragma unroll 1
-          for (; c < kKeys; c += 32) {
-            float z[32];
-            gdn::tmem_ld32(s_addr + c, z);
-            cap_scores(a, poly, s_addr + c, z);
-            if (edge) hide(lo - key0 - c, hi - key0 - c, -INFINITY, z);
-            const float mx = ceilf(max32(z)) + kAbove;
-            if (__any_sync(0xFFFFFFFFu, mx > m)) {
-              // O is complete up to this half: S came behind the blocks before, and the
-              // first half's product is waited for.
-              if (c >= 64 && !wait(&sh.mid[t], n & 1)) break;
-              gdn::tc_fence_after();
-              const float r = move(fmaxf(m, mx), j > 0 || c >= 64);
-              if (c & 32) {
-                // The half's first 32 weights have been written: by a power of two, exactly.
-                float w[16];
-                uint32_t v[16];
-                gdn::tmem_wait_st();
-                gdn::tmem_ld16(s_addr + c / 2 - 16, w);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const float2 f = gdn::unpack_bf162(__float_as_uint(w[i]));
-                  v[i] = gdn::pack_bf162(f.x * r, f.y * r);
-                }
-                gdn::tmem_st16(s_addr + c / 2 - 16, v);
+              if (fast && h == 0) tmem_ld32_nw(s_addr + 64, x);
+              if (fast) {
+                fast = small(y, c);
+                if (fast) c += 32;
               }
+              if (!fast) tmem_wait_ld32(x);  // no load is left on its way
+              if (c > 0 && m == -INFINITY && lo < key0 + c && hi > key0) m = kAbove;
             }
-            const float by = m == -INFINITY ? 0.f : m;
+            // The rest of the half, where a score is not small.
+#pragma unroll 1
+            for (; c < 64 * h + 64; c += 32) {
+              float z[32];
+              gdn::tmem_ld32(s_addr + c, z);
+              cap_scores(a, poly, s_addr + c, z);
+              if (edge) hide(lo - key0 - c, hi - key0 - c, -INFINITY, z);
+              const float top = max32(z), mx = ceilf(top) + kAbove;
+              // Over a 16-bit cache the reference follows every larger score that is met
+              // here; otherwise where it has to.
+              if (__any_sync(0xFFFFFFFFu, kCodes && m != -INFINITY ? top > m + kOver : mx > m)) {
+                // O is complete up to this half: S came behind the blocks before, and the
+                // first half's product is waited for.
+                if (c >= 64 && !wait(&sh.mid[t], n & 1)) break;
+                gdn::tc_fence_after();
+                const float r = move(fmaxf(m, mx), j > 0 || c >= 64);
+                if (c & 32) {
+                  // The half's first 32 weights have been written: by a power of two, exactly.
+                  float w[16];
+                  uint32_t v[16];
+                  gdn::tmem_wait_st();
+                  gdn::tmem_ld16(s_addr + c / 2 - 16, w);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) z[i] -= by;
-            weights(z, c);
-            if (c & 32) publish(c > 64);
+                  for (int i = 0; i < 16; ++i) {
+                    const float2 f = gdn::unpack_bf162(__float_as_uint(w[i]));
+                    v[i] = gdn::pack_bf162(f.x * r, f.y * r);
+                  }
+                  gdn::tmem_st16(s_addr + c / 2 - 16, v);
+                }
+              }
+              const float by = m == -INFINITY ? 0.f : m;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) z[i] -= by;
+              weights(z, c);
+            }
+            if (!ok) break;
+            // On a 16-bit cache the rest of the block goes the same way.
+            if (kCodes && !fast && h == 0 && key0 >= seg_lo && key0 + kKeys <= seg_hi) {
+              fast = true;
+              ref = m == -INFINITY ? kAbove : m;
+              limit = fminf(a.cap_near, (ref + kOver) * inv_scale);
+              minus = make_float2(-ref, -ref);
+              tmem_ld32_nw(s_addr + 64, x);
+            }
+            publish(h);
           }
           if (!ok) break;
         } else {

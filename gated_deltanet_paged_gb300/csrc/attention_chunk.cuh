@@ -340,6 +340,31 @@ __device__ __forceinline__ float max32(const float (&x)[32]) {
   }
   return gdn::max3(gdn::max3(top[0], x[28], x[29]), gdn::max3(top[1], x[30], x[31]), fmaxf(top[2], top[3]));
 }
+// Of 32 capped scores whose originals are in TMEM columns from addr: those of the groups
+// of four columns in which any row of the warp has a score beyond the polynomial, less
+// `minus`, one group after the other.
+__device__ __forceinline__ void cap_far(const AttnArgs& a, uint32_t addr, float minus, float (&x)[32]) {
+  uint32_t groups = 0;
+  {
+    float s[32];
+    gdn::tmem_ld32(addr, s);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (!(gdn::max3_abs(gdn::max3_abs(s[4 * k], s[4 * k + 1], s[4 * k + 2]), s[4 * k + 3], 0.f) <= a.cap_near)) groups |= 1u << k;
+  }
+  groups = __reduce_or_sync(0xFFFFFFFFu, groups);
+#pragma unroll 1
+  for (; groups; groups &= groups - 1) {
+    const int group = __ffs(groups) - 1;
+    uint32_t z[4];
+    tmem_ld4(addr + 4 * group, z);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) z[k] = __float_as_uint(gdn::capped(__uint_as_float(z[k]), a) - minus);
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (group == k / 4) x[k] = __uint_as_float(z[k % 4]);
+  }
+}
 // Cap of 32 scores in TMEM columns from addr, into units of log2.  Where the warp's
 // scores stay within the cap (they mostly do), the polynomial, which is evaluated
 // beside the maximum that decides it.  Else any form for the groups of four columns that
@@ -354,28 +379,7 @@ __device__ __forceinline__ void cap_scores(const AttnArgs& a, const gdn::CapPoly
     x[i] = y.x;
     x[i + 1] = y.y;
   }
-  if (!__all_sync(0xFFFFFFFFu, most <= a.cap_near)) {
-    uint32_t groups = 0;
-    {
-      float s[32];
-      gdn::tmem_ld32(addr, s);
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (!(gdn::max3_abs(gdn::max3_abs(s[4 * k], s[4 * k + 1], s[4 * k + 2]), s[4 * k + 3], 0.f) <= a.cap_near)) groups |= 1u << k;
-    }
-    groups = __reduce_or_sync(0xFFFFFFFFu, groups);
-#pragma unroll 1
-    for (; groups; groups &= groups - 1) {
-      const int group = __ffs(groups) - 1;
-      uint32_t z[4];
-      tmem_ld4(addr + 4 * group, z);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) z[k] = __float_as_uint(gdn::capped(__uint_as_float(z[k]), a));
-#pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (group == k / 4) x[k] = __uint_as_float(z[k % 4]);
-    }
-  }
+  if (!__all_sync(0xFFFFFFFFu, most <= a.cap_near)) cap_far(a, addr, 0.f, x);
 }
 // Scores outside [from, to) are hidden.
 __device__ __forceinline__ void hide(int from, int to, float as, float (&x)[32]) {
@@ -1145,55 +1149,107 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
             }
             gdn::tmem_st16_nw(s_addr + c / 2, p);
           };
-          // 32 keys at a time, the next 32 scores on their way meanwhile.
-          float x[32], y[32];
-          float ref = m == -INFINITY ? kAbove : m;
-          float limit = fminf(a.cap_near, (ref + kOver) * inv_scale);
-          float2 minus = make_float2(-ref, -ref);
-          auto small = [&](float (&z)[32], int c) {
-            const float most = largest32(z, 0.f);
+          if constexpr (kCodes) {
+            // 32 keys at a time and one way for all of them: two copies of it, with the next
+            // 32 scores on their way meanwhile, are fetched more slowly than they save,
+            // and a rare way of its own for large scores costs thousands of cycles to fetch.
+#pragma unroll 1
+            for (int c = 0; c < kKeys; c += 32) {
+              float z[32];
+              gdn::tmem_ld32(s_addr + c, z);
+              if (edge) hide(lo - key0 - c, hi - key0 - c, 0.f, z);  // slots may hold anything
+              const float most = largest32(z, 0.f);
+              const float ref = m == -INFINITY ? kAbove : m;
+              const float2 minus = make_float2(-ref, -ref);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 u = gdn::capped_near(make_float2(z[i], z[i + 1]), poly, minus);
-              z[i] = u.x, z[i + 1] = u.y;
-            }
-            if (!__all_sync(0xFFFFFFFFu, most <= limit)) return false;
-            if (edge) hide(lo - key0 - c, hi - key0 - c, -INFINITY, z);
-            weights(z, c);
-            return true;
-          };
-          // Not where slots are junk (past the sequence's end, or before every window):
-          // they would take part in the choice.
-          bool fast = key0 >= seg_lo && key0 + kKeys <= seg_hi;
-          if (fast) tmem_ld32_nw(s_addr, x);
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            int c = 64 * h;  // keys done
-            if (fast) {
-              tmem_wait_ld32(x);
-              tmem_ld32_nw(s_addr + c + 32, y);
-              fast = small(x, c);
-              if (fast) c += 32;
-              tmem_wait_ld32(y);
-              if (fast && h == 0) tmem_ld32_nw(s_addr + 64, x);
-              if (fast) {
-                fast = small(y, c);
-                if (fast) c += 32;
+              for (int i = 0; i < 32; i += 2) {
+                const float2 u = gdn::capped_near(make_float2(z[i], z[i + 1]), poly, minus);
+                z[i] = u.x, z[i + 1] = u.y;
               }
-              if (!fast) tmem_wait_ld32(x);  // no load is left on its way
-              if (c > 0 && m == -INFINITY && lo < key0 + c && hi > key0) m = kAbove;
+              if (!__all_sync(0xFFFFFFFFu, most <= a.cap_near)) cap_far(a, s_addr + c, ref, z);
+              if (edge) hide(lo - key0 - c, hi - key0 - c, -INFINITY, z);
+              if (m == -INFINITY && lo < key0 + c + 32 && hi > key0 + c) m = kAbove;
+              if (!__all_sync(0xFFFFFFFFu, fminf(most * a.scale_log2, a.cap_log2) <= ref + kOver)) {
+                const float top = max32(z);  // over the reference
+                if (__any_sync(0xFFFFFFFFu, top > kOver)) {
+                  // O is complete up to this half: S came behind the blocks before, and the
+                  // first half's product is waited for.
+                  if (c >= 64 && !wait(&sh.mid[t], n & 1)) break;
+                  gdn::tc_fence_after();
+                  const float to = top > kOver ? ceilf(top + ref) + kAbove : ref;
+                  const bool none = m == -INFINITY;  // a row that has seen no key yet
+                  const float r = move(to, j > 0 || c >= 64);
+                  if (none) m = -INFINITY;
+                  if (c & 32) {
+                    // The half's first 32 weights have been written.
+                    float w[16];
+                    uint32_t v[16];
+                    gdn::tmem_wait_st();
+                    gdn::tmem_ld16(s_addr + c / 2 - 16, w);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                      const float2 f = gdn::unpack_bf162(__float_as_uint(w[i]));
+                      v[i] = gdn::pack_bf162(f.x * r, f.y * r);
+                    }
+                    gdn::tmem_st16(s_addr + c / 2 - 16, v);
+                  }
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) z[i] += ref - to;
+                }
+              }
+              weights(z, c);
+              if (c & 32) publish(c > 64);
             }
-            // The rest of the half, where a score is not small.
+          } else {
+            // 32 keys at a time, the next 32 scores on their way meanwhile.
+            float x[32], y[32];
+            const float ref = m == -INFINITY ? kAbove : m;
+            const float limit = fminf(a.cap_near, (ref + kOver) * inv_scale);
+            const float2 minus = make_float2(-ref, -ref);
+            auto small = [&](float (&z)[32], int c) {
+              const float most = largest32(z, 0.f);
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 u = gdn::capped_near(make_float2(z[i], z[i + 1]), poly, minus);
+                z[i] = u.x, z[i + 1] = u.y;
+              }
+              if (!__all_sync(0xFFFFFFFFu, most <= limit)) return false;
+              if (edge) hide(lo - key0 - c, hi - key0 - c, -INFINITY, z);
+              weights(z, c);
+              return true;
+            };
+            int c = 0;  // keys done
+            // Not where slots are junk (past the sequence's end, or before every window):
+            // they would take part in the choice.
+            if (key0 >= seg_lo && key0 + kKeys <= seg_hi) {
+              tmem_ld32_nw(s_addr, x);
 #pragma unroll 1
-            for (; c < 64 * h + 64; c += 32) {
+              for (int h = 0; h < 2; ++h) {
+                tmem_wait_ld32(x);
+                tmem_ld32_nw(s_addr + 64 * h + 32, y);
+                if (!small(x, 64 * h)) break;
+                c += 32;
+                tmem_wait_ld32(y);
+                if (h == 0) tmem_ld32_nw(s_addr + 64, x);
+                if (!small(y, 64 * h + 32)) break;
+                c += 32;
+                publish(h);
+              }
+              if (c < kKeys) {  // no load is left on its way
+                tmem_wait_ld32(x);
+                pin32(y);
+              }
+            }
+            if (c > 0 && m == -INFINITY && lo < key0 + c && hi > key0) m = kAbove;
+            // The rest of a block with a score that is not small.
+#pragma unroll 1
+            for (; c < kKeys; c += 32) {
               float z[32];
               gdn::tmem_ld32(s_addr + c, z);
               cap_scores(a, poly, s_addr + c, z);
               if (edge) hide(lo - key0 - c, hi - key0 - c, -INFINITY, z);
-              const float top = max32(z), mx = ceilf(top) + kAbove;
-              // Over a 16-bit cache the reference follows every larger score that is met
-              // here; otherwise where it has to.
-              if (__any_sync(0xFFFFFFFFu, kCodes && m != -INFINITY ? top > m + kOver : mx > m)) {
+              const float mx = ceilf(max32(z)) + kAbove;
+              if (__any_sync(0xFFFFFFFFu, mx > m)) {
                 // O is complete up to this half: S came behind the blocks before, and the
                 // first half's product is waited for.
                 if (c >= 64 && !wait(&sh.mid[t], n & 1)) break;
@@ -1217,17 +1273,8 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
 #pragma unroll
               for (int i = 0; i < 32; ++i) z[i] -= by;
               weights(z, c);
+              if (c & 32) publish(c > 64);
             }
-            if (!ok) break;
-            // On a 16-bit cache the rest of the block goes the same way.
-            if (kCodes && !fast && h == 0 && key0 >= seg_lo && key0 + kKeys <= seg_hi) {
-              fast = true;
-              ref = m == -INFINITY ? kAbove : m;
-              limit = fminf(a.cap_near, (ref + kOver) * inv_scale);
-              minus = make_float2(-ref, -ref);
-              tmem_ld32_nw(s_addr + 64, x);
-            }
-            publish(h);
           }
           if (!ok) break;
         } else {

@@ -245,19 +245,6 @@ __device__ __forceinline__ void release(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) gdn::mbar_arrive(bar);
 }
-// 32 bytes of a row at once, a whole sector of HBM per lane, where the address
-// allows it.
-__device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8], bool aligned32) {
-  if (!aligned32) {
-    static_cast<uint4*>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
-    static_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
-    return;
-  }
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
 // Four columns of this thread's TMEM lane, waited for.
 __device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
   asm volatile(
@@ -731,7 +718,7 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
                   uint32_t y[8];
 #pragma unroll
                   for (int e = 0; e < 8; ++e) y[e] = gdn::pack_bf162(x[16 * i + 2 * e] * inv, x[16 * i + 2 * e + 1] * inv);
-                  store32(dst + c + 16 * i, y, aligned32);
+                  gdn::store32(dst + c + 16 * i, y, aligned32);
                 }
               }
             }

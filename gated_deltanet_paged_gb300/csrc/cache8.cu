@@ -19,6 +19,8 @@
 //     a head at a time in registers, from the load to the codes, and finds the largest
 //     by one reduction.  The group's sines and cosines are evaluated once for all
 //     heads.
+#include <type_traits>
+
 #include "cache8.cuh"
 #include "rotate.cuh"
 
@@ -52,85 +54,177 @@ __device__ __forceinline__ void offsets(const NormRope& n, int unit, int* first,
     *second = *first + W;
   }
 }
-// Sines and cosines of a token in the order in which lanes read them, two pairs of a
-// unit beside those of the next one: lanes of a head read 16 bytes each, side by side.
+// Cosines, then sines of a token in the order in which lanes read them: four pairs of a
+// unit beside those of the next one, so that the lanes of a head read 16 bytes each, side
+// by side.
 template <int W>
 __device__ __forceinline__ int cs_at(int pair, int units) {
-  if constexpr (W == 1) return pair;
+  constexpr int Q = W < 4 ? W : 4;
   const int unit = pair / W, i = pair % W;
-  return ((i >> 1) * units + unit) * 2 + (i & 1);
+  return ((i / Q) * units + unit) * Q + i % Q;
 }
+// What a unit's pairs take from shared memory: cosines and sines, or the weights of the
+// first and of the second elements; two arrays, half_dim apart.
 template <int W>
-struct CsOf {
-  const float2* cs;
-  int unit, units;
-  __device__ __forceinline__ float2 operator()(int i) const {
-    if constexpr (W == 1) return cs[unit];
-    return cs[((i >> 1) * units + unit) * 2 + (i & 1)];
+struct Two {
+  float c[W], s[W];
+  __device__ __forceinline__ void read(const float* cs, int half_dim, int unit, int units) {
+    constexpr int Q = W < 4 ? W : 4;
+#pragma unroll
+    for (int i = 0; i < W; i += Q) {
+      const float* at = cs + ((i / Q) * units + unit) * Q;
+      if constexpr (Q == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(at), y = *reinterpret_cast<const float4*>(at + half_dim);
+        c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+        s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
+      } else {
+#pragma unroll
+        for (int k = 0; k < Q; ++k) c[i + k] = at[k], s[i + k] = at[half_dim + k];
+      }
+    }
   }
 };
 
-// A lane's part of a head: U units, lane `at` of `lanes` has units at, at + lanes, ...
-template <int W, int U>
-struct Part {
-  float x[U][W], y[U][W];
-  __device__ __forceinline__ void unpack(const Piece<W> (&a)[U], const Piece<W> (&b)[U]) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < W; ++i) x[u][i] = gdn::get<W>(a[u], i), y[u][i] = gdn::get<W>(b[u], i);
-  }
-  // Over the root mean square of the head, times the weights.  Lanes of units past the
-  // head hold zeros.
-  __device__ __forceinline__ void norm(const NormRope& n, const Piece<W> (&wa)[U], const Piece<W> (&wb)[U], int lanes) {
-    float s = 0.f;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < W; ++i) s = fmaf(x[u][i], x[u][i], fmaf(y[u][i], y[u][i], s));
-    for (int o = lanes >> 1; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    const float r = rsqrtf(fmaf(s, n.inv_dim, n.eps));
-#pragma unroll
-    for (int u = 0; u < U; ++u)
+// W pairs of a head in fp32, the first elements of the pairs and the second ones; of what
+// is not rotated, any two halves.
+template <int W>
+struct Pairs {
+  float e[W], o[W];
+  template <bool kInterleaved>
+  __device__ __forceinline__ void unpack(const Piece<W>& a, const Piece<W>& b) {
+    if constexpr (kInterleaved) {
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        x[u][i] *= r * (gdn::get<W>(wa[u], i) + n.offset);
-        y[u][i] *= r * (gdn::get<W>(wb[u], i) + n.offset);
+        e[i] = 2 * i < W ? gdn::get<W>(a, (2 * i) % W) : gdn::get<W>(b, (2 * i) % W);
+        o[i] = 2 * i + 1 < W ? gdn::get<W>(a, (2 * i + 1) % W) : gdn::get<W>(b, (2 * i + 1) % W);
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) e[i] = gdn::get<W>(a, i), o[i] = gdn::get<W>(b, i);
+    }
+  }
+  // In the order of the head's elements.
+  template <bool kInterleaved>
+  __device__ __forceinline__ void ordered(float (&x)[W], float (&y)[W]) const {
+    if constexpr (kInterleaved) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        if (2 * i < W) x[(2 * i) % W] = e[i]; else y[(2 * i) % W] = e[i];
+        if (2 * i + 1 < W) x[(2 * i + 1) % W] = o[i]; else y[(2 * i + 1) % W] = o[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) x[i] = e[i], y[i] = o[i];
+    }
+  }
+  __device__ __forceinline__ float squares() const {
+    if constexpr (W == 1) return fmaf(e[0], e[0], o[0] * o[0]);
+    float2 t = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i + 1 < W; i += 2) {
+      t = __ffma2_rn(make_float2(e[i], e[i + 1]), make_float2(e[i], e[i + 1]), t);
+      t = __ffma2_rn(make_float2(o[i], o[i + 1]), make_float2(o[i], o[i + 1]), t);
+    }
+    return t.x + t.y;
+  }
+  __device__ __forceinline__ void scale(float r, const Two<W>& w) {
+    if constexpr (W == 1) {
+      e[0] *= w.c[0] * r;
+      o[0] *= w.s[0] * r;
+    }
+    const float2 r2 = make_float2(r, r);
+#pragma unroll
+    for (int i = 0; i + 1 < W; i += 2) {
+      const float2 x = __fmul2_rn(make_float2(e[i], e[i + 1]), __fmul2_rn(make_float2(w.c[i], w.c[i + 1]), r2));
+      const float2 y = __fmul2_rn(make_float2(o[i], o[i + 1]), __fmul2_rn(make_float2(w.s[i], w.s[i + 1]), r2));
+      e[i] = x.x, e[i + 1] = x.y, o[i] = y.x, o[i + 1] = y.y;
+    }
+  }
+  __device__ __forceinline__ void turn(const Two<W>& t) {
+    if constexpr (W == 1) {
+      const float a = e[0], b = o[0];
+      e[0] = fmaf(a, t.c[0], -b * t.s[0]);
+      o[0] = fmaf(a, t.s[0], b * t.c[0]);
+    }
+#pragma unroll
+    for (int i = 0; i + 1 < W; i += 2) {
+      const float2 a = make_float2(e[i], e[i + 1]), b = make_float2(o[i], o[i + 1]);
+      const float2 c = make_float2(t.c[i], t.c[i + 1]), s = make_float2(t.s[i], t.s[i + 1]);
+      const float2 x = __ffma2_rn(a, c, __fmul2_rn(b, make_float2(-s.x, -s.y))), y = __ffma2_rn(a, s, __fmul2_rn(b, c));
+      e[i] = x.x, e[i + 1] = x.y, o[i] = y.x, o[i + 1] = y.y;
+    }
   }
 };
+
+// A kind's weights to shared memory by a block, offset included.
+template <int W, bool kInterleaved>
+__device__ __forceinline__ void weights_to(const NormRope& n, const __nv_bfloat16* w, float* to, int half_dim, int units) {
+  for (int i = threadIdx.x; i < units * W; i += blockDim.x) {
+    const int unit = i / W, k = i % W;
+    int first, second;
+    offsets<W>(n, unit, &first, &second);
+    to[cs_at<W>(i, units)] = __bfloat162float(w[kInterleaved ? first + 2 * k : first + k]) + n.offset;
+    to[half_dim + cs_at<W>(i, units)] = __bfloat162float(w[kInterleaved ? first + 2 * k + 1 : second + k]) + n.offset;
+  }
+}
+// Over the root mean square of the head, of which `lanes` lanes have units at, at + lanes,
+// ..., times the weights.  Lanes of units past the head hold zeros.
+template <int W, int U>
+__device__ __forceinline__ void norm(Pairs<W> (&p)[U], const NormRope& n, const float* weights, int half_dim, int at, int units,
+                                     int lanes) {
+  float s = 0.f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) s += p[u].squares();
+  for (int o = lanes >> 1; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  const float r = rsqrtf(fmaf(s, n.inv_dim, n.eps));
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (at + u * lanes >= units) continue;
+    Two<W> w;
+    w.read(weights, half_dim, at + u * lanes, units);
+    p[u].scale(r, w);
+  }
+}
 
 // ------------------------------------------------------------------ norm and rotation
 constexpr int kWarps = 4;
 constexpr int kBatch = 4;   // heads in flight per lane
 constexpr int kMaxDim = 256;
 
+// One kind of heads, queries or keys.
+struct NormHeads {
+  const __nv_bfloat16* x;
+  __nv_bfloat16* y;
+  const __nv_bfloat16* weight;
+  int64_t x_stride, y_stride;
+  int32_t H;
+  int32_t steps;  // of as many heads as a warp takes at a time
+};
 struct NormArgs {
-  const __nv_bfloat16* q;
-  const __nv_bfloat16* k;
-  __nv_bfloat16* q_out;
-  __nv_bfloat16* k_out;
-  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+  NormHeads kind[2];
   const int32_t* positions;
   NormRope n;
-  int32_t T, Hq, Hkv, D;
+  int32_t T, D;
   int32_t units;   // per head: D / (2 W)
   int32_t lanes;   // per head, a power of two
   int32_t slices;  // warps per token
 };
 
-template <int W>
-__global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormArgs a) {
+template <int W, bool kInterleaved>
+__global__ void __launch_bounds__(kWarps * 32, 5) norm_rope_kernel(const __grid_constant__ NormArgs a) {
   constexpr int U = W == 1 ? 4 : W == 2 ? 2 : 1;  // D / (2 W) <= 32 U
-  __shared__ float2 cs_all[kWarps][kMaxDim / 2];
+  // Weights and sines wait in shared memory: in registers they leave room for fewer warps,
+  // and HBM is fed by the loads of many (65,536 tokens of 40 heads 216 us, so 236; with 80
+  // registers some are spilled, 251).
+  __shared__ alignas(16) float cs_all[kWarps][kMaxDim];
+  __shared__ alignas(16) float weights[2][kMaxDim];
   gdn::pdl_wait();
   gdn::pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  const unsigned id = blockIdx.x * kWarps + warp;
   const int t = static_cast<int>(id / a.slices), slice = static_cast<int>(id % a.slices);
-  if (t >= a.T) return;
-  const int heads = a.Hq + a.Hkv, per = 32 / a.lanes;  // heads at a time
-  const int at = lane & (a.lanes - 1), stride = a.slices * per;
+  const int per = 32 / a.lanes, at = lane & (a.lanes - 1), sub = lane / a.lanes;  // `per` heads at a time
+  const int q_steps = a.kind[0].steps, steps = t < a.T ? q_steps + a.kind[1].steps : 0;
   int first[U], second[U];
   bool mine[U];
 #pragma unroll
@@ -139,67 +233,62 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormArgs a
     mine[u] = at + u * a.lanes < a.units;
   }
   Piece<W> pa[kBatch][U], pb[kBatch][U];
-  auto load = [&](int h0) {
+  auto load = [&](int j, int step) {
+    const NormHeads& k = a.kind[step >= q_steps ? 1 : 0];
+    const int h = (step >= q_steps ? step - q_steps : step) * per + sub;
+    const __nv_bfloat16* src = k.x + t * k.x_stride + h * a.D;
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int h = h0 + j * stride;
-      const __nv_bfloat16* src = h < a.Hq ? a.q + t * a.q_stride + static_cast<int64_t>(h) * a.D
-                                          : a.k + t * a.k_stride + static_cast<int64_t>(h - a.Hq) * a.D;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        pa[j][u] = pb[j][u] = Piece<W>{};
-        if (h >= heads || !mine[u]) continue;
-        pa[j][u] = gdn::load_piece<W>(src + first[u]);
-        pb[j][u] = gdn::load_piece<W>(src + second[u]);
-      }
+    for (int u = 0; u < U; ++u) {
+      pa[j][u] = pb[j][u] = Piece<W>{};
+      if (step >= steps || h >= k.H || !mine[u]) continue;
+      pa[j][u] = gdn::load_piece<W>(src + first[u]);
+      pb[j][u] = gdn::load_piece<W>(src + second[u]);
     }
   };
-  int h0 = slice * per + lane / a.lanes;
-  load(h0);
-  Piece<W> qa[U], qb[U], ka[U], kb[U];  // weights
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    qa[u] = qb[u] = ka[u] = kb[u] = Piece<W>{};
-    if (!mine[u]) continue;
-    qa[u] = gdn::load_piece<W>(a.n.q_weight + first[u]);
-    qb[u] = gdn::load_piece<W>(a.n.q_weight + second[u]);
-    if (!a.Hkv) continue;
-    ka[u] = gdn::load_piece<W>(a.n.k_weight + first[u]);
-    kb[u] = gdn::load_piece<W>(a.n.k_weight + second[u]);
+  for (int j = 0; j < kBatch; ++j) load(j, slice + j * a.slices);
+  weights_to<W, kInterleaved>(a.n, a.kind[0].weight, weights[0], kMaxDim / 2, a.units);
+  if (a.kind[1].H) weights_to<W, kInterleaved>(a.n, a.kind[1].weight, weights[1], kMaxDim / 2, a.units);
+  float* cs = cs_all[warp];
+  if (a.n.half && steps) {
+    const int position = a.positions[t];
+#pragma unroll 1
+    for (int pair = lane; pair < a.n.half; pair += 32) {
+      const float2 x = gdn::pair_turn(position, a.n.freq[pair], a.n.amplitude, 1.f);
+      const int to = cs_at<W>(pair, a.units);
+      cs[to] = x.x;
+      cs[kMaxDim / 2 + to] = x.y;
+    }
   }
-  float2* cs = cs_all[warp];
-  const int position = a.n.half ? a.positions[t] : 0;
-#pragma unroll
-  for (int i = 0; i < kMaxDim / 64; ++i) {
-    const int pair = lane + 32 * i;
-    if (pair < a.n.half) cs[cs_at<W>(pair, a.units)] = gdn::pair_turn(position, a.n.freq[pair], a.n.amplitude, 1.f);
-  }
-  __syncwarp();
-  // All lanes go through as many steps: the norm's shuffles take the whole warp.
-  for (int base = slice * per; base < heads; base += kBatch * stride, h0 += kBatch * stride) {
+  __syncthreads();
+  for (int s0 = slice; s0 < steps; s0 += kBatch * a.slices) {
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int h = h0 + j * stride;
-      const bool is_k = h >= a.Hq;
-      Part<W, U> p;
-      p.unpack(pa[j], pb[j]);
-      Piece<W> wa[U], wb[U];
+      const int step = s0 + j * a.slices;
+      if (step >= steps) break;
+      const bool is_k = step >= q_steps;
+      const NormHeads& k = a.kind[is_k ? 1 : 0];
+      Pairs<W> p[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) wa[u] = is_k ? ka[u] : qa[u], wb[u] = is_k ? kb[u] : qb[u];
-      p.norm(a.n, wa, wb, a.lanes);
-      if (h >= heads) continue;
-      __nv_bfloat16* dst = is_k ? a.k_out + t * a.k_out_stride + static_cast<int64_t>(h - a.Hq) * a.D
-                                : a.q_out + t * a.q_out_stride + static_cast<int64_t>(h) * a.D;
+      for (int u = 0; u < U; ++u) p[u].template unpack<kInterleaved>(pa[j][u], pb[j][u]);
+      load(j, step + kBatch * a.slices);
+      norm<W, U>(p, a.n, weights[is_k ? 1 : 0], kMaxDim / 2, at, a.units, a.lanes);
+      const int h = (is_k ? step - q_steps : step) * per + sub;
+      __nv_bfloat16* dst = k.y + t * k.y_stride + h * a.D;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int unit = at + u * a.lanes;
-        if (!mine[u]) continue;
-        if (unit * W < a.n.half) gdn::turn<W>(p.x[u], p.y[u], CsOf<W>{cs, unit, a.units}, a.n.interleaved != 0);
-        gdn::store_piece<W>(dst + first[u], gdn::pack<W>(p.x[u]));
-        gdn::store_piece<W>(dst + second[u], gdn::pack<W>(p.y[u]));
+        if (h >= k.H || !mine[u]) continue;
+        if ((at + u * a.lanes) * W < a.n.half) {
+          Two<W> turn;
+          turn.read(cs, kMaxDim / 2, at + u * a.lanes, a.units);
+          p[u].turn(turn);
+        }
+        float x[W], y[W];
+        p[u].template ordered<kInterleaved>(x, y);
+        gdn::store_piece<W>(dst + first[u], gdn::pack<W>(x));
+        gdn::store_piece<W>(dst + second[u], gdn::pack<W>(y));
       }
     }
-    load(h0 + kBatch * stride);
   }
 }
 
@@ -264,7 +353,9 @@ __device__ __forceinline__ void report_refused(const PagedTokens& p) {
 }
 
 // ----------------------------------------------------------------------------- append
-constexpr int kAppendWarps = 8;
+// Warps of a CTA.
+template <bool kWide>
+constexpr int kAppendWarps = kWide ? 8 : 4;
 
 struct AppendArgs {
   const __nv_bfloat16* q;
@@ -293,14 +384,52 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[W], flo
   }
 }
 
-template <int D, int W>
-__global__ void __launch_bounds__(kAppendWarps * 32) append8_kernel(const AppendArgs a) {
+// The group's scale and codes in one head, of a warp (kWide) or of the lanes of a head.
+struct Slot {
+  uint8_t* codes;  // of row 0
+  uint8_t* scale;
+  uint32_t before;  // scale of the earlier tokens, 0: there are none
+};
+// The scale byte for a largest value (its bits; numbers that are not negative compare as
+// those do): the least e with it <= 448 * 2^e, 448 = 1.75 * 2^8, and no less than before.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t bits, uint32_t before) {
+  const int least = static_cast<int>(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return max(static_cast<uint32_t>(min(max(least, gdn::kScaleLeast), gdn::kScaleMost)), before);
+}
+// Earlier tokens' codes, rounded to the scale that has grown (by 2^-126 all of them become
+// zero, as by less); a lane takes every `lanes`-th 16 of them.
+template <int D>
+__device__ __forceinline__ void round_again(const Slot& s, int64_t token_stride, int rows, uint32_t byte, int lane, int lanes) {
+  const float by = __uint_as_float(max(127 - static_cast<int>(byte - s.before), 1) << 23);
+#pragma unroll 1
+  for (int i = lane; i < rows * (D / 16); i += lanes) {
+    uint4* x = reinterpret_cast<uint4*>(s.codes + i / (D / 16) * token_stride + i % (D / 16) * 16);
+    uint4 four = *x;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&four);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t lo, hi;
+      gdn::e4m3_to_half4(w[k], lo, hi);
+      const float2 f = gdn::half2_to_float2(lo), f2 = gdn::half2_to_float2(hi);
+      w[k] = gdn::to_e4m3(f.x * by, f.y * by) | gdn::to_e4m3(f2.x * by, f2.y * by) << 16;
+    }
+    *x = four;
+  }
+}
+
+// kWide: a warp takes all rows of a group's head at a time.  Otherwise, where groups have
+// a new token or two, the lanes of a head take its rows one after the other, and a
+// warp as many heads as it has lanes for; rows behind the first are read twice.
+template <int D, int W, bool kInterleaved, bool kWide>
+__global__ void __launch_bounds__(kAppendWarps<kWide> * 32, kWide ? 2 : 4) append8_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int kWarpsOf = kAppendWarps<kWide>;
   constexpr int kUnits = D / (2 * W);
   constexpr int kLanes = kUnits < 32 ? kUnits : 32;  // per head
   constexpr int U = kUnits / kLanes;
   constexpr int kPer = 32 / kLanes;                  // heads or rows at a time
   constexpr int kSteps = kGroup / kPer;
-  __shared__ alignas(16) float2 cs[kGroup][D / 2];
+  __shared__ alignas(16) float cs[kGroup][D];
+  __shared__ alignas(16) float q_weights[D], k_weights[D];
   gdn::pdl_wait();
   gdn::pdl_launch_dependents();
   if (blockIdx.x == a.groups) {
@@ -309,153 +438,183 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append8_kernel(const Append
   }
   Group g;
   if (!find_group(a.paged, blockIdx.x, &g)) return;  // all threads alike
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, at = lane % kLanes;
-  const int worker = blockIdx.y * kAppendWarps + warp, workers = gridDim.y * kAppendWarps;
-  if (a.n.half) {
-    for (int r = g.rows0 + warp; r < g.rows1; r += kAppendWarps)
-      for (int pair = lane; pair < a.n.half; pair += 32)
-        cs[r][cs_at<W>(pair, kUnits)] = gdn::pair_turn(g.position + r, a.n.freq[pair], a.n.amplitude, 1.f);
-    __syncthreads();
-  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, at = lane % kLanes, sub = lane / kLanes;
+  const int worker = blockIdx.y * kWarpsOf + warp, workers = gridDim.y * kWarpsOf;
+  const bool normed = a.n.q_weight != nullptr;
   int first[U], second[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) offsets<W>(a.n, at + u * kLanes, &first[u], &second[u]);
-  const bool normed = a.n.q_weight != nullptr;
-  auto weights = [&](const __nv_bfloat16* w, Piece<W> (&wa)[U], Piece<W> (&wb)[U]) {
+  auto load = [&](const __nv_bfloat16* src, bool there, Piece<W> (&pa)[U], Piece<W> (&pb)[U]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      wa[u] = wb[u] = Piece<W>{};
-      if (!normed) continue;
-      wa[u] = gdn::load_piece<W>(w + first[u]);
-      wb[u] = gdn::load_piece<W>(w + second[u]);
+      pa[u] = pb[u] = Piece<W>{};
+      if (!there) continue;
+      pa[u] = gdn::load_piece<W>(src + first[u]);
+      pb[u] = gdn::load_piece<W>(src + second[u]);
     }
   };
-  auto turned = [&](Part<W, U>& p, int row) {
+  // Unpacked, over its norm, rotated for the group's row.
+  auto take = [&](const Piece<W> (&pa)[U], const Piece<W> (&pb)[U], const float* w, bool computed, int row,
+                  Pairs<W> (&p)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) p[u].template unpack<kInterleaved>(pa[u], pb[u]);
+    if (!computed) return;
+    if (normed) norm<W, U>(p, a.n, w, D / 2, at, kUnits, kLanes);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int unit = at + u * kLanes;
-      if (unit * W < a.n.half) gdn::turn<W>(p.x[u], p.y[u], CsOf<W>{cs[row], unit, kUnits}, a.n.interleaved != 0);
+      if (unit * W >= a.n.half) continue;
+      Two<W> t;
+      t.read(cs[row], D / 2, unit, kUnits);
+      p[u].turn(t);
     }
   };
 
-  // Queries: kPer heads of a row at a time.
-  if (a.Hq) {
-    Piece<W> wa[U], wb[U];
-    weights(a.n.q_weight, wa, wb);
-    const int per_row = (a.Hq + kPer - 1) / kPer, jobs = (g.rows1 - g.rows0) * per_row;
-    for (int j0 = worker; j0 < jobs; j0 += kSteps * workers) {
-      Piece<W> pa[kSteps][U], pb[kSteps][U];
+  // Queries: kPer heads of a row at a time.  The first are asked for before the sines.
+  const int per_row = (a.Hq + kPer - 1) / kPer, jobs = (g.rows1 - g.rows0) * per_row;
+  constexpr int kAhead = 4;
+  Piece<W> pa[kAhead][U], pb[kAhead][U];
+  auto load_queries = [&](int j0) {
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const int j = j0 + i * workers, row = g.rows0 + j / per_row, h = j % per_row * kPer + lane / kLanes;
-        const __nv_bfloat16* src = a.q + (g.token + row) * a.q_stride + static_cast<int64_t>(h) * D;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          pa[i][u] = pb[i][u] = Piece<W>{};
-          if (j >= jobs || h >= a.Hq) continue;
-          pa[i][u] = gdn::load_piece<W>(src + first[u]);
-          pb[i][u] = gdn::load_piece<W>(src + second[u]);
-        }
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = j0 + i * workers, row = g.rows0 + j / max(per_row, 1), h = j % max(per_row, 1) * kPer + sub;
+      load(a.q + (g.token + row) * a.q_stride + static_cast<int64_t>(h) * D, j < jobs && h < a.Hq, pa[i], pb[i]);
+    }
+  };
+  load_queries(worker);
+  if (a.n.half) {
+    for (int r = g.rows0 + warp; r < g.rows1; r += kWarpsOf)
+      for (int pair = lane; pair < a.n.half; pair += 32) {
+        const float2 x = gdn::pair_turn(g.position + r, a.n.freq[pair], a.n.amplitude, 1.f);
+        cs[r][cs_at<W>(pair, kUnits)] = x.x;
+        cs[r][D / 2 + cs_at<W>(pair, kUnits)] = x.y;
       }
+  }
+  if (normed) {
+    weights_to<W, kInterleaved>(a.n, a.n.q_weight, q_weights, D / 2, kUnits);
+    weights_to<W, kInterleaved>(a.n, a.n.k_weight, k_weights, D / 2, kUnits);
+  }
+  __syncthreads();
+  for (int j0 = worker; j0 < jobs; j0 += kAhead * workers) {
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const int j = j0 + i * workers, row = g.rows0 + j / per_row, h = j % per_row * kPer + lane / kLanes;
-        if (j >= jobs) break;
-        Part<W, U> p;
-        p.unpack(pa[i], pb[i]);
-        if (normed) p.norm(a.n, wa, wb, kLanes);
-        turned(p, row);
-        if (h >= a.Hq) continue;
-        __nv_bfloat16* dst = a.q_out + ((g.token + row) * a.Hq + h) * D;
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = j0 + i * workers, row = g.rows0 + j / per_row, h = j % per_row * kPer + sub;
+      if (j >= jobs) break;
+      Pairs<W> p[U];
+      take(pa[i], pb[i], q_weights, true, row, p);
+      if (h >= a.Hq) continue;
+      __nv_bfloat16* dst = a.q_out + ((g.token + row) * a.Hq + h) * D;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          gdn::store_piece<W>(dst + first[u], gdn::pack<W>(p.x[u]));
-          gdn::store_piece<W>(dst + second[u], gdn::pack<W>(p.y[u]));
-        }
+      for (int u = 0; u < U; ++u) {
+        float x[W], y[W];
+        p[u].template ordered<kInterleaved>(x, y);
+        gdn::store_piece<W>(dst + first[u], gdn::pack<W>(x));
+        gdn::store_piece<W>(dst + second[u], gdn::pack<W>(y));
       }
     }
+    if (j0 + kAhead * workers < jobs) load_queries(j0 + kAhead * workers);
   }
 
   if (g.page < 0) {
     if (worker == 0 && lane == 0) gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_ID, g.seq);
     return;
   }
-  // Keys and values: all rows of a head at a time.
-  Piece<W> wa[U], wb[U];
-  weights(a.n.k_weight, wa, wb);
-  for (int item = worker; item < 2 * a.Hkv; item += workers) {
-    const bool is_k = item < a.Hkv;
-    const int h = is_k ? item : item - a.Hkv;
-    const __nv_bfloat16* src = (is_k ? a.k : a.v) + static_cast<int64_t>(h) * D;
-    const int64_t stride = is_k ? a.k_stride : a.v_stride;
-    uint8_t* codes = a.cache.codes[is_k ? 0 : 1] + g.page * a.cache.page_stride + g.slot * a.cache.token_stride +
-                     h * a.cache.head_stride;
-    uint8_t* scale = a.cache.scales[is_k ? 0 : 1] + g.page * a.cache.scale_page +
-                     g.slot / kGroup * a.cache.scale_group + h * a.cache.scale_head;
-    const uint32_t before = g.rows0 > 0 ? *scale : 0u;  // earlier tokens' scale
-    Piece<W> pa[kSteps][U], pb[kSteps][U];
+  // Keys, then values: item h, or Hkv + h.
+  auto slot_of = [&](int kv, int h) {
+    Slot s;
+    s.codes = a.cache.codes[kv] + g.page * a.cache.page_stride + g.slot * a.cache.token_stride + h * a.cache.head_stride;
+    s.scale = a.cache.scales[kv] + g.page * a.cache.scale_page + g.slot / kGroup * a.cache.scale_group + h * a.cache.scale_head;
+    s.before = g.rows0 > 0 ? *s.scale : 0u;
+    return s;
+  };
+  auto most_of = [&](const Pairs<W> (&p)[U], float most) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int row = i * kPer + lane / kLanes;
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        pa[i][u] = pb[i][u] = Piece<W>{};
-        if (row < g.rows0 || row >= g.rows1) continue;
-        pa[i][u] = gdn::load_piece<W>(src + (g.token + row) * stride + first[u]);
-        pb[i][u] = gdn::load_piece<W>(src + (g.token + row) * stride + second[u]);
-      }
+      for (int k = 0; k < W; ++k) most = gdn::max3_abs(most, p[u].e[k], p[u].o[k]);
+    return most;
+  };
+  auto store = [&](const Slot& s, int row, const Pairs<W> (&p)[U], float inv) {
+    uint8_t* dst = s.codes + row * a.cache.token_stride;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float x[W], y[W];
+      p[u].template ordered<kInterleaved>(x, y);
+      store_codes<W>(dst + first[u], x, inv);
+      store_codes<W>(dst + second[u], y, inv);
     }
-    Part<W, U> p[kSteps];
-    float most = 0.f;
+  };
+  const auto inverse = [](uint32_t byte) { return __uint_as_float((254u - min(byte, 253u)) << 23); };
+  if constexpr (kWide) {
+    for (int item = worker; item < 2 * a.Hkv; item += workers) {
+      const bool is_k = item < a.Hkv;
+      const int h = is_k ? item : item - a.Hkv;
+      const __nv_bfloat16* src = (is_k ? a.k : a.v) + static_cast<int64_t>(h) * D;
+      const int64_t stride = is_k ? a.k_stride : a.v_stride;
+      const Slot slot = slot_of(is_k ? 0 : 1, h);
+      Piece<W> xa[kSteps][U], xb[kSteps][U];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int row = i * kPer + lane / kLanes;
-      const bool there = row >= g.rows0 && row < g.rows1;
-      p[i].unpack(pa[i], pb[i]);
-      if (is_k) {
-        if (normed) p[i].norm(a.n, wa, wb, kLanes);
-        if (there) turned(p[i], row);
+      for (int i = 0; i < kSteps; ++i) {
+        const int row = i * kPer + sub;
+        load(src + (g.token + row) * stride, row >= g.rows0 && row < g.rows1, xa[i], xb[i]);
       }
+      Pairs<W> p[kSteps][U];
+      float most = 0.f;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int i = 0; i < kSteps; ++i) {
+        const int row = i * kPer + sub;
+        take(xa[i], xb[i], k_weights, is_k, min(max(row, g.rows0), g.rows1 - 1), p[i]);
+        most = most_of(p[i], most);
+      }
+      const uint32_t byte = scale_byte(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)), slot.before);
+      const float inv = inverse(byte);
+      __syncwarp();  // every lane has read the scale
+      if (lane == 0) *slot.scale = static_cast<uint8_t>(byte);
 #pragma unroll
-        for (int k = 0; k < W; ++k) most = fmaxf(most, fmaxf(fabsf(p[i].x[u][k]), fabsf(p[i].y[u][k])));
+      for (int i = 0; i < kSteps; ++i) {
+        const int row = i * kPer + sub;
+        if (row >= g.rows0 && row < g.rows1) store(slot, row, p[i], inv);
+      }
+      if (g.rows0 > 0 && byte > slot.before) round_again<D>(slot, a.cache.token_stride, g.rows0, byte, lane, 32);
     }
-    // Numbers that are not negative compare as their bits do.  448 = 1.75 * 2^8.
-    const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
-    const int least = static_cast<int>(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    const uint32_t byte = max(static_cast<uint32_t>(min(max(least, gdn::kScaleLeast), gdn::kScaleMost)), before);
-    const float inv = __uint_as_float((254u - min(byte, 253u)) << 23);
-    __syncwarp();  // every lane has read the scale
-    if (lane == 0) *scale = static_cast<uint8_t>(byte);
+  } else {
+    for (int item0 = worker * kPer; item0 < 2 * a.Hkv; item0 += workers * kPer) {
+      const int item = min(item0 + sub, 2 * a.Hkv - 1);
+      const bool there = item0 + sub < 2 * a.Hkv, is_k = item < a.Hkv;
+      const int h = is_k ? item : item - a.Hkv;
+      const __nv_bfloat16* src = (is_k ? a.k : a.v) + g.token * (is_k ? a.k_stride : a.v_stride) + static_cast<int64_t>(h) * D;
+      const int64_t stride = is_k ? a.k_stride : a.v_stride;
+      const Slot slot = slot_of(is_k ? 0 : 1, h);
+      Pairs<W> p[U];
+      // Keys and values may stand side by side in a warp, which takes the norm together.
+      auto row_of = [&](int row) {
+        Piece<W> xa[U], xb[U];
+        load(src + row * stride, true, xa, xb);
+        Pairs<W> raw[U];
+        take(xa, xb, k_weights, false, row, raw);
+        take(xa, xb, k_weights, true, row, p);
+        if (is_k) return;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int row = i * kPer + lane / kLanes;
-      if (row < g.rows0 || row >= g.rows1) continue;
-      uint8_t* dst = codes + row * a.cache.token_stride;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        store_codes<W>(dst + first[u], p[i].x[u], inv);
-        store_codes<W>(dst + second[u], p[i].y[u], inv);
+        for (int u = 0; u < U; ++u) p[u] = raw[u];
+      };
+      float most = 0.f;
+#pragma unroll 1
+      for (int row = g.rows1 - 1; row >= g.rows0; --row) {
+        row_of(row);
+        most = most_of(p, most);
       }
-    }
-    if (g.rows0 > 0 && byte > before) {
-      // Earlier tokens' codes, rounded to the scale that has grown (by 2^-126 all of
-      // them become zero, as by less).
-      const float by = __uint_as_float(max(127 - static_cast<int>(byte - before), 1) << 23);
-      for (int i = lane; i < g.rows0 * (D / 16); i += 32) {
-        uint4* x = reinterpret_cast<uint4*>(codes + i / (D / 16) * a.cache.token_stride + i % (D / 16) * 16);
-        uint4 four = *x;
-        uint32_t* w = reinterpret_cast<uint32_t*>(&four);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t lo, hi;
-          gdn::e4m3_to_half4(w[k], lo, hi);
-          const float2 f = gdn::half2_to_float2(lo), f2 = gdn::half2_to_float2(hi);
-          w[k] = gdn::to_e4m3(f.x * by, f.y * by) | gdn::to_e4m3(f2.x * by, f2.y * by) << 16;
-        }
-        *x = four;
+      for (int o = 1; o < kLanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+      const uint32_t byte = scale_byte(__float_as_uint(most), slot.before);
+      const float inv = inverse(byte);
+      __syncwarp();  // every lane has read the scale
+      if (there && at == 0) *slot.scale = static_cast<uint8_t>(byte);
+#pragma unroll 1
+      for (int row = g.rows0; row < g.rows1; ++row) {
+        if (row > g.rows0) row_of(row);  // the first row's was taken last
+        if (there) store(slot, row, p, inv);
       }
+      if (there && g.rows0 > 0 && byte > slot.before) round_again<D>(slot, a.cache.token_stride, g.rows0, byte, at, kLanes);
     }
   }
 }
@@ -470,10 +629,11 @@ struct ReadArgs {
   __nv_bfloat16* out[2];
   int32_t Hkv, D;
   int32_t groups;
+  int32_t aligned32;  // of both outputs
 };
 
-// A CTA takes a group of 16 tokens, a thread 16 codes at a time: HBM-bound, 3 bytes
-// an element.
+// A CTA takes a group of 16 tokens, a thread 16 codes of a head in one row after the other:
+// HBM-bound, 3 bytes an element.
 __global__ void __launch_bounds__(kReadThreads) read8_kernel(const ReadArgs a) {
   gdn::pdl_wait();
   gdn::pdl_launch_dependents();
@@ -484,36 +644,39 @@ __global__ void __launch_bounds__(kReadThreads) read8_kernel(const ReadArgs a) {
   Group g;
   if (!find_group(a.paged, blockIdx.x, &g)) return;
   if (g.page < 0 && threadIdx.x == 0) gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_ID, g.seq);
-  const int chunks = a.D / 16, per_row = a.Hkv * chunks, one = (g.rows1 - g.rows0) * per_row;
-  for (int j0 = threadIdx.x; j0 < 2 * one; j0 += kReadBatch * kReadThreads) {
-    uint4 x[kReadBatch];
-    float s[kReadBatch];
-    __nv_bfloat16* dst[kReadBatch];
-#pragma unroll
-    for (int i = 0; i < kReadBatch; ++i) {
-      int j = j0 + i * kReadThreads;
-      x[i] = make_uint4(0, 0, 0, 0);
-      s[i] = 0.f;
-      dst[i] = nullptr;
-      if (j >= 2 * one) continue;
-      const int kv = j >= one ? 1 : 0;
-      j -= kv * one;
-      const int row = g.rows0 + j / per_row, in_row = j % per_row, h = in_row / chunks, c = in_row % chunks;
-      dst[i] = a.out[kv] + (g.token + row) * a.Hkv * a.D + in_row * 16;
-      if (g.page < 0) continue;
-      x[i] = *reinterpret_cast<const uint4*>(a.cache.codes[kv] + g.page * a.cache.page_stride +
-                                             (g.slot + row) * a.cache.token_stride + h * a.cache.head_stride + c * 16);
-      s[i] = gdn::scale_of(a.cache.scales[kv][g.page * a.cache.scale_page + g.slot / kGroup * a.cache.scale_group +
-                                              h * a.cache.scale_head]);
+  const int chunks = a.D / 16, per_row = a.Hkv * chunks;  // 16 codes each
+  // Where a row's chunks are fewer than threads, rows stand side by side.
+  const int beside = max(1, kReadThreads / (2 * per_row));
+  const int row0 = g.rows0 + (beside > 1 ? static_cast<int>(threadIdx.x) / (2 * per_row) : 0);
+  if (row0 >= g.rows0 + beside) return;
+  for (int j = beside > 1 ? static_cast<int>(threadIdx.x) % (2 * per_row) : threadIdx.x; j < 2 * per_row; j += kReadThreads) {
+    const int kv = j >= per_row ? 1 : 0, in_row = j - kv * per_row, h = in_row / chunks, c = in_row % chunks;
+    const uint8_t* src = nullptr;
+    float f = 0.f;
+    if (g.page >= 0) {
+      src = a.cache.codes[kv] + g.page * a.cache.page_stride + g.slot * a.cache.token_stride + h * a.cache.head_stride + c * 16;
+      f = gdn::scale_of(a.cache.scales[kv][g.page * a.cache.scale_page + g.slot / kGroup * a.cache.scale_group +
+                                           h * a.cache.scale_head]);
     }
+    const float2 scale = make_float2(f, f);
+    __nv_bfloat16* const dst = a.out[kv] + g.token * a.Hkv * a.D + in_row * 16;
+    for (int r0 = row0; r0 < g.rows1; r0 += kReadBatch * beside) {
+      uint4 x[kReadBatch];
 #pragma unroll
-    for (int i = 0; i < kReadBatch; ++i) {
-      if (!dst[i]) continue;
-      const float2 scale = make_float2(s[i], s[i]);
-      const uint2 y0 = gdn::e4m3_to_bf16(x[i].x, scale), y1 = gdn::e4m3_to_bf16(x[i].y, scale);
-      const uint2 y2 = gdn::e4m3_to_bf16(x[i].z, scale), y3 = gdn::e4m3_to_bf16(x[i].w, scale);
-      reinterpret_cast<uint4*>(dst[i])[0] = make_uint4(y0.x, y0.y, y1.x, y1.y);
-      reinterpret_cast<uint4*>(dst[i])[1] = make_uint4(y2.x, y2.y, y3.x, y3.y);
+      for (int i = 0; i < kReadBatch; ++i) {
+        const int row = r0 + i * beside;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (src && row < g.rows1) x[i] = *reinterpret_cast<const uint4*>(src + row * a.cache.token_stride);
+      }
+#pragma unroll
+      for (int i = 0; i < kReadBatch; ++i) {
+        const int row = r0 + i * beside;
+        if (row >= g.rows1) continue;
+        const uint2 y0 = gdn::e4m3_to_bf16(x[i].x, scale), y1 = gdn::e4m3_to_bf16(x[i].y, scale);
+        const uint2 y2 = gdn::e4m3_to_bf16(x[i].z, scale), y3 = gdn::e4m3_to_bf16(x[i].w, scale);
+        const uint32_t y[8] = {y0.x, y0.y, y1.x, y1.y, y2.x, y2.y, y3.x, y3.y};
+        gdn::store32(dst + static_cast<int64_t>(row) * a.Hkv * a.D, y, a.aligned32 != 0);
+      }
     }
   }
 }
@@ -542,15 +705,26 @@ NormRope norm_rope(const gdn_qk_norm* n, const int64_t* frequencies, int32_t rot
   return r;
 }
 
-template <int D>
-int launch_append(const AppendArgs& a, dim3 grid, cudaStream_t stream) {
-  const dim3 block(kAppendWarps * 32);
-  switch (gdn_host::piece_width(a.n.half, D)) {
-    case 8: return gdn_host::launch_pdl(append8_kernel<D, 8>, grid, block, 0, stream, a);
-    case 4: return gdn_host::launch_pdl(append8_kernel<D, 4>, grid, block, 0, stream, a);
-    case 2: return gdn_host::launch_pdl(append8_kernel<D, 2>, grid, block, 0, stream, a);
-    default: return gdn_host::launch_pdl(append8_kernel<D, 1>, grid, block, 0, stream, a);
+// Calls run with the widest piece, and whether pairs are interleaved.
+template <typename Run>
+int by_pairs(int32_t half, int32_t D, bool interleaved, const Run& run) {
+  const auto of = [&](auto width) {
+    return interleaved && half ? run(width, std::true_type()) : run(width, std::false_type());
+  };
+  switch (gdn_host::piece_width(half, D)) {
+    case 8: return of(std::integral_constant<int, 8>());
+    case 4: return of(std::integral_constant<int, 4>());
+    case 2: return of(std::integral_constant<int, 2>());
+    default: return of(std::integral_constant<int, 1>());
   }
+}
+
+template <int D, bool kWide>
+int launch_append(const AppendArgs& a, dim3 grid, cudaStream_t stream) {
+  return by_pairs(a.n.half, D, a.n.interleaved != 0, [&](auto width, auto interleaved) {
+    return gdn_host::launch_pdl(append8_kernel<D, decltype(width)::value, decltype(interleaved)::value, kWide>, grid,
+                                dim3(kAppendWarps<kWide> * 32), 0, stream, a);
+  });
 }
 
 }  // namespace
@@ -575,40 +749,28 @@ extern "C" int gdn_qk_norm_rope(const gdn_bf16* q, int64_t q_token_stride, gdn_b
   const int rc = gdn_host::check_device(nullptr);
   if (rc != GDN_OK) return rc;
   NormArgs a = {};
-  a.q = bf(q);
-  a.k = bf(k);
-  a.q_out = bf(q_out);
-  a.k_out = bf(k_out);
-  a.q_stride = q_token_stride;
-  a.k_stride = k_token_stride;
-  a.q_out_stride = q_out_token_stride;
-  a.k_out_stride = k_out_token_stride;
   a.positions = positions;
   a.n = norm_rope(norm, frequencies, rotary_dim, interleaved, amplitude, D);
   a.T = total_tokens;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
   a.D = D;
   const int W = gdn_host::piece_width(a.n.half, D);
   a.units = D / (2 * W);
   a.lanes = 1;
   while (a.lanes < a.units && a.lanes < 32) a.lanes <<= 1;
-  const int64_t steps = (static_cast<int64_t>(Hq) + Hkv + 32 / a.lanes - 1) / (32 / a.lanes);
+  const int per = 32 / a.lanes;
+  a.kind[0] = NormHeads{bf(q), bf(q_out), bf(norm->q_weight), q_token_stride, q_out_token_stride, Hq, (Hq + per - 1) / per};
+  a.kind[1] = NormHeads{bf(k), bf(k_out), bf(norm->k_weight), k_token_stride, k_out_token_stride, Hkv, (Hkv + per - 1) / per};
+  const int64_t steps = static_cast<int64_t>(a.kind[0].steps) + a.kind[1].steps;
   // One warp per token where that fills the GPU, as in rope.cu.
   const int64_t want = 152 * 16;
   int64_t slices = total_tokens >= want ? 1 : (want + total_tokens - 1) / total_tokens;
   if (slices > steps) slices = steps;
   a.slices = static_cast<int32_t>(slices);
-  const int64_t blocks = (total_tokens * slices + kWarps - 1) / kWarps;
-  if (blocks > 0x7FFFFFFF) return GDN_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(kWarps * 32);
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  switch (W) {
-    case 8: return gdn_host::launch_pdl(norm_rope_kernel<8>, grid, block, 0, s, a);
-    case 4: return gdn_host::launch_pdl(norm_rope_kernel<4>, grid, block, 0, s, a);
-    case 2: return gdn_host::launch_pdl(norm_rope_kernel<2>, grid, block, 0, s, a);
-    default: return gdn_host::launch_pdl(norm_rope_kernel<1>, grid, block, 0, s, a);
-  }
+  const dim3 grid(static_cast<unsigned>((total_tokens * slices + kWarps - 1) / kWarps)), block(kWarps * 32);
+  return by_pairs(a.n.half, D, interleaved != 0, [&](auto width, auto pairs) {
+    return gdn_host::launch_pdl(norm_rope_kernel<decltype(width)::value, decltype(pairs)::value>, grid, block, 0,
+                                static_cast<cudaStream_t>(stream), a);
+  });
 }
 
 extern "C" int gdn_kv_append_paged_fp8(const gdn_bf16* q, int64_t q_token_stride, gdn_bf16* q_out, const gdn_bf16* k,
@@ -649,14 +811,18 @@ extern "C" int gdn_kv_append_paged_fp8(const gdn_bf16* q, int64_t q_token_stride
   const int64_t groups = group_slots(cu_seqlens, table->num_seqs, total_tokens);
   if (groups > 0x7FFFFFFE) return GDN_ERR_UNSUPPORTED;
   a.groups = static_cast<int32_t>(groups);
+  // Sequences of a new token or two, as in decoding.
+  const bool wide = total_tokens > 2 * static_cast<int64_t>(table->num_seqs);
   // Few groups share their heads out among CTAs.
-  const int64_t most = (2 * static_cast<int64_t>(Hkv) + (Hq + 3) / 4 + kAppendWarps - 1) / kAppendWarps;
-  int64_t slices = 2 * sms / (groups + 1);
+  const int64_t most = wide ? (2 * static_cast<int64_t>(Hkv) + Hq / 4) / kAppendWarps<true> + 1
+                            : (2 * static_cast<int64_t>(Hkv) + Hq / 4) / kAppendWarps<false> + 1;
+  int64_t slices = 4 * sms / (groups + 1);
   slices = slices < 1 ? 1 : slices > most ? most : slices;
   if (slices > 65535) slices = 65535;
   const dim3 grid(static_cast<unsigned>(groups) + 1, static_cast<unsigned>(slices));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return D == 64 ? launch_append<64>(a, grid, s) : launch_append<128>(a, grid, s);
+  if (wide) return D == 64 ? launch_append<64, true>(a, grid, s) : launch_append<128, true>(a, grid, s);
+  return D == 64 ? launch_append<64, false>(a, grid, s) : launch_append<128, false>(a, grid, s);
 }
 
 extern "C" int gdn_kv_read_paged_fp8(const gdn_kv_cache_fp8* cache, const gdn_page_table* table,
@@ -676,6 +842,7 @@ extern "C" int gdn_kv_read_paged_fp8(const gdn_kv_cache_fp8* cache, const gdn_pa
   a.out[1] = bf(v_out);
   a.Hkv = cache->num_heads;
   a.D = cache->head_dim;
+  a.aligned32 = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31u) == 0;
   const int64_t groups = group_slots(cu_seqlens, table->num_seqs, total_tokens);
   if (groups > 0x7FFFFFFE) return GDN_ERR_UNSUPPORTED;
   a.groups = static_cast<int32_t>(groups);

@@ -475,6 +475,19 @@ __device__ __forceinline__ float2 unpack_bf162(uint32_t u) {
   return __bfloat1622float2(h);
 }
 
+// 32 bytes of a row at once, a whole sector of HBM per lane, where the address
+// allows it.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8], bool aligned32) {
+  if (!aligned32) {
+    static_cast<uint4*>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    return;
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 }  // namespace gdn
 
 // ---------------------------------------------------------------------------

@@ -83,33 +83,6 @@ __device__ __forceinline__ void rotate(Piece<W>& a, Piece<W>& b, const float2* c
   b = pack<W>(y);
 }
 
-// The same of pairs that are in fp32 already.
-template <int W, typename Cs>
-__device__ __forceinline__ void turn(float (&x)[W], float (&y)[W], const Cs& cs, bool interleaved) {
-  if (interleaved) {
-    float u[W], v[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      // Pair i is elements 2 i and 2 i + 1 of the 2 W.
-      const float e = 2 * i < W ? x[(2 * i) % W] : y[(2 * i) % W];
-      const float o = 2 * i + 1 < W ? x[(2 * i + 1) % W] : y[(2 * i + 1) % W];
-      const float2 c = cs(i);
-      const float re = e * c.x - o * c.y, im = e * c.y + o * c.x;
-      if (2 * i < W) u[(2 * i) % W] = re; else v[(2 * i) % W] = re;
-      if (2 * i + 1 < W) u[(2 * i + 1) % W] = im; else v[(2 * i + 1) % W] = im;
-    }
-#pragma unroll
-    for (int i = 0; i < W; ++i) x[i] = u[i], y[i] = v[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float e = x[i], o = y[i];
-      const float2 c = cs(i);
-      x[i] = e * c.x - o * c.y;
-      y[i] = e * c.y + o * c.x;
-    }
-  }
-}
 // The sequence of token t: the last b with cu_seqlens[b] <= t, by a 32-way
 // search of the warp (sequences without new tokens share their start with the
 // next one, so the last is the one that holds t).

@@ -22,8 +22,9 @@
 //   - keys are the 16 rows of the products and up to 8 query heads the columns, S = K
 //     q^T, O^T = V^T P^T: half the products, scores and accumulators of the form with
 //     the heads as rows, which has as many for 8 heads as for 16;
-//   - eight consumer warps, for which there are registers then (four, with the heads as
-//     rows: 256 sequences 0.75 ms);
+//   - four consumer warps, each with registers for two groups of keys at a time (256
+//     sequences 576 us, with the heads as rows 750; eight warps with half the
+//     registers, some of them spilled, 680);
 //   - K: the products may take the dimensions in any order, as long as q does too: a lane
 //     reads 16 consecutive codes of a key, which are four steps' operands;
 //   - V: a 16 x 16 block of bytes is transposed as it is read (ldmatrix on bytes): a lane
@@ -42,13 +43,12 @@ struct Decode8Args {
   gdn::Cache8 cache;
 };
 
-// Query heads in tiles of 8: with one, eight consumer warps of 96 registers; with two,
-// four of 168.
-template <int NT>
-constexpr int kConsumers = NT == 1 ? 8 : 4;
+constexpr int kConsumers = 4;
+constexpr int kThreads = threads_of(kConsumers);
 
+// NT: query heads in tiles of 8.
 template <int D, int NT>
-struct Smem8 : Smem<kConsumers<NT>, NT * D / 16, NT> {
+struct Smem8 : Smem<kConsumers, NT * D / 16, NT> {
   static constexpr int kGroups = kBlock<D> / gdn::kGroup;
   float scale[kStages][2][kGroups];  // the keys' scales, and the exponents of the values'
 };
@@ -86,7 +86,6 @@ template <int D, int NT>
 __device__ __forceinline__ bool end_segment(const DecodeArgs& d, Smem8<D, NT>& sh, const Walk& w,
                                             const gdn::Shares<0>& shares, float (&m)[NT][2], float (&l)[NT][2],
                                             const float (&o)[NT][D / 16][4]) {
-  constexpr int kWarps = kConsumers<NT>;
   const AttnArgs& a = d.a;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
@@ -97,7 +96,7 @@ __device__ __forceinline__ bool end_segment(const DecodeArgs& d, Smem8<D, NT>& s
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], x);
-  consumers_sync<kWarps>();  // the last item's results have been read
+  consumers_sync<kConsumers>();  // the last item's results have been read
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -106,7 +105,7 @@ __device__ __forceinline__ bool end_segment(const DecodeArgs& d, Smem8<D, NT>& s
     sh.join_ml[warp][n][lane] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
   }
   if (tid == 0) sh.stop = *static_cast<volatile int*>(&sh.abort);  // one reading for all warps
-  consumers_sync<kWarps>();
+  consumers_sync<kConsumers>();
   if (sh.stop) {
     if (tid == 0) gdn::record_error(a.paged.err_word, GDN_DEVERR_TIMEOUT, 0);
     return false;
@@ -118,19 +117,19 @@ __device__ __forceinline__ bool end_segment(const DecodeArgs& d, Smem8<D, NT>& s
   const int64_t row0 = static_cast<int64_t>(w.b) * a.Hq + w.head * a.group;
   // A tile of 16 dimensions of 8 heads per warp and turn.
 #pragma unroll
-  for (int at = warp; at < NT * D / 16; at += kWarps) {
+  for (int at = warp; at < NT * D / 16; at += kConsumers) {
     const int n = at / (D / 16), c = at % (D / 16);
-    float f[kWarps][2], top[2], sum[2] = {0.f, 0.f};
-    float4 ml[kWarps];
+    float f[kConsumers][2], top[2], sum[2] = {0.f, 0.f};
+    float4 ml[kConsumers];
     top[0] = top[1] = -INFINITY;
 #pragma unroll
-    for (int v = 0; v < kWarps; ++v) {
+    for (int v = 0; v < kConsumers; ++v) {
       ml[v] = sh.join_ml[v][n][lane];
       top[0] = fmaxf(top[0], ml[v].x);
       top[1] = fmaxf(top[1], ml[v].y);
     }
 #pragma unroll
-    for (int v = 0; v < kWarps; ++v) {
+    for (int v = 0; v < kConsumers; ++v) {
       f[v][0] = ml[v].x == -INFINITY ? 0.f : gdn::exp2_approx(ml[v].x - top[0]);
       f[v][1] = ml[v].y == -INFINITY ? 0.f : gdn::exp2_approx(ml[v].y - top[1]);
       sum[0] = fmaf(ml[v].z, f[v][0], sum[0]);
@@ -138,7 +137,7 @@ __device__ __forceinline__ bool end_segment(const DecodeArgs& d, Smem8<D, NT>& s
     }
     float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int v = 0; v < kWarps; ++v) {
+    for (int v = 0; v < kConsumers; ++v) {
       const float4 y = sh.join_o[v][at][lane];
       x[0] = fmaf(y.x, f[v][0], x[0]);
       x[1] = fmaf(y.y, f[v][1], x[1]);
@@ -170,24 +169,23 @@ __device__ __forceinline__ bool end_segment(const DecodeArgs& d, Smem8<D, NT>& s
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(threads_of(kConsumers<NT>), 2)
+__global__ void __launch_bounds__(kThreads, 2)
     decode_attention8_kernel(const __grid_constant__ Decode8Args d8, const __grid_constant__ CUtensorMap k_map,
                              const __grid_constant__ CUtensorMap v_map) {
-  constexpr int kWarps = kConsumers<NT>;
   extern __shared__ uint8_t raw[];
   Smem8<D, NT>& sh = *reinterpret_cast<Smem8<D, NT>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const DecodeArgs& d = d8.d;
   const AttnArgs& a = d.a;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
-  if (tid == kWarps * 32) {
+  if (tid == kConsumers * 32) {
     gdn::prefetch_tensormap(&k_map);
     gdn::prefetch_tensormap(&v_map);
   }
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       gdn::mbar_init(&sh.full[i], 2);
-      gdn::mbar_init(&sh.empty[i], kWarps);
+      gdn::mbar_init(&sh.empty[i], kConsumers);
     }
     gdn::mbar_init(&sh.never, 1);
     sh.abort = 0;
@@ -198,16 +196,16 @@ __global__ void __launch_bounds__(threads_of(kConsumers<NT>), 2)
 
   Walk w;
   gdn::Shares<0> shares(0, 1, 1);
-  if (!take_share<kBlock<D>>(d, sh, w, shares)) return;
+  if (!take_share<kBlock<D>, kItemCost8>(d, sh, w, shares)) return;
 
-  if (warp >= kWarps) {
+  if (warp >= kConsumers) {
     // ------------------------------------------------ keys, or values
-    const int kv = warp - kWarps;
+    const int kv = warp - kConsumers;
     gdn::TileCopies<D, kBlock<D>, 1> tiles(a, kv ? &v_map : &k_map, lane);
     gdn::ScaleCopies<kBlock<D>> scales(a, d8.cache, kv, lane);
     int n = 0;  // blocks issued
     bool ok = true;
-    while (ok && next_segment<kBlock<D>>(d, w)) {
+    while (ok && next_segment<kBlock<D>, kItemCost8>(d, w)) {
       const int first = (w.it.first + w.blk0) * kBlock<D>;
       tiles.begin(w.it.lo, w.it.hi, w.head, w.b, w.it.s.entry, first);
       scales.begin(w.it.lo, w.it.hi, w.head, w.it.s.entry, first);
@@ -236,9 +234,9 @@ __global__ void __launch_bounds__(threads_of(kConsumers<NT>), 2)
 
   // ------------------------------------------------------------ consumers
   const int g = lane >> 2, t = lane & 3;  // fragment row and column pair
-  constexpr int kSub = kBlock<D> / (16 * kWarps);  // 16-key groups of this warp
+  constexpr int kSub = kBlock<D> / (16 * kConsumers);  // 16-key groups of this warp
   int n = 0;
-  while (next_segment<kBlock<D>>(d, w)) {
+  while (next_segment<kBlock<D>, kItemCost8>(d, w)) {
     // Queries as B fragments, heads past the group are zero: of head 8 v + g, step 4 c + i
     // takes dimensions 64 c + 16 t + 4 i to + 3.
     uint32_t q[NT][D / 16][2];
@@ -474,7 +472,7 @@ int launch(const Decode8Args& base, const gdn_kv_cache_fp8* cache, const gdn_pag
   if ((rc = gdn_host::encode_codes_map(&k_map, cache->k, cache, d.d.a.box_shift)) != GDN_OK) return rc;
   if ((rc = gdn_host::encode_codes_map(&v_map, cache->v, cache, d.d.a.box_shift)) != GDN_OK) return rc;
   return launch_shared<D>(d.d, table, workspace, sms, stream, [&](int grid) {
-    return gdn_host::launch_pdl(decode_attention8_kernel<D, NT>, dim3(grid), dim3(threads_of(kConsumers<NT>)), smem, stream, d, k_map, v_map);
+    return gdn_host::launch_pdl(decode_attention8_kernel<D, NT>, dim3(grid), dim3(kThreads), smem, stream, d, k_map, v_map);
   });
 }
 

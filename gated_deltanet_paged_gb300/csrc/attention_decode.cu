@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   Walk w;
   gdn::Shares<0> shares(0, 1, 1);
-  if (!take_share<kBlock<D>>(d, sh, w, shares)) return;
+  if (!take_share<kBlock<D>, kItemCost16>(d, sh, w, shares)) return;
 
   if (warp >= kConsumers) {
     // ------------------------------------------------ keys, or values
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     gdn::TileCopies<D, kBlock<D>> tiles(a, kv ? &v_map : &k_map, lane);
     int n = 0;  // blocks issued
     bool ok = true;
-    while (ok && next_segment<kBlock<D>>(d, w)) {
+    while (ok && next_segment<kBlock<D>, kItemCost16>(d, w)) {
       tiles.begin(w.it.lo, w.it.hi, w.head, w.b, w.it.s.entry, (w.it.first + w.blk0) * kBlock<D>);
       for (int blk = w.blk0; blk < w.blk1; ++blk, ++n) {
         const int stage = n % kStages;
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // ------------------------------------------------------------ consumers
   const int g = lane >> 2, t = lane & 3;  // fragment row and column pair
   int n = 0;
-  while (next_segment<kBlock<D>>(d, w)) {
+  while (next_segment<kBlock<D>, kItemCost16>(d, w)) {
     const int h0 = w.head * a.group;  // first query head of the rows
     const int rows = a.group;
     // Queries as A fragments; rows past the group are zero.

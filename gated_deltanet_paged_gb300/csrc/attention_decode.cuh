@@ -20,8 +20,10 @@ constexpr int kRows = 16;     // query heads of a key head at most (see gdn_atte
 constexpr int kTileBytes = 16384;
 // Fixed cost of an item (its queries, the join of the warps, its stores) in
 // blocks, so that shares of many short items weigh the same as shares of long ones
-// (512 sequences of 100 to 300 keys, 8 key heads of 128: 89 us, with 4 92).
-constexpr int kItemCost = 2;
+// (512 sequences of 100 to 300 keys, 8 key heads of 128: 89 us, with 4 92).  Over an 8-bit
+// cache, whose blocks have twice the keys, one (61 sequences of up to 9,000 17.1 us, with
+// two 18.1).
+constexpr int kItemCost16 = 2, kItemCost8 = 1;
 // Smallest piece in blocks (8 key heads of 128; 1 sequence of 1,000 / 16 of 250 / of
 // 500: 9.8 / 10.9 / 12.5 us, with 4 10.9 / 11.5 / 12.5, with 8 13.6 / 13.3 / 15.0).
 constexpr int kMinShare = 2;
@@ -46,7 +48,7 @@ struct Item {
   int blocks;
   int cost;        // 0: nothing to do
 };
-template <int kBlock>
+template <int kBlock, int kItemCost>
 __device__ __forceinline__ Item load_item(const AttnArgs& a, int b) {
   Item it;
   it.s = gdn::seq_range(a.paged, b);
@@ -68,7 +70,7 @@ struct Walk {
   int blk0, blk1;     // blocks of the item in this segment
   int64_t item0;      // line position of the item
 };
-template <int kBlock>
+template <int kBlock, int kItemCost>
 __device__ __forceinline__ bool next_segment(const DecodeArgs& d, Walk& w) {
   const int per_seq = d.a.Hkv;
   if (d.whole) {
@@ -76,7 +78,7 @@ __device__ __forceinline__ bool next_segment(const DecodeArgs& d, Walk& w) {
       const int id = static_cast<int>(w.pos);
       w.pos += gridDim.x;
       const int b = id / per_seq;
-      if (b != w.b) w.b = b, w.it = load_item<kBlock>(d.a, b);
+      if (b != w.b) w.b = b, w.it = load_item<kBlock, kItemCost>(d.a, b);
       w.head = id - b * per_seq;
       w.blk0 = 0;
       w.blk1 = w.it.blocks;
@@ -88,7 +90,7 @@ __device__ __forceinline__ bool next_segment(const DecodeArgs& d, Walk& w) {
     const int64_t span = static_cast<int64_t>(w.it.cost) * per_seq;
     if (w.pos >= w.base + span) {
       w.base += span;
-      w.it = load_item<kBlock>(d.a, ++w.b);
+      w.it = load_item<kBlock, kItemCost>(d.a, ++w.b);
       continue;
     }
     w.head = gdn::small_quotient(w.pos - w.base, w.it.cost, per_seq);
@@ -135,7 +137,7 @@ __device__ __forceinline__ void consumers_sync() {
 }
 
 // This CTA's share of the line; false: none.  All threads take it together.
-template <int kBlock, int kConsumers, int kTiles, int kPairs>
+template <int kBlock, int kItemCost, int kConsumers, int kTiles, int kPairs>
 __device__ __forceinline__ bool take_share(const DecodeArgs& d, Smem<kConsumers, kTiles, kPairs>& sh, Walk& w, gdn::Shares<0>& shares) {
   constexpr int kThreads = threads_of(kConsumers);
   const AttnArgs& a = d.a;
@@ -155,7 +157,7 @@ __device__ __forceinline__ bool take_share(const DecodeArgs& d, Smem<kConsumers,
     const int b0 = min(tid * per, a.paged.num_seqs), b1 = min(b0 + per, a.paged.num_seqs);
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) {
-      const Item it = load_item<kBlock>(a, b);
+      const Item it = load_item<kBlock, kItemCost>(a, b);
       if (it.s.refused && blockIdx.x == 0) gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_TABLE, b);
       mine += it.cost;
     }
@@ -183,10 +185,10 @@ __device__ __forceinline__ bool take_share(const DecodeArgs& d, Smem<kConsumers,
       x.end = end;
       x.base = before * per_seq;
       x.b = b0;
-      x.it = load_item<kBlock>(a, b0);
+      x.it = load_item<kBlock, kItemCost>(a, b0);
       while (start >= x.base + static_cast<int64_t>(x.it.cost) * per_seq) {
         x.base += static_cast<int64_t>(x.it.cost) * per_seq;
-        x.it = load_item<kBlock>(a, ++x.b);
+        x.it = load_item<kBlock, kItemCost>(a, ++x.b);
       }
       sh.walk = x;
     }

@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(kWarps * 32, 5) norm_rope_kernel(const __grid_
   gdn::pdl_wait();
   gdn::pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned id = blockIdx.x * kWarps + warp;
-  const int t = static_cast<int>(id / a.slices), slice = static_cast<int>(id % a.slices);
+  const unsigned id = blockIdx.x * kWarps + warp, token = id / a.slices;
+  const int t = static_cast<int>(min(token, static_cast<unsigned>(a.T))), slice = static_cast<int>(id - token * a.slices);
   const int per = 32 / a.lanes, at = lane & (a.lanes - 1), sub = lane / a.lanes;  // `per` heads at a time
   const int q_steps = a.kind[0].steps, steps = t < a.T ? q_steps + a.kind[1].steps : 0;
   int first[U], second[U];

@@ -547,7 +547,9 @@ int gdn_qk_norm_rope(const gdn_bf16 *q, int64_t q_token_stride, gdn_bf16 *q_out,
  * rounded to it.  Whatever else a group's slots and its scale held is not read.
  * Infinities are stored as the largest number, NaN as NaN; neither has a say in
  * the scale of its group but that an infinity raises it to 2^119.  No two
- * sequences of a call write to one page. */
+ * sequences of a call write to one page, and since earlier tokens' codes may be
+ * rounded again, a page that is to be appended to is nobody else's: a sequence
+ * that shares one in part takes a copy of its codes and scales first. */
 int gdn_kv_append_paged_fp8(const gdn_bf16 *q, int64_t q_token_stride, gdn_bf16 *q_out, const gdn_bf16 *k,
                             int64_t k_token_stride, const gdn_bf16 *v, int64_t v_token_stride,
                             const int32_t *cu_seqlens, int32_t total_tokens, int32_t Hq,

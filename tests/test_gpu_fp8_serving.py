@@ -262,3 +262,29 @@ def test_queries_with_small_elements():
         c.view(U8)[..., 5] = 0
         b.k[i][..., 5] = 0
     check_attention8(b.fill(), decode=True)
+
+
+def test_example_on_an_8_bit_cache():
+    """The example with a recurrent and an attention layer runs on it, and its cache holds
+    the values that were appended within half a step of e4m3 (2^-4, below 2^-6 of the
+    scale 2^-10 of it; no group grows by more than its sixteen tokens)."""
+    import importlib.util
+    import os
+
+    from conftest import ROOT
+
+    spec = importlib.util.spec_from_file_location("hybrid_layers", os.path.join(ROOT, "examples", "hybrid_layers.py"))
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    layers, lengths, owned, history = ex.run((300, 64, 1, 129), steps=3, seed=4, eight_bit=True)
+    table = ex.page_table(lengths, owned)
+    cu = torch.tensor([sum(lengths[:i]) for i in range(5)], dtype=torch.int32, device="cuda")
+    _, held = gdn.gdn_kv_read_paged_fp8(*layers._cache8(), cu, sum(lengths), *table)
+    parts = [[] for _ in lengths]
+    for new, attention, (o_r, o_a) in history:
+        assert torch.isfinite(o_r).all() and torch.isfinite(o_a).all()
+        for b, v in enumerate(attention["v"].split(new)):
+            parts[b].append(v)
+    for b, y in enumerate(held.double().split(lengths)):
+        x = torch.cat(parts[b]).double()
+        assert ((x - y).abs() <= 16 * (2.0**-4 * x.abs() + 2.0**-10 * x.abs().max() / 224)).all()

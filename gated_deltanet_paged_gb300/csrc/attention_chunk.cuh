@@ -748,11 +748,13 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
         Segment done;
         bool pending = false;
         uint32_t n = 0;  // ring tiles
-        for (uint32_t segs = 0; ok && next(segs, g); ++segs) {
-          for (int i = 0; ok && i < 2 * g.blocks; ++i, ++n) {
+        for (uint32_t segs = 0;; ++segs) {
+          const bool more = next(segs, g);
+          const int count = more ? 2 * g.blocks : 0;
+          for (int i = 0; ok; ++i) {
             if (pending) {
               // At the latest where the next tile's room depends on it.
-              bool there = i >= L::kStages;
+              bool there = i >= count || i >= L::kStages;
               if (!there) {
                 there = gdn::mbar_test(&sh.stat_full[0], taken[0] & 1) && gdn::mbar_test(&sh.o_last[0], taken[0] & 1);
                 if (tile_tokens < done.tokens)
@@ -760,10 +762,11 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
                 there = __all_sync(0xFFFFFFFFu, there);
               }
               if (there) {
-                write(done);
+                write(done);  // the one place: the kernel's code is fetched more slowly than issued
                 pending = false;
               }
             }
+            if (!ok || i >= count) break;
             const uint32_t stage = n % L::kStages, at = n % kCopies;
             const int key0 = g.key0 + (i >> 1) * kKeys;
             if (!wait(&sh.code_full[at], (n / kCopies) & 1)) break;
@@ -776,12 +779,12 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
               gdn::mbar_arrive(&sh.full[stage]);
               gdn::mbar_arrive(&sh.code_empty[at]);
             }
+            ++n;
           }
-          if (ok && pending) write(done);
+          if (!ok || !more) break;
           done = g;
           pending = true;
         }
-        if (ok && pending) write(done);
       }
       if (!ok) *abort_flag = 1;
     };

@@ -42,6 +42,7 @@ __all__ = [
     "gdn_attention_decode_paged_fp8",
     "gdn_attention_workspace_bytes",
     "gdn_attention_decode_workspace_bytes",
+    "gdn_attention_fp8_workspace_bytes",
     "gdn_status_string",
     "library",
     "GdnError",
@@ -119,6 +120,7 @@ def library():
                 fn.argtypes = args
                 fn.restype = ctypes.c_int
             sizes = {"gdn_prefill_workspace_bytes": [i32] * 3, "gdn_attention_workspace_bytes": [i32] * 7,
+                     "gdn_attention_fp8_workspace_bytes": [i32] * 7,
                      "gdn_attention_decode_workspace_bytes": [i32] * 6}
             for name, args in sizes.items():
                 getattr(lib, name).argtypes = args
@@ -562,10 +564,18 @@ def gdn_kv_read_paged_fp8(k_cache, v_cache, k_scales, v_scales, cu_seqlens, tota
                                          page_indptr, last_page_len, k_out, v_out, err_word)
 
 
+def gdn_attention_fp8_workspace_bytes(num_seqs: int, total_tokens: int, Hq: int, Hkv: int, D: int, num_entries: int,
+                                      page_size: int) -> int:
+    return int(library().gdn_attention_fp8_workspace_bytes(num_seqs, total_tokens, Hq, Hkv, D, num_entries, page_size))
+
+
 def gdn_attention_paged_fp8(q, k_cache, v_cache, k_scales, v_scales, cu_seqlens, page_indices, page_indptr,
                             last_page_len, *, scale=0.0, softcap=0.0, window=-1, slopes=None, full_lens=None, o=None,
                             lse=None, return_lse=False, err_word=None, workspace=None):
-    """gdn_attention_paged over an 8-bit cache: the same options, outputs and workspace."""
+    """gdn_attention_paged over an 8-bit cache: the same options and outputs.
+    ``workspace``: at least gdn_attention_workspace_bytes(...) bytes; with
+    gdn_attention_fp8_workspace_bytes(...), which is what the call allocates without
+    one, sequences of many new tokens are turned into bf16 once (same bits, faster)."""
     return (_calls or _load_calls()).attention8(False, q, k_cache, v_cache, k_scales, v_scales, cu_seqlens, page_indices,
                                            page_indptr, last_page_len, scale, softcap, window, slopes, full_lens, o,
                                            lse, return_lse, err_word, workspace)

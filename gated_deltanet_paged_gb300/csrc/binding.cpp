@@ -301,10 +301,11 @@ struct Attention {
   at::Tensor o, lse, workspace;
   bool return_lse;
   int32_t* err;
-  int64_t need;
+  int64_t need;  // bytes of workspace that there are
 
-  Attention(PyObject* const* a, const Heads& queries, const gdn_page_table& t, bool decode, int32_t Hkv, int32_t D,
-            int32_t page_size, const c10::Device& device)
+  // codes: over an 8-bit cache, which has a use for a larger workspace.
+  Attention(PyObject* const* a, const Heads& queries, const gdn_page_table& t, bool decode, bool codes, int32_t Hkv,
+            int32_t D, int32_t page_size, const c10::Device& device)
       : q(queries) {
     scale = static_cast<float>(number(a[0]));
     options.softcap = static_cast<float>(number(a[1]));
@@ -339,6 +340,10 @@ struct Attention {
       workspace = dense(a[9], "workspace", at::kByte, device);
       if (workspace.size(0) < need)
         fail(PyExc_ValueError, "workspace holds %lld bytes, the call needs %lld", (long long)workspace.size(0), (long long)need);
+      if (codes) need = workspace.size(0);
+    } else if (codes && !decode && options.softcap <= 0.f) {
+      need = static_cast<int64_t>(gdn_attention_fp8_workspace_bytes(t.num_seqs, T, Hq, Hkv, D, t.num_entries, page_size));
+      if (need) workspace = make({need}, at::kByte, device);
     } else if (need) {
       workspace = make({need}, at::kByte, device);
     }
@@ -365,7 +370,7 @@ PyObject* attention(PyObject* const* a, Py_ssize_t n) {
   if (q.D != c.head_dim) fail(PyExc_ValueError, "q must have %d dimensions per head, got %lld", c.head_dim, (long long)q.D);
   const int32_t* cu;
   const gdn_page_table t = table(a + 5, a[4], q.T, device, &cu);
-  Attention x(a + 8, q, t, decode, c.num_heads, c.head_dim, c.page_size, device);
+  Attention x(a + 8, q, t, decode, false, c.num_heads, c.head_dim, c.page_size, device);
   const c10::cuda::CUDAGuard guard(device);
   if (decode)
     ok("gdn_attention_decode_paged",
@@ -390,7 +395,7 @@ PyObject* attention8(PyObject* const* a, Py_ssize_t n) {
   if (q.D != c.head_dim) fail(PyExc_ValueError, "q must have %d dimensions per head, got %lld", c.head_dim, (long long)q.D);
   const int32_t* cu;
   const gdn_page_table t = table(a + 7, a[6], q.T, device, &cu);
-  Attention x(a + 10, q, t, decode, c.num_heads, c.head_dim, c.page_size, device);
+  Attention x(a + 10, q, t, decode, true, c.num_heads, c.head_dim, c.page_size, device);
   const c10::cuda::CUDAGuard guard(device);
   if (decode)
     ok("gdn_attention_decode_paged_fp8",

@@ -690,6 +690,119 @@ __global__ void __launch_bounds__(kReadThreads) read8_kernel(const ReadArgs a) {
   }
 }
 
+// ----------------------------------------------------------------------------- expand
+// What the new tokens of a batch may see, out of the 8-bit cache into bf16 pages [table
+// entry, Hkv, page_size, D] of their own, so that many rows read it as it is.  The batch is
+// one line of groups of 16 tokens, and each CTA takes an equal piece.  HBM-bound, 3 bytes
+// an element.
+constexpr int kExpandThreads = 256;
+
+struct ExpandArgs {
+  Cache8 cache;
+  PagedTokens paged;
+  __nv_bfloat16* out[2];
+  int32_t* pages;  // receives 0, 1, 2, ...: the table entries' pages among `out`
+  int32_t Hkv, D, window;
+};
+
+struct Needed {
+  SeqRange s;
+  int first;   // group
+  int groups;
+};
+__device__ __forceinline__ Needed needed(const ExpandArgs& a, int b) {
+  Needed n;
+  n.s = gdn::seq_range(a.paged, b);
+  const int position = n.s.len - n.s.new_tokens;
+  n.first = a.window >= 0 ? max(0, position - a.window) / kGroup : 0;
+  n.groups = n.s.new_tokens ? (n.s.len + kGroup - 1) / kGroup - n.first : 0;
+  return n;
+}
+
+__global__ void __launch_bounds__(kExpandThreads) expand8_kernel(const __grid_constant__ ExpandArgs a) {
+  __shared__ int64_t scan[kExpandThreads / 32];
+  __shared__ int begin[2];  // sequence, group
+  gdn::pdl_wait();
+  gdn::pdl_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kExpandThreads + tid; i < a.paged.num_entries;
+       i += static_cast<int64_t>(gridDim.x) * kExpandThreads)
+    a.pages[i] = static_cast<int32_t>(i);
+  const int per = (a.paged.num_seqs + kExpandThreads - 1) / kExpandThreads;
+  const int b0 = min(tid * per, a.paged.num_seqs), b1 = min(b0 + per, a.paged.num_seqs);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += needed(a, b).groups;
+  int64_t before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, before, o);
+    if (lane >= o) before += x;
+  }
+  if (lane == 31) scan[warp] = before;
+  __syncthreads();
+  before -= mine;
+  int64_t total = 0;
+  for (int i = 0; i < kExpandThreads / 32; ++i) {
+    if (i < warp) before += scan[i];
+    total += scan[i];
+  }
+  const int64_t start = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
+  if (start < end && before <= start && start < before + mine) {
+    int b = b0;
+    int64_t rest = start - before;
+    for (int n; rest >= (n = needed(a, b).groups); ++b) rest -= n;
+    begin[0] = b;
+    begin[1] = static_cast<int>(rest);
+  }
+  __syncthreads();
+  if (start >= end) return;
+  int b = begin[0], group = begin[1];
+  Needed n = needed(a, b);
+  const int chunks = a.D / 16, per_row = a.Hkv * chunks;  // 16 codes each
+  for (int64_t at = start; at < end; ++at, ++group) {
+    while (group >= n.groups) {
+      n = needed(a, ++b);
+      group = 0;
+    }
+    const int position = (n.first + group) * kGroup, rows = min(kGroup, n.s.len - position);
+    const int in_table = position / a.paged.page_size, slot = position - in_table * a.paged.page_size;
+    const int64_t entry = static_cast<int64_t>(n.s.entry) + in_table;
+    const int page = a.paged.pages[entry];
+    const bool there = page >= 0 && page < a.paged.num_pages;
+    if (!there && tid == 0) gdn::record_error(a.paged.err_word, GDN_DEVERR_PAGE_ID, b);
+    // 16 rows of a chunk by neighbours: a row's 16 codes are 32 bytes of a run of rows.
+    for (int j0 = tid; j0 < 2 * per_row * kGroup; j0 += kReadBatch * kExpandThreads) {
+      uint4 x[kReadBatch];
+      float f[kReadBatch];
+#pragma unroll
+      for (int i = 0; i < kReadBatch; ++i) {
+        const int j = j0 + i * kExpandThreads;
+        const int c = j % chunks, row = j / chunks % kGroup, head = j / (chunks * kGroup), kv = head >= a.Hkv ? 1 : 0;
+        const int h = head - kv * a.Hkv;
+        x[i] = make_uint4(0, 0, 0, 0);
+        f[i] = 0.f;
+        if (!there || j >= 2 * per_row * kGroup || row >= rows) continue;
+        x[i] = *reinterpret_cast<const uint4*>(a.cache.codes[kv] + page * a.cache.page_stride +
+                                               (slot + row) * a.cache.token_stride + h * a.cache.head_stride + c * 16);
+        f[i] = gdn::scale_of(a.cache.scales[kv][page * a.cache.scale_page + slot / kGroup * a.cache.scale_group +
+                                                h * a.cache.scale_head]);
+      }
+#pragma unroll
+      for (int i = 0; i < kReadBatch; ++i) {
+        const int j = j0 + i * kExpandThreads;
+        const int c = j % chunks, row = j / chunks % kGroup, head = j / (chunks * kGroup), kv = head >= a.Hkv ? 1 : 0;
+        const int h = head - kv * a.Hkv;
+        if (j >= 2 * per_row * kGroup || row >= rows) continue;
+        const float2 scale = make_float2(f[i], f[i]);
+        const uint2 y0 = gdn::e4m3_to_bf16(x[i].x, scale), y1 = gdn::e4m3_to_bf16(x[i].y, scale);
+        const uint2 y2 = gdn::e4m3_to_bf16(x[i].z, scale), y3 = gdn::e4m3_to_bf16(x[i].w, scale);
+        const uint32_t y[8] = {y0.x, y0.y, y1.x, y1.y, y2.x, y2.y, y3.x, y3.y};
+        gdn::store32(a.out[kv] + ((entry * a.Hkv + h) * a.paged.page_size + slot + row) * a.D + c * 16, y, true);
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------------------- host
 bool bad_norm(const gdn_qk_norm* n, bool q, bool k) {
   return !(n->eps > 0.f) || !isfinite(n->eps) || !isfinite(n->weight_offset) ||
@@ -737,6 +850,20 @@ int launch_append(const AppendArgs& a, dim3 grid, cudaStream_t stream) {
 }
 
 }  // namespace
+
+int gdn_host::expand8(const gdn_kv_cache_fp8* cache, const PagedTokens& paged, int32_t window, gdn_bf16* k, gdn_bf16* v,
+                      int32_t* pages, int sms, cudaStream_t stream) {
+  ExpandArgs a = {};
+  a.cache = cache8(cache);
+  a.paged = paged;
+  a.out[0] = bf(k);
+  a.out[1] = bf(v);
+  a.pages = pages;
+  a.Hkv = cache->num_heads;
+  a.D = cache->head_dim;
+  a.window = window;
+  return launch_pdl(expand8_kernel, dim3(static_cast<unsigned>(6 * sms)), dim3(kExpandThreads), 0, stream, a);
+}
 
 extern "C" int gdn_qk_norm_rope(const gdn_bf16* q, int64_t q_token_stride, gdn_bf16* q_out, int64_t q_out_token_stride,
                                 const gdn_bf16* k, int64_t k_token_stride, gdn_bf16* k_out, int64_t k_out_token_stride,

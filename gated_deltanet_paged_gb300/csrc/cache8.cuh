@@ -137,4 +137,9 @@ inline gdn::Cache8 cache8(const gdn_kv_cache_fp8* c) {
                      c->head_stride, c->scale_page_stride,       c->scale_group_stride, c->scale_head_stride};
 }
 
+// What a batch's new tokens may see, as bf16 pages [num_entries, Hkv, page_size, D] (32-byte
+// aligned) in the order of the table, and their numbers.
+int expand8(const gdn_kv_cache_fp8* cache, const gdn::PagedTokens& paged, int32_t window, gdn_bf16* k, gdn_bf16* v,
+            int32_t* pages, int sms, cudaStream_t stream);
+
 }  // namespace gdn_host

@@ -46,7 +46,7 @@ template <int D, Scores kScores>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_attention_kernel(const __grid_constant__ ChunkArgs d, const __grid_constant__ CUtensorMap q_map,
                            const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-  chunk_attention<D, kScores, false>(d, q_map, k_map, v_map, gdn::Cache8{});
+  chunk_attention<D, kScores, false, false>(d, q_map, k_map, v_map, gdn::Cache8{});
 }
 
 template <int D, Scores kScores>

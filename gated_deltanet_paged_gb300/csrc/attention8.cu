@@ -12,8 +12,9 @@
 // make it 2,048 and the products take as long.  Measured: 3,500.
 //
 // Measured at 32 query heads on 8 key heads of 128: 4 prompts of 8,192 1.75 ms, 1,250
-// TFLOP/s (over a 16-bit cache 1.27); 64 mixed sequences, 16 heads, a cap of 30 and a
-// window, 3.1 ms with scores that often pass the cap's polynomial, 2.8 without.
+// TFLOP/s, by way of a bf16 copy 1.40 (over a 16-bit cache 1.27); 64 mixed sequences, 16 heads, a cap of 30 and a
+// window, 3.1 ms with scores that often pass the cap's polynomial and 2.8 without, by way
+// of a copy 2.8 and 2.4.
 #include "attention_chunk.cuh"
 
 namespace {
@@ -23,7 +24,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     chunk_attention8_kernel(const __grid_constant__ ChunkArgs d, const __grid_constant__ CUtensorMap q_map,
                             const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                             const __grid_constant__ gdn::Cache8 codes) {
-  chunk_attention<D, kScores, true>(d, q_map, k_map, v_map, codes);
+  chunk_attention<D, kScores, true, true>(d, q_map, k_map, v_map, codes);
 }
 
 template <int D, Scores kScores>
@@ -40,13 +41,35 @@ int launch(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache_fp8* cache, voi
                          });
 }
 
+// Under a cap, over a bf16 copy: the scores as over the codes.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_attention8_copied_kernel(const __grid_constant__ ChunkArgs d, const __grid_constant__ CUtensorMap q_map,
+                                   const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+  chunk_attention<D, kCapped, false, true>(d, q_map, k_map, v_map, gdn::Cache8{});
+}
+
+template <int D>
+int launch_copied(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache* cache, void* workspace, int sms, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  CUtensorMap k_map, v_map;
+  int rc;
+  if ((rc = gdn_host::encode_cache_map(&k_map, cache->k, cache, d.a.box_shift)) != GDN_OK) return rc;
+  if ((rc = gdn_host::encode_cache_map(&v_map, cache->v, cache, d.a.box_shift)) != GDN_OK) return rc;
+  const auto kernel = chunk_attention8_copied_kernel<D>;
+  return launch_chunk<D, false>(kernel, d, total_tokens, done, workspace, sms, stream,
+                                [&](dim3 grid, dim3 block, int smem, const CUtensorMap& q_map) {
+                                  return gdn_host::launch_pdl(kernel, grid, block, smem, stream, d, q_map, k_map, v_map);
+                                });
+}
+
 // A bf16 copy of what the batch sees, behind the workspace proper: the pages' numbers, then
 // keys and values.  Written once and read by many rows it takes less time than the
-// conversion of every block for every 256 rows: 4 prompts of 8,192, 32 query heads on 8
-// 1.31 ms in place of 1.75; with fewer than kCopyRows rows per sequence (tokens times query
-// heads per key head) it does not (16 tokens over 131,072: see the file's head).  Not under
-// a cap, where the softmax is what takes the time, and not for more than kCopyMost bytes.
-constexpr int64_t kCopyRows = 1024;
+// conversion of every block for every 256 rows.  At 32 query heads on 8, converted /
+// copied: 2,048 rows per sequence (tokens times query heads per key head) 512 tokens over
+// 8,000 80.6 / 77.3 us, over 131,072 799 / 744, 64 x 512 326 / 277; 8,192 rows 248 / 207; but
+// 1,024 rows 49 / 55, 408 / 455, 133 / 127.  Not for more than kCopyMost bytes.
+constexpr int64_t kCopyRows = 2048;
 constexpr size_t kCopyMost = size_t(8) << 30;
 struct Copy {
   size_t base, pages, kv, total;  // offsets, and bytes; total 0: none
@@ -88,7 +111,7 @@ extern "C" int gdn_attention_paged_fp8(const gdn_bf16* q, int64_t q_token_stride
                             cache->head_dim, table->num_entries, cache->page_size);
   const bool capped = d.a.cap_log2 > 0.f && !d.a.slopes;
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
-  if (copy.total && !capped && workspace_bytes >= copy.total && (reinterpret_cast<uintptr_t>(ws) & 31u) == 0) {
+  if (copy.total && workspace_bytes >= copy.total && (reinterpret_cast<uintptr_t>(ws) & 31u) == 0) {
     int32_t* const pages = reinterpret_cast<int32_t*>(ws + copy.base);
     gdn_bf16* const k = reinterpret_cast<gdn_bf16*>(ws + copy.base + copy.pages);
     gdn_bf16* const v = k + copy.kv / 2;
@@ -97,6 +120,14 @@ extern "C" int gdn_attention_paged_fp8(const gdn_bf16* q, int64_t q_token_stride
     const int64_t D = cache->head_dim, head = D * cache->page_size;
     const gdn_kv_cache whole = {k, v, table->num_entries, cache->page_size, cache->num_heads, cache->head_dim,
                                 head * cache->num_heads, D, head};
+    if (capped) {
+      d.tile_tokens = kRows / d.a.group;
+      d.a.paged.pages = pages;
+      d.a.paged.num_pages = table->num_entries;
+      const cudaStream_t on = static_cast<cudaStream_t>(stream);
+      return D == 64 ? launch_copied<64>(d, total_tokens, &whole, workspace, sms, on)
+                     : launch_copied<128>(d, total_tokens, &whole, workspace, sms, on);
+    }
     gdn_page_table entries = *table;
     entries.page_indices = pages;
     return gdn_attention_paged(q, q_token_stride, o, lse, cu_seqlens, total_tokens, Hq, &whole, &entries, scale, options,

@@ -446,8 +446,9 @@ enum Scores { kPlain, kBiased, kGeneral, kCapped };
 // score and 16 or 24 over that 1.65 and 1.73.
 constexpr float kAbove = 16.f, kOver = 16.f;
 
-// kCodes: the cache is in 8 bits, and `codes` says where its scales are.
-template <int D, Scores kScores, bool kCodes>
+// kCodes: the cache is in 8 bits, and `codes` says where its scales are.  kOneWay: scores
+// under a cap take one way, large or not (attention.cu's results keep their bits by two).
+template <int D, Scores kScores, bool kCodes, bool kOneWay>
 __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtensorMap& q_map, const CUtensorMap& k_map,
                                                 const CUtensorMap& v_map, const gdn::Cache8& codes) {
   using L = Layout<D, kCodes>;
@@ -1139,7 +1140,7 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
             }
             gdn::tmem_st16_nw(s_addr + c / 2, p);
           };
-          if constexpr (kCodes) {
+          if constexpr (kOneWay) {
             // 32 keys at a time and one way for all of them: two copies of it, with the next
             // 32 scores on their way meanwhile, are fetched more slowly than they save,
             // and a rare way of its own for large scores costs thousands of cycles to fetch.

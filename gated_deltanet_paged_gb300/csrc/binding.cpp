@@ -341,7 +341,7 @@ struct Attention {
       if (workspace.size(0) < need)
         fail(PyExc_ValueError, "workspace holds %lld bytes, the call needs %lld", (long long)workspace.size(0), (long long)need);
       if (codes) need = workspace.size(0);
-    } else if (codes && !decode && options.softcap <= 0.f) {
+    } else if (codes && !decode) {
       need = static_cast<int64_t>(gdn_attention_fp8_workspace_bytes(t.num_seqs, T, Hq, Hkv, D, t.num_entries, page_size));
       if (need) workspace = make({need}, at::kByte, device);
     } else if (need) {

@@ -575,7 +575,8 @@ def gdn_attention_paged_fp8(q, k_cache, v_cache, k_scales, v_scales, cu_seqlens,
     """gdn_attention_paged over an 8-bit cache: the same options and outputs.
     ``workspace``: at least gdn_attention_workspace_bytes(...) bytes; with
     gdn_attention_fp8_workspace_bytes(...), which is what the call allocates without
-    one, sequences of many new tokens are turned into bf16 once (same bits, faster)."""
+    one where there is room, what sequences of many new tokens see is turned into
+    bf16 once (same bits, faster)."""
     return (_calls or _load_calls()).attention8(False, q, k_cache, v_cache, k_scales, v_scales, cu_seqlens, page_indices,
                                            page_indptr, last_page_len, scale, softcap, window, slopes, full_lens, o,
                                            lse, return_lse, err_word, workspace)

@@ -70,7 +70,7 @@ int launch_copied(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache* cache, 
 // 8,000 80.6 / 77.3 us, over 131,072 799 / 744, 64 x 512 326 / 277; 8,192 rows 248 / 207; but
 // 1,024 rows 49 / 55, 408 / 455, 133 / 127.  Not for more than kCopyMost bytes.
 constexpr int64_t kCopyRows = 2048;
-constexpr size_t kCopyMost = size_t(8) << 30;
+constexpr size_t kCopyMost = size_t(4) << 30;
 struct Copy {
   size_t base, pages, kv, total;  // offsets, and bytes; total 0: none
 };

@@ -342,8 +342,16 @@ struct Attention {
         fail(PyExc_ValueError, "workspace holds %lld bytes, the call needs %lld", (long long)workspace.size(0), (long long)need);
       if (codes) need = workspace.size(0);
     } else if (codes && !decode) {
+      // What the call has a use for, or where there is no room for that, what it needs.
+      const int64_t least = need;
       need = static_cast<int64_t>(gdn_attention_fp8_workspace_bytes(t.num_seqs, T, Hq, Hkv, D, t.num_entries, page_size));
-      if (need) workspace = make({need}, at::kByte, device);
+      try {
+        if (need) workspace = make({need}, at::kByte, device);
+      } catch (const c10::OutOfMemoryError&) {
+        if (need == least) throw;
+        need = least;
+        if (need) workspace = make({need}, at::kByte, device);
+      }
     } else if (need) {
       workspace = make({need}, at::kByte, device);
     }

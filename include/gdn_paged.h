@@ -584,7 +584,7 @@ int gdn_attention_decode_paged_fp8(const gdn_bf16 *q, int64_t q_token_stride, gd
 
 /* Bytes of workspace that gdn_attention_paged_fp8 has a use for: what it needs,
  * gdn_attention_workspace_bytes(...), and where the sequences have 2,048 rows on
- * average a bf16 copy of every table entry's page besides, up to 8 GB. */
+ * average a bf16 copy of every table entry's page besides, up to 4 GiB. */
 size_t gdn_attention_fp8_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32_t Hq, int32_t Hkv, int32_t D,
                                          int32_t num_entries, int32_t page_size);
 

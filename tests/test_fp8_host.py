@@ -137,3 +137,17 @@ def test_bad_attention(f):
     assert f(options=options(window=3, full_lens=FAKE)) == -2
     big = table(num_entries=100000)
     assert f(table=big, ws=None) == -1 and f(table=big, wsb=16) == -1 and f(table=big, ws=FAKE + 8) == -1
+
+
+def test_workspace_sizes():
+    f, least = gdn.gdn_attention_fp8_workspace_bytes, gdn.gdn_attention_workspace_bytes
+    few = (4, 8191 // 4, 8, 2, 128, 100, 64)       # 2,047 x 4 rows, 4 sequences
+    assert f(*few) == least(*few)
+    many = (4, 2048, 8, 2, 128, 100, 64)           # 2,048 rows each
+    assert f(*many) >= least(*many) + 100 * 64 * 2 * 128 * 2 * 2 + 4 * 100
+    short = (1, 2048, 1, 1, 64, 16, 64)            # nothing is cut: the copy alone
+    assert least(*short) == 0 and f(*short) >= 16 * 64 * 64 * 2 * 2
+    huge = (1, 1 << 20, 8, 8, 128, 1 << 20, 64)    # no copy of more than 4 GiB
+    assert f(*huge) == least(*huge)
+    for bad in ((-1, 2048, 8, 2, 128, 100, 64), (4, 2048, 3, 2, 128, 100, 64), (4, 2048, 8, 2, 96, 100, 64), (4, 2048, 8, 2, 128, 100, 0)):
+        assert f(*bad) == 0

@@ -190,3 +190,24 @@ def test_caps_of_any_size(cap, decode):
     for q_scale in (0.25, 4.0, 30.0):
         b = Batch8(new, prefix, 32, 8, 2, 128, seed=17, q_scale=q_scale).fill()
         check_attention8(b, decode=decode, softcap=cap)
+
+
+def test_without_room_for_a_copy():
+    """Where the larger workspace cannot be had the call does with what it needs."""
+    b = Batch8([700, 40], [0, 300], 16, 8, 1, 64, seed=3).fill()
+    want = gdn.gdn_attention_paged_fp8(b.q, *b.cache, b.cu, *b.table)
+    indices = torch.zeros(600_000, dtype=torch.int32, device="cuda")  # a table with room for 2.4 GB of bf16 pages
+    indices[: b.indices.numel()] = b.indices
+    sizes = (2, 740, 8, 1, 64, indices.numel(), 16)
+    assert gdn.gdn_attention_fp8_workspace_bytes(*sizes) > 2 << 30
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 30)) / total)
+    try:
+        got = gdn.gdn_attention_paged_fp8(b.q, *b.cache, b.cu, indices, b.indptr, b.last)
+        torch.cuda.synchronize()
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert (got.float() - want.float()).abs().max() <= 2.0**-7 * want.float().abs().max()
+    again = gdn.gdn_attention_paged_fp8(b.q, *b.cache, b.cu, indices, b.indptr, b.last)
+    assert torch.equal(again.view(I16), got.view(I16))

@@ -152,6 +152,29 @@ def test_captured_prefill():
     assert all(torch.equal(x.view(I16), y.view(I16)) for x, y in zip(kv, kv2))
 
 
+@pytest.mark.parametrize("opts", [{}, {"softcap": 20.0}])
+def test_captured_prefill_by_way_of_a_copy(opts):
+    """Two captured calls that share one workspace and the copy in it, replayed in turn."""
+    batches = [Batch8([1500, 700], [40, 700], 64, 8, 2, 128, seed=s).fill() for s in (9, 10)]
+    n = batches[0].indices.numel()
+    ws = torch.empty(gdn.gdn_attention_fp8_workspace_bytes(2, 2200, 8, 2, 128, n, 64), dtype=U8, device="cuda")
+    assert ws.numel() > gdn.gdn_attention_workspace_bytes(2, 2200, 8, 2, 128, n, 64)
+    call = lambda b: gdn.gdn_attention_paged_fp8(b.q, *b.cache, b.cu, *b.table, workspace=ws, **opts)  # noqa: E731
+    eager = [call(b) for b in batches]
+    graphs = []
+    for b in batches:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            o = call(b)
+        graphs.append((graph, o))
+    for graph, o in graphs * 2:
+        o.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    for (_, o), want in zip(graphs, eager):
+        assert torch.equal(o.view(I16), want.view(I16))
+
+
 def test_on_another_stream():
     """Work of the caller's stream before and after the calls stays in order."""
     layer = Layer(60, seed=7)

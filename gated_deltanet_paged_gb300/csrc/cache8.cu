@@ -23,7 +23,7 @@
 //   - reading back: a thread takes 16 codes of a head in one row after the other.
 //
 // Measured: norm and rotation of 65,536 tokens of 40 heads of 128 (1.34 GB) 216 us, 6.2
-// TB/s, of 4 tokens 2.2; append of 8 ragged prompts, 32 + 8 heads (408 MB) 82 us, 5.0 TB/s,
+// TB/s, of 4 tokens 2.2; append of 8 ragged prompts, 32 + 8 heads (408 MB) 80 us, 5.1 TB/s,
 // with 16 warps per SM at 122 registers (rows read twice instead of held take fewer
 // registers and 88 to 97 us); of one token for each of 256 sequences 5.6 us, of which most
 // is latency (with all rows of a head to a warp 9.0); 4 x 16,384 tokens of 8 heads read
@@ -483,14 +483,12 @@ __global__ void __launch_bounds__(kAppendWarps<kWide> * 32, kWide ? 2 : 4) appen
   const int per_row = (a.Hq + kPer - 1) / kPer, jobs = (g.rows1 - g.rows0) * per_row;
   constexpr int kAhead = 4;
   Piece<W> pa[kAhead][U], pb[kAhead][U];
-  auto load_queries = [&](int j0) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int j = j0 + i * workers, row = g.rows0 + j / max(per_row, 1), h = j % max(per_row, 1) * kPer + sub;
-      load(a.q + (g.token + row) * a.q_stride + static_cast<int64_t>(h) * D, j < jobs && h < a.Hq, pa[i], pb[i]);
-    }
+  auto load_query = [&](int i, int j) {
+    const int row = g.rows0 + j / max(per_row, 1), h = j % max(per_row, 1) * kPer + sub;
+    load(a.q + (g.token + row) * a.q_stride + static_cast<int64_t>(h) * D, j < jobs && h < a.Hq, pa[i], pb[i]);
   };
-  load_queries(worker);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) load_query(i, worker + i * workers);
   if (a.n.half) {
     for (int r = g.rows0 + warp; r < g.rows1; r += kWarpsOf)
       for (int pair = lane; pair < a.n.half; pair += 32) {
@@ -511,6 +509,7 @@ __global__ void __launch_bounds__(kAppendWarps<kWide> * 32, kWide ? 2 : 4) appen
       if (j >= jobs) break;
       Pairs<W> p[U];
       take(pa[i], pb[i], q_weights, true, row, p);
+      if (kWide || j + kAhead * workers < jobs) load_query(i, j + kAhead * workers);  // groups of a token have few
       if (h >= a.Hq) continue;
       __nv_bfloat16* dst = a.q_out + ((g.token + row) * a.Hq + h) * D;
 #pragma unroll
@@ -521,7 +520,6 @@ __global__ void __launch_bounds__(kAppendWarps<kWide> * 32, kWide ? 2 : 4) appen
         gdn::store_piece<W>(dst + second[u], gdn::pack<W>(y));
       }
     }
-    if (j0 + kAhead * workers < jobs) load_queries(j0 + kAhead * workers);
   }
 
   if (g.page < 0) {

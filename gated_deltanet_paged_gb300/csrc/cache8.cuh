@@ -22,13 +22,8 @@ struct Cache8 {
 // with it could need; it becomes 0.
 __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// Two e4m3 codes as fp16, exactly (NaN stays NaN).
-__device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t two) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
-  return r;
-}
-// The codes in the low and in the high half of a word.
+// Four e4m3 codes as fp16, exactly (NaN stays NaN): those in the low half of a word, and
+// those in the high half.
 __device__ __forceinline__ void e4m3_to_half4(uint32_t four, uint32_t& a, uint32_t& b) {
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
       : "=r"(a), "=r"(b)

@@ -437,13 +437,15 @@ __device__ __forceinline__ void convert_tile(uint32_t codes, const float* scales
 //   kCapped: a cap and no bias.  Small scores take the cap's polynomial straight to the
 //     weights, without a maximum, 32 keys at a time.
 enum Scores { kPlain, kBiased, kGeneral, kCapped };
-// kCapped's reference is set kAbove over the largest score that a row has, or at
-// kAbove to begin with, and moves in the first block with a score of more than kOver
-// over it, either way (the cap alone would bound the weights too, but by 2^80 at 55:
-// times large values they would leave fp32).  So weights stay below 2^16, and the
-// largest of a row is 2^-48 at least.  Moving is slow, and leaves the tiles out of step
-// for a while: 64 mixed sequences take 1.54 ms, with no distance above the largest
-// score and 16 or 24 over that 1.65 and 1.73.
+// kCapped's reference is kAbove to begin with or kAbove over the largest score that a row
+// has, and moves in the first block with a score of more than kOver over it (the cap alone
+// would bound the weights too, but by 2^80 at 55, and from below by nothing: times large
+// or small values they would leave fp32).  A row's first keys may also set it below
+// kAbove: with one way (kOneWay) where all of them score below 0, with two where one of
+// the block's scores is far from 0.  So weights stay below 2^16, and the largest of a row
+// is 2^-48 at least, with one way 2^-17.  Moving is slow, and leaves the tiles out of step
+// for a while: 64 mixed sequences take 1.54 ms, with no distance above the largest score
+// and 16 or 24 over that 1.65 and 1.73.
 constexpr float kAbove = 16.f, kOver = 16.f;
 
 // kCodes: the cache is in 8 bits, and `codes` says where its scales are.  kOneWay: scores
@@ -1159,16 +1161,19 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
               }
               if (!__all_sync(0xFFFFFFFFu, most <= a.cap_near)) cap_far(a, s_addr + c, ref, z);
               if (edge) hide(lo - key0 - c, hi - key0 - c, -INFINITY, z);
-              if (m == -INFINITY && lo < key0 + c + 32 && hi > key0 + c) m = kAbove;
-              if (!__all_sync(0xFFFFFFFFu, fminf(most * a.scale_log2, a.cap_log2) <= ref + kOver)) {
+              // The first keys that a row sees set its reference, downwards too: later ones
+              // only raise it.  Such a row has nothing in O or l that would have to follow.
+              const bool first = m == -INFINITY && lo < key0 + c + 32 && hi > key0 + c;
+              if (__any_sync(0xFFFFFFFFu, first || fminf(most * a.scale_log2, a.cap_log2) > ref + kOver)) {
                 const float top = max32(z);  // over the reference
-                if (__any_sync(0xFFFFFFFFu, top > kOver)) {
+                const bool moves = top > kOver || (first && top < -kAbove);
+                const float to = moves ? ceilf(top + ref) + kAbove : ref;
+                if (__any_sync(0xFFFFFFFFu, moves && !first)) {
                   // O is complete up to this half: S came behind the blocks before, and the
                   // first half's product is waited for.
                   if (c >= 64 && !wait(&sh.mid[t], n & 1)) break;
                   gdn::tc_fence_after();
-                  const float to = top > kOver ? ceilf(top + ref) + kAbove : ref;
-                  const bool none = m == -INFINITY;  // a row that has seen no key yet
+                  const bool none = m == -INFINITY && !first;  // a row that has seen no key yet
                   const float r = move(to, j > 0 || c >= 64);
                   if (none) m = -INFINITY;
                   if (c & 32) {
@@ -1184,9 +1189,11 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
                     }
                     gdn::tmem_st16(s_addr + c / 2 - 16, v);
                   }
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) z[i] += ref - to;
+                } else if (first) {
+                  m = to;
                 }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[i] += ref - to;
               }
               weights(z, c);
               if (c & 32) publish(c > 64);

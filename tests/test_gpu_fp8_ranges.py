@@ -1,0 +1,98 @@
+"""Capped attention over the 8-bit cache at the ends of its range, on the GPU against the
+definition in 64 bits: scores far beyond either end of the cap, rows that see a single
+key, values near either end of what the format holds.  Tolerances as derived in
+attention_util.py."""
+import pytest
+import torch
+
+import gated_deltanet_paged_gb300 as gdn
+from attention_util import Batch, check_attention
+from fp8_util import E4M3, GROUP, U8, Batch8, check_attention8
+
+pytestmark = pytest.mark.gpu
+
+CAPS = [5.0, 30.0, 55.0, 70.0, 100.0, 1e3, 1e4]
+
+
+def put(b, name, of, exponent=0):
+    """Codes of one kind replaced by of(codes, sequence), their scales times 2^exponent."""
+    for i, (c, e) in enumerate(b.codes[name]):
+        c, e = of(c.float(), i).to(E4M3), e + exponent
+        b.codes[name][i] = c, e
+        getattr(b, name)[i] = c.double() * torch.exp2(e.double()).repeat_interleave(GROUP, 0)[: len(c), :, None]
+
+
+def workspace_sizes(b):
+    """(without room for a bf16 copy of what the batch sees, with it)"""
+    sizes = (len(b.new), sum(b.new), b.hq, b.hkv, b.dim, b.indices.numel(), b.ps)
+    return gdn.gdn_attention_workspace_bytes(*sizes), gdn.gdn_attention_fp8_workspace_bytes(*sizes)
+
+
+def check_both_ways(b, **opts):
+    """By way of a bf16 copy, as such a batch goes by itself, and converted in the kernel."""
+    small, large = workspace_sizes(b)
+    assert large > small
+    check_attention8(b, **opts)
+    check_attention8(b, workspace=torch.empty(max(small, 1), dtype=U8, device="cuda")[:small], **opts)
+
+
+# Every score of a row may lie at the lower end: the weights have to be taken relative to
+# the row's largest score, wherever that is (2^(x - 16) is zero for x below -142, and times
+# values of 2^-100 long before).
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("cap", CAPS)
+@pytest.mark.parametrize("sign", [-1.0, 0.0, 1.0])
+@pytest.mark.parametrize("window", [-1, 0, 1, 130])
+def test_values_of_every_size_under_a_cap(decode, cap, sign, window):
+    """sign: where all scores lie, far beyond a small cap; 0: on both sides."""
+    new, prefix, hq, hkv = ([1] * 4, [700, 0, 5, 2000], 8, 2) if decode else ([300, 3, 64], [700, 0, 1300], 32, 1)
+    for exponent in (-100, 100):
+        b = Batch8(new, prefix, 64, hq, hkv, 64, seed=43, q_scale=100.0)
+        if sign:
+            b.q[:] = b.q.abs()
+            put(b, "k", lambda c, i: sign * c.abs())
+        put(b, "v", lambda c, i: c, exponent)
+        b.fill()
+        if decode:
+            check_attention8(b, decode=True, softcap=cap, window=window)
+        else:
+            check_both_ways(b, softcap=cap, window=window)
+
+
+def swing(n, turns):
+    """n numbers between -400, where they begin (turns < 0: at 400), and 400: |turns| times there or back."""
+    return -400 * torch.cos(torch.linspace(0, torch.pi * turns, n) - (0 if turns > 0 else torch.pi))
+
+
+@pytest.mark.parametrize("cap", [30.0, 100.0, 1e3])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("turns", [1, -1, 4, -9])
+def test_scores_from_end_to_end_of_a_cap(cap, dim, decode, turns):
+    """Scores that rise (or fall, or swing) along the keys from one end of the cap to the
+    other: a row's largest one is met first, last, or again and again a little higher."""
+    new, prefix, hq, hkv = ([1] * 4, [700, 0, 5, 2000], 8, 2) if decode else ([300, 3, 64], [700, 0, 1300], 32, 1)
+    b = Batch8(new, prefix, 64, hq, hkv, dim, seed=44, q_scale=30.0, spread=1)
+    b.q[:] = b.q.abs()
+    put(b, "k", lambda c, i: swing(len(c), turns)[:, None, None].expand_as(c))
+    b.fill()
+    if decode:
+        check_attention8(b, decode=True, softcap=cap)
+    else:
+        check_both_ways(b, softcap=cap)
+
+
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("cap", CAPS[4:])
+@pytest.mark.parametrize("size", [2.0**-100, 2.0**100])
+@pytest.mark.parametrize("sign", [-1.0, 0.0, 1.0])
+@pytest.mark.parametrize("window", [-1, 0, 130])
+def test_values_of_every_size_under_a_large_cap_16_bits(decode, cap, size, sign, window):
+    """The same over the 16-bit cache, under caps that leave larger scores."""
+    new, prefix = ([1] * 4, [700, 0, 5, 2000]) if decode else ([300, 3, 64], [700, 0, 1300])
+    b = Batch(new, prefix, 64, 8, 2, 64, seed=43, q_scale=100.0)
+    if sign:
+        b.q[:] = b.q.abs()
+        b.k = [sign * k.abs() for k in b.k]
+    b.v = [(v.float() * size).bfloat16() for v in b.v]
+    check_attention(b.fill(), decode=decode, softcap=cap, window=window)

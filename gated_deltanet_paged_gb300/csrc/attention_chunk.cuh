@@ -329,7 +329,9 @@ __device__ __forceinline__ float max32(const float (&x)[32]) {
 }
 // Of 32 capped scores whose originals are in TMEM columns from addr: those of the groups
 // of four columns in which any row of the warp has a score beyond the polynomial, less
-// `minus`, one group after the other.
+// `minus`, one group after the other.  Keys that a row does not see, and whatever stands
+// in slots that no row sees, choose groups too: the scores within the polynomial have the
+// bits that they had.
 __device__ __forceinline__ void cap_far(const AttnArgs& a, uint32_t addr, float minus, float (&x)[32]) {
   uint32_t groups = 0;
   {
@@ -346,7 +348,7 @@ __device__ __forceinline__ void cap_far(const AttnArgs& a, uint32_t addr, float 
     uint32_t z[4];
     tmem_ld4(addr + 4 * group, z);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) z[k] = __float_as_uint(gdn::capped(__uint_as_float(z[k]), a) - minus);
+    for (int k = 0; k < 4; ++k) z[k] = __float_as_uint(gdn::capped(__uint_as_float(z[k]), a, minus));
 #pragma unroll
     for (int k = 0; k < 32; ++k)
       if (group == k / 4) x[k] = __uint_as_float(z[k % 4]);

@@ -165,16 +165,16 @@ __device__ __forceinline__ float2 capped_near(float2 s, const CapPoly& p, float2
 }
 // The same for one score, rounding by rounding: a score has the same bits whichever
 // of these functions took it, so that what decides between them shows nowhere.
-__device__ __forceinline__ float capped_near(float s, const AttnArgs& a) {
+__device__ __forceinline__ float near_quotient(float s, const AttnArgs& a) {
   const float t = __fmul_rn(s, s);
   float h = fmaf(a.cap_poly[4], t, a.cap_poly[3]);
   h = fmaf(h, t, a.cap_poly[2]);
   h = fmaf(h, t, a.cap_poly[1]);
-  h = fmaf(h, t, a.cap_poly[0]);
-  return __fmul_rn(s, h);
+  return fmaf(h, t, a.cap_poly[0]);
 }
-// Any score.
-__device__ __forceinline__ float capped(float s, const AttnArgs& a) {
+__device__ __forceinline__ float capped_near(float s, const AttnArgs& a) { return __fmul_rn(s, near_quotient(s, a)); }
+// A score beyond cap_near.
+__device__ __forceinline__ float capped_beyond(float s, const AttnArgs& a) {
   const float u = s * a.cap_unit, t = u * u;
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(exp2_approx(u * (2.f * kLog2e)) + 1.f));
@@ -182,8 +182,15 @@ __device__ __forceinline__ float capped(float s, const AttnArgs& a) {
   constexpr float c0 = kCapPoly[0], c1 = kCapPoly[1], c2 = kCapPoly[2], c3 = kCapPoly[3], c4 = kCapPoly[4];
   const float h = fmaf(fmaf(fmaf(fmaf(c4, t, c3), t, c2), t, c1), t, c0);
   if (fabsf(u) <= kCapNear) x = s * a.scale_log2 * h;
-  if (fabsf(s) <= a.cap_near) x = capped_near(s, a);
   return x;
+}
+// Any score.
+__device__ __forceinline__ float capped(float s, const AttnArgs& a) {
+  return fabsf(s) <= a.cap_near ? capped_near(s, a) : capped_beyond(s, a);
+}
+// ... less a reference.
+__device__ __forceinline__ float capped(float s, const AttnArgs& a, float minus) {
+  return fabsf(s) <= a.cap_near ? fmaf(s, near_quotient(s, a), -minus) : capped_beyond(s, a) - minus;
 }
 
 // A line of `total` units in equal pieces for `eff` CTAs: piece c is [start(c),

@@ -1,7 +1,7 @@
 """Capped attention over the 8-bit cache at the ends of its range, on the GPU against the
 definition in 64 bits: scores far beyond either end of the cap, rows that see a single
-key, values near either end of what the format holds.  Tolerances as derived in
-attention_util.py."""
+key, values near either end of what the format holds, and what unread slots may change
+(nothing).  Tolerances as derived in attention_util.py."""
 import pytest
 import torch
 
@@ -11,6 +11,7 @@ from fp8_util import E4M3, GROUP, U8, Batch8, check_attention8
 
 pytestmark = pytest.mark.gpu
 
+I16 = torch.int16
 CAPS = [5.0, 30.0, 55.0, 70.0, 100.0, 1e3, 1e4]
 
 
@@ -96,3 +97,38 @@ def test_values_of_every_size_under_a_large_cap_16_bits(decode, cap, size, sign,
         b.k = [sign * k.abs() for k in b.k]
     b.v = [(v.float() * size).bfloat16() for v in b.v]
     check_attention(b.fill(), decode=decode, softcap=cap, window=window)
+
+
+# A block of keys holds slots that no row sees; their scores are computed along.  Some of
+# the scores that are seen lie beyond the cap's polynomial, so that the others near them
+# are evaluated again.
+@pytest.mark.parametrize("cap", [30.0, 100.0])
+@pytest.mark.parametrize("window", [1, 20, 130])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_unread_slots_change_no_bit_under_a_cap(cap, window, dim):
+    b = Batch8([300, 3, 64], [700, 0, 1300], 64, 32, 1, dim, seed=43, q_scale=cap).fill()
+    want = check_attention8(b, softcap=cap, window=window)
+    small, large = workspace_sizes(b)
+    assert large > small
+
+    def same(size, byte):
+        ws = torch.full((max(size, 1),), byte, dtype=U8, device="cuda")[:size]
+        got = gdn.gdn_attention_paged_fp8(b.q, *b.cache, b.cu, *b.table, softcap=cap, window=window, return_lse=True,
+                                          workspace=ws)
+        for x, y in zip(got, want):
+            assert torch.equal(x.view(I16), y.view(I16)), (size, byte)
+
+    for byte in (0x00, 0x45, 0xC6, 0xFF):  # as bf16 zeros, +-thousands, NaN
+        same(large, byte)
+        same(small, byte)
+    # Tokens before every window, codes and scales.
+    gen = torch.Generator().manual_seed(5)
+    for seq, p in enumerate(b.prefix):
+        page, slot = b.slots(seq, range(max(p - window, 0)))
+        for cache in (b.k_cache, b.v_cache):
+            cache[page, slot] = torch.randint(0, 256, (len(page), 1, dim), generator=gen).to(U8).cuda()
+        for scales in (b.k_scales, b.v_scales):
+            whole = len(page) // 16 * 16
+            scales[page[:whole:16], slot[:whole:16] // 16] = 246
+    same(large, 0xFF)
+    same(small, 0xFF)

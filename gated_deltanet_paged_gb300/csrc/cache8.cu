@@ -45,7 +45,7 @@ using gdn_host::bf;
 struct NormRope {
   const __nv_bfloat16* q_weight;  // nullptr: no norm
   const __nv_bfloat16* k_weight;
-  float eps, offset, inv_dim;
+  float eps, offset, two_over_dim;
   const int64_t* freq;  // nullptr: nothing is rotated
   int32_t half;         // rotated pairs
   int32_t interleaved;
@@ -184,8 +184,9 @@ __device__ __forceinline__ void norm(Pairs<W> (&p)[U], const NormRope& n, const 
   float s = 0.f;
 #pragma unroll
   for (int u = 0; u < U; ++u) s += p[u].squares();
+  s *= 0.5f;  // 256 squares of 2^120 are more than a float
   for (int o = lanes >> 1; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  const float r = rsqrtf(fmaf(s, n.inv_dim, n.eps));
+  const float r = rsqrtf(fmaf(s, n.two_over_dim, n.eps));
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (at + u * lanes >= units) continue;
@@ -817,7 +818,7 @@ NormRope norm_rope(const gdn_qk_norm* n, const int64_t* frequencies, int32_t rot
     r.eps = n->eps;
     r.offset = n->weight_offset;
   }
-  r.inv_dim = 1.f / static_cast<float>(D);
+  r.two_over_dim = 2.f / static_cast<float>(D);
   r.freq = frequencies;
   r.half = rotary_dim / 2;
   r.interleaved = interleaved;

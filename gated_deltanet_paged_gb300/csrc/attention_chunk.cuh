@@ -1154,7 +1154,8 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
               gdn::tmem_ld32(s_addr + c, z);
               if (edge) hide(lo - key0 - c, hi - key0 - c, 0.f, z);  // slots may hold anything
               const float most = largest32(z, 0.f);
-              const float ref = m == -INFINITY ? kAbove : m;
+              const bool unset = m == -INFINITY;  // the row has seen no key yet
+              const float ref = unset ? kAbove : m;
               const float2 minus = make_float2(-ref, -ref);
 #pragma unroll
               for (int i = 0; i < 32; i += 2) {
@@ -1165,8 +1166,8 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
               if (edge) hide(lo - key0 - c, hi - key0 - c, -INFINITY, z);
               // The first keys that a row sees set its reference, downwards too: later ones
               // only raise it.  Such a row has nothing in O or l that would have to follow.
-              const bool first = m == -INFINITY && lo < key0 + c + 32 && hi > key0 + c;
-              if (__any_sync(0xFFFFFFFFu, first || fminf(most * a.scale_log2, a.cap_log2) > ref + kOver)) {
+              if (__any_sync(0xFFFFFFFFu, unset || fminf(most * a.scale_log2, a.cap_log2) > ref + kOver)) {
+                const bool first = unset && lo < key0 + c + 32 && hi > key0 + c;
                 const float top = max32(z);  // over the reference
                 const bool moves = top > kOver || (first && top < -kAbove);
                 const float to = moves ? ceilf(top + ref) + kAbove : ref;
@@ -1175,7 +1176,7 @@ __device__ __forceinline__ void chunk_attention(const ChunkArgs& d, const CUtens
                   // first half's product is waited for.
                   if (c >= 64 && !wait(&sh.mid[t], n & 1)) break;
                   gdn::tc_fence_after();
-                  const bool none = m == -INFINITY && !first;  // a row that has seen no key yet
+                  const bool none = unset && !first;
                   const float r = move(to, j > 0 || c >= 64);
                   if (none) m = -INFINITY;
                   if (c & 32) {

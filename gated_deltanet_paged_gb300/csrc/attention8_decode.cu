@@ -325,10 +325,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int u = 0; u < kSub; ++u) {
           const float ks = sh.scale[stage][0][warp * kSub + u];
           ve[u] = sh.scale[stage][1][warp * kSub + u];
+          // One factor after the other: 2^119 times a large query's is no float, where the
+          // score may be zero.
 #pragma unroll
           for (int v = 0; v < NT; ++v)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[u][v][i] *= unit[v][i & 1] * ks;
+            for (int i = 0; i < 4; ++i) s[u][v][i] = s[u][v][i] * unit[v][i & 1] * ks;
         }
         if (a.cap_log2 > 0.f) {
           float most = 0.f;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import gated_deltanet_paged_gb300 as gdn
-from attention_util import Batch, check_attention
+from attention_util import Batch, check_attention, within
 from fp8_util import E4M3, GROUP, U8, Batch8, check_attention8
 
 pytestmark = pytest.mark.gpu
@@ -132,3 +132,56 @@ def test_unread_slots_change_no_bit_under_a_cap(cap, window, dim):
             scales[page[:whole:16], slot[:whole:16] // 16] = 246
     same(large, 0xFF)
     same(small, 0xFF)
+
+
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("power", [0, 7, 14])
+@pytest.mark.parametrize("dim,hq,hkv", [(64, 4, 2), (128, 1, 1), (128, 40, 4), (64, 34, 2)])
+def test_scores_up_to_the_largest(decode, power, dim, hq, hkv):
+    """Keys and queries of one element, so that scores (up to 0.9 * 2^23) are exact: the key with
+    the largest one takes the whole softmax, and the output is its value, whatever the scales,
+    within two roundings of 2^-8: the output's, and the weight's, which is 2 to the power of
+    the score less the reference, and that is rounded to half a unit of a number of up to
+    2^24 (2^-1), so that the weight lies between 2^-0.5 and 2^0.5 and is no power of two."""
+    new, prefix = ([1] * 4, [700, 0, 5, 2000]) if decode else ([70, 3, 20], [700, 0, 1300])
+    b = Batch8(new, prefix, 64, hq, hkv, dim, seed=45, spread=20)
+    b.q[:] = 0
+    b.q[:, :, 0] = 2.0**power
+    largest = []
+
+    def keys(c, i):  # codes of 0.4 to 56 and one of 448
+        z = torch.zeros_like(c)
+        z[:, :, 0] = torch.exp2(torch.randint(-2, 6, z.shape[:2], generator=torch.Generator().manual_seed(i)).float()) * 1.75
+        largest.append(prefix[i] // 3)
+        z[largest[-1], :, 0] = 448
+        return z
+
+    for i, (c, e) in enumerate(b.codes["k"]):
+        b.codes["k"][i] = c, torch.zeros_like(e)
+    put(b, "k", keys)
+    b.fill()
+    call = gdn.gdn_attention_decode_paged_fp8 if decode else gdn.gdn_attention_paged_fp8
+    o = call(b.q, *b.cache, *([] if decode else [b.cu]), *b.table, scale=1.0)
+    want = torch.cat([b.v[i][p].expand(n, hkv, dim).repeat_interleave(hq // hkv, 1) for i, (p, n) in enumerate(zip(largest, new))])
+    within(o, want, 2.0**-7 * want.abs(), "o")
+
+
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("hq,hkv,dim", [(8, 2, 128), (3, 1, 64), (32, 2, 64)])
+def test_zero_keys_beside_the_largest_one(decode, hq, hkv, dim):
+    """A group's scale may be 2^119 for the sake of an element that the queries do not weigh:
+    its other keys' scores are zero, however large the queries are."""
+    new, prefix = ([1] * 3, [40, 200, 15]) if decode else ([20, 1], [40, 200])
+    b = Batch8(new, prefix, 16, hq, hkv, dim, seed=3)
+    b.q[:] = (b.q.sign() * 2.0**30).bfloat16()
+    b.q[:, :, 0] = 0
+
+    def keys(c, i):
+        z = torch.zeros_like(c)
+        z[::GROUP, :, 0] = 448
+        return z
+
+    for i, (c, e) in enumerate(b.codes["k"]):
+        b.codes["k"][i] = c, torch.full_like(e, 119)
+    put(b, "k", keys)
+    check_attention8(b.fill(), decode=decode)

@@ -576,7 +576,9 @@ def gdn_attention_paged_fp8(q, k_cache, v_cache, k_scales, v_scales, cu_seqlens,
     ``workspace``: at least gdn_attention_workspace_bytes(...) bytes; with
     gdn_attention_fp8_workspace_bytes(...), which is what the call allocates without
     one where there is room, what sequences of many new tokens see is turned into
-    bf16 once (same bits, faster)."""
+    bf16 once (same bits, mostly faster).  That may be twice the bytes of every page
+    of the table, up to 4 GiB: where memory is short, or single tokens over much longer
+    caches stand beside a few long prompts, pass the smaller workspace."""
     return (_calls or _load_calls()).attention8(False, q, k_cache, v_cache, k_scales, v_scales, cu_seqlens, page_indices,
                                            page_indptr, last_page_len, scale, softcap, window, slopes, full_lens, o,
                                            lse, return_lse, err_word, workspace)

@@ -4,17 +4,19 @@
 // memory: tiles of codes come by TMA into two tiles of their own, and the four epilogue
 // warps turn them into bf16 (exactly: a code has 4 significant bits and its scale is a
 // power of two) in the layout that the copies have there.  The products, the softmax and
-// the outputs are bit for bit those over a 16-bit cache that holds the same values.
+// the outputs are bit for bit those over a 16-bit cache that holds the same values, but
+// under a cap without slopes: such scores have a way of their own here, in which references
+// move at other times.
 //
 // Bound: shared memory, then the tensor cores.  Per block of 128 keys and 256 rows at
 // heads of 128 the products read 196 KB and the conversion moves 131 KB (codes in and
 // out of it, bf16 back): 2,560 cycles at 128 bytes a cycle, where a 16-bit cache's copies
 // make it 2,048 and the products take as long.  Measured: 3,500.
 //
-// Measured at 32 query heads on 8 key heads of 128: 4 prompts of 8,192 1.75 ms, 1,250
-// TFLOP/s, by way of a bf16 copy 1.40 (over a 16-bit cache 1.27); 64 mixed sequences, 16 heads, a cap of 30 and a
-// window, 3.1 ms with scores that often pass the cap's polynomial and 2.8 without, by way
-// of a copy 2.8 and 2.4.
+// Measured at 32 query heads on 8 key heads of 128: 4 prompts of 8,192 1.72 to 1.75 ms,
+// 1,250 TFLOP/s, by way of a bf16 copy 1.31 to 1.36 in short runs and 1.40 to 1.48 in long
+// ones; 64 mixed sequences, 16 heads, a cap of 30 and a window, 3.2 ms with scores that
+// often pass the cap's polynomial and 2.8 without, by way of a copy 2.9 and 2.4.
 #include "attention_chunk.cuh"
 
 namespace {
@@ -68,7 +70,14 @@ int launch_copied(ChunkArgs d, int32_t total_tokens, const gdn_kv_cache* cache, 
 // conversion of every block for every 256 rows.  At 32 query heads on 8, converted /
 // copied: 2,048 rows per sequence (tokens times query heads per key head) 512 tokens over
 // 8,000 80.6 / 77.3 us, over 131,072 799 / 744, 64 x 512 326 / 277; 8,192 rows 248 / 207; but
-// 1,024 rows 49 / 55, 408 / 455, 133 / 127.  Not for more than kCopyMost bytes.
+// 1,024 rows 49 / 55, 408 / 455, 133 / 127.  8 x 512 over 4,000: 250 / 245, under a cap 384 /
+// 358; heads of 64 195 / 190, under a cap 322 / 327; 16 query heads on 4 of 64 108 / 112, under
+// a cap 173 / 181 (with 4,096 rows 205 / 193 and 339 / 337).  Not for more than kCopyMost bytes.
+// The host knows no more than the batch's averages, and the limit stands for sequences of
+// one kind: where a few have most rows and the others most keys the copy may take longer
+// (8,192 new tokens beside 15 single ones over 100,000, 16 query heads on 4: 0.79 / 1.43 ms;
+// 4,096 beside 7 over 16,000, 32 on 8: 0.25 / 0.30; but 32,768 beside 60 over 16,000: 7.1 /
+// 6.7).
 constexpr int64_t kCopyRows = 2048;
 constexpr size_t kCopyMost = size_t(4) << 30;
 struct Copy {

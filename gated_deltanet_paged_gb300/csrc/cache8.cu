@@ -224,8 +224,8 @@ template <int W, bool kInterleaved>
 __global__ void __launch_bounds__(kWarps * 32, 5) norm_rope_kernel(const __grid_constant__ NormArgs a) {
   constexpr int U = W == 1 ? 4 : W == 2 ? 2 : 1;  // D / (2 W) <= 32 U
   // Weights and sines wait in shared memory: in registers they leave room for fewer warps,
-  // and HBM is fed by the loads of many (65,536 tokens of 40 heads 216 us, so 236; with 80
-  // registers some are spilled, 251).
+  // and HBM is fed by the loads of many (65,536 tokens of 40 heads 216 us, in registers 236,
+  // and in 80 of them, some spilled, 251).
   __shared__ alignas(16) float cs_all[kWarps][kMaxDim];
   __shared__ alignas(16) float weights[2][kMaxDim];
   gdn::pdl_wait();

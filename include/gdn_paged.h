@@ -452,7 +452,8 @@ int gdn_kv_append_paged(const gdn_bf16 *q, int64_t q_token_stride, gdn_bf16 *q_o
  * scale <= 0 selects 1 / sqrt(D).  D is 64 or 128 and Hq / Hkv at most 128.
  * Slots past a sequence's end and keys outside every token's window are not
  * read into any sum, whatever they hold; the keys and values of a sequence's
- * own tokens inside the window have to be finite.  The sum over the values is
+ * own tokens inside the window have to be finite, and scores below 2^23 in
+ * size, beyond which fp32 leaves them no fraction.  The sum over the values is
  * taken in fp32 with weights below 2^8, under a softcap without slopes between
  * 2^-48 and 2^16: values between 2^-70 and 2^90 in size keep their precision.
  * workspace: device memory, 16-byte aligned, of at least
@@ -571,7 +572,10 @@ int gdn_kv_read_paged_fp8(const gdn_kv_cache_fp8 *cache, const gdn_page_table *t
  * them, 2^-112 to 2^119, in every group that a token sees.  With a workspace of
  * gdn_attention_fp8_workspace_bytes(...) bytes a chunk that many rows read may be
  * turned into bf16 once, into the workspace, instead of for every 256 rows
- * (tokens times query heads per key head): faster, and the same bits. */
+ * (tokens times query heads per key head): mostly faster, and the same bits.
+ * It is decided by the averages of the batch: beside a few sequences of many new
+ * tokens, single ones with much longer caches make the copy the slower way, and
+ * the smaller workspace the better one. */
 int gdn_attention_paged_fp8(const gdn_bf16 *q, int64_t q_token_stride, gdn_bf16 *o, float *lse,
                             const int32_t *cu_seqlens, int32_t total_tokens, int32_t Hq,
                             const gdn_kv_cache_fp8 *cache, const gdn_page_table *table, float scale,
@@ -584,7 +588,8 @@ int gdn_attention_decode_paged_fp8(const gdn_bf16 *q, int64_t q_token_stride, gd
 
 /* Bytes of workspace that gdn_attention_paged_fp8 has a use for: what it needs,
  * gdn_attention_workspace_bytes(...), and where the sequences have 2,048 rows on
- * average a bf16 copy of every table entry's page besides, up to 4 GiB. */
+ * average a bf16 copy of every table entry's page besides, up to 4 GiB (entries
+ * that no sequence reaches, as in a table with room to spare, count too). */
 size_t gdn_attention_fp8_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32_t Hq, int32_t Hkv, int32_t D,
                                          int32_t num_entries, int32_t page_size);
 
